@@ -21,12 +21,18 @@ the modal state or the FIR window by one generated token.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 from ._lib import HyenaError, check, lib  # noqa: F401
 
 __all__ = [
     "HyenaError",
     "ModalWorkspace",
+    "RecurrenceGrads",
+    "RecurrenceWorkspace",
+    "gated_recurrence",
+    "gated_recurrence_backward",
+    "gated_recurrence_decode",
     "last_launch_count",
     "modal_decode",
     "modal_decode_complex",
@@ -42,6 +48,7 @@ __all__ = [
     "short_conv_host",
     "modal_long_conv_packed",
     "modal_state_init",
+    "recurrence_unit_states",
     "short_conv",
     "short_conv_packed",
     "short_conv_dft",
@@ -54,6 +61,7 @@ __all__ = [
 MAX_MODES = 64
 MAX_COMPLEX_MODES = 32
 MAX_TAPS = 128
+RECURRENCE_UNIT = 64
 
 
 def _torch():
@@ -655,4 +663,175 @@ def modal_decode_complex_packed(xp, group, poles, residues, Dskip, state, y=None
     rc = lib().hyena_modal_decode_complex_packed(_ptr(xp), ld, int(group), _ptr(poles), _ptr(residues),
                                                  _ptr(Dskip), _ptr(y), ld_y, _ptr(state), B, D, N, _stream(stream))
     check("hyena_modal_decode_complex_packed", rc)
+    return y
+
+
+# ------------------------------------------------------------ gated recurrence
+
+def _device(x, *others):
+    """The device index that x and the given tensors (None: absent) share,
+    which must be the current one: the call launches there."""
+    torch = _torch()
+    dev = x.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return dev
+
+
+def _reset(t, B, L):
+    torch = _torch()
+    if t is not None and (t.dtype not in (torch.bool, torch.uint8) or tuple(t.shape) != (B, L)
+                          or not t.is_contiguous()):
+        raise ValueError(f"reset must be a contiguous bool or uint8 tensor of shape {(B, L)}")
+    return t
+
+
+class RecurrenceWorkspace:
+    """Device workspace of gated_recurrence and its backward for sequences up
+    to L tokens, zero-filled once at creation."""
+
+    def __init__(self, B: int, L: int, D: int, device=None, stream=None):
+        torch = _torch()
+        n = int(lib().hyena_gated_recurrence_workspace_size(B, L, D))
+        if n == 0:
+            raise ValueError("invalid workspace shape")
+        self.nbytes = n
+        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        check("hyena_modal_workspace_init",
+              lib().hyena_modal_workspace_init(_ptr(self.buf), n, _stream(stream)))
+
+
+def recurrence_unit_states(B: int, L: int, D: int, device=None):
+    """An uninitialised buffer for gated_recurrence's ``unit_states``: the
+    state before each unit of RECURRENCE_UNIT tokens."""
+    torch = _torch()
+    return torch.empty((B, -(-L // RECURRENCE_UNIT), D), dtype=torch.float32, device=device or "cuda")
+
+
+def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normalize=True, y=None, state_in=None,
+                     state_out=None, unit_states=None, workspace: RecurrenceWorkspace | None = None, stream=None):
+    """Gated linear recurrence: s_t = a_t s_{t-1} + w_t v_t with v = x1 x2 and
+    a_t = exp(log_rate sigmoid(gate_t)) (0 where reset_t), y = x3 s + Dskip v;
+    w = sqrt(1 - a^2) with ``normalize``, else 1.
+
+    x1, x2, x3 ([B, L, D] bf16, one row stride), gate ([B, L, D] bf16);
+    log_rate, Dskip: [D] fp32; reset: [B, L] bool or uint8 or None;
+    state_in/state_out: [B, D] fp32 or None (may be the same tensor);
+    unit_states: from recurrence_unit_states, filled for the backward call.
+    Returns y ([B, L, D] bf16, allocated if not given).
+    """
+    torch = _torch()
+    s1, s2, s3, sg = _bld(x1, "x1"), _bld(x2, "x2"), _bld(x3, "x3"), _bld(gate, "gate")
+    _same_ld(s1, s2, s3)
+    B, L, D, ld = s1
+    if s2[:3] != (B, L, D) or s3[:3] != (B, L, D) or sg[:3] != (B, L, D):
+        raise ValueError("x1, x2, x3, gate shapes differ")
+    _f32(log_rate, (D,), "log_rate", False)
+    _f32(Dskip, (D,), "Dskip")
+    _reset(reset, B, L)
+    _f32(state_in, (B, D), "state_in")
+    _f32(state_out, (B, D), "state_out")
+    _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states")
+    if y is None:
+        y = torch.empty((B, L, D), dtype=torch.bfloat16, device=x1.device)
+    yB, yL, yD, ld_y = _bld(y, "y")
+    if (yB, yL, yD) != (B, L, D):
+        raise ValueError("y shape differs from x")
+    if workspace is None:
+        workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
+    _device(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states, workspace.buf)
+    rc = lib().hyena_gated_recurrence(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), sg[3], _ptr(log_rate),
+                                      _ptr(Dskip), _ptr(reset), int(bool(normalize)), _ptr(y), ld_y,
+                                      _ptr(state_in), _ptr(state_out), _ptr(unit_states), B, L, D,
+                                      _ptr(workspace.buf), workspace.nbytes, _stream(stream))
+    check("hyena_gated_recurrence", rc)
+    return y
+
+
+class RecurrenceGrads(NamedTuple):
+    """Gradients of gated_recurrence (dDskip is None without Dskip)."""
+    dx1: object
+    dx2: object
+    dx3: object
+    dgate: object
+    dlog_rate: object
+    dDskip: object
+    dstate_in: object
+
+
+def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states, reset=None, normalize=True,
+                              dstate_out=None, dx1=None, dx2=None, dx3=None, dgate=None, dstate_in=None,
+                              workspace: RecurrenceWorkspace | None = None, stream=None) -> RecurrenceGrads:
+    """Gradients of ``gated_recurrence`` from dy ([B, L, D] bf16) and, if
+    given, the gradient of its last state (dstate_out, [B, D] fp32), with the
+    forward call's inputs and the unit_states it filled.  dx1, dx2, dx3
+    (sharing a row stride), dgate and dstate_in are allocated if not given."""
+    torch = _torch()
+    s1, s2, s3, sg, sd = _bld(x1, "x1"), _bld(x2, "x2"), _bld(x3, "x3"), _bld(gate, "gate"), _bld(dy, "dy")
+    _same_ld(s1, s2, s3)
+    B, L, D, ld = s1
+    if any(s[:3] != (B, L, D) for s in (s2, s3, sg, sd)):
+        raise ValueError("dy, x1, x2, x3, gate shapes differ")
+    _f32(log_rate, (D,), "log_rate", False)
+    _f32(Dskip, (D,), "Dskip")
+    _reset(reset, B, L)
+    _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states", False)
+    _f32(dstate_out, (B, D), "dstate_out")
+    _f32(dstate_in, (B, D), "dstate_in")
+    given = (dx1, dx2, dx3)
+    if any(g is not None for g in given) and any(g is None for g in given):
+        raise ValueError("give all of dx1, dx2, dx3 or none")
+    if dx1 is None:
+        dx1, dx2, dx3 = (torch.empty((B, L, D), dtype=torch.bfloat16, device=x1.device) for _ in range(3))
+    if dgate is None:
+        dgate = torch.empty((B, L, D), dtype=torch.bfloat16, device=x1.device)
+    outs = [_bld(t, n) for t, n in ((dx1, "dx1"), (dx2, "dx2"), (dx3, "dx3"), (dgate, "dgate"))]
+    if any(s[:3] != (B, L, D) for s in outs):
+        raise ValueError("dx1, dx2, dx3, dgate shapes differ from x")
+    if len({s[3] for s in outs[:3]}) != 1:
+        raise ValueError("dx1, dx2, dx3 must share one row stride")
+    if dstate_in is None:
+        dstate_in = torch.empty((B, D), dtype=torch.float32, device=x1.device)
+    dlog_rate = torch.empty(D, dtype=torch.float32, device=x1.device)
+    dDskip = None if Dskip is None else torch.empty(D, dtype=torch.float32, device=x1.device)
+    if workspace is None:
+        workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
+    _device(x1, x2, x3, gate, dy, log_rate, Dskip, reset, unit_states, dstate_out, dx1, dx2, dx3, dgate, dstate_in,
+            workspace.buf)
+    rc = lib().hyena_gated_recurrence_backward(
+        _ptr(dy), sd[3], _ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), sg[3], _ptr(log_rate), _ptr(Dskip),
+        _ptr(reset), int(bool(normalize)), _ptr(unit_states), _ptr(dstate_out), _ptr(dx1), _ptr(dx2), _ptr(dx3),
+        outs[0][3], _ptr(dgate), outs[3][3], _ptr(dlog_rate), _ptr(dDskip), _ptr(dstate_in), B, L, D,
+        _ptr(workspace.buf), workspace.nbytes, _stream(stream))
+    check("hyena_gated_recurrence_backward", rc)
+    return RecurrenceGrads(dx1, dx2, dx3, dgate, dlog_rate, dDskip, dstate_in)
+
+
+def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=True, y=None, stream=None):
+    """One generated token through the gated recurrence: advances ``state``
+    ([B, D] fp32, in place) and returns y ([B, D] or [B, 1, D] like x1).
+    Equals ``gated_recurrence`` on a one-token sequence with state_in =
+    state_out = state, bit for bit."""
+    torch = _torch()
+    (B, D, ld), b2, b3, bg = _bd(x1, "x1"), _bd(x2, "x2"), _bd(x3, "x3"), _bd(gate, "gate")
+    if b2 != (B, D, ld) or b3 != (B, D, ld):
+        raise ValueError("x1, x2, x3 must share shape and row stride")
+    if bg[:2] != (B, D):
+        raise ValueError("gate shape differs from x")
+    _f32(log_rate, (D,), "log_rate", False)
+    _f32(Dskip, (D,), "Dskip")
+    _f32(state, (B, D), "state", False)
+    if y is None:
+        y = torch.empty_like(x1, memory_format=torch.contiguous_format)
+    yB, yD, ld_y = _bd(y, "y")
+    if (yB, yD) != (B, D):
+        raise ValueError("y shape differs from x")
+    _device(x1, x2, x3, gate, log_rate, Dskip, state, y)
+    rc = lib().hyena_gated_recurrence_decode(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), bg[2], _ptr(log_rate),
+                                             _ptr(Dskip), int(bool(normalize)), _ptr(y), ld_y, _ptr(state), B, D,
+                                             _stream(stream))
+    check("hyena_gated_recurrence_decode", rc)
     return y

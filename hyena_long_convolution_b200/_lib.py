@@ -62,6 +62,12 @@ SIGNATURES = {
     "hyena_modal_long_conv_complex_packed": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I64, _P, _P,
                                                   _I, _I, _I, _I, _P, _SZ, _P]),
     "hyena_modal_decode_complex_packed": (_I, [_P, _I64, _I, _P, _P, _P, _P, _I64, _P, _I, _I, _I, _P]),
+    "hyena_gated_recurrence_workspace_size": (_SZ, [_I, _I, _I]),
+    "hyena_gated_recurrence": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _I64, _P, _P, _P,
+                                    _I, _I, _I, _P, _SZ, _P]),
+    "hyena_gated_recurrence_backward": (_I, [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _P,
+                                             _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "hyena_gated_recurrence_decode": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _P, _I, _P, _I64, _P, _I, _I, _P]),
     "hyena_modal_state_init": (_I, [_P, _I, _I, _I, _P]),
     "hyena_workspace_check": (_I, [_P, _P]),
 }

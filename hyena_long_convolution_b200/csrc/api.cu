@@ -434,6 +434,58 @@ hyena_status_t short_decode_impl(const XSource &xs, const hyena_bf16_t *taps, co
     return HYENA_OK;
 }
 
+size_t recurrence_unit_chains(int B, int L, int D)
+{
+    return static_cast<size_t>(B) * ((static_cast<long long>(L) + RT - 1) / RT) * ((D + RCH - 1) / RCH);
+}
+
+// One more [B, L, D] tensor of a call whose B, L, D are known to be valid.
+hyena_status_t check_rows(const void *p, long long ld, int L, int D)
+{
+    if (L == 0) return HYENA_OK;
+    if (!p || ld < D) return HYENA_ERR_INVALID_ARG;
+    if ((ld % 8) || !aligned16(p)) return HYENA_ERR_ALIGNMENT;
+    if (static_cast<long long>(L) * ld * 2 >= (1ll << 40)) return HYENA_ERR_UNSUPPORTED;
+    return HYENA_OK;
+}
+
+// What forward and gradient check alike, and the arguments they share.
+hyena_status_t recurrence_args(RecArgs &a, const hyena_bf16_t *x1, const hyena_bf16_t *x2, const hyena_bf16_t *x3,
+                               int64_t ld_x, const hyena_bf16_t *gate, int64_t ld_g, const float *log_rate,
+                               const float *Dskip, const uint8_t *reset, int B, int L, int D, void *workspace,
+                               size_t workspace_bytes)
+{
+    hyena_status_t st = check_rows(gate, ld_g, L, D);
+    if (st != HYENA_OK) return st;
+    if (!log_rate) return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(log_rate) || (Dskip && !aligned16(Dskip))) return HYENA_ERR_ALIGNMENT;
+    a.x1 = x1;
+    a.x2 = x2;
+    a.x3 = x3;
+    a.ld_x = ld_x;
+    a.gate = gate;
+    a.ld_g = ld_g;
+    a.log_rate = log_rate;
+    a.Dskip = Dskip;
+    a.reset = reset;
+    a.B = B;
+    a.L = L;
+    a.D = D;
+    if (L == 0) return HYENA_OK;
+    a.nCB = (D + RCH - 1) / RCH;
+    a.units = static_cast<int>((static_cast<long long>(L) + RT - 1) / RT);
+    if (recurrence_unit_chains(B, L, D) >= (1ull << 31)) return HYENA_ERR_UNSUPPORTED;
+    a.chains = B * a.nCB;
+    if (workspace == nullptr || workspace_bytes < hyena_gated_recurrence_workspace_size(B, L, D))
+        return HYENA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return HYENA_ERR_ALIGNMENT;
+    const size_t n = static_cast<size_t>(B) * a.units * D;
+    a.P = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + 256);
+    a.A = a.P + n;
+    a.C = a.A + n;
+    return HYENA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -645,6 +697,129 @@ hyena_status_t hyena_short_decode_packed(const hyena_bf16_t *xp, int64_t ld_x, i
     const hyena_status_t st = check_packed(xp, ld_x, group, y, ld_y, B, 1, D);
     if (st != HYENA_OK) return st;
     return short_decode_impl(packed_source(xp, ld_x, group), taps, Dskip, y, ld_y, hist, B, D, K, stream);
+}
+
+size_t hyena_gated_recurrence_workspace_size(int B, int L, int D)
+{
+    if (B < 1 || L < 0 || D < 1 || D % 8) return 0;
+    return 256 + recurrence_unit_chains(B, L, D) * 96 * 16;
+}
+
+hyena_status_t hyena_gated_recurrence(const hyena_bf16_t *x1, const hyena_bf16_t *x2, const hyena_bf16_t *x3,
+                                      int64_t ld_x, const hyena_bf16_t *gate, int64_t ld_g, const float *log_rate,
+                                      const float *Dskip, const uint8_t *reset, int normalize, hyena_bf16_t *y,
+                                      int64_t ld_y, const float *state_in, float *state_out, float *unit_states,
+                                      int B, int L, int D, void *workspace, size_t workspace_bytes, void *stream)
+{
+    hyena_status_t st = check_x(x1, x2, x3, ld_x, y, ld_y, B, L, D);
+    if (st != HYENA_OK) return st;
+    RecArgs a{};
+    st = recurrence_args(a, x1, x2, x3, ld_x, gate, ld_g, log_rate, Dskip, reset, B, L, D, workspace,
+                         workspace_bytes);
+    if (st != HYENA_OK) return st;
+    if ((state_in && !aligned16(state_in)) || (state_out && !aligned16(state_out)) ||
+        (unit_states && !aligned16(unit_states)))
+        return HYENA_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (L == 0) {
+        int launches = 0;
+        st = copy_or_zero(state_out, state_in, static_cast<size_t>(B) * D * sizeof(float), s, launches);
+        if (st == HYENA_OK) g_last_launches = launches;
+        return st;
+    }
+    a.y = y;
+    a.ld_y = ld_y;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    if (unit_states) a.C = unit_states;
+    const int n = launch_recurrence(a, normalize != 0, false, s);
+    if (n < 0) return HYENA_ERR_CUDA;
+    g_last_launches = n;
+    return HYENA_OK;
+}
+
+hyena_status_t hyena_gated_recurrence_backward(const hyena_bf16_t *dy, int64_t ld_dy, const hyena_bf16_t *x1,
+                                               const hyena_bf16_t *x2, const hyena_bf16_t *x3, int64_t ld_x,
+                                               const hyena_bf16_t *gate, int64_t ld_g, const float *log_rate,
+                                               const float *Dskip, const uint8_t *reset, int normalize,
+                                               const float *unit_states, const float *dstate_out, hyena_bf16_t *dx1,
+                                               hyena_bf16_t *dx2, hyena_bf16_t *dx3, int64_t ld_dx,
+                                               hyena_bf16_t *dgate, int64_t ld_dg, float *dlog_rate, float *dDskip,
+                                               float *dstate_in, int B, int L, int D, void *workspace,
+                                               size_t workspace_bytes, void *stream)
+{
+    hyena_status_t st = check_x(x1, x2, x3, ld_x, dy, ld_dy, B, L, D);
+    if (st != HYENA_OK) return st;
+    RecArgs a{};
+    st = recurrence_args(a, x1, x2, x3, ld_x, gate, ld_g, log_rate, Dskip, reset, B, L, D, workspace,
+                         workspace_bytes);
+    if (st != HYENA_OK) return st;
+    st = check_rows(dy, ld_dy, L, D);
+    if (st == HYENA_OK) st = check_rows(dx1, ld_dx, L, D);
+    if (st == HYENA_OK) st = check_rows(dx2, ld_dx, L, D);
+    if (st == HYENA_OK) st = check_rows(dx3, ld_dx, L, D);
+    if (st == HYENA_OK) st = check_rows(dgate, ld_dg, L, D);
+    if (st != HYENA_OK) return st;
+    if (!dlog_rate || (L > 0 && !unit_states)) return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(dlog_rate) || (dDskip && !aligned16(dDskip)) || (unit_states && !aligned16(unit_states)) ||
+        (dstate_out && !aligned16(dstate_out)) || (dstate_in && !aligned16(dstate_in)))
+        return HYENA_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (L == 0) {
+        int launches = 0;
+        st = copy_or_zero(dstate_in, dstate_out, static_cast<size_t>(B) * D * sizeof(float), s, launches);
+        if (st == HYENA_OK) st = copy_or_zero(dlog_rate, nullptr, static_cast<size_t>(D) * sizeof(float), s, launches);
+        if (st == HYENA_OK) st = copy_or_zero(dDskip, nullptr, static_cast<size_t>(D) * sizeof(float), s, launches);
+        if (st == HYENA_OK) g_last_launches = launches;
+        return st;
+    }
+    a.dy = dy;
+    a.ld_dy = ld_dy;
+    a.unit_states = unit_states;
+    a.dstate_out = dstate_out;
+    a.dstate_in = dstate_in;
+    a.dx1 = dx1;
+    a.dx2 = dx2;
+    a.dx3 = dx3;
+    a.ld_dx = ld_dx;
+    a.dgate = dgate;
+    a.ld_dg = ld_dg;
+    a.dlog_rate = dlog_rate;
+    a.dDskip = dDskip;
+    const int n = launch_recurrence(a, normalize != 0, true, s);
+    if (n < 0) return HYENA_ERR_CUDA;
+    g_last_launches = n;
+    return HYENA_OK;
+}
+
+hyena_status_t hyena_gated_recurrence_decode(const hyena_bf16_t *x1, const hyena_bf16_t *x2, const hyena_bf16_t *x3,
+                                             int64_t ld_x, const hyena_bf16_t *gate, int64_t ld_g,
+                                             const float *log_rate, const float *Dskip, int normalize,
+                                             hyena_bf16_t *y, int64_t ld_y, float *state, int B, int D, void *stream)
+{
+    hyena_status_t st = check_x(x1, x2, x3, ld_x, y, ld_y, B, 1, D);
+    if (st == HYENA_OK) st = check_rows(gate, ld_g, 1, D);
+    if (st != HYENA_OK) return st;
+    if (!log_rate || !state) return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(log_rate) || !aligned16(state) || (Dskip && !aligned16(Dskip))) return HYENA_ERR_ALIGNMENT;
+    RecArgs a{};
+    a.x1 = x1;
+    a.x2 = x2;
+    a.x3 = x3;
+    a.ld_x = ld_x;
+    a.gate = gate;
+    a.ld_g = ld_g;
+    a.log_rate = log_rate;
+    a.Dskip = Dskip;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.state_out = state;
+    a.B = B;
+    a.D = D;
+    const int n = launch_recurrence_decode(a, normalize != 0, static_cast<cudaStream_t>(stream));
+    if (n < 0) return HYENA_ERR_CUDA;
+    g_last_launches = n;
+    return HYENA_OK;
 }
 
 hyena_status_t hyena_modal_state_init(float *state, int B, int D, int N, void *stream)

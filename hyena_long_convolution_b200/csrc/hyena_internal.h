@@ -215,4 +215,34 @@ int launch_fir_history(const FirArgs &a, cudaStream_t st);
 int launch_fir_dft(const CUtensorMap &m1, const CUtensorMap &m2, const CUtensorMap &m3, const FirArgs &a,
                    cudaStream_t st);
 
+// ---------------------------------------------------------------- gated recurrence
+// Units of RT tokens (HYENA_RECURRENCE_UNIT) of chains of RCH channels of one
+// batch row; arrays per unit and channel are [B][units][D].
+constexpr int RT = HYENA_RECURRENCE_UNIT;
+constexpr int RCH = 64;
+
+struct RecArgs {
+    const uint16_t *x1, *x2, *x3, *gate, *dy;
+    long long ld_x, ld_g, ld_dy;
+    const float *log_rate, *Dskip;
+    const uint8_t *reset;  // [B][L] or null
+    uint16_t *y;
+    long long ld_y;
+    const float *state_in;  // [B][D] or null
+    float *state_out;       // [B][D] or null (decode: the state, in place)
+    const float *unit_states;  // gradient: state before each unit
+    const float *dstate_out;
+    float *dstate_in;
+    uint16_t *dx1, *dx2, *dx3, *dgate;
+    long long ld_dx, ld_dg;
+    float *dlog_rate, *dDskip;
+    int B, L, D;
+    int nCB, chains, units;  // chains per batch row, B nCB, ceil(L / RT)
+    float *P, *A, *C;        // workspace: unit decays, end states, carries
+};
+
+// Forward (or, with `back`, the gradient); the number of launches or -1.
+int launch_recurrence(const RecArgs &a, bool normalize, bool back, cudaStream_t st);
+int launch_recurrence_decode(const RecArgs &a, bool normalize, cudaStream_t st);
+
 }  // namespace hyena

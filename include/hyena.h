@@ -486,6 +486,95 @@ hyena_status_t hyena_modal_decode_complex_packed(const hyena_bf16_t *xp, int64_t
 hyena_status_t hyena_modal_state_init(float *state, int B, int D, int N, void *stream);
 
 /*
+ * Gated linear recurrence (no counterpart on the pages: the modal filter with
+ * one mode per channel whose pole depends on the token, the mixer of gated
+ * linear recurrent layers), for prefill, chunked prefill and training.
+ *
+ *   l[t] = log_rate[c] * sigmoid(gate[t]);  a[t] = exp(l[t]), 0 where reset[t]
+ *   s[t] = a[t] s[t-1] + w[t] v[t],   v = x1 x2,  s[-1] = state_in
+ *   y[t] = x3[t] s[t] + Dskip[c] v[t]
+ *
+ * with w = sqrt(1 - a^2) when `normalize` is non-zero (the state then keeps
+ * the scale of v whatever the decay) and w = 1 otherwise.
+ *
+ * x1, x2, x3  [B, L, D] bf16, shared row stride ld_x; gate [B, L, D] bf16, row
+ *           stride ld_g (all four may be views of one [B, L, 4D] projection).
+ * log_rate  [D] fp32, device.  Meant to be <= 0 (a decay); a positive value
+ *           grows without normalize and gives NaN with it.
+ * Dskip     [D] fp32, device, or NULL (no skip term).
+ * reset     [B, L] bytes, device, contiguous, or NULL: non-zero starts a new
+ *           sequence at that token (packed documents).  Nothing passes a
+ *           reset, an Inf or NaN neither; a row may be all resets.
+ * state_in, state_out  [B, D] fp32, device, or NULL: the state before the
+ *           first and after the last token; may be the same array.
+ * unit_states  [B, ceil(L / HYENA_RECURRENCE_UNIT), D] fp32, device, or NULL:
+ *           receives the state before each unit of HYENA_RECURRENCE_UNIT
+ *           tokens, which hyena_gated_recurrence_backward takes.
+ * workspace at least hyena_gated_recurrence_workspace_size(B, L, D) bytes,
+ *           zero-filled once by hyena_modal_workspace_init and then used by
+ *           this operator and its gradient alone, with any B, L, D that fit;
+ *           calls sharing it must not overlap in time.
+ * Chunks of whole units reproduce the single pass bit for bit.  L == 0 is
+ * valid: state_out receives state_in (or zeros).  Gates below -87 count as
+ * -87.  Device-side waits are bounded; hyena_workspace_check reports one that
+ * ran out.
+ */
+#define HYENA_RECURRENCE_UNIT 64
+
+size_t hyena_gated_recurrence_workspace_size(int B, int L, int D);
+
+hyena_status_t hyena_gated_recurrence(const hyena_bf16_t *x1, const hyena_bf16_t *x2,
+                                      const hyena_bf16_t *x3, int64_t ld_x,
+                                      const hyena_bf16_t *gate, int64_t ld_g,
+                                      const float *log_rate, const float *Dskip,
+                                      const uint8_t *reset, int normalize,
+                                      hyena_bf16_t *y, int64_t ld_y,
+                                      const float *state_in, float *state_out, float *unit_states,
+                                      int B, int L, int D,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of hyena_gated_recurrence: from dy and dstate_out (NULL: zero),
+ * with the forward call's inputs and the unit_states it filled.
+ *
+ * dx1, dx2, dx3  [B, L, D] bf16, shared row stride ld_dx; dgate [B, L, D] bf16,
+ *           row stride ld_dg.  None may overlap an input.
+ * dlog_rate [D] fp32: summed over tokens and batch rows, written not added to.
+ * dDskip    [D] fp32 or NULL, likewise.
+ * dstate_out, dstate_in  [B, D] fp32 or NULL; may be the same array.  A long
+ *           sequence's gradient may be taken in chunks of whole units from the
+ *           last to the first, dstate_in of one being dstate_out of the next.
+ * Sums run in a fixed order: the same call gives the same bits.  Where w = 0
+ * (log_rate = 0 with normalize) the gradient through w is taken as 0.
+ * L == 0 is valid: dstate_in receives dstate_out (or zeros), the sums 0.
+ */
+hyena_status_t hyena_gated_recurrence_backward(const hyena_bf16_t *dy, int64_t ld_dy,
+                                               const hyena_bf16_t *x1, const hyena_bf16_t *x2,
+                                               const hyena_bf16_t *x3, int64_t ld_x,
+                                               const hyena_bf16_t *gate, int64_t ld_g,
+                                               const float *log_rate, const float *Dskip,
+                                               const uint8_t *reset, int normalize,
+                                               const float *unit_states, const float *dstate_out,
+                                               hyena_bf16_t *dx1, hyena_bf16_t *dx2, hyena_bf16_t *dx3,
+                                               int64_t ld_dx, hyena_bf16_t *dgate, int64_t ld_dg,
+                                               float *dlog_rate, float *dDskip, float *dstate_in,
+                                               int B, int L, int D,
+                                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One generated token through the gated recurrence: state [B, D] fp32 is
+ * advanced in place; element (b, c) of x1, x2, x3, y, gate at b * ld + c.
+ * Equals hyena_gated_recurrence with L = 1 and state_in = state_out = state
+ * bit for bit.  No workspace; one launch.
+ */
+hyena_status_t hyena_gated_recurrence_decode(const hyena_bf16_t *x1, const hyena_bf16_t *x2,
+                                             const hyena_bf16_t *x3, int64_t ld_x,
+                                             const hyena_bf16_t *gate, int64_t ld_g,
+                                             const float *log_rate, const float *Dskip, int normalize,
+                                             hyena_bf16_t *y, int64_t ld_y, float *state,
+                                             int B, int D, void *stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) a device-side error that
  * calls using this workspace recorded: HYENA_ERR_TIMEOUT if a bounded wait
  * ran out, HYENA_OK otherwise.
