@@ -28,6 +28,7 @@ from ._lib import HyenaError, check, lib  # noqa: F401
 __all__ = [
     "HyenaError",
     "ModalWorkspace",
+    "NormGrads",
     "RecurrenceGrads",
     "RecurrenceWorkspace",
     "gated_recurrence",
@@ -49,6 +50,9 @@ __all__ = [
     "modal_long_conv_packed",
     "modal_state_init",
     "recurrence_unit_states",
+    "rms_norm",
+    "rms_norm_backward",
+    "rms_norm_fp8",
     "short_conv",
     "short_conv_packed",
     "short_conv_dft",
@@ -62,6 +66,7 @@ MAX_MODES = 64
 MAX_COMPLEX_MODES = 32
 MAX_TAPS = 128
 RECURRENCE_UNIT = 64
+MAX_NORM_WIDTH = 16384
 
 
 def _torch():
@@ -835,3 +840,147 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
                                              _stream(stream))
     check("hyena_gated_recurrence_decode", rc)
     return y
+
+
+# -------------------------------------------------------------------- RMS norm
+
+def _rows(x, name, dtypes):
+    """[M, D] or [B, L, D] CUDA tensor with unit channel stride and evenly
+    spaced rows -> (rows, D, ld)."""
+    sh, st = x.shape, x.stride()
+    if x.dtype not in dtypes or not x.is_cuda or len(sh) not in (2, 3):
+        raise ValueError(f"{name} must be a CUDA tensor [rows, D] or [B, L, D] of type {' or '.join(map(str, dtypes))}")
+    if st[-1] != 1:
+        raise ValueError(f"{name} must be channel-contiguous")
+    if len(sh) == 2:
+        return sh[0], sh[1], st[0] if sh[0] > 1 else sh[1]
+    B, L, D = sh
+    ld = st[1] if L > 1 else (st[0] if B > 1 else D)
+    if B > 1 and L > 1 and st[0] != L * ld:
+        raise ValueError(f"{name}: batch stride must equal L * row stride")
+    return B * L, D, ld
+
+
+def _dtype_code(t):
+    """hyena_dtype_t of a tensor (bf16 or fp32)."""
+    return 1 if t.dtype == _torch().bfloat16 else 2
+
+
+def _norm_inputs(x, weight, residual, residual_out, rstd):
+    """Checks what both forms of the norm take -> (rows, D, ld_x, ld_r, residual type)."""
+    torch = _torch()
+    M, D, ld = _rows(x, "x", (torch.bfloat16,))
+    if weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != (D,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous fp32 or bf16 tensor of shape {(D,)}")
+    _f32(rstd, (M,), "rstd")
+    ld_r, kind = 0, 1
+    if residual is not None:
+        rM, rD, ld_r = _rows(residual, "residual", (torch.bfloat16, torch.float32))
+        if (rM, rD) != (M, D):
+            raise ValueError("residual shape differs from x")
+        kind = _dtype_code(residual)
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        if _rows(residual_out, "residual_out", (residual.dtype,)) != (M, D, ld_r):
+            raise ValueError("residual_out must have the residual's shape and row stride")
+    return M, D, ld, ld_r, kind
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, rstd=None, stream=None):
+    """Root-mean-square norm of each row of h = x + residual (or x), times
+    weight.  x: [rows, D] or [B, L, D] bf16; weight: [D] fp32 or bf16;
+    residual, residual_out: bf16 or fp32 (residual_out receives h, and may be
+    the residual itself); rstd: [rows] fp32 or None, filled for the backward
+    call.  Returns y (bf16, allocated if not given)."""
+    torch = _torch()
+    M, D, ld, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
+    if y is None:
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    yM, yD, ld_y = _rows(y, "y", (torch.bfloat16,))
+    if (yM, yD) != (M, D):
+        raise ValueError("y shape differs from x")
+    _device(x, weight, residual, residual_out, y, rstd)
+    rc = lib().hyena_rms_norm(_ptr(x), ld, _ptr(residual), _ptr(residual_out), ld_r, kind, _ptr(weight),
+                              _dtype_code(weight), eps, _ptr(y), ld_y, _ptr(rstd), M, D, _stream(stream))
+    check("hyena_rms_norm", rc)
+    return y
+
+
+def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0, q=None, scales=None, rstd=None,
+                 stream=None):
+    """``rms_norm`` with an 8-bit output: returns (q, scales) with y ~ q scale,
+    q float8_e4m3fn of x's shape and one fp32 scale per row (group = 0, shape
+    [rows]) or per 128 channels (group = 128, [rows, ceil(D / 128)])."""
+    torch = _torch()
+    M, D, ld, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (one scale per row) or 128")
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
+    if (qM, qD) != (M, D):
+        raise ValueError("q shape differs from x")
+    want = (M,) if group == 0 else (M, -(-D // 128))
+    if scales is None:
+        scales = torch.empty(want, dtype=torch.float32, device=x.device)
+    _f32(scales, want, "scales")
+    _device(x, weight, residual, residual_out, q, scales, rstd)
+    rc = lib().hyena_rms_norm_fp8(_ptr(x), ld, _ptr(residual), _ptr(residual_out), ld_r, kind, _ptr(weight),
+                                  _dtype_code(weight), eps, _ptr(q), ld_q, _ptr(scales), group, _ptr(rstd), M, D,
+                                  _stream(stream))
+    check("hyena_rms_norm_fp8", rc)
+    return q, scales
+
+
+class NormGrads(NamedTuple):
+    """Gradients of rms_norm: of x, of the residual and of the weight (fp32).
+    The gradient of a bf16 residual is dx itself."""
+    dx: object
+    dresidual: object
+    dweight: object
+
+
+def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidual=None, workspace=None,
+                      stream=None) -> NormGrads:
+    """Gradients of ``rms_norm`` (and of ``rms_norm_fp8``, its rounding passed
+    straight through) from dy (bf16), with h the forward call's residual_out
+    (or its x) and the rstd it filled; dresidual_out: the gradient of
+    residual_out, of h's type, or None.  dx (bf16) and, for an fp32 residual,
+    dresidual (fp32; may be dresidual_out) are allocated if not given;
+    ``workspace``: a uint8 tensor of rms_norm_backward_workspace_size bytes."""
+    torch = _torch()
+    M, D, ld_dy = _rows(dy, "dy", (torch.bfloat16,))
+    hM, hD, ld_h = _rows(h, "h", (torch.bfloat16, torch.float32))
+    if (hM, hD) != (M, D):
+        raise ValueError("h shape differs from dy")
+    if weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != (D,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous fp32 or bf16 tensor of shape {(D,)}")
+    _f32(rstd, (M,), "rstd", False)
+    f32 = h.dtype == torch.float32
+    if dx is None:
+        dx = torch.empty(dy.shape, dtype=torch.bfloat16, device=dy.device)
+    xM, xD, ld_dx = _rows(dx, "dx", (torch.bfloat16,))
+    if (xM, xD) != (M, D):
+        raise ValueError("dx shape differs from dy")
+    if dresidual is not None and not f32:
+        raise ValueError("the gradient of a bf16 residual is dx: give no dresidual")
+    if dresidual is None and f32:
+        dresidual = torch.empty(h.shape, dtype=torch.float32, device=dy.device)
+    lds = [0, 0]
+    for i, (t, n) in enumerate(((dresidual_out, "dresidual_out"), (dresidual, "dresidual"))):
+        if t is not None:
+            rM, rD, lds[i] = _rows(t, n, (h.dtype,))
+            if (rM, rD) != (M, D):
+                raise ValueError(f"{n} shape differs from dy")
+    dweight = torch.empty(D, dtype=torch.float32, device=dy.device)
+    need = int(lib().hyena_rms_norm_backward_workspace_size(M, D))
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dy.device)
+    _device(dy, h, weight, rstd, dresidual_out, dx, dresidual, workspace)
+    rc = lib().hyena_rms_norm_backward(_ptr(dy), ld_dy, _ptr(h), ld_h, _dtype_code(h), _ptr(weight),
+                                       _dtype_code(weight), _ptr(rstd), _ptr(dresidual_out), lds[0], _ptr(dx), ld_dx,
+                                       _ptr(dresidual), lds[1], _ptr(dweight), M, D, _ptr(workspace), workspace.numel(),
+                                       _stream(stream))
+    check("hyena_rms_norm_backward", rc)
+    return NormGrads(dx, dresidual if f32 else dx, dweight)

@@ -26,6 +26,7 @@ STATUS = {
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 SIGNATURES = {
     "hyena_status_string": (ctypes.c_char_p, [_I]),
@@ -68,6 +69,11 @@ SIGNATURES = {
     "hyena_gated_recurrence_backward": (_I, [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _P,
                                              _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
     "hyena_gated_recurrence_decode": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _P, _I, _P, _I64, _P, _I, _I, _P]),
+    "hyena_rms_norm": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I, _F, _P, _I64, _P, _I64, _I, _P]),
+    "hyena_rms_norm_fp8": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I, _F, _P, _I64, _P, _I, _P, _I64, _I, _P]),
+    "hyena_rms_norm_backward_workspace_size": (_SZ, [_I64, _I]),
+    "hyena_rms_norm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I,
+                                     _P, _SZ, _P]),
     "hyena_modal_state_init": (_I, [_P, _I, _I, _I, _P]),
     "hyena_workspace_check": (_I, [_P, _P]),
 }

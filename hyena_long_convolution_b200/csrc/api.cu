@@ -486,6 +486,56 @@ hyena_status_t recurrence_args(RecArgs &a, const hyena_bf16_t *x1, const hyena_b
     return HYENA_OK;
 }
 
+bool is_dtype(hyena_dtype_t t) { return t == HYENA_BF16 || t == HYENA_F32; }
+
+// One tensor of `rows` rows of D elements.
+hyena_status_t check_norm_rows(const void *p, long long ld, long long rows, int D)
+{
+    if (rows < 0 || D < 1) return HYENA_ERR_INVALID_ARG;
+    if (D % 8) return HYENA_ERR_ALIGNMENT;
+    if (D > HYENA_MAX_NORM_WIDTH || rows >= (1ll << 31)) return HYENA_ERR_UNSUPPORTED;
+    if (rows == 0) return HYENA_OK;
+    if (!p || ld < D) return HYENA_ERR_INVALID_ARG;
+    if ((ld % 8) || !aligned16(p)) return HYENA_ERR_ALIGNMENT;
+    return HYENA_OK;
+}
+
+// The arguments that both forms of the norm share.
+hyena_status_t norm_args(NormArgs &a, const hyena_bf16_t *x, int64_t ld_x, const void *residual, void *residual_out,
+                         int64_t ld_r, hyena_dtype_t residual_type, const void *weight, hyena_dtype_t weight_type,
+                         float eps, float *rstd, int64_t rows, int D)
+{
+    hyena_status_t st = check_norm_rows(x, ld_x, rows, D);
+    if (st == HYENA_OK && residual) st = check_norm_rows(residual, ld_r, rows, D);
+    if (st == HYENA_OK && residual_out) st = check_norm_rows(residual_out, ld_r, rows, D);
+    if (st != HYENA_OK) return st;
+    if (!weight || !is_dtype(weight_type) || (residual && !is_dtype(residual_type)) || (residual_out && !residual) ||
+        !(eps >= 0.f))
+        return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(weight) || !aligned16(rstd)) return HYENA_ERR_ALIGNMENT;
+    a.x = x;
+    a.ld_x = ld_x;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.ld_r = ld_r;
+    a.res_kind = residual_type;
+    a.weight = weight;
+    a.weight_bf16 = weight_type == HYENA_BF16;
+    a.eps = eps;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.D = D;
+    return HYENA_OK;
+}
+
+hyena_status_t norm_impl(const NormArgs &a, void *stream)
+{
+    const int n = a.rows == 0 ? 0 : launch_rms_norm(a, static_cast<cudaStream_t>(stream));
+    if (n < 0) return HYENA_ERR_CUDA;
+    g_last_launches = n;
+    return HYENA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -817,6 +867,97 @@ hyena_status_t hyena_gated_recurrence_decode(const hyena_bf16_t *x1, const hyena
     a.B = B;
     a.D = D;
     const int n = launch_recurrence_decode(a, normalize != 0, static_cast<cudaStream_t>(stream));
+    if (n < 0) return HYENA_ERR_CUDA;
+    g_last_launches = n;
+    return HYENA_OK;
+}
+
+hyena_status_t hyena_rms_norm(const hyena_bf16_t *x, int64_t ld_x, const void *residual, void *residual_out,
+                              int64_t ld_r, hyena_dtype_t residual_type, const void *weight,
+                              hyena_dtype_t weight_type, float eps, hyena_bf16_t *y, int64_t ld_y, float *rstd,
+                              int64_t rows, int D, void *stream)
+{
+    NormArgs a{};
+    hyena_status_t st =
+        norm_args(a, x, ld_x, residual, residual_out, ld_r, residual_type, weight, weight_type, eps, rstd, rows, D);
+    if (st == HYENA_OK) st = check_norm_rows(y, ld_y, rows, D);
+    if (st != HYENA_OK) return st;
+    a.y = y;
+    a.ld_y = ld_y;
+    return norm_impl(a, stream);
+}
+
+hyena_status_t hyena_rms_norm_fp8(const hyena_bf16_t *x, int64_t ld_x, const void *residual, void *residual_out,
+                                  int64_t ld_r, hyena_dtype_t residual_type, const void *weight,
+                                  hyena_dtype_t weight_type, float eps, uint8_t *q, int64_t ld_q, float *scales,
+                                  int group, float *rstd, int64_t rows, int D, void *stream)
+{
+    NormArgs a{};
+    hyena_status_t st =
+        norm_args(a, x, ld_x, residual, residual_out, ld_r, residual_type, weight, weight_type, eps, rstd, rows, D);
+    if (st == HYENA_OK) st = check_norm_rows(q, ld_q, rows, D);
+    if (st != HYENA_OK) return st;
+    if (group != 0 && group != 128) return group < 0 ? HYENA_ERR_INVALID_ARG : HYENA_ERR_UNSUPPORTED;
+    if (rows > 0 && !scales) return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(scales)) return HYENA_ERR_ALIGNMENT;
+    a.q = q;
+    a.ld_y = ld_q;
+    a.scales = scales;
+    a.group = group;
+    return norm_impl(a, stream);
+}
+
+size_t hyena_rms_norm_backward_workspace_size(int64_t rows, int D)
+{
+    if (rows < 0 || rows >= (1ll << 31) || D < 1 || D % 8 || D > HYENA_MAX_NORM_WIDTH) return 0;
+    return static_cast<size_t>(norm_parts(rows > 0 ? rows : 1)) * D * sizeof(float);
+}
+
+hyena_status_t hyena_rms_norm_backward(const hyena_bf16_t *dy, int64_t ld_dy, const void *h, int64_t ld_h,
+                                       hyena_dtype_t h_type, const void *weight, hyena_dtype_t weight_type,
+                                       const float *rstd, const void *dresidual_out, int64_t ld_r, hyena_bf16_t *dx,
+                                       int64_t ld_dx, float *dresidual, int64_t ld_dr, float *dweight, int64_t rows,
+                                       int D, void *workspace, size_t workspace_bytes, void *stream)
+{
+    hyena_status_t st = check_norm_rows(dy, ld_dy, rows, D);
+    if (st == HYENA_OK) st = check_norm_rows(h, ld_h, rows, D);
+    if (st == HYENA_OK && dresidual_out) st = check_norm_rows(dresidual_out, ld_r, rows, D);
+    if (st == HYENA_OK && dresidual) st = check_norm_rows(dresidual, ld_dr, rows, D);
+    if (st == HYENA_OK && dx) st = check_norm_rows(dx, ld_dx, rows, D);
+    if (st != HYENA_OK) return st;
+    if (!is_dtype(h_type) || !is_dtype(weight_type) || !weight || !dweight || (rows > 0 && !rstd))
+        return HYENA_ERR_INVALID_ARG;
+    if (dresidual && h_type != HYENA_F32) return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(weight) || !aligned16(rstd) || !aligned16(dweight)) return HYENA_ERR_ALIGNMENT;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        int launches = 0;
+        st = copy_or_zero(dweight, nullptr, static_cast<size_t>(D) * sizeof(float), s, launches);
+        if (st == HYENA_OK) g_last_launches = launches;
+        return st;
+    }
+    if (!workspace || workspace_bytes < hyena_rms_norm_backward_workspace_size(rows, D)) return HYENA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return HYENA_ERR_ALIGNMENT;
+    NormArgs a{};
+    a.dy = dy;
+    a.ld_y = ld_dy;
+    a.h = h;
+    a.ld_h = ld_h;
+    a.res_kind = h_type;
+    a.weight = weight;
+    a.weight_bf16 = weight_type == HYENA_BF16;
+    a.rstd_in = rstd;
+    a.dres_out = dresidual_out;
+    a.ld_r = ld_r;
+    a.dx = dx;
+    a.ld_x = ld_dx;
+    a.dres = dresidual;
+    a.ld_dr = ld_dr;
+    a.dweight = dweight;
+    a.partial = static_cast<float *>(workspace);
+    a.rows = rows;
+    a.D = D;
+    const int n = launch_rms_norm_backward(a, s);
     if (n < 0) return HYENA_ERR_CUDA;
     g_last_launches = n;
     return HYENA_OK;

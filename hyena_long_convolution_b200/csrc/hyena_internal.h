@@ -245,4 +245,42 @@ struct RecArgs {
 int launch_recurrence(const RecArgs &a, bool normalize, bool back, cudaStream_t st);
 int launch_recurrence_decode(const RecArgs &a, bool normalize, cudaStream_t st);
 
+// ---------------------------------------------------------------- RMS norm
+struct NormArgs {
+    const uint16_t *x;  // forward
+    long long ld_x;     // of x, and of dx
+    const void *residual;
+    void *residual_out;
+    long long ld_r;     // of the residual, residual_out, dres_out
+    int res_kind;       // 1 bf16, 2 fp32: type of the residual (gradient: of h)
+    const void *weight;
+    bool weight_bf16;
+    float eps;
+    uint16_t *y;        // bf16 output, or
+    uint8_t *q;         // e4m3 output with
+    float *scales;      // one scale per row (group 0) or per 128 channels
+    int group;
+    long long ld_y;     // of y or q, and of dy
+    float *rstd;
+    long long rows;
+    int D;
+    // gradient
+    const uint16_t *dy;
+    const void *h;
+    long long ld_h;
+    const float *rstd_in;
+    const void *dres_out;
+    uint16_t *dx;
+    float *dres;        // fp32 only
+    long long ld_dr;
+    float *dweight;
+    float *partial;     // workspace [norm_parts(rows)][D]
+};
+
+constexpr int kMaxNormWidth = HYENA_MAX_NORM_WIDTH;
+
+int launch_rms_norm(const NormArgs &a, cudaStream_t st);
+int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st);
+int norm_parts(long long rows);
+
 }  // namespace hyena

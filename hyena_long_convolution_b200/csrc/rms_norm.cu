@@ -1,0 +1,376 @@
+// rms_norm.cu -- root-mean-square norm with the residual's addition, its output
+// in bf16 or in 8 bits with scales, and its gradient, on sm_100a.
+//
+//   h = x + residual, rounded to the residual's type (or h = x)
+//   rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd weight
+//   bf16: y rounded once.  e4m3: for each row (or each 128 channels of it)
+//   scale = max(max|y|, 2^-100) / 448, q = y / scale rounded once.
+// Gradient, with n = h rstd and t = weight dy:
+//   dh = rstd (t - n mean(t n)) + dresidual_out;  dweight = sum over rows dy n
+//
+// One CTA per row holds it in registers between the reduction and the output,
+// so every input is read once; thread i of T owns the 8-channel vectors i,
+// i + T, ...
+#include <cuda_fp8.h>
+
+#include "hyena_device.cuh"
+#include "hyena_internal.h"
+
+namespace hyena {
+
+namespace {
+
+constexpr int kNormThreads = 512;  // most threads of a row
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100: a zero row keeps a finite scale
+constexpr unsigned int kFullMask = 0xffffffffu;
+
+__device__ __forceinline__ void load_bf16x8(float (&v)[8], const uint16_t *p)
+{
+    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = bf16x2_to_float2(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void load_f32x8(float (&v)[8], const float *p)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p + i);
+        v[i] = q.x;
+        v[i + 1] = q.y;
+        v[i + 2] = q.z;
+        v[i + 3] = q.w;
+    }
+}
+
+__device__ __forceinline__ void store_bf16x8(uint16_t *p, const float (&v)[8])
+{
+    uint4 q;
+    q.x = float2_to_bf16x2(make_float2(v[0], v[1]));
+    q.y = float2_to_bf16x2(make_float2(v[2], v[3]));
+    q.z = float2_to_bf16x2(make_float2(v[4], v[5]));
+    q.w = float2_to_bf16x2(make_float2(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(p) = q;
+}
+
+__device__ __forceinline__ void store_f32x8(float *p, const float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+// A tensor of type kind R (0 absent, 1 bf16, 2 fp32), 8 values at element o.
+template <int R>
+__device__ __forceinline__ void load8(float (&v)[8], const void *p, long long o)
+{
+    if constexpr (R == 2)
+        load_f32x8(v, static_cast<const float *>(p) + o);
+    else
+        load_bf16x8(v, static_cast<const uint16_t *>(p) + o);
+}
+
+// The weight, fp32 or bf16 (the same for the whole launch).
+__device__ __forceinline__ void load_weight(float (&v)[8], const void *p, bool bf16, int c)
+{
+    if (bf16)
+        load_bf16x8(v, static_cast<const uint16_t *>(p) + c);
+    else
+        load_f32x8(v, static_cast<const float *>(p) + c);
+}
+
+// Sum over the CTA, the same bits in every thread: within the warps by
+// butterfly, then the warps' sums in order.  `part` is used by one call only.
+__device__ __forceinline__ float block_sum(float v, float *part)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+    for (int w = 1; w < warps; ++w) v += part[w];
+    return v;
+}
+
+// Largest absolute value over the CTA as its bits: as unsigned numbers the bits
+// order as the values, and a NaN's are the largest, so that it shows.
+__device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *part)
+{
+    v = __reduce_max_sync(kFullMask, v);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+    for (int w = 1; w < warps; ++w) v = max(v, part[w]);
+    return v;
+}
+
+__device__ __forceinline__ float scale_of(unsigned int amax_bits)
+{
+    const float a = __uint_as_float(amax_bits);
+    return a < kAmaxFloor ? kAmaxFloor / kE4m3Max : a / kE4m3Max;  // NaN stays
+}
+
+__device__ __forceinline__ void store_e4m3x8(uint8_t *p, const float (&v)[8], float inv)
+{
+    unsigned short h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    uint2 q;
+    q.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
+    q.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+    *reinterpret_cast<uint2 *>(p) = q;
+}
+
+// R: the residual's type kind.  Q: 0 bf16 output, 1 e4m3 with a scale per row,
+// 2 e4m3 with a scale per 128 channels (16 neighbouring threads' vectors).
+template <int VPT, int R, int Q>
+__global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A)
+{
+    __shared__ float sum_part[32];
+    __shared__ unsigned int max_part[32];
+    const long long row = blockIdx.x;
+    const int T = blockDim.x;
+    const uint16_t *x = A.x + row * A.ld_x;
+    float h[VPT][8];
+    float sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+        if (c < A.D) {
+            load_bf16x8(h[k], x + c);
+            if constexpr (R != 0) {
+                float r[8];
+                const long long o = row * A.ld_r + c;
+                load8<R>(r, A.residual, o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[k][i] += r[i];
+                if constexpr (R == 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 f =
+                            bf16x2_to_float2(float2_to_bf16x2(make_float2(h[k][i], h[k][i + 1])));
+                        h[k][i] = f.x;
+                        h[k][i + 1] = f.y;
+                    }
+                    if (A.residual_out) store_bf16x8(static_cast<uint16_t *>(A.residual_out) + o, h[k]);
+                } else if (A.residual_out) {
+                    store_f32x8(static_cast<float *>(A.residual_out) + o, h[k]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sq = __fmaf_rn(h[k][i], h[k][i], sq);
+    }
+    const float rstd = __frsqrt_rn(block_sum(sq, sum_part) / static_cast<float>(A.D) + A.eps);
+    if (A.rstd && threadIdx.x == 0) A.rstd[row] = rstd;
+    unsigned int amax[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+        float w[8];
+        if (c < A.D) {
+            load_weight(w, A.weight, A.weight_bf16, c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0.f;
+        }
+        amax[k] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[k][i] = h[k][i] * rstd * w[i];
+            if constexpr (Q != 0) amax[k] = max(amax[k], __float_as_uint(h[k][i]) & 0x7fffffffu);
+        }
+        if constexpr (Q == 0) {
+            if (c < A.D) store_bf16x8(A.y + row * A.ld_y + c, h[k]);
+        }
+    }
+    if constexpr (Q == 1) {
+#pragma unroll
+        for (int k = 1; k < VPT; ++k) amax[0] = max(amax[0], amax[k]);
+        const float scale = scale_of(block_max(amax[0], max_part));
+        if (threadIdx.x == 0) A.scales[row] = scale;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+            if (c < A.D) store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
+        }
+    } else if constexpr (Q == 2) {
+        const int groups = (A.D + 127) / 128;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            unsigned int m = amax[k];
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, d));
+            const float scale = scale_of(m);
+            const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+            if (c < A.D) {
+                if ((threadIdx.x & 15) == 0) A.scales[row * groups + c / 128] = scale;
+                store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
+            }
+        }
+    }
+}
+
+// Gradient.  A CTA walks the rows blockIdx.x, blockIdx.x + gridDim.x, ... and
+// keeps its channels' part of dweight in registers; the parts go to `partial`
+// [gridDim.x][D].
+template <int VPT, int R>
+__global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const NormArgs A)
+{
+    __shared__ float part[2][32];
+    const int T = blockDim.x;
+    float dw[VPT][8];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
+    int turn = 0;
+    for (long long row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
+        float n[VPT][8], t[VPT][8];
+        const float rstd = A.rstd_in[row];
+        float dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+            if (c < A.D) {
+                float w[8];
+                load8<R == 2 ? 2 : 1>(n[k], A.h, row * A.ld_h + c);
+                load_bf16x8(t[k], A.dy + row * A.ld_y + c);
+                load_weight(w, A.weight, A.weight_bf16, c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    n[k][i] *= rstd;
+                    dw[k][i] = __fmaf_rn(t[k][i], n[k][i], dw[k][i]);
+                    t[k][i] *= w[i];
+                    dot = __fmaf_rn(t[k][i], n[k][i], dot);
+                }
+            }
+        }
+        const float mean = block_sum(dot, part[turn]) / static_cast<float>(A.D);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+            if (c < A.D) {
+                float r[8];
+                if (A.dres_out) {
+                    load8<R == 2 ? 2 : 1>(r, A.dres_out, row * A.ld_r + c);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = __fmaf_rn(rstd, t[k][i] - n[k][i] * mean, r[i]);
+                if (A.dx) store_bf16x8(A.dx + row * A.ld_x + c, r);
+                if constexpr (R == 2) {
+                    if (A.dres) store_f32x8(A.dres + row * A.ld_dr + c, r);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+        if (c < A.D) store_f32x8(A.partial + static_cast<long long>(blockIdx.x) * A.D + c, dw[k]);
+    }
+}
+
+// dweight: the CTAs' parts summed in double, in order.
+__global__ void __launch_bounds__(128) norm_weight_sum_kernel(const float *partial, int parts, int D, float *dweight)
+{
+    const int c = blockIdx.x * blockDim.x + threadIdx.x;
+    if (c >= D) return;
+    double s = 0.;
+    for (int p = 0; p < parts; ++p) s += partial[static_cast<long long>(p) * D + c];
+    dweight[c] = static_cast<float>(s);
+}
+
+// Vectors per thread and threads of a row of D channels.
+struct NormShape {
+    int vpt, threads;
+};
+
+NormShape norm_shape(int D)
+{
+    const int v = D / 8;
+    const int vpt = v <= 256 ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
+    return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
+}
+
+template <int VPT, int Q>
+void forward_r(const NormArgs &a, int threads, cudaStream_t st)
+{
+    const unsigned int rows = static_cast<unsigned int>(a.rows);
+    switch (a.residual ? a.res_kind : 0) {
+        case 0: rms_norm_kernel<VPT, 0, Q><<<rows, threads, 0, st>>>(a); break;
+        case 1: rms_norm_kernel<VPT, 1, Q><<<rows, threads, 0, st>>>(a); break;
+        default: rms_norm_kernel<VPT, 2, Q><<<rows, threads, 0, st>>>(a); break;
+    }
+}
+
+template <int VPT>
+void forward_q(const NormArgs &a, int threads, cudaStream_t st)
+{
+    if (!a.q)
+        forward_r<VPT, 0>(a, threads, st);
+    else if (a.group == 0)
+        forward_r<VPT, 1>(a, threads, st);
+    else
+        forward_r<VPT, 2>(a, threads, st);
+}
+
+template <int VPT>
+void backward_r(const NormArgs &a, int parts, int threads, cudaStream_t st)
+{
+    if (a.res_kind == 2)
+        rms_norm_backward_kernel<VPT, 2><<<parts, threads, 0, st>>>(a);
+    else
+        rms_norm_backward_kernel<VPT, 1><<<parts, threads, 0, st>>>(a);
+}
+
+}  // namespace
+
+int launch_rms_norm(const NormArgs &a, cudaStream_t st)
+{
+    const NormShape s = norm_shape(a.D);
+    if (s.vpt == 1)
+        forward_q<1>(a, s.threads, st);
+    else if (s.vpt == 2)
+        forward_q<2>(a, s.threads, st);
+    else
+        forward_q<4>(a, s.threads, st);
+    HYENA_TRY(cudaGetLastError(), "rms norm launch");
+    return 1;
+}
+
+int norm_parts(long long rows) { return static_cast<int>(rows < 592 ? rows : 592); }
+
+int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st)
+{
+    const NormShape s = norm_shape(a.D);
+    const int parts = norm_parts(a.rows);
+    if (s.vpt == 1)
+        backward_r<1>(a, parts, s.threads, st);
+    else if (s.vpt == 2)
+        backward_r<2>(a, parts, s.threads, st);
+    else
+        backward_r<4>(a, parts, s.threads, st);
+    norm_weight_sum_kernel<<<(a.D + 127) / 128, 128, 0, st>>>(a.partial, parts, a.D, a.dweight);
+    HYENA_TRY(cudaGetLastError(), "rms norm gradient launch");
+    return 2;
+}
+
+}  // namespace hyena

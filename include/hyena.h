@@ -575,6 +575,80 @@ hyena_status_t hyena_gated_recurrence_decode(const hyena_bf16_t *x1, const hyena
                                              int B, int D, void *stream);
 
 /*
+ * Root-mean-square norm over the channels of each row, with the residual's
+ * addition (evo2_flash README, hook table rows "blocks.N.pre_norm" and
+ * "post_norm": the norms between the residual stream and a block's input
+ * projections), in bf16 or, for an 8-bit projection, as e4m3 with scales.
+ *
+ *   h = x + residual, rounded to the residual's type   (no residual: h = x)
+ *   rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd weight
+ *
+ * rows, D   rows >= 0 rows of D channels, D a multiple of 8, at most
+ *           HYENA_MAX_NORM_WIDTH.  Row r of a tensor starts at r * ld (in
+ *           elements, a multiple of 8, >= D).
+ * x         bf16, ld_x.
+ * residual, residual_out  both of type residual_type, ld_r; residual may be
+ *           NULL (then residual_out must be), residual_out may be NULL (the
+ *           sum is not kept) and may be the residual itself (in place).
+ * weight    [D] of type weight_type.  eps >= 0.
+ * y         bf16, ld_y, rounded once.
+ * rstd      [rows] fp32 or NULL: kept for the gradient.
+ * Sums are fp32.  No output but residual_out may overlap an input.
+ */
+typedef enum { HYENA_BF16 = 1, HYENA_F32 = 2 } hyena_dtype_t;
+#define HYENA_MAX_NORM_WIDTH 16384
+
+hyena_status_t hyena_rms_norm(const hyena_bf16_t *x, int64_t ld_x,
+                              const void *residual, void *residual_out, int64_t ld_r,
+                              hyena_dtype_t residual_type,
+                              const void *weight, hyena_dtype_t weight_type, float eps,
+                              hyena_bf16_t *y, int64_t ld_y, float *rstd,
+                              int64_t rows, int D, void *stream);
+
+/*
+ * The same with y as e4m3 codes (one byte each, row stride ld_q a multiple of
+ * 8) and scales: q = y / scale rounded to nearest, y ~ q scale, where scale =
+ * max(max|y|, 2^-100) / 448 over the row (group = 0, scales [rows]) or over
+ * each 128 channels of it (group = 128, scales [rows, ceil(D / 128)]).  The
+ * maximum is taken of the unrounded y; a NaN or Inf among it shows in the
+ * scale and in the codes.
+ */
+hyena_status_t hyena_rms_norm_fp8(const hyena_bf16_t *x, int64_t ld_x,
+                                  const void *residual, void *residual_out, int64_t ld_r,
+                                  hyena_dtype_t residual_type,
+                                  const void *weight, hyena_dtype_t weight_type, float eps,
+                                  uint8_t *q, int64_t ld_q, float *scales, int group, float *rstd,
+                                  int64_t rows, int D, void *stream);
+
+/*
+ * Gradient of hyena_rms_norm (and, rounding passed straight through, of
+ * hyena_rms_norm_fp8), from dy and the gradient of residual_out:
+ *
+ *   n = h rstd;  t = weight dy;  dh = rstd (t - n mean(t n)) + dresidual_out
+ *   dweight = sum over rows of dy n
+ *
+ * dy        bf16, ld_dy.  h: the forward call's residual_out (or its x), of
+ *           type h_type, ld_h.  rstd: as the forward call left it.
+ * dresidual_out  of h's type, ld_r, or NULL (zero).
+ * dx        bf16, ld_dx: dh rounded once; the gradient of x and of a bf16
+ *           residual.  NULL if not wanted.
+ * dresidual fp32, ld_dr, with h_type HYENA_F32 only: dh, the gradient of an
+ *           fp32 residual.  NULL if not wanted; may be dresidual_out itself.
+ * dweight   [D] fp32, summed in a fixed order, written not added to.
+ * workspace at least hyena_rms_norm_backward_workspace_size(rows, D) bytes of
+ *           device memory (no initialisation; not shared by overlapping calls).
+ */
+size_t hyena_rms_norm_backward_workspace_size(int64_t rows, int D);
+
+hyena_status_t hyena_rms_norm_backward(const hyena_bf16_t *dy, int64_t ld_dy,
+                                       const void *h, int64_t ld_h, hyena_dtype_t h_type,
+                                       const void *weight, hyena_dtype_t weight_type,
+                                       const float *rstd, const void *dresidual_out, int64_t ld_r,
+                                       hyena_bf16_t *dx, int64_t ld_dx, float *dresidual, int64_t ld_dr,
+                                       float *dweight, int64_t rows, int D,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) a device-side error that
  * calls using this workspace recorded: HYENA_ERR_TIMEOUT if a bounded wait
  * ran out, HYENA_OK otherwise.
