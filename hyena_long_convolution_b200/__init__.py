@@ -911,7 +911,7 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
                  stream=None):
     """``rms_norm`` with an 8-bit output: returns (q, scales) with y ~ q scale,
     q float8_e4m3fn of x's shape and one fp32 scale per row (group = 0, shape
-    [rows]) or per 128 channels (group = 128, [rows, ceil(D / 128)])."""
+    [rows, 1]) or per 128 channels (group = 128, [rows, ceil(D / 128)])."""
     torch = _torch()
     M, D, ld, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
     if group not in (0, 128):
@@ -921,7 +921,7 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
     qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
     if (qM, qD) != (M, D):
         raise ValueError("q shape differs from x")
-    want = (M,) if group == 0 else (M, -(-D // 128))
+    want = (M, 1 if group == 0 else -(-D // 128))
     if scales is None:
         scales = torch.empty(want, dtype=torch.float32, device=x.device)
     _f32(scales, want, "scales")

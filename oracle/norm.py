@@ -22,8 +22,7 @@ def scales(y, group):
     D = y.shape[1]
     g = D if group == 0 else group
     cols = [np.abs(y[:, i:i + g]).max(1) for i in range(0, D, g)]
-    s = np.maximum(np.stack(cols, 1), AMAX_FLOOR) / E4M3_MAX
-    return s[:, 0] if group == 0 else s
+    return np.maximum(np.stack(cols, 1), AMAX_FLOOR) / E4M3_MAX
 
 
 def backward(dy, h, weight, eps, dh_out=None):

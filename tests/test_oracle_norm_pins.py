@@ -17,7 +17,7 @@ def test_rows_have_unit_mean_square():
 
 def test_scales():
     y = np.array([[1.0, -448.0, 2.0, 0.0, 0.0]])
-    assert onorm.scales(y, 0).tolist() == [1.0]
+    assert onorm.scales(y, 0).tolist() == [[1.0]]
     assert onorm.scales(y, 3).tolist() == [[1.0, 2.0 ** -100 / 448.0]]
 
 
