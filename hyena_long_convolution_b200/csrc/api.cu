@@ -449,6 +449,16 @@ hyena_status_t check_rows(const void *p, long long ld, int L, int D)
     return HYENA_OK;
 }
 
+bool encode_recurrence_maps(RecMaps &maps, const RecArgs &a)
+{
+    const uint16_t *p[5] = {a.x1, a.x2, a.x3, a.gate, a.dy};
+    const long long ld[5] = {a.ld_x, a.ld_x, a.ld_x, a.ld_g, a.ld_dy};
+    for (int k = 0; k < 5; ++k)
+        if (p[k] && !encode_x_map(&maps.m[k], separate_source(p[k], p[k], p[k], ld[k], a.D), 0, a.B, a.L, a.D, RT, RCH))
+            return false;
+    return true;
+}
+
 // What forward and gradient check alike, and the arguments they share.
 hyena_status_t recurrence_args(RecArgs &a, const hyena_bf16_t *x1, const hyena_bf16_t *x2, const hyena_bf16_t *x3,
                                int64_t ld_x, const hyena_bf16_t *gate, int64_t ld_g, const float *log_rate,
@@ -479,10 +489,11 @@ hyena_status_t recurrence_args(RecArgs &a, const hyena_bf16_t *x1, const hyena_b
     if (workspace == nullptr || workspace_bytes < hyena_gated_recurrence_workspace_size(B, L, D))
         return HYENA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return HYENA_ERR_ALIGNMENT;
-    const size_t n = static_cast<size_t>(B) * a.units * D;
-    a.P = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + 256);
-    a.A = a.P + n;
-    a.C = a.A + n;
+    a.tiles = static_cast<unsigned int>(recurrence_unit_chains(B, L, D));
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    a.hdr = reinterpret_cast<unsigned int *>(w);
+    a.rec_unit = reinterpret_cast<uint4 *>(w + kRecHeaderBytes);
+    a.rec_carry = a.rec_unit + static_cast<size_t>(a.tiles) * RCH;
     return HYENA_OK;
 }
 
@@ -752,7 +763,7 @@ hyena_status_t hyena_short_decode_packed(const hyena_bf16_t *xp, int64_t ld_x, i
 size_t hyena_gated_recurrence_workspace_size(int B, int L, int D)
 {
     if (B < 1 || L < 0 || D < 1 || D % 8) return 0;
-    return 256 + recurrence_unit_chains(B, L, D) * 96 * 16;
+    return kRecHeaderBytes + recurrence_unit_chains(B, L, D) * kRecTileBytes;
 }
 
 hyena_status_t hyena_gated_recurrence(const hyena_bf16_t *x1, const hyena_bf16_t *x2, const hyena_bf16_t *x3,
@@ -781,8 +792,10 @@ hyena_status_t hyena_gated_recurrence(const hyena_bf16_t *x1, const hyena_bf16_t
     a.ld_y = ld_y;
     a.state_in = state_in;
     a.state_out = state_out;
-    if (unit_states) a.C = unit_states;
-    const int n = launch_recurrence(a, normalize != 0, false, s);
+    a.C = unit_states;
+    RecMaps maps;
+    if (!encode_recurrence_maps(maps, a)) return HYENA_ERR_CUDA;
+    const int n = launch_recurrence(maps, a, normalize != 0, false, s);
     if (n < 0) return HYENA_ERR_CUDA;
     g_last_launches = n;
     return HYENA_OK;
@@ -836,7 +849,9 @@ hyena_status_t hyena_gated_recurrence_backward(const hyena_bf16_t *dy, int64_t l
     a.ld_dg = ld_dg;
     a.dlog_rate = dlog_rate;
     a.dDskip = dDskip;
-    const int n = launch_recurrence(a, normalize != 0, true, s);
+    RecMaps maps;
+    if (!encode_recurrence_maps(maps, a)) return HYENA_ERR_CUDA;
+    const int n = launch_recurrence(maps, a, normalize != 0, true, s);
     if (n < 0) return HYENA_ERR_CUDA;
     g_last_launches = n;
     return HYENA_OK;

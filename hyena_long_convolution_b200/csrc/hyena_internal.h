@@ -238,11 +238,25 @@ struct RecArgs {
     float *dlog_rate, *dDskip;
     int B, L, D;
     int nCB, chains, units;  // chains per batch row, B nCB, ceil(L / RT)
-    float *P, *A, *C;        // workspace: unit decays, end states, carries
+    unsigned int tiles;      // chains units
+    float *C;                // forward: unit_states or null
+    // workspace: header ([0] next ticket, [1] finished CTAs, [2] error bits,
+    // [3] epoch), then 16-byte records, all with their tag in the third word
+    unsigned int *hdr;
+    uint4 *rec_unit;         // [tiles][RCH]: (P, A), later the gradient's parts
+    uint4 *rec_carry;        // [tiles][RCH / 2]
+};
+constexpr size_t kRecHeaderBytes = 256;
+constexpr size_t kRecTileBytes = (RCH + RCH / 2) * 16;
+
+// Tensor maps [B][L][1][D] over x1, x2, x3, gate and (gradient) dy, boxes of
+// RT tokens x RCH channels.
+struct RecMaps {
+    CUtensorMap m[5];
 };
 
 // Forward (or, with `back`, the gradient); the number of launches or -1.
-int launch_recurrence(const RecArgs &a, bool normalize, bool back, cudaStream_t st);
+int launch_recurrence(const RecMaps &maps, const RecArgs &a, bool normalize, bool back, cudaStream_t st);
 int launch_recurrence_decode(const RecArgs &a, bool normalize, cudaStream_t st);
 
 // ---------------------------------------------------------------- RMS norm
