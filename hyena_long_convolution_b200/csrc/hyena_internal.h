@@ -249,10 +249,10 @@ struct RecArgs {
 constexpr size_t kRecHeaderBytes = 256;
 constexpr size_t kRecTileBytes = (RCH + RCH / 2) * 16;
 
-// Tensor maps [B][L][1][D] over x1, x2, x3, gate and (gradient) dy, boxes of
-// RT tokens x RCH channels.
+// Tensor maps [B][L][1][D], boxes of RT tokens x RCH channels: over x1, x2, x3,
+// gate and (gradient) dy, and over y or dx1, dx2, dx3, dgate.
 struct RecMaps {
-    CUtensorMap m[5];
+    CUtensorMap in[5], out[4];
 };
 
 // Forward (or, with `back`, the gradient); the number of launches or -1.

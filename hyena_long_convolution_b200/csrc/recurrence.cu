@@ -24,10 +24,10 @@
 // are handed out in time-major order by an atomic ticket, so the unit a CTA
 // waits for is always running or done.  A unit publishes 16-byte records whose
 // third word is the launch's epoch; 16 bytes are written and read at once, so a
-// record needs no flag or fence beside it.  The reader looks at the last
-// kLookBack units together: from the nearest known carry it applies the units'
-// (P, A) in order, the operations each unit itself performs, so the result does
-// not depend on what was ready.  The gradient runs the same from the right.
+// record needs no flag or fence beside it.  The reader looks at the last 16 units
+// together: from the nearest known carry it applies the units' (P, A) in order,
+// the operations each unit itself performs, so the result does not depend on
+// what was ready.  The gradient runs the same from the right.
 #include "recurrence_device.cuh"
 
 namespace hyena {
@@ -36,18 +36,19 @@ namespace {
 
 constexpr int kStages = 2;
 constexpr int kTileBytes = RT * RCH * 2;  // one tensor's rows of a unit
-constexpr int kLookBack = 4;
 
 // A unit's rows of one tensor in shared memory as a lane sees them from its
-// segment's first token: word i holds its channel pair of token i.
+// segment's first token: word i holds its channel pair of token i.  Outputs
+// take the place of the inputs they need no more, word for word.
 struct TileRows {
-    const uint32_t *p;
+    uint32_t *p;
     __device__ __forceinline__ uint32_t operator()(int i) const { return p[i * (RCH / 2)]; }
+    __device__ __forceinline__ void put(int i, float2 v) const { p[i * (RCH / 2)] = float2_to_bf16x2(v); }
 };
 
-__device__ __forceinline__ TileRows tile_rows(const unsigned char *stage, int k, int warp, int lane)
+__device__ __forceinline__ TileRows tile_rows(unsigned char *stage, int k, int warp, int lane)
 {
-    return TileRows{reinterpret_cast<const uint32_t *>(stage + k * kTileBytes) + warp * RSEG * (RCH / 2) + lane};
+    return TileRows{reinterpret_cast<uint32_t *>(stage + k * kTileBytes) + warp * RSEG * (RCH / 2) + lane};
 }
 
 // ---------------------------------------------------------------- records
@@ -77,7 +78,7 @@ __device__ __forceinline__ void store_record(uint4 *p, float a, float b, uint32_
 // it.  Unit j of a chain in processing order is tile j chains + chain.
 struct Records {
     uint4 *unit;   // [tiles][RCH]
-    uint4 *carry;  // [tiles][RCH / 2]
+    uint4 *known;  // [tiles][RCH / 2]
     int chains, chain, lane;
     uint32_t epoch;
 
@@ -90,43 +91,47 @@ struct Records {
     }
     __device__ __forceinline__ void publish_carry(int j, float2 C) const
     {
-        store_record(carry + tile(j) * (RCH / 2) + lane, C.x, C.y, epoch);
+        store_record(known + tile(j) * (RCH / 2) + lane, C.x, C.y, epoch);
     }
 
-    // The carry into unit j > 0 (all lanes of a warp).  Gives up after the
-    // bounded wait, with an error bit, and returns zero.
+    // The carry into unit j > 0 (all lanes of a warp).  One load a poll looks at
+    // the first records of the last 16 units: lanes 0-15 at carries,
+    // lanes 16-31 at (P, A).  Once a carry and every unit between are there,
+    // each lane loads its own channels' records, whose tags it checks as well.
+    // Gives up after the bounded wait, with an error bit, and returns zero.
     __device__ __forceinline__ float2 carry_into(int j, unsigned int *error) const
     {
-        const unsigned long long t0 = global_timer_ns();
+        const int back = lane & 15;
+        const bool there = back < j;
+        const size_t at = tile(there ? j - 1 - back : 0);
+        const uint4 *hint = lane < 16 ? known + at * (RCH / 2) : unit + at * RCH;
+        unsigned long long t0 = 0;
         for (;;) {
-            uint4 c[kLookBack], u0[kLookBack - 1], u1[kLookBack - 1];
-#pragma unroll
-            for (int d = 0; d < kLookBack; ++d) {
-                const int i = max(j - 1 - d, 0);
-                c[d] = load_record(carry + tile(i) * (RCH / 2) + lane);
-                if (d < kLookBack - 1) {
-                    u0[d] = load_record(unit + tile(i) * RCH + 2 * lane);
-                    u1[d] = load_record(unit + tile(i) * RCH + 2 * lane + 1);
+            const unsigned int ready = __ballot_sync(kFullMask, there && load_record(hint).z == epoch);
+            const unsigned int carries = ready & 0xffffu, units = ready >> 16;
+            const int k = __ffs(carries) - 1;  // nearest unit whose carry is known
+            if (k >= 0 && ((units + 1u) & ((1u << k) - 1u)) == 0u) {
+                bool ok = true;
+                uint4 r = load_record(known + tile(j - 1 - k) * (RCH / 2) + lane);
+                ok = r.z == epoch;
+                float2 C = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+                for (int d = k - 1; d >= 0; d -= 2) {  // two units' loads at a time
+                    const uint4 *u = unit + tile(j - 1 - d) * RCH + 2 * lane;
+                    const uint4 *v = unit + tile(j - 1 - max(d - 1, 0)) * RCH + 2 * lane;
+                    const uint4 u0 = load_record(u), u1 = load_record(u + 1);
+                    const uint4 v0 = load_record(v), v1 = load_record(v + 1);
+                    ok = ok && u0.z == epoch && u1.z == epoch && v0.z == epoch && v1.z == epoch;
+                    C = carry<true>(make_float2(__uint_as_float(u0.x), __uint_as_float(u1.x)), C,
+                                    make_float2(__uint_as_float(u0.y), __uint_as_float(u1.y)));
+                    if (d > 0)
+                        C = carry<true>(make_float2(__uint_as_float(v0.x), __uint_as_float(v1.x)), C,
+                                        make_float2(__uint_as_float(v0.y), __uint_as_float(v1.y)));
                 }
+                if (__all_sync(kFullMask, ok)) return C;
             }
-            float2 C = bcast2(0.f);
-            // nearest known carry, then forward over the units between
-            int k = kLookBack;
-#pragma unroll
-            for (int d = kLookBack - 1; d >= 0; --d)
-                if (j - 1 - d >= 0 && c[d].z == epoch) k = d;
-            bool found = k < kLookBack;
-#pragma unroll
-            for (int d = kLookBack - 1; d >= 0; --d) {
-                if (d == k) C = make_float2(__uint_as_float(c[d].x), __uint_as_float(c[d].y));
-                if (d < kLookBack - 1 && d < k) {
-                    found = found && u0[d].z == epoch && u1[d].z == epoch;
-                    C = hyena::carry(make_float2(__uint_as_float(u0[d].x), __uint_as_float(u1[d].x)), C,
-                                     make_float2(__uint_as_float(u0[d].y), __uint_as_float(u1[d].y)));
-                }
-            }
-            if (__all_sync(kFullMask, found)) return C;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
+            const unsigned long long t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs) {
                 if (lane == 0) atomicOr(error, kErrLookbackTimeout);
                 return bcast2(0.f);
             }
@@ -155,159 +160,198 @@ __device__ __forceinline__ void finish(const RecArgs &A)
     }
 }
 
-// Where a warp's lane works in a tile.
-struct Place {
-    int b, j, unit, c;    // batch row, place in processing order, unit, first channel of the pair
-    int n, nseg;          // tokens of the segment; segments of the unit that hold tokens
-    long long row;        // b L + t of the segment's first token
-    bool live;            // the channel pair exists
+// A tile: place j in processing order of a chain, the chain's batch row and
+// first channel.  j < 0: no more tiles.
+struct Tile {
+    int j, chain, b, c;
 };
 
-template <bool kBack>
-__device__ __forceinline__ Place place_of(const RecArgs &A, unsigned int tile, int warp, int lane)
+__device__ __forceinline__ Tile tile_of(const RecArgs &A, unsigned int ticket)
 {
-    Place p;
-    p.j = static_cast<int>(tile / static_cast<unsigned int>(A.chains));
-    const int chain = static_cast<int>(tile - static_cast<unsigned int>(p.j) * A.chains);
-    p.unit = kBack ? A.units - 1 - p.j : p.j;
-    p.b = chain / A.nCB;
-    p.c = (chain - p.b * A.nCB) * RCH + 2 * lane;
-    p.live = p.c < A.D;
-    if (!p.live) p.c = 0;  // reads a channel that exists, writes nothing
-    const int t0 = p.unit * RT;
-    const int rows = min(RT, A.L - t0);
-    p.nseg = (rows + RSEG - 1) / RSEG;
-    p.n = min(max(rows - warp * RSEG, 0), RSEG);
-    p.row = static_cast<long long>(p.b) * A.L + t0 + warp * RSEG;
-    return p;
+    Tile t{-1, 0, 0, 0};
+    if (ticket < A.tiles) {
+        t.j = static_cast<int>(ticket / static_cast<unsigned int>(A.chains));
+        t.chain = static_cast<int>(ticket - static_cast<unsigned int>(t.j) * A.chains);
+        t.b = t.chain / A.nCB;
+        t.c = (t.chain - t.b * A.nCB) * RCH;
+    }
+    return t;
 }
 
-// Requests a tile's rows of N tensors; one thread.
+// What forward and gradient share: two stages of N tensors' rows, their tiles
+// and barriers.  A tile's outputs leave from its stage by TMA; the stage is
+// asked to take new rows half a tile later, when that has read it.
 template <int N, bool kBack>
-__device__ __forceinline__ void request(const RecMaps &m, const RecArgs &A, unsigned int tile, unsigned char *stage,
-                                        uint64_t *bar)
-{
-    const int j = static_cast<int>(tile / static_cast<unsigned int>(A.chains));
-    const int chain = static_cast<int>(tile - static_cast<unsigned int>(j) * A.chains);
-    const int b = chain / A.nCB;
-    const int c = (chain - b * A.nCB) * RCH;
-    const int t = (kBack ? A.units - 1 - j : j) * RT;
-    mbar_arrive_expect_tx(bar, N * kTileBytes);
-#pragma unroll
-    for (int k = 0; k < N; ++k) tma_load_4d(stage + k * kTileBytes, &m.m[k], bar, c, 0, t, b);
-}
+struct Pipeline {
+    Tile tile[kStages];
+    uint64_t full[kStages];
 
-__device__ __forceinline__ uint32_t output_pair(float2 x3, float2 s, bool skip, float2 dsk, float2 v)
-{
-    const float2 o = __fmul2_rn(x3, s);
-    return float2_to_bf16x2(skip ? __ffma2_rn(dsk, v, o) : o);
-}
+    __device__ __forceinline__ void request(const RecMaps &m, const RecArgs &A, unsigned char *stages, int s, Tile t)
+    {
+        tile[s] = t;
+        if (t.j < 0) return;
+        const int row = (kBack ? A.units - 1 - t.j : t.j) * RT;
+        unsigned char *stage = stages + s * N * kTileBytes;
+        mbar_arrive_expect_tx(&full[s], N * kTileBytes);
+#pragma unroll
+        for (int k = 0; k < N; ++k) tma_load_4d(stage + k * kTileBytes, &m.in[k], &full[s], t.c, 0, row, t.b);
+    }
+    __device__ __forceinline__ void start(const RecMaps &m, const RecArgs &A, unsigned char *stages)
+    {
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+        fence_mbar_init();
+        for (int s = 0; s < kStages; ++s) request(m, A, stages, s, tile_of(A, next_tile(A, s)));
+    }
+};
+
+// A CTA: RWARPS warps that compute, and one that takes tickets, runs the copies
+// and finds the carries, so that the computing warps' registers do not have to
+// hold its work too.  The three barriers of a tile are all of the CTA's threads'.
+constexpr int kThreads = (RWARPS + 1) * 32;
+
+__device__ __forceinline__ void tile_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // ---------------------------------------------------------------- forward
 
 struct ForwardShared {
     float2 P[RWARPS][32], l[RWARPS][32], A[RWARPS][32];
-    float2 C[32];
-    uint64_t full[kStages];
-    unsigned int tile[kStages];
+    float2 C[RWARPS][32];  // the state before each segment
+    Pipeline<4, false> pipe;
 };
 
+template <bool kNorm, bool kReset, bool kFull>
+__device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *stage, int warp, int lane, int n,
+                                             float2 rate, bool skip, float2 dsk, unsigned int mask)
+{
+    const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
+    const TileRows x3 = tile_rows(stage, 2, warp, lane);
+    float2 a[RSEG], u[RSEG], l, P;
+    segment_gates<kNorm, kReset, kFull>(a, u, l, P, tile_rows(stage, 3, warp, lane), n, rate, mask);
+#pragma unroll
+    for (int i = 0; i < RSEG; ++i) {
+        if (kFull || i < n) {
+            const float2 v = product(x1(i), x2(i));
+            u[i] = kNorm ? __fmul2_rn(u[i], v) : v;
+        }
+    }
+    sh.l[warp][lane] = l;
+    sh.P[warp][lane] = P;
+    sh.A[warp][lane] = segment_end<kReset, kFull>(a, u, n, mask);
+    tile_barrier();
+    tile_barrier();
+    float2 C = sh.C[warp][lane];
+#pragma unroll
+    for (int i = 0; i < RSEG; ++i) {
+        if (kFull || i < n) {
+            C = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], C, u[i]);
+            float2 o = __fmul2_rn(bf16x2_to_float2(x3(i)), C);
+            if (skip) o = __ffma2_rn(dsk, product(x1(i), x2(i)), o);
+            x3.put(i, o);  // y takes x3's place
+        }
+    }
+}
+
+// Between the first two barriers of a tile: from the segments' sums the unit's
+// (P, A), the carry into it and the state before each segment.
+template <bool kReset>
+__device__ __forceinline__ void forward_carry(const RecArgs &A, ForwardShared &sh, Records &rec, Tile t, int nseg,
+                                              int c, bool live)
+{
+    const int lane = rec.lane;
+    float2 l = sh.l[0][lane], a = sh.A[0][lane];
+#pragma unroll
+    for (int w = 1; w < RWARPS; ++w) {
+        if (w < nseg) {
+            l = __fadd2_rn(l, sh.l[w][lane]);
+            a = carry<kReset>(sh.P[w][lane], a, sh.A[w][lane]);
+        }
+    }
+    const float2 P = decay_over(l);
+    const bool last = t.j == A.units - 1;
+    const size_t state = static_cast<size_t>(t.b) * A.D + c;
+    float2 C = bcast2(0.f);
+    rec.chain = t.chain;
+    if (t.j > 0) {
+        if (!last) rec.publish_unit(t.j, P, a);
+        C = rec.carry_into(t.j, A.hdr + 2);
+    } else if (A.state_in != nullptr) {
+        C = *reinterpret_cast<const float2 *>(A.state_in + state);
+    }
+    const float2 E = carry<true>(P, C, a);
+    if (!last) rec.publish_carry(t.j, E);
+    if (live) {
+        if (A.C != nullptr)
+            *reinterpret_cast<float2 *>(A.C + (static_cast<size_t>(t.b) * A.units + t.j) * A.D + c) = C;
+        if (last && A.state_out != nullptr) *reinterpret_cast<float2 *>(A.state_out + state) = E;
+    }
+#pragma unroll
+    for (int w = 0; w < RWARPS; ++w) {
+        if (w < nseg) {
+            sh.C[w][lane] = C;
+            C = carry<kReset>(sh.P[w][lane], C, sh.A[w][lane]);
+        }
+    }
+}
+
 template <bool kNorm, bool kReset>
-__global__ void __launch_bounds__(RWARPS * 32, 3)
+__global__ void __launch_bounds__(kThreads, 3)
     recurrence_kernel(const __grid_constant__ RecMaps maps, const RecArgs A)
 {
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ ForwardShared sh;
-    constexpr int N = 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == RWARPS * 32) sh.pipe.start(maps, A, stages);
     Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
-        fence_mbar_init();
-        for (int s = 0; s < kStages; ++s) {
-            sh.tile[s] = next_tile(A, s);
-            if (sh.tile[s] < A.tiles) request<N, false>(maps, A, sh.tile[s], stages + s * N * kTileBytes, &sh.full[s]);
-        }
-    }
     if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
-    __syncthreads();
+    tile_barrier();
+    unsigned int next = 0;
     for (int it = 0;; ++it) {
         const int st = it % kStages;
-        const unsigned int tile = sh.tile[st];
-        if (tile >= A.tiles) break;
-        const Place p = place_of<false>(A, tile, warp, lane);
-        rec.chain = static_cast<int>(tile % static_cast<unsigned int>(A.chains));
-        const unsigned char *stage = stages + st * N * kTileBytes;
-        const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
-        const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
-        const float2 rate = ldg_f2(A.log_rate + p.c);
-        const float2 dsk = A.Dskip != nullptr ? ldg_f2(A.Dskip + p.c) : bcast2(0.f);
-        const unsigned int mask = kReset ? segment_resets(A.reset, p.row, p.n, lane) : 0u;
-        const size_t state = static_cast<size_t>(p.b) * A.D + p.c;
-        if (!mbar_wait_bounded(&sh.full[st], (it / kStages) & 1) && threadIdx.x == 0)
-            atomicOr(A.hdr + 2, kErrTmaTimeout);
-
-        RecSegment s;
-        segment_gates<kNorm, kReset>(s, gate, p.n, rate, mask);
-        sh.l[warp][lane] = s.l;
-        sh.P[warp][lane] = decay_over(s.l);
-        sh.A[warp][lane] = segment_end<kNorm, kReset>(s, x1, x2, p.n, mask);
-        __syncthreads();
-        unsigned int next = 0;
-        if (threadIdx.x == 32) next = next_tile(A, it + kStages);
-        if (warp == 0) {
-            float2 l = sh.l[0][lane], a = sh.A[0][lane];
-#pragma unroll
-            for (int w = 1; w < RWARPS; ++w) {
-                if (w < p.nseg) {
-                    l = __fadd2_rn(l, sh.l[w][lane]);
-                    a = carry(sh.P[w][lane], a, sh.A[w][lane]);
+        const Tile t = sh.pipe.tile[st];
+        if (t.j < 0) break;
+        unsigned char *stage = stages + st * 4 * kTileBytes;
+        const int rows = min(RT, A.L - t.j * RT);
+        const bool live = t.c + 2 * lane < A.D;
+        const int c = live ? t.c + 2 * lane : 0;  // lanes without channels read some, and write nothing
+        if (warp < RWARPS) {
+            const int n = min(max(rows - warp * RSEG, 0), RSEG);
+            const float2 rate = ldg_f2(A.log_rate + c);
+            const bool skip = A.Dskip != nullptr;
+            const float2 dsk = skip ? ldg_f2(A.Dskip + c) : bcast2(0.f);
+            const unsigned int mask =
+                kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + t.j * RT + warp * RSEG, n, lane)
+                       : 0u;
+            if (!mbar_wait_bounded(&sh.pipe.full[st], (it / kStages) & 1) && threadIdx.x == 0)
+                atomicOr(A.hdr + 2, kErrTmaTimeout);
+            if (rows == RT)
+                forward_tile<kNorm, kReset, true>(sh, stage, warp, lane, RSEG, rate, skip, dsk, mask);
+            else
+                forward_tile<kNorm, kReset, false>(sh, stage, warp, lane, n, rate, skip, dsk, mask);
+            fence_proxy_async_smem();
+            tile_barrier();
+        } else {
+            if (lane == 0) {
+                if (it > 0) {
+                    bulk_wait_read();
+                    sh.pipe.request(maps, A, stages, st ^ 1, tile_of(A, next));
                 }
+                next = next_tile(A, it + kStages);
             }
-            const float2 P = decay_over(l);
-            const bool last = p.j == A.units - 1;
-            float2 C = bcast2(0.f);
-            if (p.j > 0) {
-                if (!last) rec.publish_unit(p.j, P, a);
-                C = rec.carry_into(p.j, A.hdr + 2);
-            } else if (A.state_in != nullptr) {
-                C = *reinterpret_cast<const float2 *>(A.state_in + state);
-            }
-            sh.C[lane] = C;
-            const float2 E = carry(P, C, a);
-            if (!last) rec.publish_carry(p.j, E);
-            if (p.live) {
-                if (A.C != nullptr)
-                    *reinterpret_cast<float2 *>(A.C + (static_cast<size_t>(p.b) * A.units + p.unit) * A.D + p.c) = C;
-                if (last && A.state_out != nullptr) *reinterpret_cast<float2 *>(A.state_out + state) = E;
-            }
-        }
-        __syncthreads();
-        float2 C = sh.C[lane];
-#pragma unroll
-        for (int w = 0; w < RWARPS - 1; ++w)
-            if (w < warp) C = carry(sh.P[w][lane], C, sh.A[w][lane]);
-        uint16_t *y = A.y + p.row * A.ld_y + p.c;
-#pragma unroll
-        for (int i = 0; i < RSEG; ++i) {
-            if (i < p.n) {
-                const float2 v = __fmul2_rn(bf16x2_to_float2(x1(i)), bf16x2_to_float2(x2(i)));
-                const float2 u = kNorm ? __fmul2_rn(s.w[i], v) : v;
-                C = kReset && (mask >> i & 1u) ? u : __ffma2_rn(s.a[i], C, u);
-                const uint32_t o = output_pair(bf16x2_to_float2(x3(i)), C, A.Dskip != nullptr, dsk, v);
-                if (p.live) *reinterpret_cast<uint32_t *>(y + i * A.ld_y) = o;
-            }
-        }
-        __syncthreads();  // the stage and the segments' sums may be overwritten
-        if (threadIdx.x == 32) {
-            sh.tile[st] = next;
-            if (next < A.tiles) {
-                fence_proxy_async_smem();
-                request<N, false>(maps, A, next, stages + st * N * kTileBytes, &sh.full[st]);
+            __syncwarp();
+            tile_barrier();
+            forward_carry<kReset>(A, sh, rec, t, (rows + RSEG - 1) / RSEG, c, live);
+            tile_barrier();
+            tile_barrier();
+            if (lane == 0) {
+                tma_store_4d(&maps.out[0], stage + 2 * kTileBytes, t.c, 0, t.j * RT, t.b);
+                bulk_commit();
             }
         }
     }
-    if (threadIdx.x == 0) finish(A);
+    if (threadIdx.x == RWARPS * 32) {
+        bulk_wait_read();
+        finish(A);
+    }
 }
 
 // ---------------------------------------------------------------- gradient
@@ -315,165 +359,203 @@ __global__ void __launch_bounds__(RWARPS * 32, 3)
 struct BackwardShared {
     float2 P[RWARPS][32], l[RWARPS][32], A[RWARPS][32], Q[RWARPS][32];
     float2 rate[RWARPS][32], skip[RWARPS][32];
-    float2 E[32];
-    uint64_t full[kStages];
-    unsigned int tile[kStages];
+    float2 E[RWARPS][32];  // the gradient from the right of each segment
+    Pipeline<5, true> pipe;
 };
 
-// The units' parts of dlog_rate and dDskip replace their (P, A) records, with
-// a tag that no launch has: by then the unit's carry is published, and a reader
-// that finds no (P, A) looks again and finds the carry.
+template <bool kNorm, bool kReset, bool kFull>
+__device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char *stage, int warp, int lane, int n,
+                                              float2 rate, bool skip, float2 dsk, float2 start, unsigned int mask)
+{
+    const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
+    const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
+    const TileRows dy = tile_rows(stage, 4, warp, lane);
+    float2 a[RSEG], w[RSEG], prev[RSEG], l, P;
+    segment_gates<kNorm, kReset, kFull>(a, w, l, P, gate, n, rate, mask);
+#pragma unroll
+    for (int i = 0; i < RSEG; ++i) {
+        if (kFull || i < n) {
+            prev[i] = product(x1(i), x2(i));  // u, until the states are known
+            if constexpr (kNorm) prev[i] = __fmul2_rn(w[i], prev[i]);
+        }
+    }
+    sh.l[warp][lane] = l;
+    sh.P[warp][lane] = P;
+    sh.A[warp][lane] = segment_end<kReset, kFull>(a, prev, n, mask);
+    sh.Q[warp][lane] = segment_left<kReset, kFull>(a, x3, dy, n, mask);
+    tile_barrier();
+    // the state before each token, while the carry from the right is found
+    float2 S = start;
+#pragma unroll
+    for (int k = 0; k < RWARPS - 1; ++k)
+        if (k < warp) S = carry<kReset>(sh.P[k][lane], S, sh.A[k][lane]);
+#pragma unroll
+    for (int i = 0; i < RSEG; ++i) {
+        if (kFull || i < n) {
+            const float2 s = kReset && (mask >> i & 1u) ? prev[i] : __ffma2_rn(a[i], S, prev[i]);
+            prev[i] = S;
+            S = s;
+        }
+    }
+    tile_barrier();
+    // dx1, dx2, dx3, dgate take the places of x1, x2, x3, gate
+    float2 e = sh.E[warp][lane], d_rate = bcast2(0.f), d_skip = bcast2(0.f);
+#pragma unroll
+    for (int i = RSEG - 1; i >= 0; --i) {
+        if (kFull || i < n) {
+            const bool cut = kReset && (mask >> i & 1u);
+            const uint32_t w1 = x1(i), w2 = x2(i), wd = dy(i);
+            const float2 d = bf16x2_to_float2(wd);
+            const float2 v = product(w1, w2);
+            const float2 q = fma_bf16x2(x3(i), wd, e);
+            x3.put(i, __fmul2_rn(d, S));
+            float2 dv = kNorm ? __fmul2_rn(w[i], q) : q;
+            if (skip) dv = __ffma2_rn(dsk, d, dv);
+            x1.put(i, __fmul2_rn(dv, bf16x2_to_float2(w2)));
+            x2.put(i, __fmul2_rn(dv, bf16x2_to_float2(w1)));
+            e = __fmul2_rn(a[i], q);
+            float2 m = prev[i];
+            S = m;
+            if constexpr (kNorm) {
+                // d w / d l = -a^2 / w; no gradient where w = 0 (log_rate = 0)
+                const float2 r = make_float2(w[i].x > 0.f ? rcp_approx(w[i].x) : 0.f,
+                                             w[i].y > 0.f ? rcp_approx(w[i].y) : 0.f);
+                const float2 av = __fmul2_rn(a[i], v);
+                m = __ffma2_rn(make_float2(-av.x, -av.y), r, m);
+            }
+            float2 dl = __fmul2_rn(e, m);
+            if (cut) dl = e = bcast2(0.f);
+            float2 eg;
+            const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
+            d_rate = __ffma2_rn(dl, sig, d_rate);
+            d_skip = __ffma2_rn(d, v, d_skip);
+            // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
+            eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
+            const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
+            gate.put(i, __fmul2_rn(__fmul2_rn(rate, dl), slope));
+        }
+    }
+    sh.rate[warp][lane] = d_rate;
+    sh.skip[warp][lane] = d_skip;
+}
+
+// As forward_carry, from the right; and once the tile is done its parts of
+// dlog_rate and dDskip.
+template <bool kReset>
+__device__ __forceinline__ void backward_carry(const RecArgs &A, BackwardShared &sh, Records &rec, Tile t, int nseg,
+                                               int c, bool live)
+{
+    const int lane = rec.lane;
+    float2 l = sh.l[0][lane], q = sh.Q[nseg - 1][lane];
+#pragma unroll
+    for (int w = 1; w < RWARPS; ++w)
+        if (w < nseg) l = __fadd2_rn(l, sh.l[w][lane]);
+#pragma unroll
+    for (int w = RWARPS - 2; w >= 0; --w)
+        if (w < nseg - 1) q = carry<kReset>(sh.P[w][lane], q, sh.Q[w][lane]);
+    const float2 P = decay_over(l);
+    const bool last = t.j == A.units - 1;
+    const size_t state = static_cast<size_t>(t.b) * A.D + c;
+    float2 E = bcast2(0.f);
+    rec.chain = t.chain;
+    if (t.j > 0) {
+        if (!last) rec.publish_unit(t.j, P, q);
+        E = rec.carry_into(t.j, A.hdr + 2);
+    } else if (A.dstate_out != nullptr) {
+        E = *reinterpret_cast<const float2 *>(A.dstate_out + state);
+    }
+    const float2 out = carry<true>(P, E, q);
+    if (!last) rec.publish_carry(t.j, out);
+    if (last && live && A.dstate_in != nullptr) *reinterpret_cast<float2 *>(A.dstate_in + state) = out;
+#pragma unroll
+    for (int w = RWARPS - 1; w >= 0; --w) {
+        if (w < nseg) {
+            sh.E[w][lane] = E;
+            E = carry<kReset>(sh.P[w][lane], E, sh.Q[w][lane]);
+        }
+    }
+}
+
+// The parts replace the unit's (P, A) record, with a tag that no launch has: by
+// then the unit's carry is published, and a reader that finds no (P, A) looks
+// again and finds the carry.
+__device__ __forceinline__ void backward_parts(const RecArgs &A, const BackwardShared &sh, Tile t, int lane)
+{
+    float2 d_rate = sh.rate[0][lane], d_skip = sh.skip[0][lane];
+#pragma unroll
+    for (int w = 1; w < RWARPS; ++w) {
+        d_rate = __fadd2_rn(d_rate, sh.rate[w][lane]);
+        d_skip = __fadd2_rn(d_skip, sh.skip[w][lane]);
+    }
+    uint4 *u = A.rec_unit + (static_cast<size_t>(t.j) * A.chains + t.chain) * RCH + 2 * lane;
+    store_record(u, d_rate.x, d_skip.x, 0u);
+    store_record(u + 1, d_rate.y, d_skip.y, 0u);
+}
+
 template <bool kNorm, bool kReset>
-__global__ void __launch_bounds__(RWARPS * 32, 2)
+__global__ void __launch_bounds__(kThreads, 2)
     recurrence_backward_kernel(const __grid_constant__ RecMaps maps, const RecArgs A)
 {
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ BackwardShared sh;
-    constexpr int N = 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == RWARPS * 32) sh.pipe.start(maps, A, stages);
     Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1);
-        fence_mbar_init();
-        for (int s = 0; s < kStages; ++s) {
-            sh.tile[s] = next_tile(A, s);
-            if (sh.tile[s] < A.tiles) request<N, true>(maps, A, sh.tile[s], stages + s * N * kTileBytes, &sh.full[s]);
-        }
-    }
     if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
-    __syncthreads();
+    tile_barrier();
+    unsigned int next = 0;
     for (int it = 0;; ++it) {
         const int st = it % kStages;
-        const unsigned int tile = sh.tile[st];
-        if (tile >= A.tiles) break;
-        const Place p = place_of<true>(A, tile, warp, lane);
-        rec.chain = static_cast<int>(tile % static_cast<unsigned int>(A.chains));
-        const unsigned char *stage = stages + st * N * kTileBytes;
-        const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
-        const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
-        const TileRows dy = tile_rows(stage, 4, warp, lane);
-        const float2 rate = ldg_f2(A.log_rate + p.c);
-        const float2 dsk = A.Dskip != nullptr ? ldg_f2(A.Dskip + p.c) : bcast2(0.f);
-        const unsigned int mask = kReset ? segment_resets(A.reset, p.row, p.n, lane) : 0u;
-        const size_t state = static_cast<size_t>(p.b) * A.D + p.c;
-        float2 S = ldg_f2(A.unit_states + (static_cast<size_t>(p.b) * A.units + p.unit) * A.D + p.c);
-        if (!mbar_wait_bounded(&sh.full[st], (it / kStages) & 1) && threadIdx.x == 0)
-            atomicOr(A.hdr + 2, kErrTmaTimeout);
-
-        RecSegment s;
-        segment_gates<kNorm, kReset>(s, gate, p.n, rate, mask);
-        sh.l[warp][lane] = s.l;
-        sh.P[warp][lane] = decay_over(s.l);
-        sh.A[warp][lane] = segment_end<kNorm, kReset>(s, x1, x2, p.n, mask);
-        sh.Q[warp][lane] = segment_left<kReset>(s, x3, dy, p.n, mask);
-        __syncthreads();
-        unsigned int next = 0;
-        if (threadIdx.x == 32) next = next_tile(A, it + kStages);
-        if (warp == 0) {
-            float2 l = sh.l[0][lane], q = sh.Q[p.nseg - 1][lane];
-#pragma unroll
-            for (int w = 1; w < RWARPS; ++w)
-                if (w < p.nseg) l = __fadd2_rn(l, sh.l[w][lane]);
-#pragma unroll
-            for (int w = RWARPS - 2; w >= 0; --w)
-                if (w < p.nseg - 1) q = carry(sh.P[w][lane], q, sh.Q[w][lane]);
-            const float2 P = decay_over(l);
-            const bool last = p.j == A.units - 1;
-            float2 E = bcast2(0.f);
-            if (p.j > 0) {
-                if (!last) rec.publish_unit(p.j, P, q);
-                E = rec.carry_into(p.j, A.hdr + 2);
-            } else if (A.dstate_out != nullptr) {
-                E = *reinterpret_cast<const float2 *>(A.dstate_out + state);
-            }
-            sh.E[lane] = E;
-            const float2 out = carry(P, E, q);
-            if (!last) rec.publish_carry(p.j, out);
-            if (last && p.live && A.dstate_in != nullptr) *reinterpret_cast<float2 *>(A.dstate_in + state) = out;
-        }
-        // the states before the segment's tokens, meanwhile
-#pragma unroll
-        for (int w = 0; w < RWARPS - 1; ++w)
-            if (w < warp) S = carry(sh.P[w][lane], S, sh.A[w][lane]);
-        float2 prev[RSEG];
-#pragma unroll
-        for (int i = 0; i < RSEG; ++i) {
-            if (i < p.n) {
-                float2 u = __fmul2_rn(bf16x2_to_float2(x1(i)), bf16x2_to_float2(x2(i)));
-                if constexpr (kNorm) u = __fmul2_rn(s.w[i], u);
-                prev[i] = S;
-                S = kReset && (mask >> i & 1u) ? u : __ffma2_rn(s.a[i], S, u);
-            }
-        }
-        __syncthreads();
-        float2 e = sh.E[lane];
-#pragma unroll
-        for (int w = RWARPS - 1; w > 0; --w)
-            if (w > warp && w < p.nseg) e = carry(sh.P[w][lane], e, sh.Q[w][lane]);
-        float2 d_rate = bcast2(0.f), d_skip = bcast2(0.f);
-        uint16_t *dx1 = A.dx1 + p.row * A.ld_dx + p.c, *dx2 = A.dx2 + p.row * A.ld_dx + p.c;
-        uint16_t *dx3 = A.dx3 + p.row * A.ld_dx + p.c, *dgate = A.dgate + p.row * A.ld_dg + p.c;
-#pragma unroll
-        for (int i = RSEG - 1; i >= 0; --i) {
-            if (i < p.n) {
-                const bool cut = kReset && (mask >> i & 1u);
-                const float2 f1 = bf16x2_to_float2(x1(i)), f2 = bf16x2_to_float2(x2(i));
-                const float2 f3 = bf16x2_to_float2(x3(i)), d = bf16x2_to_float2(dy(i));
-                const float2 v = __fmul2_rn(f1, f2);
-                const float2 q = __fadd2_rn(__fmul2_rn(f3, d), e);
-                const float2 d3 = __fmul2_rn(d, S);
-                float2 dv = kNorm ? __fmul2_rn(s.w[i], q) : q;
-                if (A.Dskip != nullptr) dv = __ffma2_rn(dsk, d, dv);
-                const float2 t = __fmul2_rn(s.a[i], q);
-                float2 m = prev[i];
-                if constexpr (kNorm) {
-                    // d w / d l = -a^2 / w; no gradient where w = 0 (log_rate = 0)
-                    const float2 r = make_float2(s.w[i].x > 0.f ? rcp_approx(s.w[i].x) : 0.f,
-                                                 s.w[i].y > 0.f ? rcp_approx(s.w[i].y) : 0.f);
-                    const float2 av = __fmul2_rn(s.a[i], v);
-                    m = __ffma2_rn(make_float2(-av.x, -av.y), r, m);
+        const Tile t = sh.pipe.tile[st];
+        if (t.j < 0) break;
+        unsigned char *stage = stages + st * 5 * kTileBytes;
+        const int unit = A.units - 1 - t.j;
+        const int rows = min(RT, A.L - unit * RT);
+        const bool live = t.c + 2 * lane < A.D;
+        const int c = live ? t.c + 2 * lane : 0;  // lanes without channels read some, and write nothing
+        if (warp < RWARPS) {
+            const int n = min(max(rows - warp * RSEG, 0), RSEG);
+            const float2 rate = ldg_f2(A.log_rate + c);
+            const bool skip = A.Dskip != nullptr;
+            const float2 dsk = skip ? ldg_f2(A.Dskip + c) : bcast2(0.f);
+            const float2 start = ldg_f2(A.unit_states + (static_cast<size_t>(t.b) * A.units + unit) * A.D + c);
+            const unsigned int mask =
+                kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + unit * RT + warp * RSEG, n, lane)
+                       : 0u;
+            if (!mbar_wait_bounded(&sh.pipe.full[st], (it / kStages) & 1) && threadIdx.x == 0)
+                atomicOr(A.hdr + 2, kErrTmaTimeout);
+            if (rows == RT)
+                backward_tile<kNorm, kReset, true>(sh, stage, warp, lane, RSEG, rate, skip, dsk, start, mask);
+            else
+                backward_tile<kNorm, kReset, false>(sh, stage, warp, lane, n, rate, skip, dsk, start, mask);
+            fence_proxy_async_smem();
+            tile_barrier();
+        } else {
+            if (lane == 0) {
+                if (it > 0) {
+                    bulk_wait_read();
+                    sh.pipe.request(maps, A, stages, st ^ 1, tile_of(A, next));
                 }
-                float2 dl = __fmul2_rn(t, m);
-                e = t;
-                S = prev[i];
-                if (cut) dl = e = bcast2(0.f);
-                float2 eg;
-                const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
-                const float2 ds = __fmul2_rn(dl, sig);
-                d_rate = __ffma2_rn(dl, sig, d_rate);
-                d_skip = __ffma2_rn(d, v, d_skip);
-                // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig
-                const float2 dg = __fmul2_rn(__fmul2_rn(rate, ds), __fmul2_rn(eg, sig));
-                if (p.live) {
-                    *reinterpret_cast<uint32_t *>(dx1 + i * A.ld_dx) = float2_to_bf16x2(__fmul2_rn(dv, f2));
-                    *reinterpret_cast<uint32_t *>(dx2 + i * A.ld_dx) = float2_to_bf16x2(__fmul2_rn(dv, f1));
-                    *reinterpret_cast<uint32_t *>(dx3 + i * A.ld_dx) = float2_to_bf16x2(d3);
-                    *reinterpret_cast<uint32_t *>(dgate + i * A.ld_dg) = float2_to_bf16x2(dg);
-                }
+                next = next_tile(A, it + kStages);
             }
-        }
-        sh.rate[warp][lane] = d_rate;
-        sh.skip[warp][lane] = d_skip;
-        __syncthreads();  // the stage and the segments' sums may be overwritten
-        if (threadIdx.x == 32) {
-            sh.tile[st] = next;
-            if (next < A.tiles) {
-                fence_proxy_async_smem();
-                request<N, true>(maps, A, next, stages + st * N * kTileBytes, &sh.full[st]);
-            }
-        }
-        if (warp == 0) {  // the next writes of these sums follow a barrier that this warp is in
+            __syncwarp();
+            tile_barrier();
+            backward_carry<kReset>(A, sh, rec, t, (rows + RSEG - 1) / RSEG, c, live);
+            tile_barrier();
+            tile_barrier();
+            if (lane == 0) {
 #pragma unroll
-            for (int w = 1; w < RWARPS; ++w) {
-                d_rate = __fadd2_rn(d_rate, sh.rate[w][lane]);
-                d_skip = __fadd2_rn(d_skip, sh.skip[w][lane]);
+                for (int k = 0; k < 4; ++k)
+                    tma_store_4d(&maps.out[k], stage + k * kTileBytes, t.c, 0, unit * RT, t.b);
+                bulk_commit();
             }
-            uint4 *u = A.rec_unit + static_cast<size_t>(tile) * RCH + 2 * lane;
-            store_record(u, d_rate.x, d_skip.x, 0u);
-            store_record(u + 1, d_rate.y, d_skip.y, 0u);
+            backward_parts(A, sh, t, lane);  // the warps' next sums follow the next tile's barriers
         }
     }
-    if (threadIdx.x == 0) finish(A);
+    if (threadIdx.x == RWARPS * 32) {
+        bulk_wait_read();
+        finish(A);
+    }
 }
 
 // dlog_rate and dDskip: the units' parts summed in double, in a fixed order: 32
@@ -515,18 +597,19 @@ __global__ void __launch_bounds__(kRecDecodeThreads) recurrence_decode_kernel(co
     const int b = static_cast<int>(i / pairs);
     const int c = 2 * static_cast<int>(i - static_cast<long long>(b) * pairs);
     const long long o = b * A.ld_x + c;
-    const float2 v = __fmul2_rn(bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(A.x1 + o)),
-                                bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(A.x2 + o)));
+    const float2 v =
+        product(*reinterpret_cast<const uint32_t *>(A.x1 + o), *reinterpret_cast<const uint32_t *>(A.x2 + o));
     const float2 f3 = bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(A.x3 + o));
     const float2 g = bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(A.gate + b * A.ld_g + c));
     float2 *st = reinterpret_cast<float2 *>(A.state_out + static_cast<size_t>(b) * A.D + c);
     const float2 S = *st;
-    const float2 dsk = A.Dskip != nullptr ? ldg_f2(A.Dskip + c) : bcast2(0.f);
     float2 a, w, e;
     decay<kNorm>(__fmul2_rn(ldg_f2(A.log_rate + c), gate_sigmoid(g, e)), a, w);
     const float2 s = __ffma2_rn(a, S, kNorm ? __fmul2_rn(w, v) : v);
     *st = s;
-    *reinterpret_cast<uint32_t *>(A.y + b * A.ld_y + c) = output_pair(f3, s, A.Dskip != nullptr, dsk, v);
+    float2 y = __fmul2_rn(f3, s);
+    if (A.Dskip != nullptr) y = __ffma2_rn(ldg_f2(A.Dskip + c), v, y);
+    *reinterpret_cast<uint32_t *>(A.y + b * A.ld_y + c) = float2_to_bf16x2(y);
 }
 
 // One persistent CTA per free place on the device, at most one per tile.
@@ -542,13 +625,13 @@ int launch_units(int tensors, const RecMaps &maps, const RecArgs &a, cudaStream_
         HYENA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                   "gated recurrence: set max dynamic shared memory");
         HYENA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "multiprocessor count");
-        HYENA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, RWARPS * 32, smem),
+        HYENA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem),
                   "gated recurrence: occupancy");
         places = sms * (per_sm > 0 ? per_sm : 1);
         configured_device = dev;
     }
     const unsigned int grid = a.tiles < static_cast<unsigned int>(places) ? a.tiles : places;
-    kernel<<<grid, RWARPS * 32, smem, st>>>(maps, a);
+    kernel<<<grid, kThreads, smem, st>>>(maps, a);
     HYENA_TRY(cudaGetLastError(), "gated recurrence launch");
     return 1;
 }

@@ -44,13 +44,6 @@ __device__ __forceinline__ float sqrt_approx(float x)
     return r;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 __device__ __forceinline__ float2 bcast2(float x) { return make_float2(x, x); }
 
 // Products that a sum takes are written as one __ffma2_rn below: left apart,
@@ -71,17 +64,31 @@ __device__ __forceinline__ float2 expm1_over_x(float2 x)
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMinGate = -87.f;  // exp(87) is finite in fp32; sigmoid(-87) = 1.6e-38
 
-// e = exp(-gate) and sigmoid(gate) of a channel pair.  Gates below -87 count as
-// -87 (the sigmoid is below 2e-38 either way); NaN stays NaN.
+// e = exp(-gate) and sigmoid(gate) = 1 / (1 + e) of a channel pair: 0 where e
+// overflows (gates below -88), NaN for NaN.
 __device__ __forceinline__ float2 gate_sigmoid(float2 g, float2 &e)
 {
-    const float2 t = __fmul2_rn(make_float2(max_nan(g.x, kMinGate), max_nan(g.y, kMinGate)), bcast2(-kLog2e));
+    const float2 t = __fmul2_rn(g, bcast2(-kLog2e));
     e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
     const float2 d = __fadd2_rn(e, bcast2(1.f));
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
+
+// a b + c of two bf16 pairs and an fp32 pair, one rounding (the product of two
+// bf16 values is exact).
+__device__ __forceinline__ float2 fma_bf16x2(uint32_t a, uint32_t b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %2;\n\tmov.b32 {bl, bh}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %4;\n\tfma.rn.f32.bf16 %1, ah, bh, %5;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(a), "r"(b), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// v = x1 x2, exact (adding -0 keeps the sign of a zero).
+__device__ __forceinline__ float2 product(uint32_t a, uint32_t b) { return fma_bf16x2(a, b, bcast2(-0.f)); }
 
 // a = exp(l) and, with kNorm, w = sqrt(1 - a^2) (0 where a rounds to 1 exactly
 // because l = 0; NaN for l > 0).
@@ -114,69 +121,62 @@ __device__ __forceinline__ float2 decay_over(float2 l)
     return a;
 }
 
-// One carry step, C <- P C + A.
-__device__ __forceinline__ float carry1(float P, float C, float A)
-{
-    return __float_as_int(P) < 0 ? A : __fmaf_rn(P, C, A);
-}
+// One carry step, C <- P C + A.  kCut: P may carry the mark of a reset.
+template <bool kCut>
 __device__ __forceinline__ float2 carry(float2 P, float2 C, float2 A)
 {
-    return make_float2(carry1(P.x, C.x, A.x), carry1(P.y, C.y, A.y));
+    const float2 r = __ffma2_rn(P, C, A);
+    if constexpr (!kCut) return r;
+    return make_float2(__float_as_int(P.x) < 0 ? A.x : r.x, __float_as_int(P.y) < 0 ? A.y : r.y);
 }
 
-// A segment's RSEG tokens of one channel pair, in registers.
-struct RecSegment {
-    float2 a[RSEG], w[RSEG];
-    float2 l;  // sum of the tokens' l
-};
-
-// Gates of a segment's first n tokens (the others: a = 1, l = 0).  `mask` bit i:
-// token i is a reset.
-template <bool kNorm, bool kReset, class Row>
-__device__ __forceinline__ void segment_gates(RecSegment &s, Row gate, int n, float2 rate, unsigned int mask)
+// Gates of a segment's first n tokens (kFull: n = RSEG): a, w, the sum l of the
+// tokens' l, and the product P of their a (for the steps within the unit only;
+// -0 if a token is a reset).  `mask` bit i: token i is a reset.
+template <bool kNorm, bool kReset, bool kFull, class Row>
+__device__ __forceinline__ void segment_gates(float2 (&a)[RSEG], float2 (&w)[RSEG], float2 &l, float2 &P, Row gate,
+                                              int n, float2 rate, unsigned int mask)
 {
-    s.l = bcast2(0.f);
+    l = bcast2(0.f);
+    P = bcast2(1.f);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
-        if (i < n) {
+        if (kFull || i < n) {
             float2 e;
             const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), e);
-            float2 l = __fmul2_rn(rate, sig);
-            s.l = __ffma2_rn(rate, sig, s.l);
-            if (kReset && (mask >> i & 1u)) l = s.l = bcast2(-INFINITY);  // a = 0, w = 1
-            decay<kNorm>(l, s.a[i], s.w[i]);
+            float2 li = __fmul2_rn(rate, sig);
+            l = i == 0 ? li : __ffma2_rn(rate, sig, l);
+            if (kReset && (mask >> i & 1u)) li = l = bcast2(-INFINITY);  // a = 0, w = 1
+            decay<kNorm>(li, a[i], w[i]);
+            P = i == 0 ? a[i] : __fmul2_rn(P, a[i]);
         }
     }
+    if (kReset && mask) P = bcast2(-0.f);
 }
 
-// End state of a segment from a zero start.
-template <bool kNorm, bool kReset, class Row>
-__device__ __forceinline__ float2 segment_end(const RecSegment &s, Row x1, Row x2, int n, unsigned int mask)
+// End state of a segment from a zero start, with u = w v.
+template <bool kReset, bool kFull>
+__device__ __forceinline__ float2 segment_end(const float2 (&a)[RSEG], const float2 (&u)[RSEG], int n,
+                                              unsigned int mask)
 {
     float2 A = bcast2(0.f);
 #pragma unroll
-    for (int i = 0; i < RSEG; ++i) {
-        if (i < n) {
-            float2 u = __fmul2_rn(bf16x2_to_float2(x1(i)), bf16x2_to_float2(x2(i)));
-            if constexpr (kNorm) u = __fmul2_rn(s.w[i], u);
-            A = i == 0 || (kReset && (mask >> i & 1u)) ? u : __ffma2_rn(s.a[i], A, u);
-        }
-    }
+    for (int i = 0; i < RSEG; ++i)
+        if (kFull || i < n) A = i == 0 || (kReset && (mask >> i & 1u)) ? u[i] : __ffma2_rn(a[i], A, u[i]);
     return A;
 }
 
 // The gradient that a segment hands to the token before it, e_t = a_t (r_t +
 // e_{t+1}) with r = x3 dy, from a zero e at its right edge.
-template <bool kReset, class Row>
-__device__ __forceinline__ float2 segment_left(const RecSegment &s, Row x3, Row dy, int n, unsigned int mask)
+template <bool kReset, bool kFull, class Row>
+__device__ __forceinline__ float2 segment_left(const float2 (&a)[RSEG], Row x3, Row dy, int n, unsigned int mask)
 {
     float2 e = bcast2(0.f);
 #pragma unroll
     for (int i = RSEG - 1; i >= 0; --i) {
-        if (i < n) {
-            const float2 r = __fmul2_rn(bf16x2_to_float2(x3(i)), bf16x2_to_float2(dy(i)));
-            e = i == n - 1 ? r : __fadd2_rn(r, e);
-            e = kReset && (mask >> i & 1u) ? bcast2(0.f) : __fmul2_rn(s.a[i], e);
+        if (kFull || i < n) {
+            e = __fmul2_rn(a[i], fma_bf16x2(x3(i), dy(i), e));
+            if (kReset && (mask >> i & 1u)) e = bcast2(0.f);
         }
     }
     return e;
@@ -188,5 +188,18 @@ __device__ __forceinline__ unsigned int segment_resets(const uint8_t *reset, lon
     const bool r = lane < n && reset[row0 + lane] != 0;
     return __ballot_sync(kFullMask, r);
 }
+
+// 4-D tiled TMA store from shared memory as one bulk group of this thread; what
+// lies outside the tensor is not written.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, int c3)
+{
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All of this thread's bulk stores have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 }  // namespace hyena

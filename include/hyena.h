@@ -515,9 +515,8 @@ hyena_status_t hyena_modal_state_init(float *state, int B, int D, int N, void *s
  *           this operator and its gradient alone, with any B, L, D that fit;
  *           calls sharing it must not overlap in time.
  * Chunks of whole units reproduce the single pass bit for bit.  L == 0 is
- * valid: state_out receives state_in (or zeros).  Gates below -87 count as
- * -87.  Device-side waits are bounded; hyena_workspace_check reports one that
- * ran out.
+ * valid: state_out receives state_in (or zeros).  Device-side waits are
+ * bounded; hyena_workspace_check reports one that ran out.
  */
 #define HYENA_RECURRENCE_UNIT 64
 
