@@ -36,6 +36,8 @@ namespace {
 
 constexpr int kStages = 2;
 constexpr int kTileBytes = RT * RCH * 2;  // one tensor's rows of a unit
+constexpr int kParamBytes = RCH * 4;      // one fp32 value a channel
+constexpr int kBatch = 4;                 // units whose records a look-back loads at a time
 
 // A unit's rows of one tensor in shared memory as a lane sees them from its
 // segment's first token: word i holds its channel pair of token i.  Outputs
@@ -94,52 +96,68 @@ struct Records {
         store_record(known + tile(j) * (RCH / 2) + lane, C.x, C.y, epoch);
     }
 
-    // The carry into unit j > 0 (all lanes of a warp).  One load a poll looks at
-    // the first records of the last 16 units: lanes 0-15 at carries,
-    // lanes 16-31 at (P, A).  Once a carry and every unit between are there,
-    // each lane loads its own channels' records, whose tags it checks as well.
-    // Gives up after the bounded wait, with an error bit, and returns zero.
-    __device__ __forceinline__ float2 carry_into(int j, unsigned int *error) const
+    // One look for the carry into unit j > 0 (all lanes of a warp); true if it is
+    // known.  One load looks at the first records of the last 16 units: lanes
+    // 0-15 at known carries, lanes 16-31 at units.  Once a carry and every unit
+    // behind it are there, each lane loads its own channels' records, whose tags
+    // it checks as well.
+    __device__ __forceinline__ bool look_back(int j, float2 &C) const
     {
         const int back = lane & 15;
-        const bool there = back < j;
-        const size_t at = tile(there ? j - 1 - back : 0);
-        const uint4 *hint = lane < 16 ? known + at * (RCH / 2) : unit + at * RCH;
-        unsigned long long t0 = 0;
-        for (;;) {
-            const unsigned int ready = __ballot_sync(kFullMask, there && load_record(hint).z == epoch);
-            const unsigned int carries = ready & 0xffffu, units = ready >> 16;
-            const int k = __ffs(carries) - 1;  // nearest unit whose carry is known
-            if (k >= 0 && ((units + 1u) & ((1u << k) - 1u)) == 0u) {
-                bool ok = true;
-                uint4 r = load_record(known + tile(j - 1 - k) * (RCH / 2) + lane);
-                ok = r.z == epoch;
-                float2 C = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
-                for (int d = k - 1; d >= 0; d -= 2) {  // two units' loads at a time
-                    const uint4 *u = unit + tile(j - 1 - d) * RCH + 2 * lane;
-                    const uint4 *v = unit + tile(j - 1 - max(d - 1, 0)) * RCH + 2 * lane;
-                    const uint4 u0 = load_record(u), u1 = load_record(u + 1);
-                    const uint4 v0 = load_record(v), v1 = load_record(v + 1);
-                    ok = ok && u0.z == epoch && u1.z == epoch && v0.z == epoch && v1.z == epoch;
-                    C = carry<true>(make_float2(__uint_as_float(u0.x), __uint_as_float(u1.x)), C,
-                                    make_float2(__uint_as_float(u0.y), __uint_as_float(u1.y)));
-                    if (d > 0)
-                        C = carry<true>(make_float2(__uint_as_float(v0.x), __uint_as_float(v1.x)), C,
-                                        make_float2(__uint_as_float(v0.y), __uint_as_float(v1.y)));
-                }
-                if (__all_sync(kFullMask, ok)) return C;
+        const size_t at = tile(max(j - 1 - back, 0));
+        const uint4 hint = load_record(lane < 16 ? known + at * (RCH / 2) : unit + at * RCH);
+        const unsigned int ready = __ballot_sync(kFullMask, back < j && hint.z == epoch);
+        const unsigned int units = ready >> 16;
+        const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
+        if (k < 0 || ((units + 1u) & ((1u << k) - 1u)) != 0u) return false;
+        const uint4 r = load_record(known + tile(j - 1 - k) * (RCH / 2) + lane);
+        bool found = r.z == epoch;
+        C = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+        for (int d = k - 1; d >= 0; d -= kBatch) {
+            uint4 u0[kBatch], u1[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const uint4 *u = unit + tile(j - 1 - max(d - i, 0)) * RCH + 2 * lane;
+                u0[i] = load_record(u);
+                u1[i] = load_record(u + 1);
             }
-            const unsigned long long t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > kWaitLimitNs) {
-                if (lane == 0) atomicOr(error, kErrLookbackTimeout);
-                return bcast2(0.f);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (d >= i) {
+                    found = found && u0[i].z == epoch && u1[i].z == epoch;
+                    C = apply(u0[i], u1[i], C);
+                }
             }
         }
+        return __all_sync(kFullMask, found);
+    }
+
+    static __device__ __forceinline__ float2 apply(uint4 u0, uint4 u1, float2 C)
+    {
+        return carry<true>(make_float2(__uint_as_float(u0.x), __uint_as_float(u1.x)), C,
+                           make_float2(__uint_as_float(u0.y), __uint_as_float(u1.y)));
     }
 };
 
 // ---------------------------------------------------------------- work items
+
+// The parameter k of a lane's channel pair; lanes without channels read what
+// the shared memory holds, and write nothing.
+__device__ __forceinline__ float2 param(const unsigned char *params, int k, int lane)
+{
+    return reinterpret_cast<const float2 *>(params + k * kParamBytes)[lane];
+}
+
+// Tokens behind the sequence's end, as the last unit's copy holds them (zeros):
+// a gate of -inf makes them pass the state on as it is (a = 1), and x1 = -0
+// their input -0, which adds nothing to any value, -0 neither.
+__device__ __forceinline__ void pad_tail(const TileRows &x1, const TileRows &gate, int n)
+{
+    for (int i = max(n, 0); i < RSEG; ++i) {
+        x1.p[i * (RCH / 2)] = 0x80008000u;
+        gate.p[i * (RCH / 2)] = 0xff80ff80u;
+    }
+}
 
 // The next tile of this CTA (called by one thread).  Sequences of one unit have
 // nothing to wait for and need no ticket.
@@ -178,38 +196,90 @@ __device__ __forceinline__ Tile tile_of(const RecArgs &A, unsigned int ticket)
     return t;
 }
 
-// What forward and gradient share: two stages of N tensors' rows, their tiles
-// and barriers.  A tile's outputs leave from its stage by TMA; the stage is
+// What forward and gradient share: two stages of N tensors' rows and the
+// channels' parameters, their tiles and barriers.  A tile's outputs leave from its stage by TMA; the stage is
 // asked to take new rows half a tile later, when that has read it.
 template <int N, bool kBack>
 struct Pipeline {
+    static constexpr int kBytes = N * kTileBytes + 3 * kParamBytes;  // rows; log_rate, Dskip, start states
     Tile tile[kStages];
     uint64_t full[kStages];
+    uint64_t sums, carried, done;  // of the current tile: segments' sums, states before them, outputs
+    unsigned int *error;
 
     __device__ __forceinline__ void request(const RecMaps &m, const RecArgs &A, unsigned char *stages, int s, Tile t)
     {
         tile[s] = t;
         if (t.j < 0) return;
-        const int row = (kBack ? A.units - 1 - t.j : t.j) * RT;
-        unsigned char *stage = stages + s * N * kTileBytes;
-        mbar_arrive_expect_tx(&full[s], N * kTileBytes);
+        const int unit = kBack ? A.units - 1 - t.j : t.j;
+        unsigned char *stage = stages + s * kBytes, *params = stage + N * kTileBytes;
+        const uint32_t bytes = 4u * min(RCH, A.D - t.c);  // a multiple of 32: D is one of 8
+        mbar_arrive_expect_tx(&full[s], N * kTileBytes + bytes * (1 + (A.Dskip != nullptr) + kBack));
 #pragma unroll
-        for (int k = 0; k < N; ++k) tma_load_4d(stage + k * kTileBytes, &m.in[k], &full[s], t.c, 0, row, t.b);
+        for (int k = 0; k < N; ++k) tma_load_4d(stage + k * kTileBytes, &m.in[k], &full[s], t.c, 0, unit * RT, t.b);
+        bulk_load(params, A.log_rate + t.c, bytes, &full[s]);
+        if (A.Dskip != nullptr) bulk_load(params + kParamBytes, A.Dskip + t.c, bytes, &full[s]);
+        if (kBack)
+            bulk_load(params + 2 * kParamBytes,
+                      A.unit_states + (static_cast<size_t>(t.b) * A.units + unit) * A.D + t.c, bytes, &full[s]);
     }
     __device__ __forceinline__ void start(const RecMaps &m, const RecArgs &A, unsigned char *stages)
     {
         for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+        mbar_init(&sums, RWARPS);
+        mbar_init(&carried, 1);
+        mbar_init(&done, RWARPS);
+        error = A.hdr + 2;
         fence_mbar_init();
         for (int s = 0; s < kStages; ++s) request(m, A, stages, s, tile_of(A, next_tile(A, s)));
+    }
+    __device__ __forceinline__ void wait(uint64_t *bar, int turn)
+    {
+        if (!mbar_wait_bounded(bar, turn & 1)) atomicOr(error, kErrLocalTimeout);
+    }
+    // This warp's part of a barrier that counts warps.
+    __device__ __forceinline__ void arrive(uint64_t *bar, int lane)
+    {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    }
+
+    // The control warp's part of a tile until the carry C into it and its own sums are
+    // known.  Looking back starts while the sums are formed; `sums_ready()` runs
+    // once they are, with the carry known or not.  Gives up after the bounded wait.
+    template <class F>
+    __device__ __forceinline__ void find_carry(const Records &rec, int j, int it, const float *initial, bool live,
+                                               float2 &C, F sums_ready)
+    {
+        bool found = j == 0, summed = false;
+        C = bcast2(0.f);
+        if (found && initial != nullptr && live) C = *reinterpret_cast<const float2 *>(initial);
+        unsigned long long t0 = 0;
+        for (;;) {
+            if (!found) found = rec.look_back(j, C);
+            if (!summed) {
+                if (found)
+                    wait(&sums, it);
+                summed = found || __all_sync(kFullMask, mbar_test_wait(&sums, it & 1));
+                if (summed) sums_ready(found);
+            }
+            if (found && summed) return;
+            const unsigned long long t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (__any_sync(kFullMask, t - t0 > kWaitLimitNs)) {
+                if (rec.lane == 0) atomicOr(error, kErrLookbackTimeout);
+                C = bcast2(0.f);
+                if (summed) return;
+                found = true;
+            }
+        }
     }
 };
 
 // A CTA: RWARPS warps that compute, and one that takes tickets, runs the copies
 // and finds the carries, so that the computing warps' registers do not have to
-// hold its work too.  The three barriers of a tile are all of the CTA's threads'.
+// hold its work too.
 constexpr int kThreads = (RWARPS + 1) * 32;
-
-__device__ __forceinline__ void tile_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // ---------------------------------------------------------------- forward
 
@@ -219,77 +289,73 @@ struct ForwardShared {
     Pipeline<4, false> pipe;
 };
 
-template <bool kNorm, bool kReset, bool kFull>
+template <bool kNorm, bool kReset>
 __device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *stage, int warp, int lane, int n,
-                                             float2 rate, bool skip, float2 dsk, unsigned int mask)
+                                             bool skip, unsigned int mask, int it)
 {
     const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
-    const TileRows x3 = tile_rows(stage, 2, warp, lane);
+    const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
+    const unsigned char *params = stage + 4 * kTileBytes;
+    if (n < RSEG) pad_tail(x1, gate, n);
     float2 a[RSEG], u[RSEG], l, P;
-    segment_gates<kNorm, kReset, kFull>(a, u, l, P, tile_rows(stage, 3, warp, lane), n, rate, mask);
+    segment_gates<kNorm, kReset>(a, u, l, P, gate, finite_rate(param(params, 0, lane)), mask);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
-        if (kFull || i < n) {
-            const float2 v = product(x1(i), x2(i));
-            u[i] = kNorm ? __fmul2_rn(u[i], v) : v;
-        }
+        const float2 v = product(x1(i), x2(i));
+        u[i] = kNorm ? __fmul2_rn(u[i], v) : v;
     }
     sh.l[warp][lane] = l;
     sh.P[warp][lane] = P;
-    sh.A[warp][lane] = segment_end<kReset, kFull>(a, u, n, mask);
-    tile_barrier();
-    tile_barrier();
+    sh.A[warp][lane] = segment_end<kReset>(a, u, mask);
+    sh.pipe.arrive(&sh.pipe.sums, lane);
+    sh.pipe.wait(&sh.pipe.carried, it);
     float2 C = sh.C[warp][lane];
+    const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
-        if (kFull || i < n) {
-            C = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], C, u[i]);
-            float2 o = __fmul2_rn(bf16x2_to_float2(x3(i)), C);
-            if (skip) o = __ffma2_rn(dsk, product(x1(i), x2(i)), o);
-            x3.put(i, o);  // y takes x3's place
-        }
+        C = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], C, u[i]);
+        float2 o = __fmul2_rn(bf16x2_to_float2(x3(i)), C);
+        if (skip) o = __ffma2_rn(dsk, product(x1(i), x2(i)), o);
+        x3.put(i, o);  // y takes x3's place
     }
 }
 
-// Between the first two barriers of a tile: from the segments' sums the unit's
-// (P, A), the carry into it and the state before each segment.
+// The control warp's part of a tile: from the segments' sums the unit's (P, A),
+// the carry into it and the state before each segment.
 template <bool kReset>
-__device__ __forceinline__ void forward_carry(const RecArgs &A, ForwardShared &sh, Records &rec, Tile t, int nseg,
-                                              int c, bool live)
+__device__ __forceinline__ void forward_carry(const RecArgs &A, ForwardShared &sh, Records &rec, Tile t, int it)
 {
     const int lane = rec.lane;
-    float2 l = sh.l[0][lane], a = sh.A[0][lane];
+    const bool last = t.j == A.units - 1;
+    const int c = t.c + 2 * lane;
+    const bool live = c < A.D;
+    const size_t state = static_cast<size_t>(t.b) * A.D + c;
+    float2 C, P, a;
+    rec.chain = t.chain;
+    sh.pipe.find_carry(rec, t.j, it, A.state_in ? A.state_in + state : nullptr, live, C, [&](bool found) {
+        float2 l = sh.l[0][lane];
+        a = sh.A[0][lane];
 #pragma unroll
-    for (int w = 1; w < RWARPS; ++w) {
-        if (w < nseg) {
+        for (int w = 1; w < RWARPS; ++w) {
             l = __fadd2_rn(l, sh.l[w][lane]);
             a = carry<kReset>(sh.P[w][lane], a, sh.A[w][lane]);
         }
-    }
-    const float2 P = decay_over(l);
-    const bool last = t.j == A.units - 1;
-    const size_t state = static_cast<size_t>(t.b) * A.D + c;
-    float2 C = bcast2(0.f);
-    rec.chain = t.chain;
-    if (t.j > 0) {
-        if (!last) rec.publish_unit(t.j, P, a);
-        C = rec.carry_into(t.j, A.hdr + 2);
-    } else if (A.state_in != nullptr) {
-        C = *reinterpret_cast<const float2 *>(A.state_in + state);
-    }
+        P = decay_over(l);
+        if (!found && !last) rec.publish_unit(t.j, P, a);
+    });
     const float2 E = carry<true>(P, C, a);
     if (!last) rec.publish_carry(t.j, E);
-    if (live) {
-        if (A.C != nullptr)
-            *reinterpret_cast<float2 *>(A.C + (static_cast<size_t>(t.b) * A.units + t.j) * A.D + c) = C;
-        if (last && A.state_out != nullptr) *reinterpret_cast<float2 *>(A.state_out + state) = E;
-    }
+    const float2 start = C;
 #pragma unroll
     for (int w = 0; w < RWARPS; ++w) {
-        if (w < nseg) {
-            sh.C[w][lane] = C;
-            C = carry<kReset>(sh.P[w][lane], C, sh.A[w][lane]);
-        }
+        sh.C[w][lane] = C;
+        C = carry<kReset>(sh.P[w][lane], C, sh.A[w][lane]);
+    }
+    sh.pipe.arrive(&sh.pipe.carried, lane);
+    if (live) {
+        if (A.C != nullptr)
+            *reinterpret_cast<float2 *>(A.C + (static_cast<size_t>(t.b) * A.units + t.j) * A.D + c) = start;
+        if (last && A.state_out != nullptr) *reinterpret_cast<float2 *>(A.state_out + state) = E;
     }
 }
 
@@ -303,55 +369,36 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (threadIdx.x == RWARPS * 32) sh.pipe.start(maps, A, stages);
     Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
     if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
-    tile_barrier();
+    __syncthreads();
     unsigned int next = 0;
     for (int it = 0;; ++it) {
         const int st = it % kStages;
         const Tile t = sh.pipe.tile[st];
         if (t.j < 0) break;
-        unsigned char *stage = stages + st * 4 * kTileBytes;
-        const int rows = min(RT, A.L - t.j * RT);
-        const bool live = t.c + 2 * lane < A.D;
-        const int c = live ? t.c + 2 * lane : 0;  // lanes without channels read some, and write nothing
+        unsigned char *stage = stages + st * sh.pipe.kBytes;
         if (warp < RWARPS) {
-            const int n = min(max(rows - warp * RSEG, 0), RSEG);
-            const float2 rate = ldg_f2(A.log_rate + c);
-            const bool skip = A.Dskip != nullptr;
-            const float2 dsk = skip ? ldg_f2(A.Dskip + c) : bcast2(0.f);
+            const int n = min(A.L - t.j * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
             const unsigned int mask =
                 kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + t.j * RT + warp * RSEG, n, lane)
                        : 0u;
-            if (!mbar_wait_bounded(&sh.pipe.full[st], (it / kStages) & 1) && threadIdx.x == 0)
-                atomicOr(A.hdr + 2, kErrTmaTimeout);
-            if (rows == RT)
-                forward_tile<kNorm, kReset, true>(sh, stage, warp, lane, RSEG, rate, skip, dsk, mask);
-            else
-                forward_tile<kNorm, kReset, false>(sh, stage, warp, lane, n, rate, skip, dsk, mask);
+            sh.pipe.wait(&sh.pipe.full[st], it / kStages);
+            forward_tile<kNorm, kReset>(sh, stage, warp, lane, n, A.Dskip != nullptr, mask, it);
             fence_proxy_async_smem();
-            tile_barrier();
+            sh.pipe.arrive(&sh.pipe.done, lane);
         } else {
-            if (lane == 0) {
-                if (it > 0) {
-                    bulk_wait_read();
-                    sh.pipe.request(maps, A, stages, st ^ 1, tile_of(A, next));
-                }
-                next = next_tile(A, it + kStages);
-            }
-            __syncwarp();
-            tile_barrier();
-            forward_carry<kReset>(A, sh, rec, t, (rows + RSEG - 1) / RSEG, c, live);
-            tile_barrier();
-            tile_barrier();
+            if (lane == 0) next = next_tile(A, it + kStages);
+            forward_carry<kReset>(A, sh, rec, t, it);
+            sh.pipe.wait(&sh.pipe.done, it);
             if (lane == 0) {
                 tma_store_4d(&maps.out[0], stage + 2 * kTileBytes, t.c, 0, t.j * RT, t.b);
                 bulk_commit();
+                bulk_wait_read();
+                sh.pipe.request(maps, A, stages, st, tile_of(A, next));
             }
+            __syncwarp();
         }
     }
-    if (threadIdx.x == RWARPS * 32) {
-        bulk_wait_read();
-        finish(A);
-    }
+    if (threadIdx.x == RWARPS * 32) finish(A);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -359,121 +406,121 @@ __global__ void __launch_bounds__(kThreads, 3)
 struct BackwardShared {
     float2 P[RWARPS][32], l[RWARPS][32], A[RWARPS][32], Q[RWARPS][32];
     float2 rate[RWARPS][32], skip[RWARPS][32];
+    float2 S[RWARPS][32];  // the state before each segment
     float2 E[RWARPS][32];  // the gradient from the right of each segment
+    uint64_t started;      // S is known
     Pipeline<5, true> pipe;
 };
 
-template <bool kNorm, bool kReset, bool kFull>
+template <bool kNorm, bool kReset>
 __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char *stage, int warp, int lane, int n,
-                                              float2 rate, bool skip, float2 dsk, float2 start, unsigned int mask)
+                                              bool skip, unsigned int mask, int it)
 {
     const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
     const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
     const TileRows dy = tile_rows(stage, 4, warp, lane);
+    const unsigned char *params = stage + 5 * kTileBytes;
+    if (n < RSEG) pad_tail(x1, gate, n);
+    const float2 rate = finite_rate(param(params, 0, lane));
     float2 a[RSEG], w[RSEG], prev[RSEG], l, P;
-    segment_gates<kNorm, kReset, kFull>(a, w, l, P, gate, n, rate, mask);
+    segment_gates<kNorm, kReset>(a, w, l, P, gate, rate, mask);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
-        if (kFull || i < n) {
-            prev[i] = product(x1(i), x2(i));  // u, until the states are known
-            if constexpr (kNorm) prev[i] = __fmul2_rn(w[i], prev[i]);
-        }
+        prev[i] = product(x1(i), x2(i));  // u, until the states are known
+        if constexpr (kNorm) prev[i] = __fmul2_rn(w[i], prev[i]);
     }
     sh.l[warp][lane] = l;
     sh.P[warp][lane] = P;
-    sh.A[warp][lane] = segment_end<kReset, kFull>(a, prev, n, mask);
-    sh.Q[warp][lane] = segment_left<kReset, kFull>(a, x3, dy, n, mask);
-    tile_barrier();
+    sh.A[warp][lane] = segment_end<kReset>(a, prev, mask);
+    sh.Q[warp][lane] = segment_left<kReset>(a, x3, dy, mask);
+    sh.pipe.arrive(&sh.pipe.sums, lane);
     // the state before each token, while the carry from the right is found
-    float2 S = start;
-#pragma unroll
-    for (int k = 0; k < RWARPS - 1; ++k)
-        if (k < warp) S = carry<kReset>(sh.P[k][lane], S, sh.A[k][lane]);
+    sh.pipe.wait(&sh.started, it);
+    float2 S = sh.S[warp][lane];
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
-        if (kFull || i < n) {
-            const float2 s = kReset && (mask >> i & 1u) ? prev[i] : __ffma2_rn(a[i], S, prev[i]);
-            prev[i] = S;
-            S = s;
-        }
+        const float2 s = kReset && (mask >> i & 1u) ? prev[i] : __ffma2_rn(a[i], S, prev[i]);
+        prev[i] = S;
+        S = s;
     }
-    tile_barrier();
+    sh.pipe.wait(&sh.pipe.carried, it);
+    const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
     // dx1, dx2, dx3, dgate take the places of x1, x2, x3, gate
     float2 e = sh.E[warp][lane], d_rate = bcast2(0.f), d_skip = bcast2(0.f);
 #pragma unroll
     for (int i = RSEG - 1; i >= 0; --i) {
-        if (kFull || i < n) {
-            const bool cut = kReset && (mask >> i & 1u);
-            const uint32_t w1 = x1(i), w2 = x2(i), wd = dy(i);
-            const float2 d = bf16x2_to_float2(wd);
-            const float2 v = product(w1, w2);
-            const float2 q = fma_bf16x2(x3(i), wd, e);
-            x3.put(i, __fmul2_rn(d, S));
-            float2 dv = kNorm ? __fmul2_rn(w[i], q) : q;
-            if (skip) dv = __ffma2_rn(dsk, d, dv);
-            x1.put(i, __fmul2_rn(dv, bf16x2_to_float2(w2)));
-            x2.put(i, __fmul2_rn(dv, bf16x2_to_float2(w1)));
-            e = __fmul2_rn(a[i], q);
-            float2 m = prev[i];
-            S = m;
-            if constexpr (kNorm) {
-                // d w / d l = -a^2 / w; no gradient where w = 0 (log_rate = 0)
-                const float2 r = make_float2(w[i].x > 0.f ? rcp_approx(w[i].x) : 0.f,
-                                             w[i].y > 0.f ? rcp_approx(w[i].y) : 0.f);
-                const float2 av = __fmul2_rn(a[i], v);
-                m = __ffma2_rn(make_float2(-av.x, -av.y), r, m);
-            }
-            float2 dl = __fmul2_rn(e, m);
-            if (cut) dl = e = bcast2(0.f);
-            float2 eg;
-            const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
-            d_rate = __ffma2_rn(dl, sig, d_rate);
-            d_skip = __ffma2_rn(d, v, d_skip);
-            // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
-            eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
-            const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
-            gate.put(i, __fmul2_rn(__fmul2_rn(rate, dl), slope));
+        const bool cut = kReset && (mask >> i & 1u);
+        const uint32_t w1 = x1(i), w2 = x2(i), wd = dy(i);
+        const float2 d = bf16x2_to_float2(wd);
+        const float2 v = product(w1, w2);
+        const float2 q = fma_bf16x2(x3(i), wd, e);
+        x3.put(i, __fmul2_rn(d, S));
+        float2 dv = kNorm ? __fmul2_rn(w[i], q) : q;
+        if (skip) dv = __ffma2_rn(dsk, d, dv);
+        x1.put(i, __fmul2_rn(dv, bf16x2_to_float2(w2)));
+        x2.put(i, __fmul2_rn(dv, bf16x2_to_float2(w1)));
+        e = __fmul2_rn(a[i], q);
+        float2 m = prev[i];
+        S = m;
+        if constexpr (kNorm) {
+            // d w / d l = -a^2 / w; no gradient where w = 0 (log_rate = 0)
+            const float2 r = make_float2(w[i].x > 0.f ? rcp_approx(w[i].x) : 0.f,
+                                         w[i].y > 0.f ? rcp_approx(w[i].y) : 0.f);
+            const float2 av = __fmul2_rn(a[i], v);
+            m = __ffma2_rn(make_float2(-av.x, -av.y), r, m);
         }
+        float2 dl = __fmul2_rn(e, m);
+        if (cut) dl = e = bcast2(0.f);
+        float2 eg;
+        const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
+        d_rate = __ffma2_rn(dl, sig, d_rate);
+        d_skip = __ffma2_rn(d, v, d_skip);
+        // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
+        eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
+        const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
+        gate.put(i, __fmul2_rn(__fmul2_rn(rate, dl), slope));
     }
     sh.rate[warp][lane] = d_rate;
     sh.skip[warp][lane] = d_skip;
 }
 
-// As forward_carry, from the right; and once the tile is done its parts of
-// dlog_rate and dDskip.
+// As forward_carry, from the right, with the states before the segments on the
+// way.
 template <bool kReset>
-__device__ __forceinline__ void backward_carry(const RecArgs &A, BackwardShared &sh, Records &rec, Tile t, int nseg,
-                                               int c, bool live)
+__device__ __forceinline__ void backward_carry(const RecArgs &A, BackwardShared &sh, Records &rec, Tile t,
+                                               const unsigned char *params, int it)
 {
     const int lane = rec.lane;
-    float2 l = sh.l[0][lane], q = sh.Q[nseg - 1][lane];
-#pragma unroll
-    for (int w = 1; w < RWARPS; ++w)
-        if (w < nseg) l = __fadd2_rn(l, sh.l[w][lane]);
-#pragma unroll
-    for (int w = RWARPS - 2; w >= 0; --w)
-        if (w < nseg - 1) q = carry<kReset>(sh.P[w][lane], q, sh.Q[w][lane]);
-    const float2 P = decay_over(l);
     const bool last = t.j == A.units - 1;
+    const int c = t.c + 2 * lane;
+    const bool live = c < A.D;
     const size_t state = static_cast<size_t>(t.b) * A.D + c;
-    float2 E = bcast2(0.f);
+    float2 E, P, q;
     rec.chain = t.chain;
-    if (t.j > 0) {
-        if (!last) rec.publish_unit(t.j, P, q);
-        E = rec.carry_into(t.j, A.hdr + 2);
-    } else if (A.dstate_out != nullptr) {
-        E = *reinterpret_cast<const float2 *>(A.dstate_out + state);
-    }
+    sh.pipe.find_carry(rec, t.j, it, A.dstate_out ? A.dstate_out + state : nullptr, live, E, [&](bool found) {
+        float2 S = param(params, 2, lane), l = sh.l[0][lane];  // the sums follow the tile's copy, the start states among it
+#pragma unroll
+        for (int w = 0; w < RWARPS; ++w) {
+            sh.S[w][lane] = S;
+            S = carry<kReset>(sh.P[w][lane], S, sh.A[w][lane]);
+            if (w > 0) l = __fadd2_rn(l, sh.l[w][lane]);
+        }
+        sh.pipe.arrive(&sh.started, lane);
+        q = sh.Q[RWARPS - 1][lane];
+#pragma unroll
+        for (int w = RWARPS - 2; w >= 0; --w) q = carry<kReset>(sh.P[w][lane], q, sh.Q[w][lane]);
+        P = decay_over(l);
+        if (!found && !last) rec.publish_unit(t.j, P, q);
+    });
     const float2 out = carry<true>(P, E, q);
     if (!last) rec.publish_carry(t.j, out);
-    if (last && live && A.dstate_in != nullptr) *reinterpret_cast<float2 *>(A.dstate_in + state) = out;
 #pragma unroll
     for (int w = RWARPS - 1; w >= 0; --w) {
-        if (w < nseg) {
-            sh.E[w][lane] = E;
-            E = carry<kReset>(sh.P[w][lane], E, sh.Q[w][lane]);
-        }
+        sh.E[w][lane] = E;
+        E = carry<kReset>(sh.P[w][lane], E, sh.Q[w][lane]);
     }
+    sh.pipe.arrive(&sh.pipe.carried, lane);
+    if (last && live && A.dstate_in != nullptr) *reinterpret_cast<float2 *>(A.dstate_in + state) = out;
 }
 
 // The parts replace the unit's (P, A) record, with a tag that no launch has: by
@@ -499,63 +546,48 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ BackwardShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == RWARPS * 32) sh.pipe.start(maps, A, stages);
+    if (threadIdx.x == RWARPS * 32) {
+        mbar_init(&sh.started, 1);
+        sh.pipe.start(maps, A, stages);
+    }
     Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
     if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
-    tile_barrier();
+    __syncthreads();
     unsigned int next = 0;
     for (int it = 0;; ++it) {
         const int st = it % kStages;
         const Tile t = sh.pipe.tile[st];
         if (t.j < 0) break;
-        unsigned char *stage = stages + st * 5 * kTileBytes;
+        unsigned char *stage = stages + st * sh.pipe.kBytes;
         const int unit = A.units - 1 - t.j;
-        const int rows = min(RT, A.L - unit * RT);
-        const bool live = t.c + 2 * lane < A.D;
-        const int c = live ? t.c + 2 * lane : 0;  // lanes without channels read some, and write nothing
         if (warp < RWARPS) {
-            const int n = min(max(rows - warp * RSEG, 0), RSEG);
-            const float2 rate = ldg_f2(A.log_rate + c);
-            const bool skip = A.Dskip != nullptr;
-            const float2 dsk = skip ? ldg_f2(A.Dskip + c) : bcast2(0.f);
-            const float2 start = ldg_f2(A.unit_states + (static_cast<size_t>(t.b) * A.units + unit) * A.D + c);
+            const int n = min(A.L - unit * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
             const unsigned int mask =
                 kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + unit * RT + warp * RSEG, n, lane)
                        : 0u;
-            if (!mbar_wait_bounded(&sh.pipe.full[st], (it / kStages) & 1) && threadIdx.x == 0)
-                atomicOr(A.hdr + 2, kErrTmaTimeout);
-            if (rows == RT)
-                backward_tile<kNorm, kReset, true>(sh, stage, warp, lane, RSEG, rate, skip, dsk, start, mask);
-            else
-                backward_tile<kNorm, kReset, false>(sh, stage, warp, lane, n, rate, skip, dsk, start, mask);
+            sh.pipe.wait(&sh.pipe.full[st], it / kStages);
+            backward_tile<kNorm, kReset>(sh, stage, warp, lane, n, A.Dskip != nullptr, mask, it);
             fence_proxy_async_smem();
-            tile_barrier();
+            sh.pipe.arrive(&sh.pipe.done, lane);
         } else {
-            if (lane == 0) {
-                if (it > 0) {
-                    bulk_wait_read();
-                    sh.pipe.request(maps, A, stages, st ^ 1, tile_of(A, next));
-                }
-                next = next_tile(A, it + kStages);
-            }
-            __syncwarp();
-            tile_barrier();
-            backward_carry<kReset>(A, sh, rec, t, (rows + RSEG - 1) / RSEG, c, live);
-            tile_barrier();
-            tile_barrier();
+            if (lane == 0) next = next_tile(A, it + kStages);
+            backward_carry<kReset>(A, sh, rec, t, stage + 5 * kTileBytes, it);
+            sh.pipe.wait(&sh.pipe.done, it);
             if (lane == 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     tma_store_4d(&maps.out[k], stage + k * kTileBytes, t.c, 0, unit * RT, t.b);
                 bulk_commit();
             }
-            backward_parts(A, sh, t, lane);  // the warps' next sums follow the next tile's barriers
+            backward_parts(A, sh, t, lane);  // the warps' next sums follow the next tile's carry
+            if (lane == 0) {
+                bulk_wait_read();
+                sh.pipe.request(maps, A, stages, st, tile_of(A, next));
+            }
+            __syncwarp();
         }
     }
-    if (threadIdx.x == RWARPS * 32) {
-        bulk_wait_read();
-        finish(A);
-    }
+    if (threadIdx.x == RWARPS * 32) finish(A);
 }
 
 // dlog_rate and dDskip: the units' parts summed in double, in a fixed order: 32
@@ -604,7 +636,7 @@ __global__ void __launch_bounds__(kRecDecodeThreads) recurrence_decode_kernel(co
     float2 *st = reinterpret_cast<float2 *>(A.state_out + static_cast<size_t>(b) * A.D + c);
     const float2 S = *st;
     float2 a, w, e;
-    decay<kNorm>(__fmul2_rn(ldg_f2(A.log_rate + c), gate_sigmoid(g, e)), a, w);
+    decay<kNorm>(__fmul2_rn(finite_rate(ldg_f2(A.log_rate + c)), gate_sigmoid(g, e)), a, w);
     const float2 s = __ffma2_rn(a, S, kNorm ? __fmul2_rn(w, v) : v);
     *st = s;
     float2 y = __fmul2_rn(f3, s);
@@ -617,7 +649,7 @@ template <auto kernel>
 int launch_units(int tensors, const RecMaps &maps, const RecArgs &a, cudaStream_t st)
 {
     thread_local int configured_device = -1, places = 0;  // per kernel and thread
-    const int smem = kStages * tensors * kTileBytes;
+    const int smem = kStages * (tensors * kTileBytes + 3 * kParamBytes);
     int dev = 0;
     HYENA_TRY(cudaGetDevice(&dev), "gated recurrence: current device");
     if (configured_device != dev) {

@@ -75,6 +75,15 @@ __device__ __forceinline__ float2 gate_sigmoid(float2 g, float2 &e)
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
+// A rate of -inf counts as the lowest finite one: times a sigmoid of 0 it has to be 0.
+__device__ __forceinline__ float2 finite_rate(float2 r)
+{
+    float2 f;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(f.x) : "f"(r.x), "f"(-3.402823466e38f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(f.y) : "f"(r.y), "f"(-3.402823466e38f));
+    return f;
+}
+
 // a b + c of two bf16 pairs and an fp32 pair, one rounding (the product of two
 // bf16 values is exact).
 __device__ __forceinline__ float2 fma_bf16x2(uint32_t a, uint32_t b, float2 c)
@@ -130,54 +139,46 @@ __device__ __forceinline__ float2 carry(float2 P, float2 C, float2 A)
     return make_float2(__float_as_int(P.x) < 0 ? A.x : r.x, __float_as_int(P.y) < 0 ? A.y : r.y);
 }
 
-// Gates of a segment's first n tokens (kFull: n = RSEG): a, w, the sum l of the
-// tokens' l, and the product P of their a (for the steps within the unit only;
-// -0 if a token is a reset).  `mask` bit i: token i is a reset.
-template <bool kNorm, bool kReset, bool kFull, class Row>
+// Gates of a segment: a, w, the sum l of the tokens' l, and the product P of
+// their a (for the steps within the unit only; -0 if a token is a reset).
+// `mask` bit i: token i is a reset.
+template <bool kNorm, bool kReset, class Row>
 __device__ __forceinline__ void segment_gates(float2 (&a)[RSEG], float2 (&w)[RSEG], float2 &l, float2 &P, Row gate,
-                                              int n, float2 rate, unsigned int mask)
+                                              float2 rate, unsigned int mask)
 {
-    l = bcast2(0.f);
-    P = bcast2(1.f);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
-        if (kFull || i < n) {
-            float2 e;
-            const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), e);
-            float2 li = __fmul2_rn(rate, sig);
-            l = i == 0 ? li : __ffma2_rn(rate, sig, l);
-            if (kReset && (mask >> i & 1u)) li = l = bcast2(-INFINITY);  // a = 0, w = 1
-            decay<kNorm>(li, a[i], w[i]);
-            P = i == 0 ? a[i] : __fmul2_rn(P, a[i]);
-        }
+        float2 e;
+        const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), e);
+        float2 li = __fmul2_rn(rate, sig);
+        l = i == 0 ? li : __ffma2_rn(rate, sig, l);
+        if (kReset && (mask >> i & 1u)) li = l = bcast2(-INFINITY);  // a = 0, w = 1
+        decay<kNorm>(li, a[i], w[i]);
+        P = i == 0 ? a[i] : __fmul2_rn(P, a[i]);
     }
     if (kReset && mask) P = bcast2(-0.f);
 }
 
 // End state of a segment from a zero start, with u = w v.
-template <bool kReset, bool kFull>
-__device__ __forceinline__ float2 segment_end(const float2 (&a)[RSEG], const float2 (&u)[RSEG], int n,
-                                              unsigned int mask)
+template <bool kReset>
+__device__ __forceinline__ float2 segment_end(const float2 (&a)[RSEG], const float2 (&u)[RSEG], unsigned int mask)
 {
-    float2 A = bcast2(0.f);
+    float2 A = u[0];
 #pragma unroll
-    for (int i = 0; i < RSEG; ++i)
-        if (kFull || i < n) A = i == 0 || (kReset && (mask >> i & 1u)) ? u[i] : __ffma2_rn(a[i], A, u[i]);
+    for (int i = 1; i < RSEG; ++i) A = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], A, u[i]);
     return A;
 }
 
 // The gradient that a segment hands to the token before it, e_t = a_t (r_t +
 // e_{t+1}) with r = x3 dy, from a zero e at its right edge.
-template <bool kReset, bool kFull, class Row>
-__device__ __forceinline__ float2 segment_left(const float2 (&a)[RSEG], Row x3, Row dy, int n, unsigned int mask)
+template <bool kReset, class Row>
+__device__ __forceinline__ float2 segment_left(const float2 (&a)[RSEG], Row x3, Row dy, unsigned int mask)
 {
     float2 e = bcast2(0.f);
 #pragma unroll
     for (int i = RSEG - 1; i >= 0; --i) {
-        if (kFull || i < n) {
-            e = __fmul2_rn(a[i], fma_bf16x2(x3(i), dy(i), e));
-            if (kReset && (mask >> i & 1u)) e = bcast2(0.f);
-        }
+        e = __fmul2_rn(a[i], fma_bf16x2(x3(i), dy(i), e));
+        if (kReset && (mask >> i & 1u)) e = bcast2(0.f);
     }
     return e;
 }
@@ -187,6 +188,16 @@ __device__ __forceinline__ unsigned int segment_resets(const uint8_t *reset, lon
 {
     const bool r = lane < n && reset[row0 + lane] != 0;
     return __ballot_sync(kFullMask, r);
+}
+
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into
+// this CTA's shared memory, counted by `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
 // 4-D tiled TMA store from shared memory as one bulk group of this thread; what
