@@ -455,12 +455,14 @@ bool encode_recurrence_maps(RecMaps &maps, const RecArgs &a)
         CUtensorMap *map;
         const uint16_t *p;
         long long ld;
-    } const all[] = {{&maps.in[0], a.x1, a.ld_x},    {&maps.in[1], a.x2, a.ld_x},     {&maps.in[2], a.x3, a.ld_x},
-                     {&maps.in[3], a.gate, a.ld_g},  {&maps.in[4], a.dy, a.ld_dy},    {&maps.out[0], a.y, a.ld_y},
-                     {&maps.out[0], a.dx1, a.ld_dx}, {&maps.out[1], a.dx2, a.ld_dx},  {&maps.out[2], a.dx3, a.ld_dx},
-                     {&maps.out[3], a.dgate, a.ld_dg}};
+        int rows;
+    } const all[] = {{&maps.in[0], a.x1, a.ld_x, RT},       {&maps.in[1], a.x2, a.ld_x, RT},
+                     {&maps.in[2], a.x3, a.ld_x, RT},       {&maps.in[3], a.gate, a.ld_g, RT},
+                     {&maps.in[4], a.dy, a.ld_dy, RT},      {&maps.out[0], a.y, a.ld_y, RSEG},
+                     {&maps.out[0], a.dx1, a.ld_dx, RSEG},  {&maps.out[1], a.dx2, a.ld_dx, RSEG},
+                     {&maps.out[2], a.dx3, a.ld_dx, RSEG},  {&maps.out[3], a.dgate, a.ld_dg, RSEG}};
     for (const auto &m : all)
-        if (m.p && !encode_x_map(m.map, separate_source(m.p, m.p, m.p, m.ld, a.D), 0, a.B, a.L, a.D, RT, RCH))
+        if (m.p && !encode_x_map(m.map, separate_source(m.p, m.p, m.p, m.ld, a.D), 0, a.B, a.L, a.D, m.rows, RCH))
             return false;
     return true;
 }

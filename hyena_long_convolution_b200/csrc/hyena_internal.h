@@ -220,6 +220,8 @@ int launch_fir_dft(const CUtensorMap &m1, const CUtensorMap &m2, const CUtensorM
 // batch row; arrays per unit and channel are [B][units][D].
 constexpr int RT = HYENA_RECURRENCE_UNIT;
 constexpr int RCH = 64;
+constexpr int RWARPS = 8;          // computing warps of a CTA, one time segment each
+constexpr int RSEG = RT / RWARPS;  // tokens per segment
 
 struct RecArgs {
     const uint16_t *x1, *x2, *x3, *gate, *dy;
@@ -249,8 +251,8 @@ struct RecArgs {
 constexpr size_t kRecHeaderBytes = 256;
 constexpr size_t kRecTileBytes = (RCH + RCH / 2) * 16;
 
-// Tensor maps [B][L][1][D], boxes of RT tokens x RCH channels: over x1, x2, x3,
-// gate and (gradient) dy, and over y or dx1, dx2, dx3, dgate.
+// Tensor maps [B][L][1][D]: over x1, x2, x3, gate and (gradient) dy in boxes of
+// RT tokens x RCH channels, and over y or dx1, dx2, dx3, dgate in boxes of RSEG.
 struct RecMaps {
     CUtensorMap in[5], out[4];
 };

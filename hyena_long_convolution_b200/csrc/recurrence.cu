@@ -96,17 +96,21 @@ struct Records {
         store_record(known + tile(j) * (RCH / 2) + lane, C.x, C.y, epoch);
     }
 
-    // One look for the carry into unit j > 0 (all lanes of a warp); true if it is
-    // known.  One load looks at the first records of the last 16 units: lanes
-    // 0-15 at known carries, lanes 16-31 at units.  Once a carry and every unit
-    // behind it are there, each lane loads its own channels' records, whose tags
-    // it checks as well.
-    __device__ __forceinline__ bool look_back(int j, float2 &C) const
+    // Looking for the carry into unit j > 0, by all lanes of a warp.  glance():
+    // one load of the first records of the last 16 units, lanes 0-15 known
+    // carries, lanes 16-31 units.  look_back(): with what it brought, true if the
+    // carry can be formed: once a known carry and every unit behind it are there,
+    // each lane loads its own channels' records, whose tags it checks as well.
+    __device__ __forceinline__ uint32_t glance(int j) const
     {
         const int back = lane & 15;
         const size_t at = tile(max(j - 1 - back, 0));
-        const uint4 hint = load_record(lane < 16 ? known + at * (RCH / 2) : unit + at * RCH);
-        const unsigned int ready = __ballot_sync(kFullMask, back < j && hint.z == epoch);
+        const uint32_t tag = load_record(lane < 16 ? known + at * (RCH / 2) : unit + at * RCH).z;
+        return back < j ? tag : epoch - 1u;
+    }
+    __device__ __forceinline__ bool look_back(int j, uint32_t seen, float2 &C) const
+    {
+        const unsigned int ready = __ballot_sync(kFullMask, seen == epoch);
         const unsigned int units = ready >> 16;
         const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
         if (k < 0 || ((units + 1u) & ((1u << k) - 1u)) != 0u) return false;
@@ -197,20 +201,26 @@ __device__ __forceinline__ Tile tile_of(const RecArgs &A, unsigned int ticket)
 }
 
 // What forward and gradient share: two stages of N tensors' rows and the
-// channels' parameters, their tiles and barriers.  A tile's outputs leave from its stage by TMA; the stage is
-// asked to take new rows half a tile later, when that has read it.
+// channels' parameters, their tiles and barriers.  A tile's outputs leave from
+// its stage, each warp's rows by a TMA store of its own; the stage takes new
+// rows once the warps, in the next tile, have seen their stores read it.
 template <int N, bool kBack>
 struct Pipeline {
     static constexpr int kBytes = N * kTileBytes + 3 * kParamBytes;  // rows; log_rate, Dskip, start states
     Tile tile[kStages];
     uint64_t full[kStages];
-    uint64_t sums, carried, done;  // of the current tile: segments' sums, states before them, outputs
+    uint64_t sums, carried;  // of the current tile: the segments' sums, the carry into it
+    uint64_t freed;          // the previous tile's stage
     unsigned int *error;
 
+    // One thread.  A tile that is none only ends the wait for it.
     __device__ __forceinline__ void request(const RecMaps &m, const RecArgs &A, unsigned char *stages, int s, Tile t)
     {
         tile[s] = t;
-        if (t.j < 0) return;
+        if (t.j < 0) {
+            mbar_arrive(&full[s]);
+            return;
+        }
         const int unit = kBack ? A.units - 1 - t.j : t.j;
         unsigned char *stage = stages + s * kBytes, *params = stage + N * kTileBytes;
         const uint32_t bytes = 4u * min(RCH, A.D - t.c);  // a multiple of 32: D is one of 8
@@ -228,7 +238,7 @@ struct Pipeline {
         for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
         mbar_init(&sums, RWARPS);
         mbar_init(&carried, 1);
-        mbar_init(&done, RWARPS);
+        mbar_init(&freed, RWARPS);
         error = A.hdr + 2;
         fence_mbar_init();
         for (int s = 0; s < kStages; ++s) request(m, A, stages, s, tile_of(A, next_tile(A, s)));
@@ -243,51 +253,110 @@ struct Pipeline {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     }
-
-    // The control warp's part of a tile until the carry C into it and its own sums are
-    // known.  Looking back starts while the sums are formed; `sums_ready()` runs
-    // once they are, with the carry known or not.  Gives up after the bounded wait.
-    template <class F>
-    __device__ __forceinline__ void find_carry(const Records &rec, int j, int it, const float *initial, bool live,
-                                               float2 &C, F sums_ready)
+    // A computing warp, some time into tile `it`: its stores of the tile before
+    // have read their stage.
+    __device__ __forceinline__ void release(int it, int lane)
     {
-        bool found = j == 0, summed = false;
-        C = bcast2(0.f);
-        if (found && initial != nullptr && live) C = *reinterpret_cast<const float2 *>(initial);
-        unsigned long long t0 = 0;
-        for (;;) {
-            if (!found) found = rec.look_back(j, C);
-            if (!summed) {
-                if (found)
-                    wait(&sums, it);
-                summed = found || __all_sync(kFullMask, mbar_test_wait(&sums, it & 1));
-                if (summed) sums_ready(found);
-            }
-            if (found && summed) return;
-            const unsigned long long t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (__any_sync(kFullMask, t - t0 > kWaitLimitNs)) {
-                if (rec.lane == 0) atomicOr(error, kErrLookbackTimeout);
-                C = bcast2(0.f);
-                if (summed) return;
-                found = true;
-            }
-        }
+        if (it == 0 || lane != 0) return;
+        bulk_wait_read();
+        mbar_arrive(&freed);
     }
 };
 
-// A CTA: RWARPS warps that compute, and one that takes tickets, runs the copies
+// A CTA: RWARPS warps that compute, and one that takes tickets, asks for rows
 // and finds the carries, so that the computing warps' registers do not have to
 // hold its work too.
 constexpr int kThreads = (RWARPS + 1) * 32;
 
+// The control warp.  What differs between forward and gradient is its Work:
+//   sums()       from the segments' sums of tile t: P and A of its unit
+//   initial(c)   the carry into the first unit;  known(t, C, E)  what else to
+//                write once the carry C into the unit and E behind it are known
+//   parts(t, s)  once tile t in stage s is done
+template <int N, bool kBack, class Work>
+__device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const RecMaps &maps, const RecArgs &A,
+                                             unsigned char *stages, float2 *carry_in, int lane, Work work)
+{
+    Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
+    if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
+    Tile before{};
+    for (int it = 0;; ++it) {
+        const int st = it % kStages;
+        const Tile t = pipe.tile[st];
+        if (t.j < 0) {
+            if (it > 0) {
+                pipe.wait(&pipe.freed, it - 1);
+                work.parts(before, st ^ 1);
+            }
+            break;
+        }
+        unsigned int next = 0;
+        bool asked = it == 0, summed = false, found = t.j == 0;
+        if (!asked && lane == 0) next = next_tile(A, it + 1);
+        const auto ask = [&] {  // the tile before is done: its stage takes the next one's rows
+            work.parts(before, st ^ 1);
+            if (lane == 0) pipe.request(maps, A, stages, st ^ 1, tile_of(A, next));
+            __syncwarp();
+            asked = true;
+        };
+        float2 C = found ? work.initial(t) : bcast2(0.f), P, a;
+        const bool last = t.j == A.units - 1;
+        rec.chain = t.chain;
+        unsigned long long t0 = 0;
+        for (;;) {
+            // the glance's load is under way while the CTA's own barriers are looked at
+            const uint32_t seen = found ? 0u : rec.glance(t.j);
+            if (!asked && __all_sync(kFullMask, mbar_test_wait(&pipe.freed, (it - 1) & 1))) ask();
+            if (!summed) {
+                if (found) pipe.wait(&pipe.sums, it);
+                summed = found || __all_sync(kFullMask, mbar_test_wait(&pipe.sums, it & 1));
+                if (summed) {
+                    work.sums(st, P, a);
+                    if (!found && !last) rec.publish_unit(t.j, P, a);
+                }
+            }
+            if (!found) found = rec.look_back(t.j, seen, C);
+            if (found && summed) break;
+            const unsigned long long now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (!found && __any_sync(kFullMask, now - t0 > kWaitLimitNs)) {
+                if (lane == 0) atomicOr(pipe.error, kErrLookbackTimeout);
+                C = bcast2(0.f);
+                found = true;
+                if (summed) break;
+            }
+        }
+        const float2 E = carry<true>(P, C, a);
+        if (!last) rec.publish_carry(t.j, E);
+        carry_in[lane] = C;
+        pipe.arrive(&pipe.carried, lane);
+        work.known(t, C, E);
+        if (!asked) {
+            pipe.wait(&pipe.freed, it - 1);
+            ask();
+        }
+        before = t;
+    }
+    if (lane == 0) finish(A);
+}
+
 // ---------------------------------------------------------------- forward
 
+// The segments' sums take the place of the first gates of each warp's own rows.
+struct ForwardSums {
+    float2 P[32], A[32], l[32];
+};
+static_assert(sizeof(ForwardSums) <= RSEG * RCH * 2, "a segment's sums fit in its rows of one tensor");
+
 struct ForwardShared {
-    float2 P[RWARPS][32], l[RWARPS][32], A[RWARPS][32];
-    float2 C[RWARPS][32];  // the state before each segment
+    float2 C[32];  // the carry into the tile
     Pipeline<4, false> pipe;
 };
+
+__device__ __forceinline__ ForwardSums &forward_sums(unsigned char *stage, int warp)
+{
+    return *reinterpret_cast<ForwardSums *>(stage + 3 * kTileBytes + warp * RSEG * RCH * 2);
+}
 
 template <bool kNorm, bool kReset>
 __device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *stage, int warp, int lane, int n,
@@ -299,17 +368,27 @@ __device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *s
     if (n < RSEG) pad_tail(x1, gate, n);
     float2 a[RSEG], u[RSEG], l, P;
     segment_gates<kNorm, kReset>(a, u, l, P, gate, finite_rate(param(params, 0, lane)), mask);
+    sh.pipe.release(it, lane);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
         const float2 v = product(x1(i), x2(i));
         u[i] = kNorm ? __fmul2_rn(u[i], v) : v;
     }
-    sh.l[warp][lane] = l;
-    sh.P[warp][lane] = P;
-    sh.A[warp][lane] = segment_end<kReset>(a, u, mask);
+    ForwardSums &own = forward_sums(stage, warp);
+    __syncwarp();  // the warp has read its gates
+    own.l[lane] = l;
+    own.P[lane] = P;
+    own.A[lane] = segment_end<kReset>(a, u, mask);
     sh.pipe.arrive(&sh.pipe.sums, lane);
     sh.pipe.wait(&sh.pipe.carried, it);
-    float2 C = sh.C[warp][lane];
+    float2 C = sh.C[lane];
+#pragma unroll
+    for (int w = 0; w < RWARPS - 1; ++w) {
+        if (w < warp) {
+            const ForwardSums &f = forward_sums(stage, w);
+            C = carry<kReset>(f.P[lane], C, f.A[lane]);
+        }
+    }
     const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
@@ -320,44 +399,42 @@ __device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *s
     }
 }
 
-// The control warp's part of a tile: from the segments' sums the unit's (P, A),
-// the carry into it and the state before each segment.
 template <bool kReset>
-__device__ __forceinline__ void forward_carry(const RecArgs &A, ForwardShared &sh, Records &rec, Tile t, int it)
-{
-    const int lane = rec.lane;
-    const bool last = t.j == A.units - 1;
-    const int c = t.c + 2 * lane;
-    const bool live = c < A.D;
-    const size_t state = static_cast<size_t>(t.b) * A.D + c;
-    float2 C, P, a;
-    rec.chain = t.chain;
-    sh.pipe.find_carry(rec, t.j, it, A.state_in ? A.state_in + state : nullptr, live, C, [&](bool found) {
-        float2 l = sh.l[0][lane];
-        a = sh.A[0][lane];
+struct ForwardWork {
+    const RecArgs &A;
+    unsigned char *stages;
+    int lane;
+
+    __device__ __forceinline__ size_t state(Tile t) const { return static_cast<size_t>(t.b) * A.D + t.c + 2 * lane; }
+    __device__ __forceinline__ bool live(Tile t) const { return t.c + 2 * lane < A.D; }
+    __device__ __forceinline__ float2 initial(Tile t) const
+    {
+        return A.state_in != nullptr && live(t) ? *reinterpret_cast<const float2 *>(A.state_in + state(t))
+                                                : bcast2(0.f);
+    }
+    __device__ __forceinline__ void sums(int st, float2 &P, float2 &a) const
+    {
+        unsigned char *stage = stages + st * Pipeline<4, false>::kBytes;
+        float2 l = forward_sums(stage, 0).l[lane];
+        a = forward_sums(stage, 0).A[lane];
 #pragma unroll
         for (int w = 1; w < RWARPS; ++w) {
-            l = __fadd2_rn(l, sh.l[w][lane]);
-            a = carry<kReset>(sh.P[w][lane], a, sh.A[w][lane]);
+            const ForwardSums &f = forward_sums(stage, w);
+            l = __fadd2_rn(l, f.l[lane]);
+            a = carry<kReset>(f.P[lane], a, f.A[lane]);
         }
         P = decay_over(l);
-        if (!found && !last) rec.publish_unit(t.j, P, a);
-    });
-    const float2 E = carry<true>(P, C, a);
-    if (!last) rec.publish_carry(t.j, E);
-    const float2 start = C;
-#pragma unroll
-    for (int w = 0; w < RWARPS; ++w) {
-        sh.C[w][lane] = C;
-        C = carry<kReset>(sh.P[w][lane], C, sh.A[w][lane]);
     }
-    sh.pipe.arrive(&sh.pipe.carried, lane);
-    if (live) {
+    __device__ __forceinline__ void known(Tile t, float2 C, float2 E) const
+    {
+        if (!live(t)) return;
         if (A.C != nullptr)
-            *reinterpret_cast<float2 *>(A.C + (static_cast<size_t>(t.b) * A.units + t.j) * A.D + c) = start;
-        if (last && A.state_out != nullptr) *reinterpret_cast<float2 *>(A.state_out + state) = E;
+            *reinterpret_cast<float2 *>(A.C + (static_cast<size_t>(t.b) * A.units + t.j) * A.D + t.c + 2 * lane) = C;
+        if (t.j == A.units - 1 && A.state_out != nullptr)
+            *reinterpret_cast<float2 *>(A.state_out + state(t)) = E;
     }
-}
+    __device__ __forceinline__ void parts(Tile, int) const {}
+};
 
 template <bool kNorm, bool kReset>
 __global__ void __launch_bounds__(kThreads, 3)
@@ -367,54 +444,47 @@ __global__ void __launch_bounds__(kThreads, 3)
     __shared__ ForwardShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == RWARPS * 32) sh.pipe.start(maps, A, stages);
-    Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
-    if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
     __syncthreads();
-    unsigned int next = 0;
+    if (warp == RWARPS) {
+        control_warp(sh.pipe, maps, A, stages, sh.C, lane, ForwardWork<kReset>{A, stages, lane});
+        return;
+    }
     for (int it = 0;; ++it) {
         const int st = it % kStages;
+        sh.pipe.wait(&sh.pipe.full[st], it / kStages);
         const Tile t = sh.pipe.tile[st];
-        if (t.j < 0) break;
+        if (t.j < 0) {
+            sh.pipe.release(it, lane);
+            break;
+        }
         unsigned char *stage = stages + st * sh.pipe.kBytes;
-        if (warp < RWARPS) {
-            const int n = min(A.L - t.j * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
-            const unsigned int mask =
-                kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + t.j * RT + warp * RSEG, n, lane)
-                       : 0u;
-            sh.pipe.wait(&sh.pipe.full[st], it / kStages);
-            forward_tile<kNorm, kReset>(sh, stage, warp, lane, n, A.Dskip != nullptr, mask, it);
-            fence_proxy_async_smem();
-            sh.pipe.arrive(&sh.pipe.done, lane);
-        } else {
-            if (lane == 0) next = next_tile(A, it + kStages);
-            forward_carry<kReset>(A, sh, rec, t, it);
-            sh.pipe.wait(&sh.pipe.done, it);
-            if (lane == 0) {
-                tma_store_4d(&maps.out[0], stage + 2 * kTileBytes, t.c, 0, t.j * RT, t.b);
-                bulk_commit();
-                bulk_wait_read();
-                sh.pipe.request(maps, A, stages, st, tile_of(A, next));
-            }
-            __syncwarp();
+        const int n = min(A.L - t.j * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
+        const unsigned int mask =
+            kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + t.j * RT + warp * RSEG, n, lane) : 0u;
+        forward_tile<kNorm, kReset>(sh, stage, warp, lane, n, A.Dskip != nullptr, mask, it);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (n > 0)
+                tma_store_4d(&maps.out[0], stage + 2 * kTileBytes + warp * RSEG * RCH * 2, t.c, 0,
+                             t.j * RT + warp * RSEG, t.b);
+            bulk_commit();
         }
     }
-    if (threadIdx.x == RWARPS * 32) finish(A);
 }
 
 // ---------------------------------------------------------------- gradient
 
 struct BackwardShared {
-    float2 P[RWARPS][32], l[RWARPS][32], A[RWARPS][32], Q[RWARPS][32];
-    float2 rate[RWARPS][32], skip[RWARPS][32];
-    float2 S[RWARPS][32];  // the state before each segment
-    float2 E[RWARPS][32];  // the gradient from the right of each segment
-    uint64_t started;      // S is known
+    float2 P[kStages][RWARPS][32], A[kStages][RWARPS][32], Q[kStages][RWARPS][32], l[kStages][RWARPS][32];
+    float2 rate[kStages][RWARPS][32], skip[kStages][RWARPS][32];
+    float2 E[32];  // the carry into the tile, from the right
     Pipeline<5, true> pipe;
 };
 
 template <bool kNorm, bool kReset>
-__device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char *stage, int warp, int lane, int n,
-                                              bool skip, unsigned int mask, int it)
+__device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char *stage, int st, int warp, int lane,
+                                              int n, bool skip, unsigned int mask, int it)
 {
     const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
     const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
@@ -424,19 +494,23 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
     const float2 rate = finite_rate(param(params, 0, lane));
     float2 a[RSEG], w[RSEG], prev[RSEG], l, P;
     segment_gates<kNorm, kReset>(a, w, l, P, gate, rate, mask);
+    sh.pipe.release(it, lane);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
         prev[i] = product(x1(i), x2(i));  // u, until the states are known
         if constexpr (kNorm) prev[i] = __fmul2_rn(w[i], prev[i]);
     }
-    sh.l[warp][lane] = l;
-    sh.P[warp][lane] = P;
-    sh.A[warp][lane] = segment_end<kReset>(a, prev, mask);
-    sh.Q[warp][lane] = segment_left<kReset>(a, x3, dy, mask);
+    sh.l[st][warp][lane] = l;
+    sh.P[st][warp][lane] = P;
+    sh.A[st][warp][lane] = segment_end<kReset>(a, prev, mask);
+    sh.Q[st][warp][lane] = segment_left<kReset>(a, x3, dy, mask);
     sh.pipe.arrive(&sh.pipe.sums, lane);
     // the state before each token, while the carry from the right is found
-    sh.pipe.wait(&sh.started, it);
-    float2 S = sh.S[warp][lane];
+    sh.pipe.wait(&sh.pipe.sums, it);
+    float2 S = param(params, 2, lane);
+#pragma unroll
+    for (int k = 0; k < RWARPS - 1; ++k)
+        if (k < warp) S = carry<kReset>(sh.P[st][k][lane], S, sh.A[st][k][lane]);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
         const float2 s = kReset && (mask >> i & 1u) ? prev[i] : __ffma2_rn(a[i], S, prev[i]);
@@ -445,8 +519,11 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
     }
     sh.pipe.wait(&sh.pipe.carried, it);
     const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
+    float2 e = sh.E[lane], d_rate = bcast2(0.f), d_skip = bcast2(0.f);
+#pragma unroll
+    for (int k = RWARPS - 1; k > 0; --k)
+        if (k > warp) e = carry<kReset>(sh.P[st][k][lane], e, sh.Q[st][k][lane]);
     // dx1, dx2, dx3, dgate take the places of x1, x2, x3, gate
-    float2 e = sh.E[warp][lane], d_rate = bcast2(0.f), d_skip = bcast2(0.f);
 #pragma unroll
     for (int i = RSEG - 1; i >= 0; --i) {
         const bool cut = kReset && (mask >> i & 1u);
@@ -480,64 +557,54 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
         const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
         gate.put(i, __fmul2_rn(__fmul2_rn(rate, dl), slope));
     }
-    sh.rate[warp][lane] = d_rate;
-    sh.skip[warp][lane] = d_skip;
+    sh.rate[st][warp][lane] = d_rate;
+    sh.skip[st][warp][lane] = d_skip;
 }
 
-// As forward_carry, from the right, with the states before the segments on the
-// way.
 template <bool kReset>
-__device__ __forceinline__ void backward_carry(const RecArgs &A, BackwardShared &sh, Records &rec, Tile t,
-                                               const unsigned char *params, int it)
-{
-    const int lane = rec.lane;
-    const bool last = t.j == A.units - 1;
-    const int c = t.c + 2 * lane;
-    const bool live = c < A.D;
-    const size_t state = static_cast<size_t>(t.b) * A.D + c;
-    float2 E, P, q;
-    rec.chain = t.chain;
-    sh.pipe.find_carry(rec, t.j, it, A.dstate_out ? A.dstate_out + state : nullptr, live, E, [&](bool found) {
-        float2 S = param(params, 2, lane), l = sh.l[0][lane];  // the sums follow the tile's copy, the start states among it
-#pragma unroll
-        for (int w = 0; w < RWARPS; ++w) {
-            sh.S[w][lane] = S;
-            S = carry<kReset>(sh.P[w][lane], S, sh.A[w][lane]);
-            if (w > 0) l = __fadd2_rn(l, sh.l[w][lane]);
-        }
-        sh.pipe.arrive(&sh.started, lane);
-        q = sh.Q[RWARPS - 1][lane];
-#pragma unroll
-        for (int w = RWARPS - 2; w >= 0; --w) q = carry<kReset>(sh.P[w][lane], q, sh.Q[w][lane]);
-        P = decay_over(l);
-        if (!found && !last) rec.publish_unit(t.j, P, q);
-    });
-    const float2 out = carry<true>(P, E, q);
-    if (!last) rec.publish_carry(t.j, out);
-#pragma unroll
-    for (int w = RWARPS - 1; w >= 0; --w) {
-        sh.E[w][lane] = E;
-        E = carry<kReset>(sh.P[w][lane], E, sh.Q[w][lane]);
-    }
-    sh.pipe.arrive(&sh.pipe.carried, lane);
-    if (last && live && A.dstate_in != nullptr) *reinterpret_cast<float2 *>(A.dstate_in + state) = out;
-}
+struct BackwardWork {
+    const RecArgs &A;
+    const BackwardShared &sh;
+    int lane;
 
-// The parts replace the unit's (P, A) record, with a tag that no launch has: by
-// then the unit's carry is published, and a reader that finds no (P, A) looks
-// again and finds the carry.
-__device__ __forceinline__ void backward_parts(const RecArgs &A, const BackwardShared &sh, Tile t, int lane)
-{
-    float2 d_rate = sh.rate[0][lane], d_skip = sh.skip[0][lane];
-#pragma unroll
-    for (int w = 1; w < RWARPS; ++w) {
-        d_rate = __fadd2_rn(d_rate, sh.rate[w][lane]);
-        d_skip = __fadd2_rn(d_skip, sh.skip[w][lane]);
+    __device__ __forceinline__ size_t state(Tile t) const { return static_cast<size_t>(t.b) * A.D + t.c + 2 * lane; }
+    __device__ __forceinline__ bool live(Tile t) const { return t.c + 2 * lane < A.D; }
+    __device__ __forceinline__ float2 initial(Tile t) const
+    {
+        return A.dstate_out != nullptr && live(t) ? *reinterpret_cast<const float2 *>(A.dstate_out + state(t))
+                                                  : bcast2(0.f);
     }
-    uint4 *u = A.rec_unit + (static_cast<size_t>(t.j) * A.chains + t.chain) * RCH + 2 * lane;
-    store_record(u, d_rate.x, d_skip.x, 0u);
-    store_record(u + 1, d_rate.y, d_skip.y, 0u);
-}
+    __device__ __forceinline__ void sums(int st, float2 &P, float2 &q) const
+    {
+        float2 l = sh.l[st][0][lane];
+#pragma unroll
+        for (int w = 1; w < RWARPS; ++w) l = __fadd2_rn(l, sh.l[st][w][lane]);
+        q = sh.Q[st][RWARPS - 1][lane];
+#pragma unroll
+        for (int w = RWARPS - 2; w >= 0; --w) q = carry<kReset>(sh.P[st][w][lane], q, sh.Q[st][w][lane]);
+        P = decay_over(l);
+    }
+    __device__ __forceinline__ void known(Tile t, float2, float2 E) const
+    {
+        if (live(t) && t.j == A.units - 1 && A.dstate_in != nullptr)
+            *reinterpret_cast<float2 *>(A.dstate_in + state(t)) = E;
+    }
+    // The unit's parts of dlog_rate and dDskip replace its (P, A) record, with a
+    // tag that no launch has: by then the unit's carry is published, and a reader
+    // that finds no (P, A) looks again and finds the carry.
+    __device__ __forceinline__ void parts(Tile t, int st) const
+    {
+        float2 d_rate = sh.rate[st][0][lane], d_skip = sh.skip[st][0][lane];
+#pragma unroll
+        for (int w = 1; w < RWARPS; ++w) {
+            d_rate = __fadd2_rn(d_rate, sh.rate[st][w][lane]);
+            d_skip = __fadd2_rn(d_skip, sh.skip[st][w][lane]);
+        }
+        uint4 *u = A.rec_unit + (static_cast<size_t>(t.j) * A.chains + t.chain) * RCH + 2 * lane;
+        store_record(u, d_rate.x, d_skip.x, 0u);
+        store_record(u + 1, d_rate.y, d_skip.y, 0u);
+    }
+};
 
 template <bool kNorm, bool kReset>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -546,48 +613,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ BackwardShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == RWARPS * 32) {
-        mbar_init(&sh.started, 1);
-        sh.pipe.start(maps, A, stages);
-    }
-    Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
-    if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
+    if (threadIdx.x == RWARPS * 32) sh.pipe.start(maps, A, stages);
     __syncthreads();
-    unsigned int next = 0;
+    if (warp == RWARPS) {
+        control_warp(sh.pipe, maps, A, stages, sh.E, lane, BackwardWork<kReset>{A, sh, lane});
+        return;
+    }
     for (int it = 0;; ++it) {
         const int st = it % kStages;
+        sh.pipe.wait(&sh.pipe.full[st], it / kStages);
         const Tile t = sh.pipe.tile[st];
-        if (t.j < 0) break;
+        if (t.j < 0) {
+            sh.pipe.release(it, lane);
+            break;
+        }
         unsigned char *stage = stages + st * sh.pipe.kBytes;
         const int unit = A.units - 1 - t.j;
-        if (warp < RWARPS) {
-            const int n = min(A.L - unit * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
-            const unsigned int mask =
-                kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + unit * RT + warp * RSEG, n, lane)
-                       : 0u;
-            sh.pipe.wait(&sh.pipe.full[st], it / kStages);
-            backward_tile<kNorm, kReset>(sh, stage, warp, lane, n, A.Dskip != nullptr, mask, it);
-            fence_proxy_async_smem();
-            sh.pipe.arrive(&sh.pipe.done, lane);
-        } else {
-            if (lane == 0) next = next_tile(A, it + kStages);
-            backward_carry<kReset>(A, sh, rec, t, stage + 5 * kTileBytes, it);
-            sh.pipe.wait(&sh.pipe.done, it);
-            if (lane == 0) {
+        const int n = min(A.L - unit * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
+        const unsigned int mask =
+            kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + unit * RT + warp * RSEG, n, lane) : 0u;
+        backward_tile<kNorm, kReset>(sh, stage, st, warp, lane, n, A.Dskip != nullptr, mask, it);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (n > 0) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    tma_store_4d(&maps.out[k], stage + k * kTileBytes, t.c, 0, unit * RT, t.b);
-                bulk_commit();
+                    tma_store_4d(&maps.out[k], stage + k * kTileBytes + warp * RSEG * RCH * 2, t.c, 0,
+                                 unit * RT + warp * RSEG, t.b);
             }
-            backward_parts(A, sh, t, lane);  // the warps' next sums follow the next tile's carry
-            if (lane == 0) {
-                bulk_wait_read();
-                sh.pipe.request(maps, A, stages, st, tile_of(A, next));
-            }
-            __syncwarp();
+            bulk_commit();
         }
     }
-    if (threadIdx.x == RWARPS * 32) finish(A);
 }
 
 // dlog_rate and dDskip: the units' parts summed in double, in a fixed order: 32

@@ -19,8 +19,6 @@
 
 namespace hyena {
 
-constexpr int RWARPS = 8;            // warps per CTA, one time segment each
-constexpr int RSEG = RT / RWARPS;    // tokens per segment
 constexpr unsigned int kFullMask = 0xffffffffu;
 
 __device__ __forceinline__ float ex2_approx(float x)
