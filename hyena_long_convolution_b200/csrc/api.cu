@@ -500,8 +500,7 @@ hyena_status_t recurrence_args(RecArgs &a, const hyena_bf16_t *x1, const hyena_b
     a.tiles = static_cast<unsigned int>(recurrence_unit_chains(B, L, D));
     unsigned char *w = static_cast<unsigned char *>(workspace);
     a.hdr = reinterpret_cast<unsigned int *>(w);
-    a.rec_unit = reinterpret_cast<uint4 *>(w + kRecHeaderBytes);
-    a.rec_carry = a.rec_unit + static_cast<size_t>(a.tiles) * RCH;
+    a.records = reinterpret_cast<uint4 *>(w + kRecHeaderBytes);
     return HYENA_OK;
 }
 

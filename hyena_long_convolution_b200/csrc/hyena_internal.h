@@ -245,8 +245,7 @@ struct RecArgs {
     // workspace: header ([0] next ticket, [1] finished CTAs, [2] error bits,
     // [3] epoch), then 16-byte records, all with their tag in the third word
     unsigned int *hdr;
-    uint4 *rec_unit;         // [tiles][RCH]: (P, A), later the gradient's parts
-    uint4 *rec_carry;        // [tiles][RCH / 2]
+    uint4 *records;          // [tiles][3][RCH / 2]: P, A (later the gradient's parts), carry
 };
 constexpr size_t kRecHeaderBytes = 256;
 constexpr size_t kRecTileBytes = (RCH + RCH / 2) * 16;

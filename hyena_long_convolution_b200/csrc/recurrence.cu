@@ -76,24 +76,29 @@ __device__ __forceinline__ void store_record(uint4 *p, float a, float b, uint32_
                  : "memory");
 }
 
-// What a unit publishes: per channel (P, A), per channel pair the carry behind
-// it.  Unit j of a chain in processing order is tile j chains + chain.
+// What a unit publishes, a record a channel pair each: its P, its A, and the
+// carry behind it.  Unit j of a chain in processing order is tile j chains +
+// chain.
+enum { kRecP, kRecA, kRecCarry };
+
 struct Records {
-    uint4 *unit;   // [tiles][RCH]
-    uint4 *known;  // [tiles][RCH / 2]
+    uint4 *base;  // [tiles][3][RCH / 2]
     int chains, chain, lane;
     uint32_t epoch;
 
-    __device__ __forceinline__ size_t tile(int j) const { return static_cast<size_t>(j) * chains + chain; }
+    __device__ __forceinline__ uint4 *at(int j, int kind) const
+    {
+        return base + ((static_cast<size_t>(j) * chains + chain) * 3 + kind) * (RCH / 2);
+    }
+
     __device__ __forceinline__ void publish_unit(int j, float2 P, float2 A) const
     {
-        uint4 *u = unit + tile(j) * RCH + 2 * lane;
-        store_record(u, P.x, A.x, epoch);
-        store_record(u + 1, P.y, A.y, epoch);
+        store_record(at(j, kRecP) + lane, P.x, P.y, epoch);
+        store_record(at(j, kRecA) + lane, A.x, A.y, epoch);
     }
     __device__ __forceinline__ void publish_carry(int j, float2 C) const
     {
-        store_record(known + tile(j) * (RCH / 2) + lane, C.x, C.y, epoch);
+        store_record(at(j, kRecCarry) + lane, C.x, C.y, epoch);
     }
 
     // Looking for the carry into unit j > 0, by all lanes of a warp.  glance():
@@ -104,8 +109,7 @@ struct Records {
     __device__ __forceinline__ uint32_t glance(int j) const
     {
         const int back = lane & 15;
-        const size_t at = tile(max(j - 1 - back, 0));
-        const uint32_t tag = load_record(lane < 16 ? known + at * (RCH / 2) : unit + at * RCH).z;
+        const uint32_t tag = load_record(at(max(j - 1 - back, 0), lane < 16 ? kRecCarry : kRecA)).z;
         return back < j ? tag : epoch - 1u;
     }
     __device__ __forceinline__ bool look_back(int j, uint32_t seen, float2 &C) const
@@ -114,32 +118,30 @@ struct Records {
         const unsigned int units = ready >> 16;
         const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
         if (k < 0 || ((units + 1u) & ((1u << k) - 1u)) != 0u) return false;
-        const uint4 r = load_record(known + tile(j - 1 - k) * (RCH / 2) + lane);
+        const uint4 r = load_record(at(j - 1 - k, kRecCarry) + lane);
         bool found = r.z == epoch;
-        C = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+        C = pair_of(r);
         for (int d = k - 1; d >= 0; d -= kBatch) {
-            uint4 u0[kBatch], u1[kBatch];
+            uint4 P[kBatch], A[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const uint4 *u = unit + tile(j - 1 - max(d - i, 0)) * RCH + 2 * lane;
-                u0[i] = load_record(u);
-                u1[i] = load_record(u + 1);
+                P[i] = load_record(at(j - 1 - max(d - i, 0), kRecP) + lane);
+                A[i] = load_record(at(j - 1 - max(d - i, 0), kRecA) + lane);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 if (d >= i) {
-                    found = found && u0[i].z == epoch && u1[i].z == epoch;
-                    C = apply(u0[i], u1[i], C);
+                    found = found && P[i].z == epoch && A[i].z == epoch;
+                    C = carry<true>(pair_of(P[i]), C, pair_of(A[i]));
                 }
             }
         }
         return __all_sync(kFullMask, found);
     }
 
-    static __device__ __forceinline__ float2 apply(uint4 u0, uint4 u1, float2 C)
+    static __device__ __forceinline__ float2 pair_of(uint4 r)
     {
-        return carry<true>(make_float2(__uint_as_float(u0.x), __uint_as_float(u1.x)), C,
-                           make_float2(__uint_as_float(u0.y), __uint_as_float(u1.y)));
+        return make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
     }
 };
 
@@ -277,7 +279,7 @@ template <int N, bool kBack, class Work>
 __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const RecMaps &maps, const RecArgs &A,
                                              unsigned char *stages, float2 *carry_in, int lane, Work work)
 {
-    Records rec{A.rec_unit, A.rec_carry, A.chains, 0, lane, 0u};
+    Records rec{A.records, A.chains, 0, lane, 0u};
     if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
     Tile before{};
     for (int it = 0;; ++it) {
@@ -600,9 +602,9 @@ struct BackwardWork {
             d_rate = __fadd2_rn(d_rate, sh.rate[st][w][lane]);
             d_skip = __fadd2_rn(d_skip, sh.skip[st][w][lane]);
         }
-        uint4 *u = A.rec_unit + (static_cast<size_t>(t.j) * A.chains + t.chain) * RCH + 2 * lane;
-        store_record(u, d_rate.x, d_skip.x, 0u);
-        store_record(u + 1, d_rate.y, d_skip.y, 0u);
+        uint4 *u = A.records + (static_cast<size_t>(t.j) * A.chains + t.chain) * (3 * RCH / 2) + lane;
+        store_record(u + kRecP * (RCH / 2), d_rate.x, d_rate.y, 0u);
+        store_record(u + kRecA * (RCH / 2), d_skip.x, d_skip.y, 0u);
     }
 };
 
@@ -647,30 +649,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-// dlog_rate and dDskip: the units' parts summed in double, in a fixed order: 32
-// channels a CTA, 32 warps of which each takes every 32nd part.
+// dlog_rate and dDskip: the units' parts summed in double, in a fixed order: a
+// CTA takes one of the two for a chain's channels over all batch rows and
+// units, each of its 32 warps every 32nd part, a lane a channel pair.
 __global__ void __launch_bounds__(1024) unit_sum_kernel(const RecArgs A)
 {
-    __shared__ double sum[2][32][33];
+    __shared__ double sum[32][2 * 32 + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = blockIdx.x & 1, cb = blockIdx.x >> 1;
+    const int kind = blockIdx.x & 1, cb = blockIdx.x >> 1;
+    float *out = kind == kRecP ? A.dlog_rate : A.dDskip;
+    if (out == nullptr) return;
     const long long parts = static_cast<long long>(A.B) * A.units;
-    double r = 0., d = 0.;
+    double x = 0., y = 0.;
     for (long long k = warp; k < parts; k += 32) {
         const long long j = k / A.B, b = k - j * A.B;
-        const uint4 q = A.rec_unit[(static_cast<size_t>(j) * A.chains + b * A.nCB + cb) * RCH + half * 32 + lane];
-        r += __uint_as_float(q.x);
-        d += __uint_as_float(q.y);
+        const uint4 q = A.records[((static_cast<size_t>(j) * A.chains + b * A.nCB + cb) * 3 + kind) * (RCH / 2) + lane];
+        x += __uint_as_float(q.x);
+        y += __uint_as_float(q.y);
     }
-    sum[0][warp][lane] = r;
-    sum[1][warp][lane] = d;
+    sum[warp][2 * lane] = x;
+    sum[warp][2 * lane + 1] = y;
     __syncthreads();
-    const int c = cb * RCH + half * 32 + lane;
-    if (warp > 1 || c >= A.D) return;
-    float *out = warp == 0 ? A.dlog_rate : A.dDskip;
-    if (out == nullptr) return;
+    const int c = cb * RCH + threadIdx.x;
+    if (threadIdx.x >= RCH || c >= A.D) return;
     double v = 0.;
-    for (int w = 0; w < 32; ++w) v += sum[warp][w][lane];
+    for (int w = 0; w < 32; ++w) v += sum[w][threadIdx.x];
     out[c] = static_cast<float>(v);
 }
 
