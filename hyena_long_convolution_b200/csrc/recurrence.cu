@@ -102,19 +102,30 @@ struct Records {
     }
 
     // Looking for the carry into unit j > 0, by all lanes of a warp.  glance():
-    // one load of the first records of the last 16 units, lanes 0-15 known
-    // carries, lanes 16-31 units.  look_back(): with what it brought, true if the
-    // carry can be formed: once a known carry and every unit behind it are there,
-    // each lane loads its own channels' records, whose tags it checks as well.
-    __device__ __forceinline__ uint32_t glance(int j) const
+    // the carry behind the unit before, and by one load more the first records of
+    // the last 16 units, lanes 0-15 their carries, lanes 16-31 their sums.
+    // look_back(): with what that brought, true if the carry can be formed: where
+    // the nearest is not there yet, from the nearest that is, once every unit
+    // behind it is there; each lane then loads its own channels' records.  The tag
+    // of every record that is used is checked.
+    struct Glance {
+        uint4 nearest;
+        uint32_t first;
+    };
+    __device__ __forceinline__ Glance glance(int j) const
     {
+        Glance g;
+        g.nearest = load_record(at(j - 1, kRecCarry) + lane);
         const int back = lane & 15;
         const uint32_t tag = load_record(at(max(j - 1 - back, 0), lane < 16 ? kRecCarry : kRecA)).z;
-        return back < j ? tag : epoch - 1u;
+        g.first = back < j ? tag : epoch - 1u;
+        return g;
     }
-    __device__ __forceinline__ bool look_back(int j, uint32_t seen, float2 &C) const
+    __device__ __forceinline__ bool look_back(int j, const Glance &g, float2 &C) const
     {
-        const unsigned int ready = __ballot_sync(kFullMask, seen == epoch);
+        C = pair_of(g.nearest);
+        if (__all_sync(kFullMask, g.nearest.z == epoch)) return true;
+        const unsigned int ready = __ballot_sync(kFullMask, g.first == epoch);
         const unsigned int units = ready >> 16;
         const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
         if (k < 0 || ((units + 1u) & ((1u << k) - 1u)) != 0u) return false;
@@ -307,7 +318,8 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
         unsigned long long t0 = 0;
         for (;;) {
             // the glance's load is under way while the CTA's own barriers are looked at
-            const uint32_t seen = found ? 0u : rec.glance(t.j);
+            Records::Glance seen{};
+            if (!found) seen = rec.glance(t.j);
             if (!asked && __all_sync(kFullMask, mbar_test_wait(&pipe.freed, (it - 1) & 1))) ask();
             if (!summed) {
                 if (found) pipe.wait(&pipe.sums, it);
