@@ -676,14 +676,29 @@ def modal_decode_complex_packed(xp, group, poles, residues, Dskip, state, y=None
 def _device(x, *others):
     """The device index that x and the given tensors (None: absent) share,
     which must be the current one: the call launches there."""
-    torch = _torch()
     dev = x.get_device()
+    if dev < 0 or dev != _torch()._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current CUDA device")
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one CUDA device")
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
     return dev
+
+
+def _like(x, shape, name):
+    """Row stride of a bf16 [B, L, D] tensor of the given shape, as _bld (the
+    device is checked by _device): few queries, as this runs ten times a call."""
+    if x.dtype is not _torch().bfloat16 or x.shape != shape:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(shape)}")
+    st = x.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name} must be channel-contiguous")
+    B, L, D = shape
+    if L > 1:
+        if B > 1 and st[0] != L * st[1]:
+            raise ValueError(f"{name}: batch stride must equal L * row stride")
+        return st[1]
+    return st[0] if B > 1 and L == 1 else D
 
 
 def _reset(t, B, L):
@@ -729,11 +744,13 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     Returns y ([B, L, D] bf16, allocated if not given).
     """
     torch = _torch()
-    s1, s2, s3, sg = _bld(x1, "x1"), _bld(x2, "x2"), _bld(x3, "x3"), _bld(gate, "gate")
-    _same_ld(s1, s2, s3)
-    B, L, D, ld = s1
-    if s2[:3] != (B, L, D) or s3[:3] != (B, L, D) or sg[:3] != (B, L, D):
-        raise ValueError("x1, x2, x3, gate shapes differ")
+    shape = x1.shape
+    if len(shape) != 3:
+        raise ValueError("x1 must be a 3-D bf16 CUDA tensor [B, L, D]")
+    B, L, D = shape
+    ld, ld_g = _like(x1, shape, "x1"), _like(gate, shape, "gate")
+    if _like(x2, shape, "x2") != ld or _like(x3, shape, "x3") != ld:
+        raise ValueError("x1, x2, x3 must share one row stride")
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _reset(reset, B, L)
@@ -741,14 +758,13 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     _f32(state_out, (B, D), "state_out")
     _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states")
     if y is None:
-        y = torch.empty((B, L, D), dtype=torch.bfloat16, device=x1.device)
-    yB, yL, yD, ld_y = _bld(y, "y")
-    if (yB, yL, yD) != (B, L, D):
-        raise ValueError("y shape differs from x")
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x1.device)
+    ld_y = _like(y, shape, "y")
+    _device(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states,
+            None if workspace is None else workspace.buf)
     if workspace is None:
         workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
-    _device(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states, workspace.buf)
-    rc = lib().hyena_gated_recurrence(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), sg[3], _ptr(log_rate),
+    rc = lib().hyena_gated_recurrence(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), ld_g, _ptr(log_rate),
                                       _ptr(Dskip), _ptr(reset), int(bool(normalize)), _ptr(y), ld_y,
                                       _ptr(state_in), _ptr(state_out), _ptr(unit_states), B, L, D,
                                       _ptr(workspace.buf), workspace.nbytes, _stream(stream))
@@ -775,41 +791,45 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
     forward call's inputs and the unit_states it filled.  dx1, dx2, dx3
     (sharing a row stride), dgate and dstate_in are allocated if not given."""
     torch = _torch()
-    s1, s2, s3, sg, sd = _bld(x1, "x1"), _bld(x2, "x2"), _bld(x3, "x3"), _bld(gate, "gate"), _bld(dy, "dy")
-    _same_ld(s1, s2, s3)
-    B, L, D, ld = s1
-    if any(s[:3] != (B, L, D) for s in (s2, s3, sg, sd)):
-        raise ValueError("dy, x1, x2, x3, gate shapes differ")
+    shape = x1.shape
+    if len(shape) != 3:
+        raise ValueError("x1 must be a 3-D bf16 CUDA tensor [B, L, D]")
+    B, L, D = shape
+    ld, ld_g, ld_dy = _like(x1, shape, "x1"), _like(gate, shape, "gate"), _like(dy, shape, "dy")
+    if _like(x2, shape, "x2") != ld or _like(x3, shape, "x3") != ld:
+        raise ValueError("x1, x2, x3 must share one row stride")
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _reset(reset, B, L)
     _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states", False)
     _f32(dstate_out, (B, D), "dstate_out")
     _f32(dstate_in, (B, D), "dstate_in")
-    given = (dx1, dx2, dx3)
-    if any(g is not None for g in given) and any(g is None for g in given):
+    dev, bf16 = x1.device, torch.bfloat16
+    if dx1 is None and dx2 is None and dx3 is None:
+        dx1, dx2, dx3 = (torch.empty(shape, dtype=bf16, device=dev) for _ in range(3))
+        ld_dx = D
+    elif dx1 is None or dx2 is None or dx3 is None:
         raise ValueError("give all of dx1, dx2, dx3 or none")
-    if dx1 is None:
-        dx1, dx2, dx3 = (torch.empty((B, L, D), dtype=torch.bfloat16, device=x1.device) for _ in range(3))
+    else:
+        ld_dx = _like(dx1, shape, "dx1")
+        if _like(dx2, shape, "dx2") != ld_dx or _like(dx3, shape, "dx3") != ld_dx:
+            raise ValueError("dx1, dx2, dx3 must share one row stride")
     if dgate is None:
-        dgate = torch.empty((B, L, D), dtype=torch.bfloat16, device=x1.device)
-    outs = [_bld(t, n) for t, n in ((dx1, "dx1"), (dx2, "dx2"), (dx3, "dx3"), (dgate, "dgate"))]
-    if any(s[:3] != (B, L, D) for s in outs):
-        raise ValueError("dx1, dx2, dx3, dgate shapes differ from x")
-    if len({s[3] for s in outs[:3]}) != 1:
-        raise ValueError("dx1, dx2, dx3 must share one row stride")
+        dgate, ld_dg = torch.empty(shape, dtype=bf16, device=dev), D
+    else:
+        ld_dg = _like(dgate, shape, "dgate")
     if dstate_in is None:
-        dstate_in = torch.empty((B, D), dtype=torch.float32, device=x1.device)
-    dlog_rate = torch.empty(D, dtype=torch.float32, device=x1.device)
-    dDskip = None if Dskip is None else torch.empty(D, dtype=torch.float32, device=x1.device)
-    if workspace is None:
-        workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
+        dstate_in = torch.empty((B, D), dtype=torch.float32, device=dev)
+    dlog_rate = torch.empty(D, dtype=torch.float32, device=dev)
+    dDskip = None if Dskip is None else torch.empty(D, dtype=torch.float32, device=dev)
     _device(x1, x2, x3, gate, dy, log_rate, Dskip, reset, unit_states, dstate_out, dx1, dx2, dx3, dgate, dstate_in,
-            workspace.buf)
+            None if workspace is None else workspace.buf)
+    if workspace is None:
+        workspace = RecurrenceWorkspace(B, L, D, device=dev, stream=stream)
     rc = lib().hyena_gated_recurrence_backward(
-        _ptr(dy), sd[3], _ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), sg[3], _ptr(log_rate), _ptr(Dskip),
+        _ptr(dy), ld_dy, _ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), ld_g, _ptr(log_rate), _ptr(Dskip),
         _ptr(reset), int(bool(normalize)), _ptr(unit_states), _ptr(dstate_out), _ptr(dx1), _ptr(dx2), _ptr(dx3),
-        outs[0][3], _ptr(dgate), outs[3][3], _ptr(dlog_rate), _ptr(dDskip), _ptr(dstate_in), B, L, D,
+        ld_dx, _ptr(dgate), ld_dg, _ptr(dlog_rate), _ptr(dDskip), _ptr(dstate_in), B, L, D,
         _ptr(workspace.buf), workspace.nbytes, _stream(stream))
     check("hyena_gated_recurrence_backward", rc)
     return RecurrenceGrads(dx1, dx2, dx3, dgate, dlog_rate, dDskip, dstate_in)
@@ -820,22 +840,22 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     ([B, D] fp32, in place) and returns y ([B, D] or [B, 1, D] like x1).
     Equals ``gated_recurrence`` on a one-token sequence with state_in =
     state_out = state, bit for bit."""
-    torch = _torch()
-    (B, D, ld), b2, b3, bg = _bd(x1, "x1"), _bd(x2, "x2"), _bd(x3, "x3"), _bd(gate, "gate")
-    if b2 != (B, D, ld) or b3 != (B, D, ld):
+    (B, D, ld), (gB, gD, ld_g) = _bd(x1, "x1"), _bd(gate, "gate")
+    if _bd(x2, "x2") != (B, D, ld) or _bd(x3, "x3") != (B, D, ld):
         raise ValueError("x1, x2, x3 must share shape and row stride")
-    if bg[:2] != (B, D):
+    if gB != B or gD != D:
         raise ValueError("gate shape differs from x")
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _f32(state, (B, D), "state", False)
     if y is None:
-        y = torch.empty_like(x1, memory_format=torch.contiguous_format)
-    yB, yD, ld_y = _bd(y, "y")
-    if (yB, yD) != (B, D):
-        raise ValueError("y shape differs from x")
+        y, ld_y = x1.new_empty(x1.shape), D
+    else:
+        yB, yD, ld_y = _bd(y, "y")
+        if (yB, yD) != (B, D):
+            raise ValueError("y shape differs from x")
     _device(x1, x2, x3, gate, log_rate, Dskip, state, y)
-    rc = lib().hyena_gated_recurrence_decode(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), bg[2], _ptr(log_rate),
+    rc = lib().hyena_gated_recurrence_decode(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), ld_g, _ptr(log_rate),
                                              _ptr(Dskip), int(bool(normalize)), _ptr(y), ld_y, _ptr(state), B, D,
                                              _stream(stream))
     check("hyena_gated_recurrence_decode", rc)
@@ -845,15 +865,16 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
 # -------------------------------------------------------------------- RMS norm
 
 def _rows(x, name, dtypes):
-    """[M, D] or [B, L, D] CUDA tensor with unit channel stride and evenly
-    spaced rows -> (rows, D, ld)."""
+    """[M, D] or [B, L, D] tensor with unit channel stride and evenly spaced
+    rows -> (rows, D, ld); the device is checked by _device."""
     sh, st = x.shape, x.stride()
-    if x.dtype not in dtypes or not x.is_cuda or len(sh) not in (2, 3):
+    if x.dtype not in dtypes or len(sh) not in (2, 3):
         raise ValueError(f"{name} must be a CUDA tensor [rows, D] or [B, L, D] of type {' or '.join(map(str, dtypes))}")
     if st[-1] != 1:
         raise ValueError(f"{name} must be channel-contiguous")
     if len(sh) == 2:
-        return sh[0], sh[1], st[0] if sh[0] > 1 else sh[1]
+        M, D = sh
+        return M, D, st[0] if M > 1 else D
     B, L, D = sh
     ld = st[1] if L > 1 else (st[0] if B > 1 else D)
     if B > 1 and L > 1 and st[0] != L * ld:

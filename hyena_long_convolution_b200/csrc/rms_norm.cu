@@ -225,37 +225,92 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
     }
 }
 
+// One row's inputs of the gradient as a thread holds them between their loads
+// and their use: kH 16-byte words of h, dy, and kH of dresidual_out.
+template <int VPT, int R>
+struct GradRow {
+    static constexpr int kH = R == 2 ? 2 : 1;
+    uint4 h[VPT][kH], dy[VPT], dres[VPT][kH];
+
+    __device__ __forceinline__ void load(const NormArgs &A, long long row)
+    {
+        constexpr int kSize = R == 2 ? 4 : 2;
+        if (row >= A.rows) return;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x));
+            if (c >= A.D) continue;
+            const uint4 *ph = reinterpret_cast<const uint4 *>(static_cast<const char *>(A.h) +
+                                                              (row * A.ld_h + c) * kSize);
+            const uint4 *pr = reinterpret_cast<const uint4 *>(static_cast<const char *>(A.dres_out) +
+                                                              (row * A.ld_r + c) * kSize);
+            dy[k] = *reinterpret_cast<const uint4 *>(A.dy + row * A.ld_y + c);
+#pragma unroll
+            for (int i = 0; i < kH; ++i) {
+                h[k][i] = ph[i];
+                dres[k][i] = A.dres_out ? pr[i] : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+    template <int K>
+    static __device__ __forceinline__ void unpack(float (&v)[8], const uint4 (&q)[K])
+    {
+        if constexpr (K == 1) {
+            const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = bf16x2_to_float2(w[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        } else {
+            const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        }
+    }
+};
+
 // Gradient.  A CTA walks the rows blockIdx.x, blockIdx.x + gridDim.x, ... and
-// keeps its channels' part of dweight in registers; the parts go to `partial`
-// [gridDim.x][D].
+// keeps its channels' weight and part of dweight in registers; the parts go to
+// `partial` [gridDim.x][D].  HBM-bound (8 bytes an element with a bf16 residual):
+// the next row's loads are under way while this one is reduced and written.
 template <int VPT, int R>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const NormArgs A)
 {
     __shared__ float part[2][32];
     const int T = blockDim.x;
-    float dw[VPT][8];
+    float dw[VPT][8], w[VPT][8];
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
+    for (int k = 0; k < VPT; ++k) {
+        const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
+        if (c < A.D) load_weight(w[k], A.weight, A.weight_bf16, c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
+    }
+    GradRow<VPT, R> now, next;
+    next.load(A, blockIdx.x);
+    float rstd_next = A.rstd_in[blockIdx.x];
     int turn = 0;
     for (long long row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
+        now = next;
+        const float rstd = rstd_next;
+        next.load(A, row + gridDim.x);
+        if (row + gridDim.x < A.rows) rstd_next = A.rstd_in[row + gridDim.x];
         float n[VPT][8], t[VPT][8];
-        const float rstd = A.rstd_in[row];
         float dot = 0.f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < A.D) {
-                float w[8];
-                load8<R == 2 ? 2 : 1>(n[k], A.h, row * A.ld_h + c);
-                load_bf16x8(t[k], A.dy + row * A.ld_y + c);
-                load_weight(w, A.weight, A.weight_bf16, c);
+                now.unpack(n[k], now.h[k]);
+                const uint4 dy[1] = {now.dy[k]};
+                now.unpack(t[k], dy);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     n[k][i] *= rstd;
                     dw[k][i] = __fmaf_rn(t[k][i], n[k][i], dw[k][i]);
-                    t[k][i] *= w[i];
+                    t[k][i] *= w[k][i];
                     dot = __fmaf_rn(t[k][i], n[k][i], dot);
                 }
             }
@@ -266,12 +321,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < A.D) {
                 float r[8];
-                if (A.dres_out) {
-                    load8<R == 2 ? 2 : 1>(r, A.dres_out, row * A.ld_r + c);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) r[i] = 0.f;
-                }
+                now.unpack(r, now.dres[k]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) r[i] = __fmaf_rn(rstd, t[k][i] - n[k][i] * mean, r[i]);
                 if (A.dx) store_bf16x8(A.dx + row * A.ld_x + c, r);
@@ -288,13 +338,20 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
     }
 }
 
-// dweight: the CTAs' parts summed in double, in order.
-__global__ void __launch_bounds__(128) norm_weight_sum_kernel(const float *partial, int parts, int D, float *dweight)
+// dweight: the CTAs' parts summed in double, in a fixed order: a CTA takes 32
+// channels, each of its warps every 32nd part.
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float *partial, int parts, int D, float *dweight)
 {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= D) return;
+    __shared__ double sum[32][33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * 32 + lane;
     double s = 0.;
-    for (int p = 0; p < parts; ++p) s += partial[static_cast<long long>(p) * D + c];
+    if (c < D)
+        for (int p = warp; p < parts; p += 32) s += partial[static_cast<long long>(p) * D + c];
+    sum[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || c >= D) return;
+    for (int w = 1; w < 32; ++w) s += sum[w][lane];
     dweight[c] = static_cast<float>(s);
 }
 
@@ -356,11 +413,21 @@ int launch_rms_norm(const NormArgs &a, cudaStream_t st)
     return 1;
 }
 
-int norm_parts(long long rows) { return static_cast<int>(rows < 592 ? rows : 592); }
+// CTAs of the gradient: two a SM (as many as its registers allow at D = 4096),
+// and no more than rows.
+int norm_parts(long long rows) { return static_cast<int>(rows < 296 ? rows : 296); }
+
+// More threads than the forward takes: a thread of the gradient holds two rows.
+NormShape gradient_shape(int D)
+{
+    const int v = D / 8;
+    const int vpt = v <= kNormThreads ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
+    return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
+}
 
 int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st)
 {
-    const NormShape s = norm_shape(a.D);
+    const NormShape s = gradient_shape(a.D);
     const int parts = norm_parts(a.rows);
     if (s.vpt == 1)
         backward_r<1>(a, parts, s.threads, st);
@@ -368,7 +435,7 @@ int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st)
         backward_r<2>(a, parts, s.threads, st);
     else
         backward_r<4>(a, parts, s.threads, st);
-    norm_weight_sum_kernel<<<(a.D + 127) / 128, 128, 0, st>>>(a.partial, parts, a.D, a.dweight);
+    norm_weight_sum_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, parts, a.D, a.dweight);
     HYENA_TRY(cudaGetLastError(), "rms norm gradient launch");
     return 2;
 }
