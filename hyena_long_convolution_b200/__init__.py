@@ -115,12 +115,12 @@ def _same_ld(*xs):
 
 
 def _f32(t, shape, name, allow_none=True):
-    torch = _torch()
     if t is None:
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    torch = _torch()
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)}")
     return t
 
@@ -685,20 +685,27 @@ def _device(x, *others):
     return dev
 
 
-def _like(x, shape, name):
+def _like(x, shape, st, ld, name):
     """Row stride of a bf16 [B, L, D] tensor of the given shape, as _bld (the
-    device is checked by _device): few queries, as this runs ten times a call."""
+    device is checked by _device); the usual case, the stride of a tensor whose
+    row stride ld is known, is settled by comparing."""
     if x.dtype is not _torch().bfloat16 or x.shape != shape:
         raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(shape)}")
-    st = x.stride()
-    if st[2] != 1:
+    xst = x.stride()
+    if xst == st:
+        return ld
+    if xst[2] != 1:
         raise ValueError(f"{name} must be channel-contiguous")
     B, L, D = shape
     if L > 1:
-        if B > 1 and st[0] != L * st[1]:
+        if B > 1 and xst[0] != L * xst[1]:
             raise ValueError(f"{name}: batch stride must equal L * row stride")
-        return st[1]
-    return st[0] if B > 1 and L == 1 else D
+        return xst[1]
+    return xst[0] if B > 1 and L == 1 else D
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 def _reset(t, B, L):
@@ -744,13 +751,14 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     Returns y ([B, L, D] bf16, allocated if not given).
     """
     torch = _torch()
-    shape = x1.shape
+    shape, st = x1.shape, x1.stride()
     if len(shape) != 3:
         raise ValueError("x1 must be a 3-D bf16 CUDA tensor [B, L, D]")
     B, L, D = shape
-    ld, ld_g = _like(x1, shape, "x1"), _like(gate, shape, "gate")
-    if _like(x2, shape, "x2") != ld or _like(x3, shape, "x3") != ld:
+    ld = _like(x1, shape, None, 0, "x1")
+    if _like(x2, shape, st, ld, "x2") != ld or _like(x3, shape, st, ld, "x3") != ld:
         raise ValueError("x1, x2, x3 must share one row stride")
+    ld_g = _like(gate, shape, st, ld, "gate")
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _reset(reset, B, L)
@@ -758,16 +766,17 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     _f32(state_out, (B, D), "state_out")
     _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states")
     if y is None:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=x1.device)
-    ld_y = _like(y, shape, "y")
+        y, ld_y = torch.empty_like(x1, memory_format=torch.contiguous_format), D
+    else:
+        ld_y = _like(y, shape, st, ld, "y")
     _device(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states,
             None if workspace is None else workspace.buf)
     if workspace is None:
         workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
-    rc = lib().hyena_gated_recurrence(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), ld_g, _ptr(log_rate),
-                                      _ptr(Dskip), _ptr(reset), int(bool(normalize)), _ptr(y), ld_y,
-                                      _ptr(state_in), _ptr(state_out), _ptr(unit_states), B, L, D,
-                                      _ptr(workspace.buf), workspace.nbytes, _stream(stream))
+    rc = lib().hyena_gated_recurrence(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
+                                      log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0,
+                                      y.data_ptr(), ld_y, _opt(state_in), _opt(state_out), _opt(unit_states),
+                                      B, L, D, workspace.buf.data_ptr(), workspace.nbytes, _stream(stream))
     check("hyena_gated_recurrence", rc)
     return y
 
@@ -791,46 +800,48 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
     forward call's inputs and the unit_states it filled.  dx1, dx2, dx3
     (sharing a row stride), dgate and dstate_in are allocated if not given."""
     torch = _torch()
-    shape = x1.shape
+    shape, st = x1.shape, x1.stride()
     if len(shape) != 3:
         raise ValueError("x1 must be a 3-D bf16 CUDA tensor [B, L, D]")
     B, L, D = shape
-    ld, ld_g, ld_dy = _like(x1, shape, "x1"), _like(gate, shape, "gate"), _like(dy, shape, "dy")
-    if _like(x2, shape, "x2") != ld or _like(x3, shape, "x3") != ld:
+    ld = _like(x1, shape, None, 0, "x1")
+    if _like(x2, shape, st, ld, "x2") != ld or _like(x3, shape, st, ld, "x3") != ld:
         raise ValueError("x1, x2, x3 must share one row stride")
+    ld_g, ld_dy = _like(gate, shape, st, ld, "gate"), _like(dy, shape, st, ld, "dy")
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _reset(reset, B, L)
     _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states", False)
     _f32(dstate_out, (B, D), "dstate_out")
     _f32(dstate_in, (B, D), "dstate_in")
-    dev, bf16 = x1.device, torch.bfloat16
+    dense = torch.contiguous_format
     if dx1 is None and dx2 is None and dx3 is None:
-        dx1, dx2, dx3 = (torch.empty(shape, dtype=bf16, device=dev) for _ in range(3))
+        dx1, dx2, dx3 = (torch.empty_like(x1, memory_format=dense) for _ in range(3))
         ld_dx = D
     elif dx1 is None or dx2 is None or dx3 is None:
         raise ValueError("give all of dx1, dx2, dx3 or none")
     else:
-        ld_dx = _like(dx1, shape, "dx1")
-        if _like(dx2, shape, "dx2") != ld_dx or _like(dx3, shape, "dx3") != ld_dx:
+        ld_dx = _like(dx1, shape, st, ld, "dx1")
+        if _like(dx2, shape, st, ld, "dx2") != ld_dx or _like(dx3, shape, st, ld, "dx3") != ld_dx:
             raise ValueError("dx1, dx2, dx3 must share one row stride")
     if dgate is None:
-        dgate, ld_dg = torch.empty(shape, dtype=bf16, device=dev), D
+        dgate, ld_dg = torch.empty_like(x1, memory_format=dense), D
     else:
-        ld_dg = _like(dgate, shape, "dgate")
+        ld_dg = _like(dgate, shape, st, ld, "dgate")
     if dstate_in is None:
-        dstate_in = torch.empty((B, D), dtype=torch.float32, device=dev)
-    dlog_rate = torch.empty(D, dtype=torch.float32, device=dev)
-    dDskip = None if Dskip is None else torch.empty(D, dtype=torch.float32, device=dev)
+        dstate_in = unit_states.new_empty((B, D))
+    dlog_rate = torch.empty_like(log_rate)
+    dDskip = None if Dskip is None else torch.empty_like(Dskip)
     _device(x1, x2, x3, gate, dy, log_rate, Dskip, reset, unit_states, dstate_out, dx1, dx2, dx3, dgate, dstate_in,
             None if workspace is None else workspace.buf)
     if workspace is None:
-        workspace = RecurrenceWorkspace(B, L, D, device=dev, stream=stream)
+        workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
     rc = lib().hyena_gated_recurrence_backward(
-        _ptr(dy), ld_dy, _ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), ld_g, _ptr(log_rate), _ptr(Dskip),
-        _ptr(reset), int(bool(normalize)), _ptr(unit_states), _ptr(dstate_out), _ptr(dx1), _ptr(dx2), _ptr(dx3),
-        ld_dx, _ptr(dgate), ld_dg, _ptr(dlog_rate), _ptr(dDskip), _ptr(dstate_in), B, L, D,
-        _ptr(workspace.buf), workspace.nbytes, _stream(stream))
+        dy.data_ptr(), ld_dy, x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
+        log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0, unit_states.data_ptr(),
+        _opt(dstate_out), dx1.data_ptr(), dx2.data_ptr(), dx3.data_ptr(), ld_dx, dgate.data_ptr(), ld_dg,
+        dlog_rate.data_ptr(), _opt(dDskip), dstate_in.data_ptr(), B, L, D, workspace.buf.data_ptr(),
+        workspace.nbytes, _stream(stream))
     check("hyena_gated_recurrence_backward", rc)
     return RecurrenceGrads(dx1, dx2, dx3, dgate, dlog_rate, dDskip, dstate_in)
 
@@ -840,24 +851,27 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     ([B, D] fp32, in place) and returns y ([B, D] or [B, 1, D] like x1).
     Equals ``gated_recurrence`` on a one-token sequence with state_in =
     state_out = state, bit for bit."""
-    (B, D, ld), (gB, gD, ld_g) = _bd(x1, "x1"), _bd(gate, "gate")
-    if _bd(x2, "x2") != (B, D, ld) or _bd(x3, "x3") != (B, D, ld):
-        raise ValueError("x1, x2, x3 must share shape and row stride")
-    if gB != B or gD != D:
-        raise ValueError("gate shape differs from x")
+    B, D, ld = _bd(x1, "x1")
+    shape, st, bf16 = x1.shape, x1.stride(), x1.dtype
+    for t, name in ((x2, "x2"), (x3, "x3"), (gate, "gate")):
+        if t.dtype is not bf16 or t.shape != shape:
+            raise ValueError(f"{name} must be a bf16 CUDA tensor of x1's shape")
+    if (x2.stride() != st or x3.stride() != st) and (_bd(x2, "x2")[2] != ld or _bd(x3, "x3")[2] != ld):
+        raise ValueError("x1, x2, x3 must share one row stride")
+    ld_g = ld if gate.stride() == st else _bd(gate, "gate")[2]
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _f32(state, (B, D), "state", False)
     if y is None:
-        y, ld_y = x1.new_empty(x1.shape), D
+        y, ld_y = x1.new_empty(shape), D
     else:
         yB, yD, ld_y = _bd(y, "y")
         if (yB, yD) != (B, D):
             raise ValueError("y shape differs from x")
     _device(x1, x2, x3, gate, log_rate, Dskip, state, y)
-    rc = lib().hyena_gated_recurrence_decode(_ptr(x1), _ptr(x2), _ptr(x3), ld, _ptr(gate), ld_g, _ptr(log_rate),
-                                             _ptr(Dskip), int(bool(normalize)), _ptr(y), ld_y, _ptr(state), B, D,
-                                             _stream(stream))
+    rc = lib().hyena_gated_recurrence_decode(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
+                                             log_rate.data_ptr(), _opt(Dskip), 1 if normalize else 0, y.data_ptr(),
+                                             ld_y, state.data_ptr(), B, D, _stream(stream))
     check("hyena_gated_recurrence_decode", rc)
     return y
 
@@ -882,30 +896,40 @@ def _rows(x, name, dtypes):
     return B * L, D, ld
 
 
+def _weight(t, D):
+    """hyena_dtype_t of a norm weight."""
+    torch = _torch()
+    if (t.dtype is not torch.float32 and t.dtype is not torch.bfloat16) or t.shape != (D,) or not t.is_contiguous():
+        raise ValueError(f"weight must be a contiguous fp32 or bf16 tensor of shape {(D,)}")
+    return _dtype_code(t)
+
+
 def _dtype_code(t):
     """hyena_dtype_t of a tensor (bf16 or fp32)."""
-    return 1 if t.dtype == _torch().bfloat16 else 2
+    return 1 if t.dtype is _torch().bfloat16 else 2
 
 
 def _norm_inputs(x, weight, residual, residual_out, rstd):
-    """Checks what both forms of the norm take -> (rows, D, ld_x, ld_r, residual type)."""
+    """Checks what both forms of the norm take -> (rows, D, ld_x, weight type,
+    ld_r, residual type)."""
     torch = _torch()
     M, D, ld = _rows(x, "x", (torch.bfloat16,))
-    if weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != (D,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous fp32 or bf16 tensor of shape {(D,)}")
+    wt = _weight(weight, D)
     _f32(rstd, (M,), "rstd")
     ld_r, kind = 0, 1
     if residual is not None:
         rM, rD, ld_r = _rows(residual, "residual", (torch.bfloat16, torch.float32))
-        if (rM, rD) != (M, D):
+        if rM != M or rD != D:
             raise ValueError("residual shape differs from x")
         kind = _dtype_code(residual)
-    if residual_out is not None:
-        if residual is None:
-            raise ValueError("residual_out needs a residual")
-        if _rows(residual_out, "residual_out", (residual.dtype,)) != (M, D, ld_r):
-            raise ValueError("residual_out must have the residual's shape and row stride")
-    return M, D, ld, ld_r, kind
+        if residual_out is not None and (
+                residual_out.dtype is not residual.dtype or residual_out.shape != residual.shape
+                or (residual_out.stride() != residual.stride()
+                    and _rows(residual_out, "residual_out", (residual.dtype,))[2] != ld_r)):
+            raise ValueError("residual_out must have the residual's type, shape and row stride")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    return M, D, ld, wt, ld_r, kind
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, rstd=None, stream=None):
@@ -915,15 +939,16 @@ def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, rstd
     the residual itself); rstd: [rows] fp32 or None, filled for the backward
     call.  Returns y (bf16, allocated if not given)."""
     torch = _torch()
-    M, D, ld, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
+    M, D, ld, wt, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    yM, yD, ld_y = _rows(y, "y", (torch.bfloat16,))
-    if (yM, yD) != (M, D):
-        raise ValueError("y shape differs from x")
+        y, ld_y = torch.empty_like(x, memory_format=torch.contiguous_format), D
+    else:
+        yM, yD, ld_y = _rows(y, "y", (torch.bfloat16,))
+        if yM != M or yD != D:
+            raise ValueError("y shape differs from x")
     _device(x, weight, residual, residual_out, y, rstd)
-    rc = lib().hyena_rms_norm(_ptr(x), ld, _ptr(residual), _ptr(residual_out), ld_r, kind, _ptr(weight),
-                              _dtype_code(weight), eps, _ptr(y), ld_y, _ptr(rstd), M, D, _stream(stream))
+    rc = lib().hyena_rms_norm(x.data_ptr(), ld, _opt(residual), _opt(residual_out), ld_r, kind, weight.data_ptr(), wt,
+                              eps, y.data_ptr(), ld_y, _opt(rstd), M, D, _stream(stream))
     check("hyena_rms_norm", rc)
     return y
 
@@ -934,22 +959,24 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
     q float8_e4m3fn of x's shape and one fp32 scale per row (group = 0, shape
     [rows, 1]) or per 128 channels (group = 128, [rows, ceil(D / 128)])."""
     torch = _torch()
-    M, D, ld, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
+    M, D, ld, wt, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
     if group not in (0, 128):
         raise ValueError("group must be 0 (one scale per row) or 128")
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
-    if (qM, qD) != (M, D):
-        raise ValueError("q shape differs from x")
+        q, ld_q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), D
+    else:
+        qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
+        if qM != M or qD != D:
+            raise ValueError("q shape differs from x")
     want = (M, 1 if group == 0 else -(-D // 128))
     if scales is None:
-        scales = torch.empty(want, dtype=torch.float32, device=x.device)
-    _f32(scales, want, "scales")
+        scales = x.new_empty(want, dtype=torch.float32)
+    else:
+        _f32(scales, want, "scales")
     _device(x, weight, residual, residual_out, q, scales, rstd)
-    rc = lib().hyena_rms_norm_fp8(_ptr(x), ld, _ptr(residual), _ptr(residual_out), ld_r, kind, _ptr(weight),
-                                  _dtype_code(weight), eps, _ptr(q), ld_q, _ptr(scales), group, _ptr(rstd), M, D,
-                                  _stream(stream))
+    rc = lib().hyena_rms_norm_fp8(x.data_ptr(), ld, _opt(residual), _opt(residual_out), ld_r, kind,
+                                  weight.data_ptr(), wt, eps, q.data_ptr(), ld_q, scales.data_ptr(), group,
+                                  _opt(rstd), M, D, _stream(stream))
     check("hyena_rms_norm_fp8", rc)
     return q, scales
 
@@ -973,35 +1000,38 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
     torch = _torch()
     M, D, ld_dy = _rows(dy, "dy", (torch.bfloat16,))
     hM, hD, ld_h = _rows(h, "h", (torch.bfloat16, torch.float32))
-    if (hM, hD) != (M, D):
+    if hM != M or hD != D:
         raise ValueError("h shape differs from dy")
-    if weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != (D,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous fp32 or bf16 tensor of shape {(D,)}")
+    wt, ht = _weight(weight, D), _dtype_code(h)
     _f32(rstd, (M,), "rstd", False)
-    f32 = h.dtype == torch.float32
     if dx is None:
-        dx = torch.empty(dy.shape, dtype=torch.bfloat16, device=dy.device)
-    xM, xD, ld_dx = _rows(dx, "dx", (torch.bfloat16,))
-    if (xM, xD) != (M, D):
-        raise ValueError("dx shape differs from dy")
-    if dresidual is not None and not f32:
-        raise ValueError("the gradient of a bf16 residual is dx: give no dresidual")
-    if dresidual is None and f32:
-        dresidual = torch.empty(h.shape, dtype=torch.float32, device=dy.device)
-    lds = [0, 0]
-    for i, (t, n) in enumerate(((dresidual_out, "dresidual_out"), (dresidual, "dresidual"))):
-        if t is not None:
-            rM, rD, lds[i] = _rows(t, n, (h.dtype,))
-            if (rM, rD) != (M, D):
-                raise ValueError(f"{n} shape differs from dy")
-    dweight = torch.empty(D, dtype=torch.float32, device=dy.device)
-    need = int(lib().hyena_rms_norm_backward_workspace_size(M, D))
+        dx, ld_dx = torch.empty_like(dy, memory_format=torch.contiguous_format), D
+    else:
+        xM, xD, ld_dx = _rows(dx, "dx", (torch.bfloat16,))
+        if xM != M or xD != D:
+            raise ValueError("dx shape differs from dy")
+    ld_r = ld_dr = 0
+    if dresidual_out is not None:
+        rM, rD, ld_r = _rows(dresidual_out, "dresidual_out", (h.dtype,))
+        if rM != M or rD != D:
+            raise ValueError("dresidual_out shape differs from dy")
+    if ht == 1:
+        if dresidual is not None:
+            raise ValueError("the gradient of a bf16 residual is dx: give no dresidual")
+    elif dresidual is None:
+        dresidual, ld_dr = torch.empty_like(h, memory_format=torch.contiguous_format), D
+    else:
+        rM, rD, ld_dr = _rows(dresidual, "dresidual", (h.dtype,))
+        if rM != M or rD != D:
+            raise ValueError("dresidual shape differs from dy")
+    dweight = rstd.new_empty(D)
     if workspace is None:
+        need = int(lib().hyena_rms_norm_backward_workspace_size(M, D))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dy.device)
     _device(dy, h, weight, rstd, dresidual_out, dx, dresidual, workspace)
-    rc = lib().hyena_rms_norm_backward(_ptr(dy), ld_dy, _ptr(h), ld_h, _dtype_code(h), _ptr(weight),
-                                       _dtype_code(weight), _ptr(rstd), _ptr(dresidual_out), lds[0], _ptr(dx), ld_dx,
-                                       _ptr(dresidual), lds[1], _ptr(dweight), M, D, _ptr(workspace), workspace.numel(),
-                                       _stream(stream))
+    rc = lib().hyena_rms_norm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, ht, weight.data_ptr(), wt,
+                                       rstd.data_ptr(), _opt(dresidual_out), ld_r, dx.data_ptr(), ld_dx,
+                                       _opt(dresidual), ld_dr, dweight.data_ptr(), M, D, workspace.data_ptr(),
+                                       workspace.nbytes, _stream(stream))
     check("hyena_rms_norm_backward", rc)
-    return NormGrads(dx, dresidual if f32 else dx, dweight)
+    return NormGrads(dx, dx if ht == 1 else dresidual, dweight)

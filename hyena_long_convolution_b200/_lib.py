@@ -90,6 +90,8 @@ class HyenaError(RuntimeError):
 
 def lib() -> ctypes.CDLL:
     global _lib
+    if _lib is not None:  # the common case without the lock
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(SO):
