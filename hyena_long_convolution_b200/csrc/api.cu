@@ -451,18 +451,11 @@ hyena_status_t check_rows(const void *p, long long ld, int L, int D)
 
 bool encode_recurrence_maps(RecMaps &maps, const RecArgs &a)
 {
-    struct {
-        CUtensorMap *map;
-        const uint16_t *p;
-        long long ld;
-        int rows;
-    } const all[] = {{&maps.in[0], a.x1, a.ld_x, RT},       {&maps.in[1], a.x2, a.ld_x, RT},
-                     {&maps.in[2], a.x3, a.ld_x, RT},       {&maps.in[3], a.gate, a.ld_g, RT},
-                     {&maps.in[4], a.dy, a.ld_dy, RT},      {&maps.out[0], a.y, a.ld_y, RSEG},
-                     {&maps.out[0], a.dx1, a.ld_dx, RSEG},  {&maps.out[1], a.dx2, a.ld_dx, RSEG},
-                     {&maps.out[2], a.dx3, a.ld_dx, RSEG},  {&maps.out[3], a.dgate, a.ld_dg, RSEG}};
-    for (const auto &m : all)
-        if (m.p && !encode_x_map(m.map, separate_source(m.p, m.p, m.p, m.ld, a.D), 0, a.B, a.L, a.D, m.rows, RCH))
+    const uint16_t *p[5] = {a.x1, a.x2, a.x3, a.gate, a.dy};
+    const long long ld[5] = {a.ld_x, a.ld_x, a.ld_x, a.ld_g, a.ld_dy};
+    for (int k = 0; k < 5; ++k)
+        if (p[k] && !encode_x_map(&maps.in[k], separate_source(p[k], p[k], p[k], ld[k], a.D), 0, a.B, a.L, a.D, RT,
+                                  RCH))
             return false;
     return true;
 }

@@ -250,10 +250,10 @@ struct RecArgs {
 constexpr size_t kRecHeaderBytes = 256;
 constexpr size_t kRecTileBytes = (RCH + RCH / 2) * 16;
 
-// Tensor maps [B][L][1][D]: over x1, x2, x3, gate and (gradient) dy in boxes of
-// RT tokens x RCH channels, and over y or dx1, dx2, dx3, dgate in boxes of RSEG.
+// Tensor maps [B][L][1][D] over x1, x2, x3, gate and (gradient) dy, boxes of RT
+// tokens x RCH channels.
 struct RecMaps {
-    CUtensorMap in[5], out[4];
+    CUtensorMap in[5];
 };
 
 // Forward (or, with `back`, the gradient); the number of launches or -1.

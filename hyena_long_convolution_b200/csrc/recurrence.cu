@@ -40,12 +40,10 @@ constexpr int kParamBytes = RCH * 4;      // one fp32 value a channel
 constexpr int kBatch = 4;                 // units whose records a look-back loads at a time
 
 // A unit's rows of one tensor in shared memory as a lane sees them from its
-// segment's first token: word i holds its channel pair of token i.  Outputs
-// take the place of the inputs they need no more, word for word.
+// segment's first token: word i holds its channel pair of token i.
 struct TileRows {
     uint32_t *p;
     __device__ __forceinline__ uint32_t operator()(int i) const { return p[i * (RCH / 2)]; }
-    __device__ __forceinline__ void put(int i, float2 v) const { p[i * (RCH / 2)] = float2_to_bf16x2(v); }
 };
 
 __device__ __forceinline__ TileRows tile_rows(unsigned char *stage, int k, int warp, int lane)
@@ -214,9 +212,10 @@ __device__ __forceinline__ Tile tile_of(const RecArgs &A, unsigned int ticket)
 }
 
 // What forward and gradient share: two stages of N tensors' rows and the
-// channels' parameters, their tiles and barriers.  A tile's outputs leave from
-// its stage, each warp's rows by a TMA store of its own; the stage takes new
-// rows once the warps, in the next tile, have seen their stores read it.
+// channels' parameters, their tiles and barriers.  Outputs go straight to global
+// memory, a warp 128 bytes of a row at a time (as TMA stores from the stage,
+// eight small ones a tensor, they cost the gradient 10%), so a stage takes new
+// rows as soon as the warps are through with the tile.
 template <int N, bool kBack>
 struct Pipeline {
     static constexpr int kBytes = N * kTileBytes + 3 * kParamBytes;  // rows; log_rate, Dskip, start states
@@ -265,14 +264,6 @@ struct Pipeline {
     {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
-    }
-    // A computing warp, some time into tile `it`: its stores of the tile before
-    // have read their stage.
-    __device__ __forceinline__ void release(int it, int lane)
-    {
-        if (it == 0 || lane != 0) return;
-        bulk_wait_read();
-        mbar_arrive(&freed);
     }
 };
 
@@ -373,16 +364,17 @@ __device__ __forceinline__ ForwardSums &forward_sums(unsigned char *stage, int w
 }
 
 template <bool kNorm, bool kReset>
-__device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *stage, int warp, int lane, int n,
-                                             bool skip, unsigned int mask, int it)
+__device__ __forceinline__ void forward_tile(ForwardShared &sh, const RecArgs &A, const Tile &t, int row,
+                                             unsigned char *stage, int warp, int lane, int n, unsigned int mask,
+                                             int it)
 {
+    const bool skip = A.Dskip != nullptr;
     const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
     const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
     const unsigned char *params = stage + 4 * kTileBytes;
     if (n < RSEG) pad_tail(x1, gate, n);
     float2 a[RSEG], u[RSEG], l, P;
     segment_gates<kNorm, kReset>(a, u, l, P, gate, finite_rate(param(params, 0, lane)), mask);
-    sh.pipe.release(it, lane);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
         const float2 v = product(x1(i), x2(i));
@@ -393,6 +385,7 @@ __device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *s
     own.l[lane] = l;
     own.P[lane] = P;
     own.A[lane] = segment_end<kReset>(a, u, mask);
+    fence_proxy_async_smem();  // before the stage's next rows
     sh.pipe.arrive(&sh.pipe.sums, lane);
     sh.pipe.wait(&sh.pipe.carried, it);
     float2 C = sh.C[lane];
@@ -404,12 +397,15 @@ __device__ __forceinline__ void forward_tile(ForwardShared &sh, unsigned char *s
         }
     }
     const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
+    const int m_out = t.c + 2 * lane < A.D ? n : 0;  // tokens that this lane writes
+    uint16_t *y = A.y + (static_cast<long long>(t.b) * A.L + row) * A.ld_y + t.c + 2 * lane;
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
         C = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], C, u[i]);
         float2 o = __fmul2_rn(bf16x2_to_float2(x3(i)), C);
         if (skip) o = __ffma2_rn(dsk, product(x1(i), x2(i)), o);
-        x3.put(i, o);  // y takes x3's place
+        if (i < m_out) *reinterpret_cast<uint32_t *>(y) = float2_to_bf16x2(o);
+        y += A.ld_y;
     }
 }
 
@@ -468,22 +464,14 @@ __global__ void __launch_bounds__(kThreads, 3)
         sh.pipe.wait(&sh.pipe.full[st], it / kStages);
         const Tile t = sh.pipe.tile[st];
         if (t.j < 0) {
-            sh.pipe.release(it, lane);
             break;
         }
         unsigned char *stage = stages + st * sh.pipe.kBytes;
         const int n = min(A.L - t.j * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
         const unsigned int mask =
             kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + t.j * RT + warp * RSEG, n, lane) : 0u;
-        forward_tile<kNorm, kReset>(sh, stage, warp, lane, n, A.Dskip != nullptr, mask, it);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (n > 0)
-                tma_store_4d(&maps.out[0], stage + 2 * kTileBytes + warp * RSEG * RCH * 2, t.c, 0,
-                             t.j * RT + warp * RSEG, t.b);
-            bulk_commit();
-        }
+        forward_tile<kNorm, kReset>(sh, A, t, t.j * RT + warp * RSEG, stage, warp, lane, n, mask, it);
+        sh.pipe.arrive(&sh.pipe.freed, lane);
     }
 }
 
@@ -497,9 +485,11 @@ struct BackwardShared {
 };
 
 template <bool kNorm, bool kReset>
-__device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char *stage, int st, int warp, int lane,
-                                              int n, bool skip, unsigned int mask, int it)
+__device__ __forceinline__ void backward_tile(BackwardShared &sh, const RecArgs &A, const Tile &t, int row,
+                                              unsigned char *stage, int st, int warp, int lane, int n,
+                                              unsigned int mask, int it)
 {
+    const bool skip = A.Dskip != nullptr;
     const TileRows x1 = tile_rows(stage, 0, warp, lane), x2 = tile_rows(stage, 1, warp, lane);
     const TileRows x3 = tile_rows(stage, 2, warp, lane), gate = tile_rows(stage, 3, warp, lane);
     const TileRows dy = tile_rows(stage, 4, warp, lane);
@@ -508,7 +498,6 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
     const float2 rate = finite_rate(param(params, 0, lane));
     float2 a[RSEG], w[RSEG], prev[RSEG], l, P;
     segment_gates<kNorm, kReset>(a, w, l, P, gate, rate, mask);
-    sh.pipe.release(it, lane);
 #pragma unroll
     for (int i = 0; i < RSEG; ++i) {
         prev[i] = product(x1(i), x2(i));  // u, until the states are known
@@ -537,7 +526,10 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
 #pragma unroll
     for (int k = RWARPS - 1; k > 0; --k)
         if (k > warp) e = carry<kReset>(sh.P[st][k][lane], e, sh.Q[st][k][lane]);
-    // dx1, dx2, dx3, dgate take the places of x1, x2, x3, gate
+    const int m_out = t.c + 2 * lane < A.D ? n : 0;  // tokens that this lane writes
+    const long long at = static_cast<long long>(t.b) * A.L + row + RSEG - 1;
+    uint16_t *o1 = A.dx1 + at * A.ld_dx + t.c + 2 * lane, *o2 = A.dx2 + at * A.ld_dx + t.c + 2 * lane;
+    uint16_t *o3 = A.dx3 + at * A.ld_dx + t.c + 2 * lane, *og = A.dgate + at * A.ld_dg + t.c + 2 * lane;
 #pragma unroll
     for (int i = RSEG - 1; i >= 0; --i) {
         const bool cut = kReset && (mask >> i & 1u);
@@ -545,11 +537,17 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
         const float2 d = bf16x2_to_float2(wd);
         const float2 v = product(w1, w2);
         const float2 q = fma_bf16x2(x3(i), wd, e);
-        x3.put(i, __fmul2_rn(d, S));
+        const bool put = i < m_out;
+        if (put) *reinterpret_cast<uint32_t *>(o3) = float2_to_bf16x2(__fmul2_rn(d, S));
         float2 dv = kNorm ? __fmul2_rn(w[i], q) : q;
         if (skip) dv = __ffma2_rn(dsk, d, dv);
-        x1.put(i, __fmul2_rn(dv, bf16x2_to_float2(w2)));
-        x2.put(i, __fmul2_rn(dv, bf16x2_to_float2(w1)));
+        if (put) {
+            *reinterpret_cast<uint32_t *>(o1) = float2_to_bf16x2(__fmul2_rn(dv, bf16x2_to_float2(w2)));
+            *reinterpret_cast<uint32_t *>(o2) = float2_to_bf16x2(__fmul2_rn(dv, bf16x2_to_float2(w1)));
+        }
+        o1 -= A.ld_dx;
+        o2 -= A.ld_dx;
+        o3 -= A.ld_dx;
         e = __fmul2_rn(a[i], q);
         float2 m = prev[i];
         S = m;
@@ -569,7 +567,8 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, unsigned char 
         // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
         eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
         const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
-        gate.put(i, __fmul2_rn(__fmul2_rn(rate, dl), slope));
+        if (put) *reinterpret_cast<uint32_t *>(og) = float2_to_bf16x2(__fmul2_rn(__fmul2_rn(rate, dl), slope));
+        og -= A.ld_dg;
     }
     sh.rate[st][warp][lane] = d_rate;
     sh.skip[st][warp][lane] = d_skip;
@@ -638,7 +637,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         sh.pipe.wait(&sh.pipe.full[st], it / kStages);
         const Tile t = sh.pipe.tile[st];
         if (t.j < 0) {
-            sh.pipe.release(it, lane);
             break;
         }
         unsigned char *stage = stages + st * sh.pipe.kBytes;
@@ -646,18 +644,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int n = min(A.L - unit * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
         const unsigned int mask =
             kReset ? segment_resets(A.reset, static_cast<long long>(t.b) * A.L + unit * RT + warp * RSEG, n, lane) : 0u;
-        backward_tile<kNorm, kReset>(sh, stage, st, warp, lane, n, A.Dskip != nullptr, mask, it);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (n > 0) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tma_store_4d(&maps.out[k], stage + k * kTileBytes + warp * RSEG * RCH * 2, t.c, 0,
-                                 unit * RT + warp * RSEG, t.b);
-            }
-            bulk_commit();
-        }
+        backward_tile<kNorm, kReset>(sh, A, t, unit * RT + warp * RSEG, stage, st, warp, lane, n, mask, it);
+        if (n < RSEG) fence_proxy_async_smem();  // what pad_tail wrote, before the stage's next rows
+        sh.pipe.arrive(&sh.pipe.freed, lane);
     }
 }
 
