@@ -925,7 +925,7 @@ hyena_status_t hyena_rms_norm_fp8(const hyena_bf16_t *x, int64_t ld_x, const voi
 size_t hyena_rms_norm_backward_workspace_size(int64_t rows, int D)
 {
     if (rows < 0 || rows >= (1ll << 31) || D < 1 || D % 8 || D > HYENA_MAX_NORM_WIDTH) return 0;
-    return static_cast<size_t>(norm_parts(rows > 0 ? rows : 1)) * D * sizeof(float);
+    return static_cast<size_t>(norm_parts(rows > 0 ? rows : 1, D)) * D * sizeof(float);
 }
 
 hyena_status_t hyena_rms_norm_backward(const hyena_bf16_t *dy, int64_t ld_dy, const void *h, int64_t ld_h,

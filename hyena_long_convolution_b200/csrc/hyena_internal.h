@@ -289,13 +289,15 @@ struct NormArgs {
     float *dres;        // fp32 only
     long long ld_dr;
     float *dweight;
-    float *partial;     // workspace [norm_parts(rows)][D]
+    float *partial;     // workspace [norm_parts(rows, D)][D]
+    int stages;         // of the kernel's ring, and whether dres_out goes through it
+    bool stage_dres;
 };
 
 constexpr int kMaxNormWidth = HYENA_MAX_NORM_WIDTH;
 
 int launch_rms_norm(const NormArgs &a, cudaStream_t st);
 int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st);
-int norm_parts(long long rows);
+int norm_parts(long long rows, int D);
 
 }  // namespace hyena

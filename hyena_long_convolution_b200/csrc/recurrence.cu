@@ -255,9 +255,13 @@ struct Pipeline {
         fence_mbar_init();
         for (int s = 0; s < kStages; ++s) request(m, A, stages, s, tile_of(A, next_tile(A, s)));
     }
+    // Longer than a look-back waits, so that one that gives up does not put the
+    // CTA's own warps out of step.
     __device__ __forceinline__ void wait(uint64_t *bar, int turn)
     {
-        if (!mbar_wait_bounded(bar, turn & 1)) atomicOr(error, kErrLocalTimeout);
+        for (int i = 0; i < 4; ++i)
+            if (mbar_wait_bounded(bar, turn & 1)) return;
+        atomicOr(error, kErrLocalTimeout);
     }
     // This warp's part of a barrier that counts warps.
     __device__ __forceinline__ void arrive(uint64_t *bar, int lane)

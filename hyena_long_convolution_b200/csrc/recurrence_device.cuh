@@ -188,14 +188,4 @@ __device__ __forceinline__ unsigned int segment_resets(const uint8_t *reset, lon
     return __ballot_sync(kFullMask, r);
 }
 
-// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into
-// this CTA's shared memory, counted by `bar`.
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 }  // namespace hyena

@@ -8,9 +8,10 @@
 // Gradient, with n = h rstd and t = weight dy:
 //   dh = rstd (t - n mean(t n)) + dresidual_out;  dweight = sum over rows dy n
 //
-// One CTA per row holds it in registers between the reduction and the output,
-// so every input is read once; thread i of T owns the 8-channel vectors i,
-// i + T, ...
+// Forward: a CTA a row (a warp, up to 256 channels) holds it in registers
+// between the reduction and the output, so every input is read once; thread i of
+// T owns the 8-channel vectors i, i + T, ...  HBM-bound: 32768 rows of 4096
+// channels with a bf16 residual take 170 us, 98% of the measured copy bandwidth.
 #include <cuda_fp8.h>
 
 #include "hyena_device.cuh"
@@ -21,6 +22,8 @@ namespace hyena {
 namespace {
 
 constexpr int kNormThreads = 512;  // most threads of a row
+constexpr int kNormStages = 6;     // most stages of the gradient's ring
+constexpr int kNormSmem = 200 * 1024;
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100: a zero row keeps a finite scale
 constexpr unsigned int kFullMask = 0xffffffffu;
@@ -139,7 +142,8 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
 {
     __shared__ float sum_part[32];
     __shared__ unsigned int max_part[32];
-    const long long row = blockIdx.x;
+    const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row >= A.rows) return;  // with several rows a CTA, which are a warp each
     const int T = blockDim.x;
     const uint16_t *x = A.x + row * A.ld_x;
     float h[VPT][8];
@@ -225,61 +229,42 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
     }
 }
 
-// One row's inputs of the gradient as a thread holds them between their loads
-// and their use: kH 16-byte words of h, dy, and kH of dresidual_out.
-template <int VPT, int R>
-struct GradRow {
-    static constexpr int kH = R == 2 ? 2 : 1;
-    uint4 h[VPT][kH], dy[VPT], dres[VPT][kH];
-
-    __device__ __forceinline__ void load(const NormArgs &A, long long row)
-    {
-        constexpr int kSize = R == 2 ? 4 : 2;
-        if (row >= A.rows) return;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int c = 8 * (static_cast<int>(threadIdx.x) + k * static_cast<int>(blockDim.x));
-            if (c >= A.D) continue;
-            const uint4 *ph = reinterpret_cast<const uint4 *>(static_cast<const char *>(A.h) +
-                                                              (row * A.ld_h + c) * kSize);
-            const uint4 *pr = reinterpret_cast<const uint4 *>(static_cast<const char *>(A.dres_out) +
-                                                              (row * A.ld_r + c) * kSize);
-            dy[k] = *reinterpret_cast<const uint4 *>(A.dy + row * A.ld_y + c);
-#pragma unroll
-            for (int i = 0; i < kH; ++i) {
-                h[k][i] = ph[i];
-                dres[k][i] = A.dres_out ? pr[i] : make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-    }
-    template <int K>
-    static __device__ __forceinline__ void unpack(float (&v)[8], const uint4 (&q)[K])
-    {
-        if constexpr (K == 1) {
-            const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = bf16x2_to_float2(w[i]);
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
-        } else {
-            const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-        }
-    }
-};
-
 // Gradient.  A CTA walks the rows blockIdx.x, blockIdx.x + gridDim.x, ... and
 // keeps its channels' weight and part of dweight in registers; the parts go to
-// `partial` [gridDim.x][D].  HBM-bound (8 bytes an element with a bf16 residual):
-// the next row's loads are under way while this one is reduced and written.
+// `partial` [gridDim.x][D].  HBM-bound (8 bytes an element with a bf16
+// residual): rows come through a ring of A.stages stages of shared memory, a
+// bulk copy a tensor, and are read from there on both sides of the row's
+// reduction (holding the next row in registers instead kept 49 KB an SM under
+// way and reached 75% of the copy bandwidth).
 template <int VPT, int R>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const NormArgs A)
 {
+    constexpr int kSize = R == 2 ? 4 : 2;  // of h and dresidual_out
+    extern __shared__ __align__(128) unsigned char stages[];
     __shared__ float part[2][32];
+    __shared__ uint64_t full[kNormStages];
     const int T = blockDim.x;
+    const int S = A.stages;
+    const uint32_t dy_bytes = 2u * A.D, h_bytes = kSize * static_cast<uint32_t>(A.D);
+    const bool copy_dres = A.dres_out != nullptr && A.stage_dres;
+    const uint32_t stage_bytes = dy_bytes + h_bytes * (1 + copy_dres);
+    const auto request = [&](long long row, int s) {  // one thread
+        unsigned char *to = stages + s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_load(to, A.dy + row * A.ld_y, dy_bytes, &full[s]);
+        bulk_load(to + dy_bytes, static_cast<const char *>(A.h) + row * A.ld_h * kSize, h_bytes, &full[s]);
+        if (copy_dres)
+            bulk_load(to + dy_bytes + h_bytes, static_cast<const char *>(A.dres_out) + row * A.ld_r * kSize, h_bytes,
+                      &full[s]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+        fence_mbar_init();
+        for (int s = 0; s < S; ++s) {
+            const long long row = blockIdx.x + static_cast<long long>(s) * gridDim.x;
+            if (row < A.rows) request(row, s);
+        }
+    }
     float dw[VPT][8], w[VPT][8];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
@@ -288,47 +273,64 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
     }
-    GradRow<VPT, R> now, next;
-    next.load(A, blockIdx.x);
-    float rstd_next = A.rstd_in[blockIdx.x];
-    int turn = 0;
-    for (long long row = blockIdx.x; row < A.rows; row += gridDim.x, turn ^= 1) {
-        now = next;
-        const float rstd = rstd_next;
-        next.load(A, row + gridDim.x);
-        if (row + gridDim.x < A.rows) rstd_next = A.rstd_in[row + gridDim.x];
-        float n[VPT][8], t[VPT][8];
+    __syncthreads();
+    int s = 0, turn = 0;  // stage, and how often the ring has gone round
+    long long behind = blockIdx.x + static_cast<long long>(S - 1) * gridDim.x;  // the newest row asked for
+    for (long long row = blockIdx.x, i = 0; row < A.rows; row += gridDim.x, ++i) {
+        const float rstd = A.rstd_in[row];
+        if (!mbar_wait_bounded(&full[s], turn & 1) && threadIdx.x == 0)
+            A.dweight[0] = __int_as_float(0x7fc00000);  // a copy that never came: not passed off as a result
+        const unsigned char *st = stages + s * stage_bytes;
+        const uint16_t *dy = reinterpret_cast<const uint16_t *>(st);
+        const unsigned char *h = st + dy_bytes;
         float dot = 0.f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < A.D) {
-                now.unpack(n[k], now.h[k]);
-                const uint4 dy[1] = {now.dy[k]};
-                now.unpack(t[k], dy);
+                float n[8], d[8];
+                load8<R == 2 ? 2 : 1>(n, h, c);
+                load_bf16x8(d, dy + c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    n[k][i] *= rstd;
-                    dw[k][i] = __fmaf_rn(t[k][i], n[k][i], dw[k][i]);
-                    t[k][i] *= w[k][i];
-                    dot = __fmaf_rn(t[k][i], n[k][i], dot);
+                for (int j = 0; j < 8; ++j) {
+                    n[j] *= rstd;
+                    dw[k][j] = __fmaf_rn(d[j], n[j], dw[k][j]);
+                    dot = __fmaf_rn(d[j] * w[k][j], n[j], dot);
                 }
             }
         }
-        const float mean = block_sum(dot, part[turn]) / static_cast<float>(A.D);
+        const float mean = block_sum(dot, part[i & 1]) / static_cast<float>(A.D);
+        // behind the reduction every thread is through with the row before
+        if (i > 0) {
+            behind += gridDim.x;
+            if (threadIdx.x == 0 && behind < A.rows) request(behind, s == 0 ? S - 1 : s - 1);
+        }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < A.D) {
-                float r[8];
-                now.unpack(r, now.dres[k]);
+                float n[8], d[8], r[8];
+                load8<R == 2 ? 2 : 1>(n, h, c);
+                load_bf16x8(d, dy + c);
+                if (copy_dres) {
+                    load8<R == 2 ? 2 : 1>(r, h + h_bytes, c);
+                } else if (A.dres_out) {
+                    load8<R == 2 ? 2 : 1>(r, A.dres_out, row * A.ld_r + c);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r[i] = __fmaf_rn(rstd, t[k][i] - n[k][i] * mean, r[i]);
+                    for (int j = 0; j < 8; ++j) r[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = __fmaf_rn(rstd, d[j] * w[k][j] - n[j] * rstd * mean, r[j]);
                 if (A.dx) store_bf16x8(A.dx + row * A.ld_x + c, r);
                 if constexpr (R == 2) {
                     if (A.dres) store_f32x8(A.dres + row * A.ld_dr + c, r);
                 }
             }
+        }
+        if (++s == S) {
+            s = 0;
+            ++turn;
         }
     }
 #pragma unroll
@@ -370,11 +372,14 @@ NormShape norm_shape(int D)
 template <int VPT, int Q>
 void forward_r(const NormArgs &a, int threads, cudaStream_t st)
 {
-    const unsigned int rows = static_cast<unsigned int>(a.rows);
+    // Rows of one warp go eight to a CTA where there are enough of them
+    const unsigned int per = threads == 32 && a.rows >= 8 * 148 ? 8 : 1;
+    const unsigned int grid = static_cast<unsigned int>((a.rows + per - 1) / per);
+    const dim3 block(threads, per);
     switch (a.residual ? a.res_kind : 0) {
-        case 0: rms_norm_kernel<VPT, 0, Q><<<rows, threads, 0, st>>>(a); break;
-        case 1: rms_norm_kernel<VPT, 1, Q><<<rows, threads, 0, st>>>(a); break;
-        default: rms_norm_kernel<VPT, 2, Q><<<rows, threads, 0, st>>>(a); break;
+        case 0: rms_norm_kernel<VPT, 0, Q><<<grid, block, 0, st>>>(a); break;
+        case 1: rms_norm_kernel<VPT, 1, Q><<<grid, block, 0, st>>>(a); break;
+        default: rms_norm_kernel<VPT, 2, Q><<<grid, block, 0, st>>>(a); break;
     }
 }
 
@@ -389,13 +394,49 @@ void forward_q(const NormArgs &a, int threads, cudaStream_t st)
         forward_r<VPT, 2>(a, threads, st);
 }
 
-template <int VPT>
-void backward_r(const NormArgs &a, int parts, int threads, cudaStream_t st)
+// CTAs of the gradient an SM holds, by their registers and 200 KB of stages (at D
+// = 4096 two: 105 us for 16384 rows; three, which do not fit at once, 119), and in
+// all, no more than rows.
+int gradient_ctas(int D) { return D <= 512 ? 16 : (D <= 1024 ? 8 : (D <= 2048 ? 4 : (D <= 8192 ? 2 : 1))); }
+
+// More threads than the forward takes, and with them more CTAs' work hidden.
+NormShape gradient_shape(int D)
 {
-    if (a.res_kind == 2)
-        rms_norm_backward_kernel<VPT, 2><<<parts, threads, 0, st>>>(a);
-    else
-        rms_norm_backward_kernel<VPT, 1><<<parts, threads, 0, st>>>(a);
+    const int v = D / 8;
+    const int vpt = v <= kNormThreads ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
+    return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
+}
+
+// The ring of a gradient CTA: as many stages as its part of an SM's shared memory
+// holds, two at least; without dresidual_out where two with it exceed an SM's shared
+// memory (an fp32 one of more than 11K channels).
+template <int VPT, int R>
+int launch_gradient(NormArgs a, int parts, int threads, cudaStream_t st)
+{
+    thread_local int configured_device = -1;
+    int dev = 0;
+    HYENA_TRY(cudaGetDevice(&dev), "rms norm gradient: current device");
+    auto kernel = rms_norm_backward_kernel<VPT, R>;
+    if (configured_device != dev) {
+        HYENA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem),
+                  "rms norm gradient: set max dynamic shared memory");
+        configured_device = dev;
+    }
+    const int size = R == 2 ? 4 : 2;
+    int bytes = a.D * (2 + 2 * size);
+    a.stage_dres = 2 * bytes <= kNormSmem;
+    if (!a.stage_dres || !a.dres_out) bytes = a.D * (2 + size);
+    a.stages = kNormSmem / gradient_ctas(a.D) / bytes;
+    a.stages = a.stages < 2 ? 2 : (a.stages > kNormStages ? kNormStages : a.stages);
+    kernel<<<parts, threads, a.stages * bytes, st>>>(a);
+    return 0;
+}
+
+template <int VPT>
+int backward_r(const NormArgs &a, int parts, int threads, cudaStream_t st)
+{
+    return a.res_kind == 2 ? launch_gradient<VPT, 2>(a, parts, threads, st)
+                           : launch_gradient<VPT, 1>(a, parts, threads, st);
 }
 
 }  // namespace
@@ -413,28 +454,20 @@ int launch_rms_norm(const NormArgs &a, cudaStream_t st)
     return 1;
 }
 
-// CTAs of the gradient: two a SM (as many as its registers allow at D = 4096),
-// and no more than rows.
-int norm_parts(long long rows) { return static_cast<int>(rows < 296 ? rows : 296); }
-
-// More threads than the forward takes: a thread of the gradient holds two rows.
-NormShape gradient_shape(int D)
+int norm_parts(long long rows, int D)
 {
-    const int v = D / 8;
-    const int vpt = v <= kNormThreads ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
-    return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
+    const int most = 148 * gradient_ctas(D);
+    return static_cast<int>(rows < most ? rows : most);
 }
 
 int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st)
 {
     const NormShape s = gradient_shape(a.D);
-    const int parts = norm_parts(a.rows);
-    if (s.vpt == 1)
-        backward_r<1>(a, parts, s.threads, st);
-    else if (s.vpt == 2)
-        backward_r<2>(a, parts, s.threads, st);
-    else
-        backward_r<4>(a, parts, s.threads, st);
+    const int parts = norm_parts(a.rows, a.D);
+    const int rc = s.vpt == 1   ? backward_r<1>(a, parts, s.threads, st)
+                   : s.vpt == 2 ? backward_r<2>(a, parts, s.threads, st)
+                                : backward_r<4>(a, parts, s.threads, st);
+    if (rc < 0) return rc;
     norm_weight_sum_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, parts, a.D, a.dweight);
     HYENA_TRY(cudaGetLastError(), "rms norm gradient launch");
     return 2;
