@@ -685,6 +685,15 @@ def _device(x, *others):
     return dev
 
 
+def _current(stream):
+    """Makes a given stream (a torch Stream or a raw handle) the current one, so
+    that what the call allocates belongs to it as well."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _like(x, shape, st, ld, name):
     """Row stride of a bf16 [B, L, D] tensor of the given shape, as _bld (the
     device is checked by _device); the usual case, the stride of a tensor whose
@@ -750,6 +759,10 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     unit_states: from recurrence_unit_states, filled for the backward call.
     Returns y ([B, L, D] bf16, allocated if not given).
     """
+    if stream is not None:
+        with _current(stream):
+            return gated_recurrence(x1, x2, x3, gate, log_rate, Dskip, reset, normalize, y, state_in, state_out,
+                                    unit_states, workspace)
     torch = _torch()
     shape, st = x1.shape, x1.stride()
     if len(shape) != 3:
@@ -772,11 +785,11 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     _device(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states,
             None if workspace is None else workspace.buf)
     if workspace is None:
-        workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
+        workspace = RecurrenceWorkspace(B, L, D, device=x1.device)
     rc = lib().hyena_gated_recurrence(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
                                       log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0,
                                       y.data_ptr(), ld_y, _opt(state_in), _opt(state_out), _opt(unit_states),
-                                      B, L, D, workspace.buf.data_ptr(), workspace.nbytes, _stream(stream))
+                                      B, L, D, workspace.buf.data_ptr(), workspace.nbytes, _stream(None))
     check("hyena_gated_recurrence", rc)
     return y
 
@@ -799,6 +812,10 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
     given, the gradient of its last state (dstate_out, [B, D] fp32), with the
     forward call's inputs and the unit_states it filled.  dx1, dx2, dx3
     (sharing a row stride), dgate and dstate_in are allocated if not given."""
+    if stream is not None:
+        with _current(stream):
+            return gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states, reset, normalize,
+                                             dstate_out, dx1, dx2, dx3, dgate, dstate_in, workspace)
     torch = _torch()
     shape, st = x1.shape, x1.stride()
     if len(shape) != 3:
@@ -835,13 +852,13 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
     _device(x1, x2, x3, gate, dy, log_rate, Dskip, reset, unit_states, dstate_out, dx1, dx2, dx3, dgate, dstate_in,
             None if workspace is None else workspace.buf)
     if workspace is None:
-        workspace = RecurrenceWorkspace(B, L, D, device=x1.device, stream=stream)
+        workspace = RecurrenceWorkspace(B, L, D, device=x1.device)
     rc = lib().hyena_gated_recurrence_backward(
         dy.data_ptr(), ld_dy, x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
         log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0, unit_states.data_ptr(),
         _opt(dstate_out), dx1.data_ptr(), dx2.data_ptr(), dx3.data_ptr(), ld_dx, dgate.data_ptr(), ld_dg,
         dlog_rate.data_ptr(), _opt(dDskip), dstate_in.data_ptr(), B, L, D, workspace.buf.data_ptr(),
-        workspace.nbytes, _stream(stream))
+        workspace.nbytes, _stream(None))
     check("hyena_gated_recurrence_backward", rc)
     return RecurrenceGrads(dx1, dx2, dx3, dgate, dlog_rate, dDskip, dstate_in)
 
@@ -851,6 +868,9 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     ([B, D] fp32, in place) and returns y ([B, D] or [B, 1, D] like x1).
     Equals ``gated_recurrence`` on a one-token sequence with state_in =
     state_out = state, bit for bit."""
+    if stream is not None:
+        with _current(stream):
+            return gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize, y)
     B, D, ld = _bd(x1, "x1")
     shape, st, bf16 = x1.shape, x1.stride(), x1.dtype
     for t, name in ((x2, "x2"), (x3, "x3"), (gate, "gate")):
@@ -871,7 +891,7 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     _device(x1, x2, x3, gate, log_rate, Dskip, state, y)
     rc = lib().hyena_gated_recurrence_decode(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
                                              log_rate.data_ptr(), _opt(Dskip), 1 if normalize else 0, y.data_ptr(),
-                                             ld_y, state.data_ptr(), B, D, _stream(stream))
+                                             ld_y, state.data_ptr(), B, D, _stream(None))
     check("hyena_gated_recurrence_decode", rc)
     return y
 
@@ -938,6 +958,9 @@ def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, rstd
     residual, residual_out: bf16 or fp32 (residual_out receives h, and may be
     the residual itself); rstd: [rows] fp32 or None, filled for the backward
     call.  Returns y (bf16, allocated if not given)."""
+    if stream is not None:
+        with _current(stream):
+            return rms_norm(x, weight, eps, residual, residual_out, y, rstd)
     torch = _torch()
     M, D, ld, wt, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
     if y is None:
@@ -948,7 +971,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, rstd
             raise ValueError("y shape differs from x")
     _device(x, weight, residual, residual_out, y, rstd)
     rc = lib().hyena_rms_norm(x.data_ptr(), ld, _opt(residual), _opt(residual_out), ld_r, kind, weight.data_ptr(), wt,
-                              eps, y.data_ptr(), ld_y, _opt(rstd), M, D, _stream(stream))
+                              eps, y.data_ptr(), ld_y, _opt(rstd), M, D, _stream(None))
     check("hyena_rms_norm", rc)
     return y
 
@@ -958,6 +981,9 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
     """``rms_norm`` with an 8-bit output: returns (q, scales) with y ~ q scale,
     q float8_e4m3fn of x's shape and one fp32 scale per row (group = 0, shape
     [rows, 1]) or per 128 channels (group = 128, [rows, ceil(D / 128)])."""
+    if stream is not None:
+        with _current(stream):
+            return rms_norm_fp8(x, weight, eps, residual, residual_out, group, q, scales, rstd)
     torch = _torch()
     M, D, ld, wt, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
     if group not in (0, 128):
@@ -976,7 +1002,7 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
     _device(x, weight, residual, residual_out, q, scales, rstd)
     rc = lib().hyena_rms_norm_fp8(x.data_ptr(), ld, _opt(residual), _opt(residual_out), ld_r, kind,
                                   weight.data_ptr(), wt, eps, q.data_ptr(), ld_q, scales.data_ptr(), group,
-                                  _opt(rstd), M, D, _stream(stream))
+                                  _opt(rstd), M, D, _stream(None))
     check("hyena_rms_norm_fp8", rc)
     return q, scales
 
@@ -997,6 +1023,9 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
     residual_out, of h's type, or None.  dx (bf16) and, for an fp32 residual,
     dresidual (fp32; may be dresidual_out) are allocated if not given;
     ``workspace``: a uint8 tensor of rms_norm_backward_workspace_size bytes."""
+    if stream is not None:
+        with _current(stream):
+            return rms_norm_backward(dy, h, weight, rstd, dresidual_out, dx, dresidual, workspace)
     torch = _torch()
     M, D, ld_dy = _rows(dy, "dy", (torch.bfloat16,))
     hM, hD, ld_h = _rows(h, "h", (torch.bfloat16, torch.float32))
@@ -1032,6 +1061,6 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
     rc = lib().hyena_rms_norm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, ht, weight.data_ptr(), wt,
                                        rstd.data_ptr(), _opt(dresidual_out), ld_r, dx.data_ptr(), ld_dx,
                                        _opt(dresidual), ld_dr, dweight.data_ptr(), M, D, workspace.data_ptr(),
-                                       workspace.nbytes, _stream(stream))
+                                       workspace.nbytes, _stream(None))
     check("hyena_rms_norm_backward", rc)
     return NormGrads(dx, dx if ht == 1 else dresidual, dweight)

@@ -177,6 +177,13 @@ def test_other_stream_and_graph_replay():
         got = all_of()
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    # the stream given instead of made current
+    for st in (side, side.cuda_stream):
+        y = hy.rms_norm(x, w, EPS, residual=r, residual_out=ho, rstd=rstd, stream=st)
+        q, s = hy.rms_norm_fp8(x, w, EPS, residual=r, stream=st)
+        g = hy.rms_norm_backward(dy, ho, w, rstd, dresidual_out=dho, stream=st)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, (y, q.float(), s, g.dx, g.dweight)))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = all_of()

@@ -352,6 +352,14 @@ def test_one_workspace_many_shapes_streams_and_graphs():
         g2 = run_backward(hy, c, u2, True, workspace=ws2)
     side.synchronize()
     assert same(y, y2) and all(same(a, b) for a, b in zip(g, g2))
+    # the stream given instead of made current, as an object and as a handle; scratch of the call's own
+    for st in (side, side.cuda_stream):
+        y2, s2, u2 = run_forward(hy, c, True, stream=st)
+        g2 = run_backward(hy, c, u2, True, stream=st)
+        d2 = hy.gated_recurrence_decode(*(c[k][:, 0] for k in FWD[:4]), c["log_rate"], c["Dskip"],
+                                        c["state_in"].clone(), stream=st)
+        side.synchronize()
+        assert same(y, y2) and all(same(a, b) for a, b in zip(g, g2)) and d2.shape == (2, 200)
     graphs, outs = [], []
     for c, *_ in (ref[0], ref[2]):  # two graphs, one workspace, replayed in turn
         graph = torch.cuda.CUDAGraph()
