@@ -110,20 +110,25 @@ struct Records {
         uint4 nearest;
         uint32_t first;
     };
-    __device__ __forceinline__ Glance glance(int j) const
+    struct Spot {  // what a unit's glances look at, worked out once
+        const uint4 *nearest, *first;
+        bool there;
+    };
+    __device__ __forceinline__ Spot spot(int j) const
     {
-        Glance g;
-        g.nearest = load_record(at(j - 1, kRecCarry) + lane);
         const int back = lane & 15;
-        const uint32_t tag = load_record(at(max(j - 1 - back, 0), lane < 16 ? kRecCarry : kRecA)).z;
-        g.first = back < j ? tag : epoch - 1u;
-        return g;
+        return Spot{at(max(j - 1, 0), kRecCarry) + lane, at(max(j - 1 - back, 0), lane < 16 ? kRecCarry : kRecA),
+                    back < j};
     }
-    __device__ __forceinline__ bool look_back(int j, const Glance &g, float2 &C) const
+    __device__ __forceinline__ Glance glance(const Spot &s) const
+    {
+        return Glance{load_record(s.nearest), load_record(s.first).z};
+    }
+    __device__ __forceinline__ bool look_back(int j, const Spot &s, const Glance &g, float2 &C) const
     {
         C = pair_of(g.nearest);
         if (__all_sync(kFullMask, g.nearest.z == epoch)) return true;
-        const unsigned int ready = __ballot_sync(kFullMask, g.first == epoch);
+        const unsigned int ready = __ballot_sync(kFullMask, s.there && g.first == epoch);
         const unsigned int units = ready >> 16;
         const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
         if (k < 0 || ((units + 1u) & ((1u << k) - 1u)) != 0u) return false;
@@ -310,11 +315,12 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
         float2 C = found ? work.initial(t) : bcast2(0.f), P, a;
         const bool last = t.j == A.units - 1;
         rec.chain = t.chain;
+        const Records::Spot spot = rec.spot(t.j);
         unsigned long long t0 = 0;
         for (;;) {
             // the glance's load is under way while the CTA's own barriers are looked at
             Records::Glance seen{};
-            if (!found) seen = rec.glance(t.j);
+            if (!found) seen = rec.glance(spot);
             if (!asked && __all_sync(kFullMask, mbar_test_wait(&pipe.freed, (it - 1) & 1))) ask();
             if (!summed) {
                 if (found) pipe.wait(&pipe.sums, it);
@@ -324,7 +330,7 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
                     if (!found && !last) rec.publish_unit(t.j, P, a);
                 }
             }
-            if (!found) found = rec.look_back(t.j, seen, C);
+            if (!found) found = rec.look_back(t.j, spot, seen, C);
             if (found && summed) break;
             const unsigned long long now = global_timer_ns();
             if (t0 == 0) t0 = now;
