@@ -132,25 +132,44 @@ struct Records {
         const unsigned int units = ready >> 16;
         const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
         if (k < 0 || ((units + 1u) & ((1u << k) - 1u)) != 0u) return false;
-        const uint4 r = load_record(at(j - 1 - k, kRecCarry) + lane);
-        bool found = r.z == epoch;
+        // the carry and the kBatch farthest units behind it in one round trip to L2,
+        // which a loop from the first batch on would make two
+        const uint4 *from = at(j - 1 - k, kRecCarry) + lane;
+        const uint4 r = load_record(from);
+        Sums u;
+        load_sums(j - k, j - 1, u);
         C = pair_of(r);
-        for (int d = k - 1; d >= 0; d -= kBatch) {
-            uint4 P[kBatch], A[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                P[i] = load_record(at(j - 1 - max(d - i, 0), kRecP) + lane);
-                A[i] = load_record(at(j - 1 - max(d - i, 0), kRecA) + lane);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (d >= i) {
-                    found = found && P[i].z == epoch && A[i].z == epoch;
-                    C = carry<true>(pair_of(P[i]), C, pair_of(A[i]));
-                }
-            }
+        bool found = r.z == epoch;
+        apply(min(k, kBatch), u, C, found);
+        for (int d = k - kBatch; d > 0; d -= kBatch) {
+            load_sums(j - d, j - 1, u);
+            apply(min(d, kBatch), u, C, found);
         }
         return __all_sync(kFullMask, found);
+    }
+
+    // Of kBatch units from `first` on (the last one again behind `last`), and their
+    // first n applied to C.
+    struct Sums {
+        uint4 P[kBatch], A[kBatch];
+    };
+    __device__ __forceinline__ void load_sums(int first, int last, Sums &u) const
+    {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            u.P[i] = load_record(at(min(first + i, last), kRecP) + lane);
+            u.A[i] = load_record(at(min(first + i, last), kRecA) + lane);
+        }
+    }
+    __device__ __forceinline__ void apply(int n, const Sums &u, float2 &C, bool &found) const
+    {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i < n) {
+                found = found && u.P[i].z == epoch && u.A[i].z == epoch;
+                C = carry<true>(pair_of(u.P[i]), C, pair_of(u.A[i]));
+            }
+        }
     }
 
     static __device__ __forceinline__ float2 pair_of(uint4 r)
