@@ -6,7 +6,7 @@
 #include <cstdio>
 #include <mutex>
 
-#include "hyena_internal.h"
+#include "layer_internal.h"
 
 namespace hyena {
 

@@ -14,8 +14,8 @@
 // unit is formed from the sum of its l, not as a product of rounded a.
 #pragma once
 
-#include "hyena_device.cuh"
-#include "hyena_internal.h"
+#include "layer_device.cuh"
+#include "layer_internal.h"
 
 namespace hyena {
 

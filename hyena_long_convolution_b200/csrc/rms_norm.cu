@@ -14,8 +14,8 @@
 // channels with a bf16 residual take 170 us, 98% of the measured copy bandwidth.
 #include <cuda_fp8.h>
 
-#include "hyena_device.cuh"
-#include "hyena_internal.h"
+#include "layer_device.cuh"
+#include "layer_internal.h"
 
 namespace hyena {
 
