@@ -28,6 +28,8 @@
 // together: from the nearest known carry it applies the units' (P, A) in order,
 // the operations each unit itself performs, so the result does not depend on
 // what was ready.  The gradient runs the same from the right.
+#include <type_traits>
+
 #include "recurrence_device.cuh"
 
 namespace hyena {
@@ -428,14 +430,20 @@ __device__ __forceinline__ void forward_tile(ForwardShared &sh, const RecArgs &A
     const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
     const int m_out = t.c + 2 * lane < A.D ? n : 0;  // tokens that this lane writes
     uint16_t *y = A.y + (static_cast<long long>(t.b) * A.L + row) * A.ld_y + t.c + 2 * lane;
+    const auto write = [&](auto whole) {  // the warp writes all of its rows: no test at each
 #pragma unroll
-    for (int i = 0; i < RSEG; ++i) {
-        C = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], C, u[i]);
-        float2 o = __fmul2_rn(bf16x2_to_float2(x3(i)), C);
-        if (skip) o = __ffma2_rn(dsk, product(x1(i), x2(i)), o);
-        if (i < m_out) *reinterpret_cast<uint32_t *>(y) = float2_to_bf16x2(o);
-        y += A.ld_y;
-    }
+        for (int i = 0; i < RSEG; ++i) {
+            C = kReset && (mask >> i & 1u) ? u[i] : __ffma2_rn(a[i], C, u[i]);
+            float2 o = __fmul2_rn(bf16x2_to_float2(x3(i)), C);
+            if (skip) o = __ffma2_rn(dsk, product(x1(i), x2(i)), o);
+            if (decltype(whole)::value || i < m_out) *reinterpret_cast<uint32_t *>(y) = float2_to_bf16x2(o);
+            y += A.ld_y;
+        }
+    };
+    if (__all_sync(kFullMask, m_out == RSEG))
+        write(std::true_type());
+    else
+        write(std::false_type());
 }
 
 template <bool kReset>
@@ -559,46 +567,52 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, const RecArgs 
     const long long at = static_cast<long long>(t.b) * A.L + row + RSEG - 1;
     uint16_t *o1 = A.dx1 + at * A.ld_dx + t.c + 2 * lane, *o2 = A.dx2 + at * A.ld_dx + t.c + 2 * lane;
     uint16_t *o3 = A.dx3 + at * A.ld_dx + t.c + 2 * lane, *og = A.dgate + at * A.ld_dg + t.c + 2 * lane;
+    const auto write = [&](auto whole) {  // the warp writes all of its rows: no test at each
 #pragma unroll
-    for (int i = RSEG - 1; i >= 0; --i) {
-        const bool cut = kReset && (mask >> i & 1u);
-        const uint32_t w1 = x1(i), w2 = x2(i), wd = dy(i);
-        const float2 d = bf16x2_to_float2(wd);
-        const float2 v = product(w1, w2);
-        const float2 q = fma_bf16x2(x3(i), wd, e);
-        const bool put = i < m_out;
-        if (put) *reinterpret_cast<uint32_t *>(o3) = float2_to_bf16x2(__fmul2_rn(d, S));
-        float2 dv = kNorm ? __fmul2_rn(w[i], q) : q;
-        if (skip) dv = __ffma2_rn(dsk, d, dv);
-        if (put) {
-            *reinterpret_cast<uint32_t *>(o1) = float2_to_bf16x2(__fmul2_rn(dv, bf16x2_to_float2(w2)));
-            *reinterpret_cast<uint32_t *>(o2) = float2_to_bf16x2(__fmul2_rn(dv, bf16x2_to_float2(w1)));
+        for (int i = RSEG - 1; i >= 0; --i) {
+            const bool cut = kReset && (mask >> i & 1u);
+            const uint32_t w1 = x1(i), w2 = x2(i), wd = dy(i);
+            const float2 d = bf16x2_to_float2(wd);
+            const float2 v = product(w1, w2);
+            const float2 q = fma_bf16x2(x3(i), wd, e);
+            const bool put = decltype(whole)::value || i < m_out;
+            if (put) *reinterpret_cast<uint32_t *>(o3) = float2_to_bf16x2(__fmul2_rn(d, S));
+            float2 dv = kNorm ? __fmul2_rn(w[i], q) : q;
+            if (skip) dv = __ffma2_rn(dsk, d, dv);
+            if (put) {
+                *reinterpret_cast<uint32_t *>(o1) = float2_to_bf16x2(__fmul2_rn(dv, bf16x2_to_float2(w2)));
+                *reinterpret_cast<uint32_t *>(o2) = float2_to_bf16x2(__fmul2_rn(dv, bf16x2_to_float2(w1)));
+            }
+            o1 -= A.ld_dx;
+            o2 -= A.ld_dx;
+            o3 -= A.ld_dx;
+            e = __fmul2_rn(a[i], q);
+            float2 m = prev[i];
+            S = m;
+            if constexpr (kNorm) {
+                // d w / d l = -a^2 / w; no gradient where w = 0 (log_rate = 0)
+                const float2 r = make_float2(w[i].x > 0.f ? rcp_approx(w[i].x) : 0.f,
+                                             w[i].y > 0.f ? rcp_approx(w[i].y) : 0.f);
+                const float2 av = __fmul2_rn(a[i], v);
+                m = __ffma2_rn(make_float2(-av.x, -av.y), r, m);
+            }
+            float2 dl = __fmul2_rn(e, m);
+            if (cut) dl = e = bcast2(0.f);
+            float2 eg;
+            const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
+            d_rate = __ffma2_rn(dl, sig, d_rate);
+            d_skip = __ffma2_rn(d, v, d_skip);
+            // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
+            eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
+            const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
+            if (put) *reinterpret_cast<uint32_t *>(og) = float2_to_bf16x2(__fmul2_rn(__fmul2_rn(rate, dl), slope));
+            og -= A.ld_dg;
         }
-        o1 -= A.ld_dx;
-        o2 -= A.ld_dx;
-        o3 -= A.ld_dx;
-        e = __fmul2_rn(a[i], q);
-        float2 m = prev[i];
-        S = m;
-        if constexpr (kNorm) {
-            // d w / d l = -a^2 / w; no gradient where w = 0 (log_rate = 0)
-            const float2 r = make_float2(w[i].x > 0.f ? rcp_approx(w[i].x) : 0.f,
-                                         w[i].y > 0.f ? rcp_approx(w[i].y) : 0.f);
-            const float2 av = __fmul2_rn(a[i], v);
-            m = __ffma2_rn(make_float2(-av.x, -av.y), r, m);
-        }
-        float2 dl = __fmul2_rn(e, m);
-        if (cut) dl = e = bcast2(0.f);
-        float2 eg;
-        const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
-        d_rate = __ffma2_rn(dl, sig, d_rate);
-        d_skip = __ffma2_rn(d, v, d_skip);
-        // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
-        eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
-        const float2 slope = __fmul2_rn(__fmul2_rn(eg, sig), sig);
-        if (put) *reinterpret_cast<uint32_t *>(og) = float2_to_bf16x2(__fmul2_rn(__fmul2_rn(rate, dl), slope));
-        og -= A.ld_dg;
-    }
+    };
+    if (__all_sync(kFullMask, m_out == RSEG))
+        write(std::true_type());
+    else
+        write(std::false_type());
     sh.rate[st][warp][lane] = d_rate;
     sh.skip[st][warp][lane] = d_skip;
 }
