@@ -1057,6 +1057,8 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
     if workspace is None:
         need = int(lib().hyena_rms_norm_backward_workspace_size(M, D))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dy.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
     _device(dy, h, weight, rstd, dresidual_out, dx, dresidual, workspace)
     rc = lib().hyena_rms_norm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, ht, weight.data_ptr(), wt,
                                        rstd.data_ptr(), _opt(dresidual_out), ld_r, dx.data_ptr(), ld_dx,

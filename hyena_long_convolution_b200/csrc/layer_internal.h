@@ -35,11 +35,13 @@ struct RecArgs {
     unsigned int tiles;      // chains units
     float *C;                // forward: unit_states or null
     // workspace: header ([0] next ticket, [1] finished CTAs, [2] error bits,
-    // [3] epoch), then 16-byte records, all with their tag in the third word
+    // [4..5] launches so far, the next one's epoch - 1), then 16-byte records, all
+    // with their tag in the second half
     unsigned int *hdr;
     uint4 *records;          // [tiles][3][RCH / 2]: P, A (later the gradient's parts), carry
 };
 constexpr size_t kRecHeaderBytes = 256;
+constexpr int kRecEpoch = 4;  // header word
 constexpr size_t kRecTileBytes = (RCH + RCH / 2) * 16;
 
 // Tensor maps [B][L][1][D] over x1, x2, x3, gate and (gradient) dy, boxes of RT

@@ -23,11 +23,12 @@
 // from the units before it and writes its outputs from the same copy.  Units
 // are handed out in time-major order by an atomic ticket, so the unit a CTA
 // waits for is always running or done.  A unit publishes 16-byte records whose
-// third word is the launch's epoch; 16 bytes are written and read at once, so a
-// record needs no flag or fence beside it.  The reader looks at the last 16 units
-// together: from the nearest known carry it applies the units' (P, A) in order,
-// the operations each unit itself performs, so the result does not depend on
-// what was ready.  The gradient runs the same from the right.
+// second half is the launch's number in 64 bits, which no earlier record has; 16
+// bytes are written and read at once, so a record needs no flag or fence beside
+// it.  The reader looks at the last 16 units together: from the nearest known
+// carry it applies the units' (P, A) in order, the operations each unit itself
+// performs, so the result does not depend on what was ready.  The gradient runs
+// the same from the right.
 #include <type_traits>
 
 #include "recurrence_device.cuh"
@@ -55,24 +56,29 @@ __device__ __forceinline__ TileRows tile_rows(unsigned char *stage, int k, int w
 
 // ---------------------------------------------------------------- records
 
-__device__ __forceinline__ uint4 load_record(const uint4 *p)
+struct Record {
+    float2 v;
+    unsigned long long tag;
+};
+
+__device__ __forceinline__ Record load_record(const uint4 *p)
 {
     unsigned long long lo, hi;
     asm volatile("{\n\t.reg .b128 t;\n\tld.relaxed.gpu.global.b128 t, [%2];\n\tmov.b128 {%0, %1}, t;\n\t}"
                  : "=l"(lo), "=l"(hi)
                  : "l"(p)
                  : "memory");
-    return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
-                      static_cast<uint32_t>(hi >> 32));
+    return Record{make_float2(__uint_as_float(static_cast<uint32_t>(lo)),
+                              __uint_as_float(static_cast<uint32_t>(lo >> 32))),
+                  hi};
 }
 
-__device__ __forceinline__ void store_record(uint4 *p, float a, float b, uint32_t tag)
+__device__ __forceinline__ void store_record(uint4 *p, float2 v, unsigned long long tag)
 {
     const unsigned long long lo =
-        __float_as_uint(a) | static_cast<unsigned long long>(__float_as_uint(b)) << 32;
-    const unsigned long long hi = tag;
+        __float_as_uint(v.x) | static_cast<unsigned long long>(__float_as_uint(v.y)) << 32;
     asm volatile("{\n\t.reg .b128 t;\n\tmov.b128 t, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], t;\n\t}" ::"l"(p),
-                 "l"(lo), "l"(hi)
+                 "l"(lo), "l"(tag)
                  : "memory");
 }
 
@@ -84,7 +90,7 @@ enum { kRecP, kRecA, kRecCarry };
 struct Records {
     uint4 *base;  // [tiles][3][RCH / 2]
     int chains, chain, lane;
-    uint32_t epoch;
+    unsigned long long epoch;
 
     __device__ __forceinline__ uint4 *at(int j, int kind) const
     {
@@ -93,12 +99,12 @@ struct Records {
 
     __device__ __forceinline__ void publish_unit(int j, float2 P, float2 A) const
     {
-        store_record(at(j, kRecP) + lane, P.x, P.y, epoch);
-        store_record(at(j, kRecA) + lane, A.x, A.y, epoch);
+        store_record(at(j, kRecP) + lane, P, epoch);
+        store_record(at(j, kRecA) + lane, A, epoch);
     }
     __device__ __forceinline__ void publish_carry(int j, float2 C) const
     {
-        store_record(at(j, kRecCarry) + lane, C.x, C.y, epoch);
+        store_record(at(j, kRecCarry) + lane, C, epoch);
     }
 
     // Looking for the carry into unit j > 0, by all lanes of a warp.  glance():
@@ -109,8 +115,8 @@ struct Records {
     // behind it is there; each lane then loads its own channels' records.  The tag
     // of every record that is used is checked.
     struct Glance {
-        uint4 nearest;
-        uint32_t first;
+        Record nearest;
+        unsigned long long first;  // its tag
     };
     struct Spot {  // what a unit's glances look at, worked out once
         const uint4 *nearest, *first;
@@ -124,12 +130,12 @@ struct Records {
     }
     __device__ __forceinline__ Glance glance(const Spot &s) const
     {
-        return Glance{load_record(s.nearest), load_record(s.first).z};
+        return Glance{load_record(s.nearest), load_record(s.first).tag};
     }
     __device__ __forceinline__ bool look_back(int j, const Spot &s, const Glance &g, float2 &C) const
     {
-        C = pair_of(g.nearest);
-        if (__all_sync(kFullMask, g.nearest.z == epoch)) return true;
+        C = g.nearest.v;
+        if (__all_sync(kFullMask, g.nearest.tag == epoch)) return true;
         const unsigned int ready = __ballot_sync(kFullMask, s.there && g.first == epoch);
         const unsigned int units = ready >> 16;
         const int k = __ffs(ready & 0xffffu) - 1;  // nearest known carry
@@ -137,11 +143,11 @@ struct Records {
         // the carry and the kBatch farthest units behind it in one round trip to L2,
         // which a loop from the first batch on would make two
         const uint4 *from = at(j - 1 - k, kRecCarry) + lane;
-        const uint4 r = load_record(from);
+        const Record r = load_record(from);
         Sums u;
         load_sums(j - k, j - 1, u);
-        C = pair_of(r);
-        bool found = r.z == epoch;
+        C = r.v;
+        bool found = r.tag == epoch;
         apply(min(k, kBatch), u, C, found);
         for (int d = k - kBatch; d > 0; d -= kBatch) {
             load_sums(j - d, j - 1, u);
@@ -153,7 +159,7 @@ struct Records {
     // Of kBatch units from `first` on (the last one again behind `last`), and their
     // first n applied to C.
     struct Sums {
-        uint4 P[kBatch], A[kBatch];
+        Record P[kBatch], A[kBatch];
     };
     __device__ __forceinline__ void load_sums(int first, int last, Sums &u) const
     {
@@ -168,15 +174,10 @@ struct Records {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (i < n) {
-                found = found && u.P[i].z == epoch && u.A[i].z == epoch;
-                C = carry<true>(pair_of(u.P[i]), C, pair_of(u.A[i]));
+                found = found && u.P[i].tag == epoch && u.A[i].tag == epoch;
+                C = carry<true>(u.P[i].v, C, u.A[i].v);
             }
         }
-    }
-
-    static __device__ __forceinline__ float2 pair_of(uint4 r)
-    {
-        return make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
     }
 };
 
@@ -215,7 +216,7 @@ __device__ __forceinline__ void finish(const RecArgs &A)
     if (atomicAdd(A.hdr + 1, 1u) + 1u == gridDim.x) {
         A.hdr[0] = 0u;
         A.hdr[1] = 0u;
-        A.hdr[3] += 1u;
+        *reinterpret_cast<unsigned long long *>(A.hdr + kRecEpoch) += 1u;
     }
 }
 
@@ -312,7 +313,7 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
                                              unsigned char *stages, float2 *carry_in, int lane, Work work)
 {
     Records rec{A.records, A.chains, 0, lane, 0u};
-    if (A.units > 1) rec.epoch = ld_volatile_u32(A.hdr + 3) + 1u;
+    if (A.units > 1) rec.epoch = *reinterpret_cast<const volatile unsigned long long *>(A.hdr + kRecEpoch) + 1u;
     Tile before{};
     for (int it = 0;; ++it) {
         const int st = it % kStages;
@@ -657,8 +658,8 @@ struct BackwardWork {
             d_skip = __fadd2_rn(d_skip, sh.skip[st][w][lane]);
         }
         uint4 *u = A.records + (static_cast<size_t>(t.j) * A.chains + t.chain) * (3 * RCH / 2) + lane;
-        store_record(u + kRecP * (RCH / 2), d_rate.x, d_rate.y, 0u);
-        store_record(u + kRecA * (RCH / 2), d_skip.x, d_skip.y, 0u);
+        store_record(u + kRecP * (RCH / 2), d_rate, 0u);
+        store_record(u + kRecA * (RCH / 2), d_skip, 0u);
     }
 };
 

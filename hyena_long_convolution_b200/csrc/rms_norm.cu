@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
     long long behind = blockIdx.x + static_cast<long long>(S - 1) * gridDim.x;  // the newest row asked for
     for (long long row = blockIdx.x, i = 0; row < A.rows; row += gridDim.x, ++i) {
         const float rstd = A.rstd_in[row];
-        if (!mbar_wait_bounded(&full[s], turn & 1) && threadIdx.x == 0)
-            A.dweight[0] = __int_as_float(0x7fc00000);  // a copy that never came: not passed off as a result
+        if (!mbar_wait_bounded(&full[s], turn & 1))
+            dw[0][0] = __int_as_float(0x7fc00000);  // a copy that never came is not passed off as a result
         const unsigned char *st = stages + s * stage_bytes;
         const uint16_t *dy = reinterpret_cast<const uint16_t *>(st);
         const unsigned char *h = st + dy_bytes;

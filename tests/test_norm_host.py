@@ -78,3 +78,7 @@ def test_binding_refuses():
             f(x, w)
     with pytest.raises(ValueError, match="CUDA"):
         hy.rms_norm_backward(x, x, w, torch.ones(3))
+    u8 = torch.zeros(1024, dtype=torch.uint8)
+    for work in (u8[::2], u8[:1].expand(99), torch.zeros(1024)):
+        with pytest.raises(ValueError, match="workspace"):
+            hy.rms_norm_backward(x, x, w, torch.ones(3), workspace=work)

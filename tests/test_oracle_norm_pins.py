@@ -12,7 +12,8 @@ def test_rows_have_unit_mean_square():
     np.testing.assert_allclose(onorm.forward(3.0 * h, np.ones(40), 0.0), y, rtol=1e-12)
     np.testing.assert_allclose(onorm.forward(np.zeros((1, 8)), np.ones(8), 1e-6), 0.0)
     # mean square 12.5 + eps 12.5: rms 5
-    np.testing.assert_allclose(onorm.forward(np.array([[3.0, 4.0]]), np.array([1.0, 2.0]), 12.5), [[0.6, 1.6]], rtol=1e-15)
+    y = onorm.forward(np.array([[3.0, 4.0]]), np.array([1.0, 2.0]), 12.5)
+    np.testing.assert_allclose(y, [[0.6, 1.6]], rtol=1e-15)
 
 
 def test_scales():
@@ -23,7 +24,7 @@ def test_scales():
 
 def test_gradient_against_differences():
     r = np.random.default_rng(1)
-    h, w, dy, dho = r.standard_normal((3, 7)), r.standard_normal(7), r.standard_normal((3, 7)), r.standard_normal((3, 7))
+    h, w, dy, dho = (r.standard_normal(s) for s in ((3, 7), 7, (3, 7), (3, 7)))
 
     def loss(h, w):
         return float((onorm.forward(h, w, 0.1) * dy).sum() + (h * dho).sum())

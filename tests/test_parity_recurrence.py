@@ -380,6 +380,27 @@ def test_one_workspace_many_shapes_streams_and_graphs():
     del graphs
 
 
+def test_launches_are_told_apart_past_32_bits():
+    """The records' tags count launches in 64 bits: where the lower half goes
+    round, zero-filled records and those of a launch with the same lower half are
+    not taken for this launch's."""
+    import torch
+
+    import hyena_long_convolution_b200 as hy
+    c, d = cuda(make(2, 1500, 136, seed=11)), cuda(make(2, 1500, 136, seed=12))
+    want = run_forward(hy, d, True)
+    grads = run_backward(hy, d, want[2], True)
+    ws = hy.RecurrenceWorkspace(2, 1500, 136)
+    launches = ws.buf[16:24].view(torch.int64)
+    for before in (0, 2 ** 32 - 1, 2 ** 32, 2 ** 40):
+        launches.fill_(before)
+        assert all(same(x, y) for x, y in zip(run_forward(hy, d, True, workspace=ws), want))
+        assert launches.item() == before + 1
+        run_forward(hy, c, True, workspace=ws)
+        assert all(same(x, y) for x, y in zip(run_backward(hy, d, want[2], True, workspace=ws), grads))
+        hy.workspace_check(ws)
+
+
 @pytest.mark.parametrize("B,L,D", [(1, 8192, 4096), (4, 2000, 1032), (1, 20000, 64)])
 def test_long_sequences_against_a_64_bit_scan(B, L, D):
     """Lengths the numpy oracle is slow for: the same recurrence in torch's
