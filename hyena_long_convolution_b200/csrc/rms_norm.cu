@@ -69,6 +69,8 @@ __device__ __forceinline__ void store_f32x8(float *p, const float (&v)[8])
         *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
+__device__ __forceinline__ float2 bcast2(float x) { return make_float2(x, x); }
+
 // A tensor of type kind R (0 absent, 1 bf16, 2 fp32), 8 values at element o.
 template <int R>
 __device__ __forceinline__ void load8(float (&v)[8], const void *p, long long o)
@@ -77,6 +79,32 @@ __device__ __forceinline__ void load8(float (&v)[8], const void *p, long long o)
         load_f32x8(v, static_cast<const float *>(p) + o);
     else
         load_bf16x8(v, static_cast<const uint16_t *>(p) + o);
+}
+
+// The same as channel pairs, which the arithmetic takes two at a time.
+template <int R>
+__device__ __forceinline__ void load_pairs(float2 (&v)[4], const void *p, long long o)
+{
+    if constexpr (R == 2) {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + o);
+        const float4 a = q[0], b = q[1];
+        v[0] = make_float2(a.x, a.y);
+        v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y);
+        v[3] = make_float2(b.z, b.w);
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + o);
+        v[0] = bf16x2_to_float2(q.x);
+        v[1] = bf16x2_to_float2(q.y);
+        v[2] = bf16x2_to_float2(q.z);
+        v[3] = bf16x2_to_float2(q.w);
+    }
+}
+
+__device__ __forceinline__ void store_pairs(float *p, const float2 (&v)[4])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
 
 // The weight, fp32 or bf16 (the same for the whole launch).
@@ -88,8 +116,8 @@ __device__ __forceinline__ void load_weight(float (&v)[8], const void *p, bool b
         load_f32x8(v, static_cast<const float *>(p) + c);
 }
 
-// Sum over the CTA, the same bits in every thread: within the warps by
-// butterfly, then the warps' sums in order.  `part` is used by one call only.
+// Sum over the CTA, the same bits in every thread: by butterfly within the warps
+// and again over the warps' sums (16 at most).  `part` is used by one call only.
 __device__ __forceinline__ float block_sum(float v, float *part)
 {
 #pragma unroll
@@ -98,8 +126,10 @@ __device__ __forceinline__ float block_sum(float v, float *part)
     if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = part[0];
-    for (int w = 1; w < warps; ++w) v += part[w];
+    const int w = threadIdx.x & 15;
+    v = w < warps ? part[w] : 0.f;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
     return v;
 }
 
@@ -265,41 +295,47 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
             if (row < A.rows) request(row, s);
         }
     }
-    float dw[VPT][8], w[VPT][8];
+    float2 dw[VPT][4], w[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
-        if (c < A.D) load_weight(w[k], A.weight, A.weight_bf16, c);
+        if (c < A.D) {
+            if (A.weight_bf16)
+                load_pairs<1>(w[k], A.weight, c);
+            else
+                load_pairs<2>(w[k], A.weight, c);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
+        for (int i = 0; i < 4; ++i) dw[k][i] = bcast2(0.f);
     }
+    const float per_channel = 1.f / static_cast<float>(A.D);
     __syncthreads();
     int s = 0, turn = 0;  // stage, and how often the ring has gone round
     long long behind = blockIdx.x + static_cast<long long>(S - 1) * gridDim.x;  // the newest row asked for
     for (long long row = blockIdx.x, i = 0; row < A.rows; row += gridDim.x, ++i) {
         const float rstd = A.rstd_in[row];
         if (!mbar_wait_bounded(&full[s], turn & 1))
-            dw[0][0] = __int_as_float(0x7fc00000);  // a copy that never came is not passed off as a result
+            dw[0][0].x = __int_as_float(0x7fc00000);  // a copy that never came is not passed off as a result
         const unsigned char *st = stages + s * stage_bytes;
         const uint16_t *dy = reinterpret_cast<const uint16_t *>(st);
         const unsigned char *h = st + dy_bytes;
-        float dot = 0.f;
+        float2 dot = bcast2(0.f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < A.D) {
-                float n[8], d[8];
-                load8<R == 2 ? 2 : 1>(n, h, c);
-                load_bf16x8(d, dy + c);
+                float2 n[4], d[4];
+                load_pairs<R>(n, h, c);
+                load_pairs<1>(d, dy, c);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    n[j] *= rstd;
-                    dw[k][j] = __fmaf_rn(d[j], n[j], dw[k][j]);
-                    dot = __fmaf_rn(d[j] * w[k][j], n[j], dot);
+                for (int j = 0; j < 4; ++j) {
+                    n[j] = __fmul2_rn(n[j], bcast2(rstd));
+                    dw[k][j] = __ffma2_rn(d[j], n[j], dw[k][j]);
+                    dot = __ffma2_rn(__fmul2_rn(d[j], w[k][j]), n[j], dot);
                 }
             }
         }
-        const float mean = block_sum(dot, part[i & 1]) / static_cast<float>(A.D);
+        const float mean = block_sum(dot.x + dot.y, part[i & 1]) * per_channel;
         // behind the reduction every thread is through with the row before
         if (i > 0) {
             behind += gridDim.x;
@@ -309,22 +345,33 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < A.D) {
-                float n[8], d[8], r[8];
-                load8<R == 2 ? 2 : 1>(n, h, c);
-                load_bf16x8(d, dy + c);
+                float2 n[4], d[4], r[4];
+                load_pairs<R>(n, h, c);
+                load_pairs<1>(d, dy, c);
                 if (copy_dres) {
-                    load8<R == 2 ? 2 : 1>(r, h + h_bytes, c);
+                    load_pairs<R>(r, h + h_bytes, c);
                 } else if (A.dres_out) {
-                    load8<R == 2 ? 2 : 1>(r, A.dres_out, row * A.ld_r + c);
+                    load_pairs<R>(r, A.dres_out, row * A.ld_r + c);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) r[j] = 0.f;
+                    for (int j = 0; j < 4; ++j) r[j] = bcast2(0.f);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = __fmaf_rn(rstd, d[j] * w[k][j] - n[j] * rstd * mean, r[j]);
-                if (A.dx) store_bf16x8(A.dx + row * A.ld_x + c, r);
+                for (int j = 0; j < 4; ++j) {
+                    n[j] = __fmul2_rn(n[j], bcast2(rstd));
+                    const float2 t = __ffma2_rn(n[j], bcast2(-mean), __fmul2_rn(d[j], w[k][j]));
+                    r[j] = __ffma2_rn(bcast2(rstd), t, r[j]);
+                }
+                if (A.dx) {
+                    uint4 q;
+                    q.x = float2_to_bf16x2(r[0]);
+                    q.y = float2_to_bf16x2(r[1]);
+                    q.z = float2_to_bf16x2(r[2]);
+                    q.w = float2_to_bf16x2(r[3]);
+                    *reinterpret_cast<uint4 *>(A.dx + row * A.ld_x + c) = q;
+                }
                 if constexpr (R == 2) {
-                    if (A.dres) store_f32x8(A.dres + row * A.ld_dr + c, r);
+                    if (A.dres) store_pairs(A.dres + row * A.ld_dr + c, r);
                 }
             }
         }
@@ -336,7 +383,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
-        if (c < A.D) store_f32x8(A.partial + static_cast<long long>(blockIdx.x) * A.D + c, dw[k]);
+        if (c < A.D) store_pairs(A.partial + static_cast<long long>(blockIdx.x) * A.D + c, dw[k]);
     }
 }
 
