@@ -388,20 +388,37 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
 }
 
 // dweight: the CTAs' parts summed in double, in a fixed order: a CTA takes 32
-// channels, each of its warps every 32nd part.
+// channels, eight lanes four each, and a warp's four groups of lanes every 128th
+// part; then the groups and the warps by butterfly.  Latency-bound, so that a
+// thread's loads go out together (592 parts of 1032 channels: 5.8 us, one load at a time 8.4).
 __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float *partial, int parts, int D, float *dweight)
 {
     __shared__ double sum[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 32 + lane;
-    double s = 0.;
-    if (c < D)
-        for (int p = warp; p < parts; p += 32) s += partial[static_cast<long long>(p) * D + c];
-    sum[warp][lane] = s;
+    const int c = blockIdx.x * 32 + 4 * (lane & 7);
+    double s[4] = {0., 0., 0., 0.};
+    if (c < D) {
+#pragma unroll 8
+        for (int p = 4 * warp + (lane >> 3); p < parts; p += 128) {
+            const float4 v = *reinterpret_cast<const float4 *>(partial + static_cast<long long>(p) * D + c);
+            s[0] += v.x;
+            s[1] += v.y;
+            s[2] += v.z;
+            s[3] += v.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] += __shfl_xor_sync(kFullMask, s[i], 8);
+        s[i] += __shfl_xor_sync(kFullMask, s[i], 16);
+        if (lane < 8) sum[warp][4 * lane + i] = s[i];
+    }
     __syncthreads();
-    if (warp != 0 || c >= D) return;
-    for (int w = 1; w < 32; ++w) s += sum[w][lane];
-    dweight[c] = static_cast<float>(s);
+    double v = sum[lane][warp];  // the warp's channel, a lane a warp's sum
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
+    const int out = blockIdx.x * 32 + warp;
+    if (lane == 0 && out < D) dweight[out] = static_cast<float>(v);
 }
 
 // Vectors per thread and threads of a row of D channels.
