@@ -696,7 +696,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // dlog_rate and dDskip: the units' parts summed in double, in a fixed order: a
 // CTA takes one of the two for a chain's channels over all batch rows and
-// units, each of its 32 warps every 32nd part, a lane a channel pair.
+// units, each of its 32 warps every 32nd part, a lane a channel pair; then the
+// warps by butterfly.  Latency-bound, so that a thread's loads go out together
+// (2 x 8192 x 4096: 6.6 us, one load at a time 11).
 __global__ void __launch_bounds__(1024) unit_sum_kernel(const RecArgs A)
 {
     __shared__ double sum[32][2 * 32 + 1];
@@ -704,22 +706,27 @@ __global__ void __launch_bounds__(1024) unit_sum_kernel(const RecArgs A)
     const int kind = blockIdx.x & 1, cb = blockIdx.x >> 1;
     float *out = kind == kRecP ? A.dlog_rate : A.dDskip;
     if (out == nullptr) return;
-    const long long parts = static_cast<long long>(A.B) * A.units;
+    const unsigned int parts = static_cast<unsigned int>(A.B) * A.units;  // below 2^31, as the tiles are
     double x = 0., y = 0.;
-    for (long long k = warp; k < parts; k += 32) {
-        const long long j = k / A.B, b = k - j * A.B;
-        const uint4 q = A.records[((static_cast<size_t>(j) * A.chains + b * A.nCB + cb) * 3 + kind) * (RCH / 2) + lane];
-        x += __uint_as_float(q.x);
-        y += __uint_as_float(q.y);
+    // tile j chains + b nCB + cb is (j B + b) nCB + cb
+    const uint4 *first = A.records + (static_cast<size_t>(cb) * 3 + kind) * (RCH / 2) + lane;
+#pragma unroll 8
+    for (unsigned int k = warp; k < parts; k += 32) {
+        const float2 q = *reinterpret_cast<const float2 *>(first + static_cast<size_t>(k) * A.nCB * (3 * RCH / 2));
+        x += q.x;
+        y += q.y;
     }
     sum[warp][2 * lane] = x;
     sum[warp][2 * lane + 1] = y;
     __syncthreads();
-    const int c = cb * RCH + threadIdx.x;
-    if (threadIdx.x >= RCH || c >= A.D) return;
-    double v = 0.;
-    for (int w = 0; w < 32; ++w) v += sum[w][threadIdx.x];
-    out[c] = static_cast<float>(v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // two channels a warp, a lane a warp's sum
+        double v = sum[lane][2 * warp + i];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
+        const int c = cb * RCH + 2 * warp + i;
+        if (lane == 0 && c < A.D) out[c] = static_cast<float>(v);
+    }
 }
 
 // One token per batch row: the scan's arithmetic on a unit of one token.
