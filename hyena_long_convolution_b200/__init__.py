@@ -871,6 +871,7 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     if stream is not None:
         with _current(stream):
             return gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize, y)
+    torch = _torch()
     B, D, ld = _bd(x1, "x1")
     shape, st, bf16 = x1.shape, x1.stride(), x1.dtype
     for t, name in ((x2, "x2"), (x3, "x3"), (gate, "gate")):
@@ -883,7 +884,7 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     _f32(Dskip, (D,), "Dskip")
     _f32(state, (B, D), "state", False)
     if y is None:
-        y, ld_y = x1.new_empty(shape), D
+        y, ld_y = torch.empty_like(x1, memory_format=torch.contiguous_format), D
     else:
         yB, yD, ld_y = _bd(y, "y")
         if (yB, yD) != (B, D):
