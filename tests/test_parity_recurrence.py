@@ -380,6 +380,47 @@ def test_one_workspace_many_shapes_streams_and_graphs():
     del graphs
 
 
+def test_calls_at_once_from_several_threads_and_streams():
+    """Launches that share the device, each with a workspace of its own and none
+    with all of its CTAs resident, give the bits they give alone."""
+    import threading
+
+    import torch
+
+    import hyena_long_convolution_b200 as hy
+    cases = [cuda(make(2, 4000, 1032, seed=21)), cuda(make(1, 9000, 2048, seed=22)), cuda(make(1, 20000, 64, seed=23))]
+    want = []
+    for c in cases:
+        y, s, u = run_forward(hy, c, True)
+        want.append((y, s, u, run_backward(hy, c, u, True)))
+    torch.cuda.synchronize()
+    got, failed = [None] * 3, []
+
+    def work(k):
+        try:
+            st = torch.cuda.Stream()
+            B, L, D = cases[k]["x1"].shape
+            with torch.cuda.stream(st):
+                ws = hy.RecurrenceWorkspace(B, L, D)
+                for _ in range(10):
+                    y, s, u = run_forward(hy, cases[k], True, workspace=ws)
+                    g = run_backward(hy, cases[k], u, True, workspace=ws)
+                hy.workspace_check(ws)
+            st.synchronize()
+            got[k] = (y, s, u, g)
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for (y, s, u, g), (y2, s2, u2, g2) in zip(got, want):
+        assert same(y, y2) and same(s, s2) and same(u, u2) and all(same(a, b) for a, b in zip(g, g2))
+
+
 def test_launches_are_told_apart_past_32_bits():
     """The records' tags count launches in 64 bits: where the lower half goes
     round, zero-filled records and those of a launch with the same lower half are
