@@ -69,9 +69,15 @@ RECURRENCE_UNIT = 64
 MAX_NORM_WIDTH = 16384
 
 
+_torch_module = None  # imported by the first call; a statement in each costs it 0.1 us every time
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -673,16 +679,17 @@ def modal_decode_complex_packed(xp, group, poles, residues, Dskip, state, y=None
 
 # ------------------------------------------------------------ gated recurrence
 
-def _device(x, *others):
-    """The device index that x and the given tensors (None: absent) share,
-    which must be the current one: the call launches there."""
+def _here(x, *others):
+    """The current stream's handle, once x and the given tensors (None: absent)
+    are known to be on the current device: the call launches there."""
+    C = _torch()._C
     dev = x.get_device()
-    if dev < 0 or dev != _torch()._C._cuda_getDevice():
+    if dev < 0 or dev != C._cuda_getDevice():
         raise ValueError("tensors must be on the current CUDA device")
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one CUDA device")
-    return dev
+    return C._cuda_getCurrentRawStream(dev)
 
 
 def _current(stream):
@@ -696,7 +703,7 @@ def _current(stream):
 
 def _like(x, shape, st, ld, name):
     """Row stride of a bf16 [B, L, D] tensor of the given shape, as _bld (the
-    device is checked by _device); the usual case, the stride of a tensor whose
+    device is checked by _here); the usual case, the stride of a tensor whose
     row stride ld is known, is settled by comparing."""
     if x.dtype is not _torch().bfloat16 or x.shape != shape:
         raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(shape)}")
@@ -778,18 +785,18 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     _f32(state_in, (B, D), "state_in")
     _f32(state_out, (B, D), "state_out")
     _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states")
+    here = _here(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states,
+                 None if workspace is None else workspace.buf)
     if y is None:
         y, ld_y = torch.empty_like(x1, memory_format=torch.contiguous_format), D
     else:
         ld_y = _like(y, shape, st, ld, "y")
-    _device(x1, x2, x3, gate, log_rate, Dskip, reset, y, state_in, state_out, unit_states,
-            None if workspace is None else workspace.buf)
     if workspace is None:
         workspace = RecurrenceWorkspace(B, L, D, device=x1.device)
     rc = lib().hyena_gated_recurrence(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
                                       log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0,
                                       y.data_ptr(), ld_y, _opt(state_in), _opt(state_out), _opt(unit_states),
-                                      B, L, D, workspace.buf.data_ptr(), workspace.nbytes, _stream(None))
+                                      B, L, D, workspace.buf.data_ptr(), workspace.nbytes, here)
     check("hyena_gated_recurrence", rc)
     return y
 
@@ -831,6 +838,8 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
     _f32(unit_states, (B, -(-L // RECURRENCE_UNIT), D), "unit_states", False)
     _f32(dstate_out, (B, D), "dstate_out")
     _f32(dstate_in, (B, D), "dstate_in")
+    here = _here(x1, x2, x3, gate, dy, log_rate, Dskip, reset, unit_states, dstate_out, dx1, dx2, dx3, dgate,
+                 dstate_in, None if workspace is None else workspace.buf)
     dense = torch.contiguous_format
     if dx1 is None and dx2 is None and dx3 is None:
         dx1, dx2, dx3 = (torch.empty_like(x1, memory_format=dense) for _ in range(3))
@@ -849,8 +858,6 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
         dstate_in = unit_states.new_empty((B, D))
     dlog_rate = torch.empty_like(log_rate)
     dDskip = None if Dskip is None else torch.empty_like(Dskip)
-    _device(x1, x2, x3, gate, dy, log_rate, Dskip, reset, unit_states, dstate_out, dx1, dx2, dx3, dgate, dstate_in,
-            None if workspace is None else workspace.buf)
     if workspace is None:
         workspace = RecurrenceWorkspace(B, L, D, device=x1.device)
     rc = lib().hyena_gated_recurrence_backward(
@@ -858,7 +865,7 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
         log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0, unit_states.data_ptr(),
         _opt(dstate_out), dx1.data_ptr(), dx2.data_ptr(), dx3.data_ptr(), ld_dx, dgate.data_ptr(), ld_dg,
         dlog_rate.data_ptr(), _opt(dDskip), dstate_in.data_ptr(), B, L, D, workspace.buf.data_ptr(),
-        workspace.nbytes, _stream(None))
+        workspace.nbytes, here)
     check("hyena_gated_recurrence_backward", rc)
     return RecurrenceGrads(dx1, dx2, dx3, dgate, dlog_rate, dDskip, dstate_in)
 
@@ -883,16 +890,16 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
     _f32(log_rate, (D,), "log_rate", False)
     _f32(Dskip, (D,), "Dskip")
     _f32(state, (B, D), "state", False)
+    here = _here(x1, x2, x3, gate, log_rate, Dskip, state, y)
     if y is None:
         y, ld_y = torch.empty_like(x1, memory_format=torch.contiguous_format), D
     else:
         yB, yD, ld_y = _bd(y, "y")
         if (yB, yD) != (B, D):
             raise ValueError("y shape differs from x")
-    _device(x1, x2, x3, gate, log_rate, Dskip, state, y)
     rc = lib().hyena_gated_recurrence_decode(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
                                              log_rate.data_ptr(), _opt(Dskip), 1 if normalize else 0, y.data_ptr(),
-                                             ld_y, state.data_ptr(), B, D, _stream(None))
+                                             ld_y, state.data_ptr(), B, D, here)
     check("hyena_gated_recurrence_decode", rc)
     return y
 
@@ -901,7 +908,7 @@ def gated_recurrence_decode(x1, x2, x3, gate, log_rate, Dskip, state, normalize=
 
 def _rows(x, name, dtypes):
     """[M, D] or [B, L, D] tensor with unit channel stride and evenly spaced
-    rows -> (rows, D, ld); the device is checked by _device."""
+    rows -> (rows, D, ld); the device is checked by _here."""
     sh, st = x.shape, x.stride()
     if x.dtype not in dtypes or len(sh) not in (2, 3):
         raise ValueError(f"{name} must be a CUDA tensor [rows, D] or [B, L, D] of type {' or '.join(map(str, dtypes))}")
@@ -964,15 +971,15 @@ def rms_norm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, rstd
             return rms_norm(x, weight, eps, residual, residual_out, y, rstd)
     torch = _torch()
     M, D, ld, wt, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
+    here = _here(x, weight, residual, residual_out, y, rstd)
     if y is None:
         y, ld_y = torch.empty_like(x, memory_format=torch.contiguous_format), D
     else:
         yM, yD, ld_y = _rows(y, "y", (torch.bfloat16,))
         if yM != M or yD != D:
             raise ValueError("y shape differs from x")
-    _device(x, weight, residual, residual_out, y, rstd)
     rc = lib().hyena_rms_norm(x.data_ptr(), ld, _opt(residual), _opt(residual_out), ld_r, kind, weight.data_ptr(), wt,
-                              eps, y.data_ptr(), ld_y, _opt(rstd), M, D, _stream(None))
+                              eps, y.data_ptr(), ld_y, _opt(rstd), M, D, here)
     check("hyena_rms_norm", rc)
     return y
 
@@ -989,6 +996,7 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
     M, D, ld, wt, ld_r, kind = _norm_inputs(x, weight, residual, residual_out, rstd)
     if group not in (0, 128):
         raise ValueError("group must be 0 (one scale per row) or 128")
+    here = _here(x, weight, residual, residual_out, q, scales, rstd)
     if q is None:
         q, ld_q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), D
     else:
@@ -1000,10 +1008,9 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
         scales = x.new_empty(want, dtype=torch.float32)
     else:
         _f32(scales, want, "scales")
-    _device(x, weight, residual, residual_out, q, scales, rstd)
     rc = lib().hyena_rms_norm_fp8(x.data_ptr(), ld, _opt(residual), _opt(residual_out), ld_r, kind,
                                   weight.data_ptr(), wt, eps, q.data_ptr(), ld_q, scales.data_ptr(), group,
-                                  _opt(rstd), M, D, _stream(None))
+                                  _opt(rstd), M, D, here)
     check("hyena_rms_norm_fp8", rc)
     return q, scales
 
@@ -1034,6 +1041,9 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
         raise ValueError("h shape differs from dy")
     wt, ht = _weight(weight, D), _dtype_code(h)
     _f32(rstd, (M,), "rstd", False)
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    here = _here(dy, h, weight, rstd, dresidual_out, dx, dresidual, workspace)
     if dx is None:
         dx, ld_dx = torch.empty_like(dy, memory_format=torch.contiguous_format), D
     else:
@@ -1058,12 +1068,9 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
     if workspace is None:
         need = int(lib().hyena_rms_norm_backward_workspace_size(M, D))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dy.device)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    _device(dy, h, weight, rstd, dresidual_out, dx, dresidual, workspace)
     rc = lib().hyena_rms_norm_backward(dy.data_ptr(), ld_dy, h.data_ptr(), ld_h, ht, weight.data_ptr(), wt,
                                        rstd.data_ptr(), _opt(dresidual_out), ld_r, dx.data_ptr(), ld_dx,
                                        _opt(dresidual), ld_dr, dweight.data_ptr(), M, D, workspace.data_ptr(),
-                                       workspace.nbytes, _stream(None))
+                                       workspace.nbytes, here)
     check("hyena_rms_norm_backward", rc)
     return NormGrads(dx, dx if ht == 1 else dresidual, dweight)

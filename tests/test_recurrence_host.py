@@ -83,4 +83,4 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="reset"):
         hy._reset(torch.zeros(2, 4, dtype=torch.bool), 2, 5)
     with pytest.raises(ValueError, match="current"):
-        hy._device(x)
+        hy._here(x)
