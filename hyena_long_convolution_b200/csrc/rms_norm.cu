@@ -25,6 +25,10 @@ namespace {
 constexpr int kNormThreads = 512;  // most threads of a row
 constexpr int kNormStages = 6;     // most stages of the gradient's ring
 constexpr int kNormSmem = 200 * 1024;
+constexpr int kNarrowWidth = 256;    // widest row that the gradient takes by lanes of a warp
+constexpr int kNarrowThreads = 256;
+constexpr int kNarrowTurns = 3;
+constexpr int kNarrowCtas = 2;  // an SM, by its registers
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100: a zero row keeps a finite scale
 constexpr unsigned int kFullMask = 0xffffffffu;
@@ -82,30 +86,64 @@ __device__ __forceinline__ void load8(float (&v)[8], const void *p, long long o)
         load_bf16x8(v, static_cast<const uint16_t *>(p) + o);
 }
 
-// The same as channel pairs, which the arithmetic takes two at a time.
+// The same as it is in memory, and as channel pairs, which the arithmetic takes two
+// at a time.
 template <int R>
-__device__ __forceinline__ void load_pairs(float2 (&v)[4], const void *p, long long o)
-{
-    if constexpr (R == 2) {
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + o);
-        const float4 a = q[0], b = q[1];
-        v[0] = make_float2(a.x, a.y);
-        v[1] = make_float2(a.z, a.w);
-        v[2] = make_float2(b.x, b.y);
-        v[3] = make_float2(b.z, b.w);
-    } else {
-        const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + o);
+struct Vector {
+    uint4 q{0u, 0u, 0u, 0u};
+    __device__ __forceinline__ void load(const void *p, long long o)
+    {
+        q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + o);
+    }
+    __device__ __forceinline__ void pairs(float2 (&v)[4]) const
+    {
         v[0] = bf16x2_to_float2(q.x);
         v[1] = bf16x2_to_float2(q.y);
         v[2] = bf16x2_to_float2(q.z);
         v[3] = bf16x2_to_float2(q.w);
     }
+};
+
+template <>
+struct Vector<2> {
+    float4 a{0.f, 0.f, 0.f, 0.f}, b{0.f, 0.f, 0.f, 0.f};
+    __device__ __forceinline__ void load(const void *p, long long o)
+    {
+        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + o);
+        a = q[0];
+        b = q[1];
+    }
+    __device__ __forceinline__ void pairs(float2 (&v)[4]) const
+    {
+        v[0] = make_float2(a.x, a.y);
+        v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y);
+        v[3] = make_float2(b.z, b.w);
+    }
+};
+
+template <int R>
+__device__ __forceinline__ void load_pairs(float2 (&v)[4], const void *p, long long o)
+{
+    Vector<R> t;
+    t.load(p, o);
+    t.pairs(v);
 }
 
 __device__ __forceinline__ void store_pairs(float *p, const float2 (&v)[4])
 {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+
+__device__ __forceinline__ void store_bf16_pairs(uint16_t *p, const float2 (&v)[4])
+{
+    uint4 q;
+    q.x = float2_to_bf16x2(v[0]);
+    q.y = float2_to_bf16x2(v[1]);
+    q.z = float2_to_bf16x2(v[2]);
+    q.w = float2_to_bf16x2(v[3]);
+    *reinterpret_cast<uint4 *>(p) = q;
 }
 
 // The weight, fp32 or bf16 (the same for the whole launch).
@@ -365,14 +403,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
                     const float2 t = __ffma2_rn(n[j], bcast2(-mean), __fmul2_rn(d[j], w[k][j]));
                     r[j] = __ffma2_rn(bcast2(rstd), t, r[j]);
                 }
-                if (A.dx) {
-                    uint4 q;
-                    q.x = float2_to_bf16x2(r[0]);
-                    q.y = float2_to_bf16x2(r[1]);
-                    q.z = float2_to_bf16x2(r[2]);
-                    q.w = float2_to_bf16x2(r[3]);
-                    *reinterpret_cast<uint4 *>(A.dx + row * A.ld_x + c) = q;
-                }
+                if (A.dx) store_bf16_pairs(A.dx + row * A.ld_x + c, r);
                 if constexpr (R == 2) {
                     if (A.dres) store_pairs(A.dres + row * A.ld_dr + c, r);
                 }
@@ -387,6 +418,96 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
     for (int k = 0; k < VPT; ++k) {
         const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
         if (c < A.D) store_pairs(A.partial + static_cast<long long>(blockIdx.x) * A.D + c, dw[k]);
+    }
+}
+
+// Gradient of short rows (of heads, say): G lanes a row, 8 channels each, 32 / G
+// rows a warp, and kNarrowTurns rows' loads of a lane under way together, from
+// global memory; no row needs the CTA's other warps.  90 us for 524288 x 128 and
+// for 262144 x 256 (83 at the copy bandwidth); by the kernel above, where a short
+// row leaves most lanes idle, 103 and 130.  Registers for three CTAs an SM spill
+// (116 us for 524288 x 128); two turns instead of three take 95 and 99.
+template <int G, int R>
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas) rms_norm_backward_narrow_kernel(const NormArgs A)
+{
+    constexpr int kRows = 32 / G;
+    constexpr int kTurns = kNarrowTurns;
+    __shared__ float part[kNarrowThreads / 32][8 * G];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = lane / G, c = 8 * (lane % G);
+    const bool live = c < A.D;
+    const float per_channel = 1.f / static_cast<float>(A.D);
+    float2 w[4], dw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = dw[j] = bcast2(0.f);
+    if (live) {
+        if (A.weight_bf16)
+            load_pairs<1>(w, A.weight, c);
+        else
+            load_pairs<2>(w, A.weight, c);
+    }
+    const long long step = static_cast<long long>(gridDim.x) * (kNarrowThreads / 32) * kRows;
+    long long base = (static_cast<long long>(blockIdx.x) * (kNarrowThreads / 32) + warp) * kRows;
+    for (; base < A.rows; base += step * kTurns) {
+        Vector<R> h[kTurns], dres[kTurns];
+        Vector<1> dy[kTurns];
+        float rstd[kTurns];
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const long long row = base + u * step + sub;
+            rstd[u] = 0.f;
+            h[u] = dres[u] = Vector<R>();
+            dy[u] = Vector<1>();
+            if (live && row < A.rows) {
+                rstd[u] = A.rstd_in[row];
+                h[u].load(A.h, row * A.ld_h + c);
+                dy[u].load(A.dy, row * A.ld_y + c);
+                if (A.dres_out) dres[u].load(A.dres_out, row * A.ld_r + c);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const long long row = base + u * step + sub;
+            float2 n[4], d[4], r[4], dot = bcast2(0.f);
+            h[u].pairs(n);
+            dy[u].pairs(d);
+            dres[u].pairs(r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                n[j] = __fmul2_rn(n[j], bcast2(rstd[u]));
+                dw[j] = __ffma2_rn(d[j], n[j], dw[j]);
+                d[j] = __fmul2_rn(d[j], w[j]);
+                dot = __ffma2_rn(d[j], n[j], dot);
+            }
+            float mean = dot.x + dot.y;
+#pragma unroll
+            for (int k = G / 2; k > 0; k >>= 1) mean += __shfl_xor_sync(kFullMask, mean, k);
+            mean *= per_channel;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[j] = __ffma2_rn(bcast2(rstd[u]), __ffma2_rn(n[j], bcast2(-mean), d[j]), r[j]);
+            if (live && row < A.rows) {
+                if (A.dx) store_bf16_pairs(A.dx + row * A.ld_x + c, r);
+                if constexpr (R == 2) {
+                    if (A.dres) store_pairs(A.dres + row * A.ld_dr + c, r);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int k = G; k < 32; k <<= 1) {
+            dw[j].x += __shfl_xor_sync(kFullMask, dw[j].x, k);
+            dw[j].y += __shfl_xor_sync(kFullMask, dw[j].y, k);
+        }
+    }
+    if (sub == 0) store_pairs(&part[warp][c], dw);
+    __syncthreads();
+    if (threadIdx.x < A.D) {
+        float s = 0.f;
+        for (int k = 0; k < kNarrowThreads / 32; ++k) s += part[k][threadIdx.x];
+        A.partial[static_cast<long long>(blockIdx.x) * A.D + threadIdx.x] = s;
     }
 }
 
@@ -464,7 +585,11 @@ void forward_q(const NormArgs &a, int threads, cudaStream_t st)
 // CTAs of the gradient an SM holds, by their registers and 200 KB of stages (for
 // 16384 x 4096 two took 105 us where three, which do not fit at once, took 119), and
 // in all, no more than rows.
-int gradient_ctas(int D) { return D <= 512 ? 16 : (D <= 1024 ? 8 : (D <= 2048 ? 4 : (D <= 8192 ? 2 : 1))); }
+int gradient_ctas(int D)
+{
+    if (D <= kNarrowWidth) return kNarrowCtas;
+    return D <= 512 ? 16 : (D <= 1024 ? 8 : (D <= 2048 ? 4 : (D <= 8192 ? 2 : 1)));
+}
 
 // More threads than the forward takes, and with them more CTAs' work hidden.
 NormShape gradient_shape(int D)
@@ -472,6 +597,18 @@ NormShape gradient_shape(int D)
     const int v = D / 8;
     const int vpt = v <= kNormThreads ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
     return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
+}
+
+// Lanes a row of the gradient of short rows.
+int narrow_lanes(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
+
+template <int G>
+void launch_narrow(const NormArgs &a, int parts, cudaStream_t st)
+{
+    if (a.res_kind == 2)
+        rms_norm_backward_narrow_kernel<G, 2><<<parts, kNarrowThreads, 0, st>>>(a);
+    else
+        rms_norm_backward_narrow_kernel<G, 1><<<parts, kNarrowThreads, 0, st>>>(a);
 }
 
 // The ring of a gradient CTA: as many stages as its part of an SM's shared memory
@@ -524,6 +661,8 @@ int launch_rms_norm(const NormArgs &a, cudaStream_t st)
 int norm_parts(long long rows, int D)
 {
     const int most = 148 * gradient_ctas(D);
+    const int per = D <= kNarrowWidth ? kNarrowThreads / narrow_lanes(D) : 1;  // rows a CTA takes at a time
+    rows = (rows + per - 1) / per;
     return static_cast<int>(rows < most ? rows : most);
 }
 
@@ -531,9 +670,17 @@ int launch_rms_norm_backward(const NormArgs &a, cudaStream_t st)
 {
     const NormShape s = gradient_shape(a.D);
     const int parts = norm_parts(a.rows, a.D);
-    const int rc = s.vpt == 1   ? backward_r<1>(a, parts, s.threads, st)
-                   : s.vpt == 2 ? backward_r<2>(a, parts, s.threads, st)
-                                : backward_r<4>(a, parts, s.threads, st);
+    int rc = 0;
+    if (a.D > kNarrowWidth)
+        rc = s.vpt == 1   ? backward_r<1>(a, parts, s.threads, st)
+             : s.vpt == 2 ? backward_r<2>(a, parts, s.threads, st)
+                          : backward_r<4>(a, parts, s.threads, st);
+    else if (narrow_lanes(a.D) == 8)
+        launch_narrow<8>(a, parts, st);
+    else if (narrow_lanes(a.D) == 16)
+        launch_narrow<16>(a, parts, st);
+    else
+        launch_narrow<32>(a, parts, st);
     if (rc < 0) return rc;
     norm_weight_sum_kernel<<<(a.D + 31) / 32, 1024, 0, st>>>(a.partial, parts, a.D, a.dweight);
     HYENA_TRY(cudaGetLastError(), "rms norm gradient launch");
