@@ -8,7 +8,7 @@
 // Gradient, with n = h rstd and t = weight dy:
 //   dh = rstd (t - n mean(t n)) + dresidual_out;  dweight = sum over rows dy n
 //
-// Forward: a CTA a row (a warp, up to 256 channels) holds it in registers
+// Forward: a CTA a row (8 to 32 lanes, up to 256 channels) holds it in registers
 // between the reduction and the output, so every input is read once; thread i of
 // T owns the 8-channel vectors i, i + T, ...  HBM-bound: 32768 rows of 4096
 // channels with a bf16 residual take 168 us, 99% of the measured copy bandwidth;
@@ -25,7 +25,7 @@ namespace {
 constexpr int kNormThreads = 512;  // most threads of a row
 constexpr int kNormStages = 6;     // most stages of the gradient's ring
 constexpr int kNormSmem = 200 * 1024;
-constexpr int kNarrowWidth = 256;    // widest row that the gradient takes by lanes of a warp
+constexpr int kNarrowWidth = 256;    // widest row that lanes of one warp take
 constexpr int kNarrowThreads = 256;
 constexpr int kNarrowTurns = 3;
 constexpr int kNarrowCtas = 2;  // an SM, by its registers
@@ -155,14 +155,16 @@ __device__ __forceinline__ void load_weight(float (&v)[8], const void *p, bool b
         load_f32x8(v, static_cast<const float *>(p) + c);
 }
 
-// Sum over the CTA, the same bits in every thread: by butterfly within the warps
-// and again over the warps' sums (16 at most).  `part` is used by one call only.
+// Sum over a row's threads, the blockDim.x of a CTA (or, below 32, of neighbouring
+// lanes), the same bits in every thread: by butterfly within the warps and again
+// over the warps' sums (16 at most).  `part` is used by one call only.
 __device__ __forceinline__ float block_sum(float v, float *part)
 {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
+    for (int d = 16; d > 0; d >>= 1)
+        if (d < static_cast<int>(blockDim.x)) v += __shfl_xor_sync(kFullMask, v, d);
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
+    if (warps <= 1) return v;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     const int w = threadIdx.x & 15;
@@ -172,12 +174,18 @@ __device__ __forceinline__ float block_sum(float v, float *part)
     return v;
 }
 
-// Largest absolute value over the CTA as its bits: as unsigned numbers the bits
+// Largest absolute value over a row's threads as its bits: as unsigned numbers the bits
 // order as the values, and a NaN's are the largest, so that it shows.
 __device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *part)
 {
-    v = __reduce_max_sync(kFullMask, v);
     const int warps = blockDim.x >> 5;
+    if (warps == 0) {
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1)
+            if (d < static_cast<int>(blockDim.x)) v = max(v, __shfl_xor_sync(kFullMask, v, d));
+        return v;
+    }
+    v = __reduce_max_sync(kFullMask, v);
     if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -212,15 +220,15 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
     __shared__ float sum_part[32];
     __shared__ unsigned int max_part[32];
     const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (row >= A.rows) return;  // with several rows a CTA, which are a warp each
     const int T = blockDim.x;
+    const int width = row < A.rows ? A.D : 0;  // none for what is over in the last of several rows' CTAs
     const uint16_t *x = A.x + row * A.ld_x;
     float h[VPT][8];
     float sq = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
-        if (c < A.D) {
+        if (c < width) {
             load_bf16x8(h[k], x + c);
             if constexpr (R != 0) {
                 float r[8];
@@ -249,13 +257,13 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
         for (int i = 0; i < 8; ++i) sq = __fmaf_rn(h[k][i], h[k][i], sq);
     }
     const float rstd = __frsqrt_rn(block_sum(sq, sum_part) / static_cast<float>(A.D) + A.eps);
-    if (A.rstd && threadIdx.x == 0) A.rstd[row] = rstd;
+    if (A.rstd && threadIdx.x == 0 && width) A.rstd[row] = rstd;
     unsigned int amax[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
         float w[8];
-        if (c < A.D) {
+        if (c < width) {
             load_weight(w, A.weight, A.weight_bf16, c);
         } else {
 #pragma unroll
@@ -268,18 +276,18 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
             if constexpr (Q != 0) amax[k] = max(amax[k], __float_as_uint(h[k][i]) & 0x7fffffffu);
         }
         if constexpr (Q == 0) {
-            if (c < A.D) store_bf16x8(A.y + row * A.ld_y + c, h[k]);
+            if (c < width) store_bf16x8(A.y + row * A.ld_y + c, h[k]);
         }
     }
     if constexpr (Q == 1) {
 #pragma unroll
         for (int k = 1; k < VPT; ++k) amax[0] = max(amax[0], amax[k]);
         const float scale = scale_of(block_max(amax[0], max_part));
-        if (threadIdx.x == 0) A.scales[row] = scale;
+        if (threadIdx.x == 0 && width) A.scales[row] = scale;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
-            if (c < A.D) store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
+            if (c < width) store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
         }
     } else if constexpr (Q == 2) {
         const int groups = (A.D + 127) / 128;
@@ -287,10 +295,11 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
         for (int k = 0; k < VPT; ++k) {
             unsigned int m = amax[k];
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, d));
+            for (int d = 8; d > 0; d >>= 1)
+                if (d < T) m = max(m, __shfl_xor_sync(kFullMask, m, d));
             const float scale = scale_of(m);
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
-            if (c < A.D) {
+            if (c < width) {
                 if ((threadIdx.x & 15) == 0) A.scales[row * groups + c / 128] = scale;
                 store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
             }
@@ -545,6 +554,9 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float *part
     if (lane == 0 && out < D) dweight[out] = static_cast<float>(v);
 }
 
+// Threads of a row of up to kNarrowWidth channels.
+int narrow_lanes(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
+
 // Vectors per thread and threads of a row of D channels.
 struct NormShape {
     int vpt, threads;
@@ -554,14 +566,17 @@ NormShape norm_shape(int D)
 {
     const int v = D / 8;
     const int vpt = v <= 256 ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
+    if (D <= kNarrowWidth) return {1, narrow_lanes(D)};
     return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
 }
 
 template <int VPT, int Q>
 void forward_r(const NormArgs &a, int threads, cudaStream_t st)
 {
-    // Rows of one warp go eight to a CTA where there are enough of them
-    const unsigned int per = threads == 32 && a.rows >= 8 * 148 ? 8 : 1;
+    // Short rows go as many to a CTA as fill 256 threads where there are enough of
+    // them, else as fill a warp
+    const unsigned int most = threads <= 32 ? 256 / threads : 1, least = threads < 32 ? 32 / threads : 1;
+    const unsigned int per = a.rows >= 148ll * most ? most : least;
     const unsigned int grid = static_cast<unsigned int>((a.rows + per - 1) / per);
     const dim3 block(threads, per);
     switch (a.residual ? a.res_kind : 0) {
@@ -598,9 +613,6 @@ NormShape gradient_shape(int D)
     const int vpt = v <= kNormThreads ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
     return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
 }
-
-// Lanes a row of the gradient of short rows.
-int narrow_lanes(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
 
 template <int G>
 void launch_narrow(const NormArgs &a, int parts, cudaStream_t st)
