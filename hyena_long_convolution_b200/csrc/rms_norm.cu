@@ -557,16 +557,20 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float *part
 // Threads of a row of up to kNarrowWidth channels.
 int narrow_lanes(int D) { return D <= 64 ? 8 : (D <= 128 ? 16 : 32); }
 
-// Vectors per thread and threads of a row of D channels.
+// Vectors per thread and threads of a row of D channels.  Without a residual a
+// row's own loads are few, and up to 1024 channels a warp a row, eight to a CTA,
+// hides them better (131072 x 512 72 -> 47 us, 65536 x 1024 57 -> 47); with one the
+// warps' registers then hold too much (65536 x 1024 82 -> 97).
 struct NormShape {
     int vpt, threads;
 };
 
-NormShape norm_shape(int D)
+NormShape norm_shape(int D, bool residual)
 {
     const int v = D / 8;
     const int vpt = v <= 256 ? 1 : (v <= 2 * kNormThreads ? 2 : 4);
     if (D <= kNarrowWidth) return {1, narrow_lanes(D)};
+    if (!residual && D <= 1024) return {D <= 512 ? 2 : 4, 32};
     return {vpt, ((v + vpt - 1) / vpt + 31) / 32 * 32};
 }
 
@@ -659,7 +663,7 @@ int backward_r(const NormArgs &a, int parts, int threads, cudaStream_t st)
 
 int launch_rms_norm(const NormArgs &a, cudaStream_t st)
 {
-    const NormShape s = norm_shape(a.D);
+    const NormShape s = norm_shape(a.D, a.residual != nullptr);
     if (s.vpt == 1)
         forward_q<1>(a, s.threads, st);
     else if (s.vpt == 2)

@@ -58,7 +58,7 @@ def check_fp8(q, s, h, w, group):
 @pytest.mark.parametrize("res", [None, "bf16", "fp32"])
 @pytest.mark.parametrize("M,D", [(1, 8), (3, 64), (2, 72), (33, 128), (5, 136), (1, 256), (2, 264), (7, 1032),
                                  (1, 2048), (2, 2056), (3, 4096), (2, 8200), (1, 16384), (601, 40),
-                                 (30001, 64), (15001, 128), (7501, 200)])
+                                 (30001, 64), (15001, 128), (7501, 200), (1301, 512), (1301, 1000)])
 def test_matches_oracle(M, D, res, weight):
     import torch
     import hyena_long_convolution_b200 as hy
