@@ -4,7 +4,7 @@
 //   h = x + residual, rounded to the residual's type (or h = x)
 //   rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd weight
 //   bf16: y rounded once.  e4m3: for each row (or each 128 channels of it)
-//   scale = max(max|y|, 2^-100) / 448, q = y / scale rounded once.
+//   scale = max(max|y|, 2^-100) / 448, q = the fp32 quotient y / scale, rounded.
 // Gradient, with n = h rstd and t = weight dy:
 //   dh = rstd (t - n mean(t n)) + dresidual_out;  dweight = sum over rows dy n
 //
@@ -200,12 +200,41 @@ __device__ __forceinline__ float scale_of(unsigned int amax_bits)
     return a < kAmaxFloor ? kAmaxFloor / kE4m3Max : a / kE4m3Max;  // NaN stays
 }
 
-__device__ __forceinline__ void store_e4m3x8(uint8_t *p, const float (&v)[8], float inv)
+// The codes of the fp32 quotients v / scale.  The product with the rounded
+// reciprocal is up to two units in the last place off, the other code next to the
+// border of two; one step with its remainder v - z scale (Markstein, 1990), which
+// one FMA forms, puts every z at, above or below a border as the quotient is: all
+// 2^23 significands of a scale, with the 13 values of v around each border, give
+// the same.  It costs 2 to 15% (8192 x 4096 with a bf16 residual 52 -> 55 us, 65536 x
+// 1024 without one 50 -> 57), division 22% (32768 x 4096 without one 139 -> 169).
+// kPairs: in packed arithmetic, which takes 132 us there where one value at a time
+// takes 151, but holds registers that cost a CTA an SM with a bf16 residual (8192 x
+// 4096 with one scale per row: 61) and with four vectors a thread (65536 x 1024: 61).
+template <bool kPairs>
+__device__ __forceinline__ void store_e4m3x8(uint8_t *p, float (&v)[8], float scale)
 {
+    if (scale < 0x1p-60f) {  // the same quotients, with no subnormal remainder
+        scale *= 0x1p+64f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= 0x1p+64f;
+    }
+    const float inv = 1.f / scale;
+    const bool step = scale < INFINITY;  // else the product: 0, NaN of an Inf, NaN
     unsigned short h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = make_float2(v[2 * i], v[2 * i + 1]);
+        float2 z;
+        if constexpr (kPairs) {
+            z = __fmul2_rn(y, bcast2(inv));
+            if (step) z = __ffma2_rn(__ffma2_rn(z, bcast2(-scale), y), bcast2(inv), z);
+        } else {
+            z = make_float2(y.x * inv, y.y * inv);
+            if (step) z.x = __fmaf_rn(__fmaf_rn(z.x, -scale, y.x), inv, z.x);
+            if (step) z.y = __fmaf_rn(__fmaf_rn(z.y, -scale, y.y), inv, z.y);
+        }
+        h[i] = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+    }
     uint2 q;
     q.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
     q.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
@@ -287,7 +316,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
-            if (c < width) store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
+            if (c < width) store_e4m3x8<VPT <= 2 && R != 1>(A.q + row * A.ld_y + c, h[k], scale);
         }
     } else if constexpr (Q == 2) {
         const int groups = (A.D + 127) / 128;
@@ -301,7 +330,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs A
             const int c = 8 * (static_cast<int>(threadIdx.x) + k * T);
             if (c < width) {
                 if ((threadIdx.x & 15) == 0) A.scales[row * groups + c / 128] = scale;
-                store_e4m3x8(A.q + row * A.ld_y + c, h[k], 1.f / scale);
+                store_e4m3x8<VPT <= 2 && R != 1>(A.q + row * A.ld_y + c, h[k], scale);
             }
         }
     }

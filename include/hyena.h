@@ -606,7 +606,8 @@ hyena_status_t hyena_rms_norm(const hyena_bf16_t *x, int64_t ld_x,
 
 /*
  * The same with y as e4m3 codes (one byte each, row stride ld_q a multiple of
- * 8) and scales: q = y / scale rounded to nearest, y ~ q scale, where scale =
+ * 8) and scales: q = the fp32 quotient y / scale rounded to nearest, ties to
+ * even, y ~ q scale, where scale =
  * max(max|y|, 2^-100) / 448 over the row (group = 0, scales [rows]) or over
  * each 128 channels of it (group = 128, scales [rows, ceil(D / 128)]).  The
  * maximum is taken of the unrounded y; a NaN or Inf among it shows in the
