@@ -380,12 +380,13 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
         const float2 E = carry<true>(P, C, a);
         if (!last) rec.publish_carry(t.j, E);
         carry_in[lane] = C;
+        // `freed` of the tile before is looked at before `carried`: it is complete, as a
+        // warp frees that tile before it adds its sums of this one, and from `carried` on
+        // the warps may complete this tile's too, whose parity is that of none before
+        if (!asked) pipe.wait(&pipe.freed, it - 1);
         pipe.arrive(&pipe.carried, lane);
         work.known(t, C, E);
-        if (!asked) {
-            pipe.wait(&pipe.freed, it - 1);
-            ask();
-        }
+        if (!asked) ask();
         before = t;
     }
     if (lane == 0) finish(A);
