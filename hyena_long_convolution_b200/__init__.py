@@ -131,6 +131,32 @@ def _f32(t, shape, name, allow_none=True):
     return t
 
 
+def _current(stream):
+    """Makes a given stream (a torch Stream or a raw handle) the current one, so
+    that what the call allocates belongs to it as well."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _zeroed(n, device, stream):
+    """n zero bytes of device memory, taken and cleared on one stream (the given
+    one, else the device's current one): taken on another, they may be a block
+    that work still pending there writes to after the clearing."""
+    torch = _torch()
+    if device is None and isinstance(stream, torch.cuda.Stream):
+        device = stream.device
+    with torch.cuda.device(device):
+        here = torch.cuda.current_device()
+        with torch.cuda.stream(None) if stream is None else _current(stream):
+            if torch.cuda.current_device() != here:
+                raise ValueError("the stream belongs to another device")
+            buf = torch.empty(n, dtype=torch.uint8, device="cuda")
+            check("hyena_modal_workspace_init", lib().hyena_modal_workspace_init(_ptr(buf), n, _stream(None)))
+    return buf
+
+
 def last_launch_count() -> int:
     """Kernels/memsets enqueued by the most recent call on this thread."""
     return int(lib().hyena_last_launch_count())
@@ -144,14 +170,11 @@ class ModalWorkspace:
     """Device workspace for modal_long_conv, zero-filled once at creation."""
 
     def __init__(self, B: int, D: int, N: int, device=None, stream=None):
-        torch = _torch()
         n = workspace_size(B, D, N)
         if n == 0:
             raise ValueError("invalid workspace shape")
         self.nbytes = n
-        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        check("hyena_modal_workspace_init",
-              lib().hyena_modal_workspace_init(_ptr(self.buf), n, _stream(stream)))
+        self.buf = _zeroed(n, device, stream)
 
     def fits(self, B: int, D: int, N: int) -> bool:
         return workspace_size(B, D, N) <= self.nbytes
@@ -263,14 +286,11 @@ class HostWorkspace:
     staging slots of `chunk` tokens and the carried state), zero-filled once."""
 
     def __init__(self, B: int, D: int, N: int, chunk: int = 2048, device=None, stream=None):
-        torch = _torch()
         n = int(lib().hyena_modal_host_workspace_size(B, D, N, chunk))
         if n == 0:
             raise ValueError("invalid host-workspace shape (chunk must be a positive multiple of 128)")
         self.nbytes, self.chunk = n, chunk
-        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        check("hyena_modal_workspace_init",
-              lib().hyena_modal_workspace_init(_ptr(self.buf), n, _stream(stream)))
+        self.buf = _zeroed(n, device, stream)
 
 
 def modal_long_conv_host(x1, x2, x3, log_poles, residues, Dskip=None, y=None, state_in=None,
@@ -692,15 +712,6 @@ def _here(x, *others):
     return C._cuda_getCurrentRawStream(dev)
 
 
-def _current(stream):
-    """Makes a given stream (a torch Stream or a raw handle) the current one, so
-    that what the call allocates belongs to it as well."""
-    torch = _torch()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
 def _like(x, shape, st, ld, name):
     """Row stride of a bf16 [B, L, D] tensor of the given shape, as _bld (the
     device is checked by _here); the usual case, the stride of a tensor whose
@@ -737,14 +748,11 @@ class RecurrenceWorkspace:
     to L tokens, zero-filled once at creation."""
 
     def __init__(self, B: int, L: int, D: int, device=None, stream=None):
-        torch = _torch()
         n = int(lib().hyena_gated_recurrence_workspace_size(B, L, D))
         if n == 0:
             raise ValueError("invalid workspace shape")
         self.nbytes = n
-        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        check("hyena_modal_workspace_init",
-              lib().hyena_modal_workspace_init(_ptr(self.buf), n, _stream(stream)))
+        self.buf = _zeroed(n, device, stream)
 
 
 def recurrence_unit_states(B: int, L: int, D: int, device=None):
