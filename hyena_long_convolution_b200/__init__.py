@@ -773,6 +773,10 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     state_in/state_out: [B, D] fp32 or None (may be the same tensor);
     unit_states: from recurrence_unit_states, filled for the backward call.
     Returns y ([B, L, D] bf16, allocated if not given).
+
+    A device wait that ran out leaves NaN and is reported by workspace_check;
+    a call without a ``workspace`` uses one of its own, so that the NaN are all
+    that shows it.
     """
     if stream is not None:
         with _current(stream):

@@ -372,7 +372,7 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
             if (t0 == 0) t0 = now;
             if (!found && __any_sync(kFullMask, now - t0 > kWaitLimitNs)) {
                 if (lane == 0) atomicOr(pipe.error, kErrLookbackTimeout);
-                C = bcast2(0.f);
+                C = bcast2(__int_as_float(0x7fffffff));
                 found = true;
                 if (summed) break;
             }

@@ -516,7 +516,8 @@ hyena_status_t hyena_modal_state_init(float *state, int B, int D, int N, void *s
  *           calls sharing it must not overlap in time.
  * Chunks of whole units reproduce the single pass bit for bit.  L == 0 is
  * valid: state_out receives state_in (or zeros).  Device-side waits are
- * bounded; hyena_workspace_check reports one that ran out.
+ * bounded: hyena_workspace_check reports one that ran out, and the outputs
+ * that it leaves undetermined (of the gradient as well) are NaN.
  */
 #define HYENA_RECURRENCE_UNIT 64
 
