@@ -296,13 +296,27 @@ struct Pipeline {
         fence_mbar_init();
         for (int s = 0; s < kStages; ++s) request(m, A, stages, s, tile_of(A, next_tile(A, s)));
     }
-    // Longer than a look-back waits, so that one that gives up does not put the
-    // CTA's own warps out of step.
-    __device__ __forceinline__ void wait(uint64_t *bar, int turn)
+    // By a whole warp.  Longer than a look-back waits, so that one that gives up does
+    // not put the CTA's own warps out of step; false if the wait ran out.  The warp
+    // then has to leave: no barrier that it counts for completes again, so that none
+    // is taken for a later phase, and the others' waits run out as well.
+    __device__ __forceinline__ bool wait(uint64_t *bar, int turn)
     {
-        for (int i = 0; i < 4; ++i)
-            if (mbar_wait_bounded(bar, turn & 1)) return;
+        if (__all_sync(kFullMask, mbar_try_wait(bar, turn & 1))) return true;
+        const unsigned long long t0 = global_timer_ns();
+        for (;;) {
+            if (__all_sync(kFullMask, mbar_try_wait(bar, turn & 1))) return true;
+            const unsigned long long t = global_timer_ns() - t0;
+            if (__any_sync(kFullMask, t > 4 * kWaitLimitNs)) break;
+        }
         atomicOr(error, kErrLocalTimeout);
+        return false;
+    }
+    // A computing warp's wait.  (A return value that its loops test took the forward
+    // of 8 x 4096 x 4096 from 223 to 227 us.)
+    __device__ __forceinline__ void wait_or_leave(uint64_t *bar, int turn)
+    {
+        if (!wait(bar, turn)) asm volatile("exit;");
     }
     // This warp's part of a barrier that counts warps.
     __device__ __forceinline__ void arrive(uint64_t *bar, int lane)
@@ -321,26 +335,35 @@ constexpr int kThreads = (RWARPS + 1) * 32;
 //   sums()       from the segments' sums of tile t: P and A of its unit
 //   initial(c)   the carry into the first unit;  known(t, C, E)  what else to
 //                write once the carry C into the unit and E behind it are known
-//   parts(t, s)  once tile t in stage s is done
+//   parts(t, s)  once tile t in stage s is done;  lost(t)  in a tile's place
+// What a wait that runs out leaves behind is NaN, so that no result passes for
+// one.  Behind a carry that was not found: all that it reaches.  Where a wait for
+// the CTA's own warps or copies ran out: the CTA's tiles from then on; rows that
+// one of its warps writes meanwhile are right (it left if its own wait had failed).
 template <int N, bool kBack, class Work>
 __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const RecMaps &maps, const RecArgs &A,
                                              unsigned char *stages, float2 *carry_in, int lane, Work work)
 {
+    const float nan = __int_as_float(0x7fffffff);
     Records rec{A.records, A.chains, 0, lane, 0u};
     if (A.units > 1) rec.epoch = *reinterpret_cast<const volatile unsigned long long *>(A.hdr + kRecEpoch) + 1u;
     Tile before{};
-    for (int it = 0;; ++it) {
+    unsigned int next = ~0u;  // the ticket of the tile after the stages'
+    bool asked = true;
+    int it = 0;
+    for (;; ++it) {
         const int st = it % kStages;
         const Tile t = pipe.tile[st];
+        asked = it == 0;
         if (t.j < 0) {
             if (it > 0) {
-                pipe.wait(&pipe.freed, it - 1);
+                if (!pipe.wait(&pipe.freed, it - 1)) break;
                 work.parts(before, st ^ 1);
             }
-            break;
+            if (lane == 0) finish(A);
+            return;
         }
-        unsigned int next = 0;
-        bool asked = it == 0, summed = false, found = t.j == 0;
+        bool summed = false, found = t.j == 0;
         if (!asked && lane == 0) next = next_tile(A, it + 1);
         const auto ask = [&] {  // the tile before is done: its stage takes the next one's rows
             work.parts(before, st ^ 1);
@@ -353,13 +376,14 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
         rec.chain = t.chain;
         const Records::Spot spot = rec.spot(t.j);
         unsigned long long t0 = 0;
+        bool ok = true;
         for (;;) {
             // the glance's load is under way while the CTA's own barriers are looked at
             Records::Glance seen{};
             if (!found) seen = rec.glance(spot);
             if (!asked && __all_sync(kFullMask, mbar_test_wait(&pipe.freed, (it - 1) & 1))) ask();
             if (!summed) {
-                if (found) pipe.wait(&pipe.sums, it);
+                if (found && !(ok = pipe.wait(&pipe.sums, it))) break;
                 summed = found || __all_sync(kFullMask, mbar_test_wait(&pipe.sums, it & 1));
                 if (summed) {
                     work.sums(st, P, a);
@@ -372,24 +396,65 @@ __device__ __forceinline__ void control_warp(Pipeline<N, kBack> &pipe, const Rec
             if (t0 == 0) t0 = now;
             if (!found && __any_sync(kFullMask, now - t0 > kWaitLimitNs)) {
                 if (lane == 0) atomicOr(pipe.error, kErrLookbackTimeout);
-                C = bcast2(__int_as_float(0x7fffffff));
+                C = bcast2(nan);
                 found = true;
                 if (summed) break;
             }
         }
+        if (!ok) break;
         const float2 E = carry<true>(P, C, a);
         if (!last) rec.publish_carry(t.j, E);
         carry_in[lane] = C;
         // `freed` of the tile before is looked at before `carried`: it is complete, as a
         // warp frees that tile before it adds its sums of this one, and from `carried` on
         // the warps may complete this tile's too, whose parity is that of none before
-        if (!asked) pipe.wait(&pipe.freed, it - 1);
+        if (!asked && !pipe.wait(&pipe.freed, it - 1)) break;
         pipe.arrive(&pipe.carried, lane);
         work.known(t, C, E);
         if (!asked) ask();
         before = t;
     }
-    if (lane == 0) finish(A);
+    // The CTA is given up: its tiles (both stages', one whose rows were not asked for,
+    // and those that it draws from here on) are lost.  It works from another address of
+    // the arguments, so that no value is held for it through the loop above (which
+    // took the gradient of 1 x 32768 x 4096 from 514 to 534 us).
+    const RecArgs *args = &A;
+    asm volatile("" : "+l"(args));
+    const Work cold = work.on(*args);
+    Records gone{args->records, args->chains, 0, lane, rec.epoch};
+    const int st = it % kStages, other = asked ? it + 1 : it - 1;
+    mbar_wait_bounded(&pipe.full[st], it / kStages & 1);  // its copies are over
+    if (other >= 0) mbar_wait_bounded(&pipe.full[st ^ 1], other / kStages & 1);
+    __syncwarp();
+#pragma unroll 1
+    for (int k = asked ? 1 : 0, turn = it + 2;; ++k) {  // next; the stages'; from there on
+        Tile t;
+        if (k == 1 || k == 2) {
+            t = pipe.tile[k - 1];
+        } else {
+            if (k > 2 && lane == 0) next = next_tile(*args, turn++);
+            t = tile_of(*args, __shfl_sync(kFullMask, next, 0));
+        }
+        if (t.j < 0 && k > 2) break;
+        if (t.j < 0) continue;
+        gone.chain = t.chain;
+        gone.publish_carry(t.j, bcast2(nan));
+        cold.known(t, bcast2(nan), bcast2(nan));
+        cold.lost(t);
+    }
+    if (lane == 0) finish(*args);
+}
+
+// NaN in the rows of a unit of a bf16 tensor, by one warp: a lane its channel
+// pair.
+__device__ __forceinline__ void lose_rows(uint16_t *p, long long ld, const RecArgs &A, const Tile &t, int unit,
+                                          int lane)
+{
+    const int c = t.c + 2 * lane;
+    if (c >= A.D) return;
+    p += (static_cast<long long>(t.b) * A.L + unit * RT) * ld + c;
+#pragma unroll 1
+    for (int i = 0; i < min(A.L - unit * RT, RT); ++i, p += ld) *reinterpret_cast<uint32_t *>(p) = 0x7fff7fffu;
 }
 
 // ---------------------------------------------------------------- forward
@@ -434,7 +499,7 @@ __device__ __forceinline__ void forward_tile(ForwardShared &sh, const RecArgs &A
     own.A[lane] = segment_end<kReset>(a, u, mask);
     fence_proxy_async_smem();  // before the stage's next rows
     sh.pipe.arrive(&sh.pipe.sums, lane);
-    sh.pipe.wait(&sh.pipe.carried, it);
+    sh.pipe.wait_or_leave(&sh.pipe.carried, it);
     float2 C = sh.C[lane];
 #pragma unroll
     for (int w = 0; w < RWARPS - 1; ++w) {
@@ -497,11 +562,13 @@ struct ForwardWork {
             *reinterpret_cast<float2 *>(A.state_out + state(t)) = E;
     }
     __device__ __forceinline__ void parts(Tile, int) const {}
+    __device__ __forceinline__ ForwardWork on(const RecArgs &a) const { return {a, stages, lane}; }
+    __device__ __forceinline__ void lost(Tile t) const { lose_rows(A.y, A.ld_y, A, t, t.j, lane); }
 };
 
 template <bool kNorm, bool kReset>
 __global__ void __launch_bounds__(kThreads, 3)
-    recurrence_kernel(const __grid_constant__ RecMaps maps, const RecArgs A)
+    recurrence_kernel(const __grid_constant__ RecMaps maps, const __grid_constant__ RecArgs A)
 {
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ ForwardShared sh;
@@ -514,11 +581,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     for (int it = 0;; ++it) {
         const int st = it % kStages;
-        sh.pipe.wait(&sh.pipe.full[st], it / kStages);
+        sh.pipe.wait_or_leave(&sh.pipe.full[st], it / kStages);
         const Tile t = sh.pipe.tile[st];
-        if (t.j < 0) {
-            break;
-        }
+        if (t.j < 0) break;
         unsigned char *stage = stages + st * sh.pipe.kBytes;
         const int n = min(A.L - t.j * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
         const unsigned int mask =
@@ -562,7 +627,7 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, const RecArgs 
     sh.Q[st][warp][lane] = segment_left<kReset>(a, x3, dy, mask);
     sh.pipe.arrive(&sh.pipe.sums, lane);
     // the state before each token, while the carry from the right is found
-    sh.pipe.wait(&sh.pipe.sums, it);
+    sh.pipe.wait_or_leave(&sh.pipe.sums, it);
     float2 S = param(params, 2, lane);
 #pragma unroll
     for (int k = 0; k < RWARPS - 1; ++k)
@@ -573,7 +638,7 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, const RecArgs 
         prev[i] = S;
         S = s;
     }
-    sh.pipe.wait(&sh.pipe.carried, it);
+    sh.pipe.wait_or_leave(&sh.pipe.carried, it);
     const float2 dsk = skip ? param(params, 1, lane) : bcast2(0.f);
     float2 e = sh.E[lane], d_rate = bcast2(0.f), d_skip = bcast2(0.f);
 #pragma unroll
@@ -676,11 +741,24 @@ struct BackwardWork {
         store_record(u + kRecP * (RCH / 2), d_rate, 0u);
         store_record(u + kRecA * (RCH / 2), d_skip, 0u);
     }
+    __device__ __forceinline__ BackwardWork on(const RecArgs &a) const { return {a, sh, lane}; }
+    __device__ __forceinline__ void lost(Tile t) const
+    {
+        const int unit = A.units - 1 - t.j;
+        uint16_t *const rows[] = {A.dx1, A.dx2, A.dx3};
+    #pragma unroll 1
+        for (int k = 0; k < 3; ++k) lose_rows(rows[k], A.ld_dx, A, t, unit, lane);
+        lose_rows(A.dgate, A.ld_dg, A, t, unit, lane);
+        const float2 nan = bcast2(__int_as_float(0x7fffffff));
+        uint4 *u = A.records + (static_cast<size_t>(t.j) * A.chains + t.chain) * (3 * RCH / 2) + lane;
+        store_record(u + kRecP * (RCH / 2), nan, 0u);
+        store_record(u + kRecA * (RCH / 2), nan, 0u);
+    }
 };
 
 template <bool kNorm, bool kReset>
 __global__ void __launch_bounds__(kThreads, 2)
-    recurrence_backward_kernel(const __grid_constant__ RecMaps maps, const RecArgs A)
+    recurrence_backward_kernel(const __grid_constant__ RecMaps maps, const __grid_constant__ RecArgs A)
 {
     extern __shared__ __align__(128) unsigned char stages[];
     __shared__ BackwardShared sh;
@@ -693,11 +771,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int it = 0;; ++it) {
         const int st = it % kStages;
-        sh.pipe.wait(&sh.pipe.full[st], it / kStages);
+        sh.pipe.wait_or_leave(&sh.pipe.full[st], it / kStages);
         const Tile t = sh.pipe.tile[st];
-        if (t.j < 0) {
-            break;
-        }
+        if (t.j < 0) break;
         unsigned char *stage = stages + st * sh.pipe.kBytes;
         const int unit = A.units - 1 - t.j;
         const int n = min(A.L - unit * RT - warp * RSEG, RSEG);  // tokens of the segment; it may have none
