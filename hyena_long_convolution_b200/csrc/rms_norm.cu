@@ -391,10 +391,15 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
     __syncthreads();
     int s = 0, turn = 0;  // stage, and how often the ring has gone round
     long long behind = blockIdx.x + static_cast<long long>(S - 1) * gridDim.x;  // the newest row asked for
+    // A copy that does not come within the wait's limit: no result is passed off from
+    // there on.  One thread's NaN reaches all of a row by its sum.
+    bool lost = false;
     for (long long row = blockIdx.x, i = 0; row < A.rows; row += gridDim.x, ++i) {
-        const float rstd = A.rstd_in[row];
-        if (!mbar_wait_bounded(&full[s], turn & 1))
-            dw[0][0].x = __int_as_float(0x7fc00000);  // a copy that never came is not passed off as a result
+        float rstd = A.rstd_in[row];
+        if (lost || !mbar_wait_bounded(&full[s], turn & 1)) {
+            lost = true;
+            rstd = __int_as_float(0x7fffffff);
+        }
         const unsigned char *st = stages + s * stage_bytes;
         const uint16_t *dy = reinterpret_cast<const uint16_t *>(st);
         const unsigned char *h = st + dy_bytes;
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
         // behind the reduction every thread is through with the row before
         if (i > 0) {
             behind += gridDim.x;
-            if (threadIdx.x == 0 && behind < A.rows) request(behind, s == 0 ? S - 1 : s - 1);
+            if (threadIdx.x == 0 && !lost && behind < A.rows) request(behind, s == 0 ? S - 1 : s - 1);
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
