@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas) rms_norm_backward
 {
     constexpr int kRows = 32 / G;
     constexpr int kTurns = kNarrowTurns;
-    __shared__ float part[kNarrowThreads / 32][8 * G];
+    __shared__ __align__(16) float part[kNarrowThreads / 32][8 * G];  // stored four at a time
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / G, c = 8 * (lane % G);
     const bool live = c < A.D;
