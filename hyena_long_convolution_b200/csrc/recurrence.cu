@@ -681,7 +681,8 @@ __device__ __forceinline__ void backward_tile(BackwardShared &sh, const RecArgs 
             if (cut) dl = e = bcast2(0.f);
             float2 eg;
             const float2 sig = gate_sigmoid(bf16x2_to_float2(gate(i)), eg);
-            d_rate = __ffma2_rn(dl, sig, d_rate);
+            // not behind the end: dl there is finite only where the last state is
+            if (decltype(whole)::value || i < n) d_rate = __ffma2_rn(dl, sig, d_rate);
             d_skip = __ffma2_rn(d, v, d_skip);
             // sig' = sig (1 - sig), with 1 - sig = exp(-gate) sig; 0 where the exponential overflows
             eg = make_float2(fminf(eg.x, 1e38f), fminf(eg.y, 1e38f));
