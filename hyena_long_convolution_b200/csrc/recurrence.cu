@@ -303,11 +303,14 @@ struct Pipeline {
     __device__ __forceinline__ bool wait(uint64_t *bar, int turn)
     {
         if (__all_sync(kFullMask, mbar_try_wait(bar, turn & 1))) return true;
-        const unsigned long long t0 = global_timer_ns();
-        for (;;) {
+        unsigned long long t0 = global_timer_ns();
+        for (int left = 4; left > 0;) {  // one span that passed while the CTA was suspended is not the end
             if (__all_sync(kFullMask, mbar_try_wait(bar, turn & 1))) return true;
-            const unsigned long long t = global_timer_ns() - t0;
-            if (__any_sync(kFullMask, t > 4 * kWaitLimitNs)) break;
+            const unsigned long long now = global_timer_ns();
+            if (__any_sync(kFullMask, now - t0 > kWaitLimitNs)) {
+                t0 = now;
+                --left;
+            }
         }
         atomicOr(error, kErrLocalTimeout);
         return false;
