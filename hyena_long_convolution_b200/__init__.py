@@ -145,15 +145,19 @@ def _zeroed(n, device, stream):
     one, else the device's current one): taken on another, they may be a block
     that work still pending there writes to after the clearing."""
     torch = _torch()
-    if device is None and isinstance(stream, torch.cuda.Stream):
-        device = stream.device
-    with torch.cuda.device(device):
-        here = torch.cuda.current_device()
-        with torch.cuda.stream(None) if stream is None else _current(stream):
-            if torch.cuda.current_device() != here:
-                raise ValueError("the stream belongs to another device")
-            buf = torch.empty(n, dtype=torch.uint8, device="cuda")
-            check("hyena_modal_workspace_init", lib().hyena_modal_workspace_init(_ptr(buf), n, _stream(None)))
+    if getattr(device, "type", None) == "cuda" and device.index == torch.cuda.current_device():
+        device = None  # the usual case, of a tensor's device
+    if device is not None or stream is not None:
+        if device is None and isinstance(stream, torch.cuda.Stream):
+            device = stream.device
+        with torch.cuda.device(device):
+            here = torch.cuda.current_device()
+            with torch.cuda.stream(None) if stream is None else _current(stream):
+                if torch.cuda.current_device() != here:
+                    raise ValueError("the stream belongs to another device")
+                return _zeroed(n, None, None)
+    buf = torch.empty(n, dtype=torch.uint8, device="cuda")
+    check("hyena_modal_workspace_init", lib().hyena_modal_workspace_init(_ptr(buf), n, _stream(None)))
     return buf
 
 
@@ -804,7 +808,7 @@ def gated_recurrence(x1, x2, x3, gate, log_rate, Dskip=None, reset=None, normali
     else:
         ld_y = _like(y, shape, st, ld, "y")
     if workspace is None:
-        workspace = RecurrenceWorkspace(B, L, D, device=x1.device)
+        workspace = RecurrenceWorkspace(B, L, D)
     rc = lib().hyena_gated_recurrence(x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
                                       log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0,
                                       y.data_ptr(), ld_y, _opt(state_in), _opt(state_out), _opt(unit_states),
@@ -871,7 +875,7 @@ def gated_recurrence_backward(dy, x1, x2, x3, gate, log_rate, Dskip, unit_states
     dlog_rate = torch.empty_like(log_rate)
     dDskip = None if Dskip is None else torch.empty_like(Dskip)
     if workspace is None:
-        workspace = RecurrenceWorkspace(B, L, D, device=x1.device)
+        workspace = RecurrenceWorkspace(B, L, D)
     rc = lib().hyena_gated_recurrence_backward(
         dy.data_ptr(), ld_dy, x1.data_ptr(), x2.data_ptr(), x3.data_ptr(), ld, gate.data_ptr(), ld_g,
         log_rate.data_ptr(), _opt(Dskip), _opt(reset), 1 if normalize else 0, unit_states.data_ptr(),
