@@ -30,13 +30,14 @@
 // performs, so the result does not depend on what was ready.  The gradient runs
 // the same from the right.
 //
-// 10 bytes a channel-token forward, 18 for the gradient, 76 and 140 instructions
-// a channel pair's token: HBM-bound where a device full of CTAs (three an SM forward, two for the
-// gradient, by their registers) is a unit or two a chain, else bound by the
-// carry's way from unit to unit.  B x L x D, of the measured copy bandwidth:
-//   8 x 4096 x 4096   forward 223 us, 94%   gradient 436 us, 86%
-//   2 x 8192 x 4096           142 us, 73%            255 us, 74%
-//   1 x 32768 x 4096          314 us, 66%            524 us, 72%
+// 10 bytes a channel-token forward, 18 for the gradient, 77 and 143 instructions
+// a channel pair's token: HBM-bound where a device full of CTAs (three an SM forward, by
+// their registers, two for the gradient, by its registers and its 106 KB of shared memory
+// each) is a unit or two a chain, else bound by the carry's way from unit to unit.
+// B x L x D, of the measured copy bandwidth (a range: two boards):
+//   8 x 4096 x 4096   forward 223-230 us, 91-94%   gradient 446 us, 84%
+//   2 x 8192 x 4096           142 us, 73%                   252 us, 75%
+//   1 x 32768 x 4096          314-326 us, 64-66%            514 us, 73%
 //   1 x 1024 x 4096            18 us, 36%
 // The tile: 64 channels make rows of 128 bytes (narrower boxes read HBM slower);
 // 64 tokens are 8 a warp, whose a and u stay in registers between the two sweeps.

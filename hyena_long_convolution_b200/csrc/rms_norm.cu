@@ -8,11 +8,12 @@
 // Gradient, with n = h rstd and t = weight dy:
 //   dh = rstd (t - n mean(t n)) + dresidual_out;  dweight = sum over rows dy n
 //
-// Forward: a CTA a row (8 to 32 lanes, up to 256 channels) holds it in registers
-// between the reduction and the output, so every input is read once; thread i of
-// T owns the 8-channel vectors i, i + T, ...  HBM-bound: 32768 rows of 4096
-// channels with a bf16 residual take 168 us, 99% of the measured copy bandwidth;
-// 8192 rows with an fp32 residual and an e4m3 output 63.5 us, 90%.
+// Forward: a CTA a row (up to 256 channels 8 to 32 lanes, up to 1024 without a
+// residual a warp, several rows to a CTA) holds it in registers between the
+// reduction and the output, so every input is read once; thread i of T owns the
+// 8-channel vectors i, i + T, ...  HBM-bound: 32768 rows of 4096 channels with a
+// bf16 residual take 168-173 us, 97-99% of the measured copy bandwidth; 8192 rows
+// with an fp32 residual and an e4m3 output 66-68 us, 85-87%.
 #include <cuda_fp8.h>
 
 #include "layer_device.cuh"
@@ -469,7 +470,8 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_backward_kernel(const N
 // global memory; no row needs the CTA's other warps.  90 us for 524288 x 128 and
 // for 262144 x 256 (83 at the copy bandwidth); by the kernel above, where a short
 // row leaves most lanes idle, 103 and 130.  Registers for three CTAs an SM spill
-// (116 us for 524288 x 128); two turns instead of three take 95 and 99.
+// (116 us for 524288 x 128), those for two 24 bytes at most where G is 8 or 16; two
+// turns instead of three take 95 and 99.
 template <int G, int R>
 __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas) rms_norm_backward_narrow_kernel(const NormArgs A)
 {
@@ -635,9 +637,11 @@ void forward_q(const NormArgs &a, int threads, cudaStream_t st)
         forward_r<VPT, 2>(a, threads, st);
 }
 
-// CTAs of the gradient an SM holds, by their registers and 200 KB of stages (for
-// 16384 x 4096 two took 105 us where three, which do not fit at once, took 119), and
-// in all, no more than rows.
+// CTAs of the gradient an SM, what it holds with a bf16 h by their registers and 200 KB
+// of stages (for 16384 x 4096 two took 105 us where three, which do not fit at once,
+// took 119).  With an fp32 h and dresidual_out two of more than 5120 channels do not
+// fit either and go one after the other: 8192 x 8192 takes 182 us, 92% of the copy
+// bandwidth (16384 x 4096, where two fit, 167 us, 100%).
 int gradient_ctas(int D)
 {
     if (D <= kNarrowWidth) return kNarrowCtas;
@@ -663,7 +667,7 @@ void launch_narrow(const NormArgs &a, int parts, cudaStream_t st)
 
 // The ring of a gradient CTA: as many stages as its part of an SM's shared memory
 // holds, two at least; without dresidual_out where two with it exceed an SM's shared
-// memory (an fp32 one of more than 11K channels).
+// memory (an fp32 one of more than 10240 channels).
 template <int VPT, int R>
 int launch_gradient(NormArgs a, int parts, int threads, cudaStream_t st)
 {
@@ -710,7 +714,7 @@ int launch_rms_norm(const NormArgs &a, cudaStream_t st)
 
 int norm_parts(long long rows, int D)
 {
-    const int most = 148 * gradient_ctas(D);
+    const int most = 148 * gradient_ctas(D);  // the SMs of the one target: the size is asked for without a device
     const int per = D <= kNarrowWidth ? kNarrowThreads / narrow_lanes(D) : 1;  // rows a CTA takes at a time
     rows = (rows + per - 1) / per;
     return static_cast<int>(rows < most ? rows : most);
