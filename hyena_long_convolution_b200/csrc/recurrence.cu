@@ -751,7 +751,7 @@ struct BackwardWork {
     {
         const int unit = A.units - 1 - t.j;
         uint16_t *const rows[] = {A.dx1, A.dx2, A.dx3};
-    #pragma unroll 1
+#pragma unroll 1
         for (int k = 0; k < 3; ++k) lose_rows(rows[k], A.ld_dx, A, t, unit, lane);
         lose_rows(A.dgate, A.ld_dg, A, t, unit, lane);
         const float2 nan = bcast2(__int_as_float(0x7fffffff));
