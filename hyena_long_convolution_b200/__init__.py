@@ -26,11 +26,19 @@ from typing import NamedTuple
 from ._lib import HyenaError, check, lib  # noqa: F401
 
 __all__ = [
+    "FfnGrads",
+    "FfnWorkspace",
     "HyenaError",
+    "MatmulWorkspace",
     "ModalWorkspace",
     "NormGrads",
     "RecurrenceGrads",
     "RecurrenceWorkspace",
+    "fp8_matmul",
+    "fp8_quantize",
+    "gated_ffn",
+    "gated_ffn_backward",
+    "gated_ffn_fp8",
     "gated_recurrence",
     "gated_recurrence_backward",
     "gated_recurrence_decode",
@@ -67,6 +75,7 @@ MAX_COMPLEX_MODES = 32
 MAX_TAPS = 128
 RECURRENCE_UNIT = 64
 MAX_NORM_WIDTH = 16384
+ACTIVATIONS = {"silu": 1, "gelu": 2, "gelu_tanh": 3, "identity": 4}
 
 
 _torch_module = None  # imported by the first call; a statement in each costs it 0.1 us every time
@@ -1090,3 +1099,301 @@ def rms_norm_backward(dy, h, weight, rstd, dresidual_out=None, dx=None, dresidua
                                        workspace.nbytes, here)
     check("hyena_rms_norm_backward", rc)
     return NormGrads(dx, dx if ht == 1 else dresidual, dweight)
+
+
+# ----------------------------------------- 8-bit products, feed-forward block
+
+def _act(name):
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    return code
+
+
+def _mat(t, shape, dtype, name):
+    """Row stride of a [rows, width] tensor with unit stride within a row."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
+    st = t.stride()
+    if st[1] != 1:
+        raise ValueError(f"{name} must be contiguous within its rows")
+    return st[0] if shape[0] > 1 else max(st[0], shape[1])
+
+
+def _pair(a, b, names):
+    """Two weights of one shape and row stride -> (rows, width, ld)."""
+    if len(a.shape) != 2:
+        raise ValueError(f"{names[0]} must be [F, D]")
+    ld = _mat(a, a.shape, a.dtype, names[0])
+    if _mat(b, a.shape, a.dtype, names[1]) != ld:
+        raise ValueError(f"{names[0]} and {names[1]} must share one row stride")
+    return a.shape[0], a.shape[1], ld
+
+
+def _codes(x, x_scales, name):
+    """Codes [M, K] or [B, L, K] with scales [M, 1] or [M, ceil(K / 128)] ->
+    (M, K, ld, group)."""
+    M, K, ld = _rows(x, name, (_torch().float8_e4m3fn,))
+    if M == 1:  # no second row: any stride will do
+        ld = -(-K // 16) * 16
+    groups = -(-K // 128)
+    if x_scales.shape == (M, groups) and groups > 1:
+        group = 128
+    else:  # one scale a row; the same thing where a row is one group
+        group = 0
+        if x_scales.shape != (M, 1):
+            raise ValueError(f"{name}'s scales must be of shape {(M, 1)} or {(M, groups)}")
+    _f32(x_scales, x_scales.shape, f"{name}'s scales", False)
+    return M, K, ld, group
+
+
+def _weight_scales(t, N, K, name):
+    _f32(t, (-(-N // 128), -(-K // 128)), name, False)
+
+
+def _out_rows(t, M, width, dtype, name):
+    """Row stride of a given [M, width] (or [B, L, width]) tensor."""
+    tM, tW, ld = _rows(t, name, (dtype,))
+    if tM != M or tW != width:
+        raise ValueError(f"{name} must be of shape [..., {width}] with {M} rows")
+    return ld
+
+
+def _kept(gate, up, M, F):
+    """(row stride, hyena_dtype_t) of the two kept products."""
+    torch = _torch()
+    if gate is None or up is None:
+        raise ValueError("give both of gate and up or neither")
+    gM, gF, ld = _rows(gate, "gate", (torch.bfloat16, torch.float32))
+    if gM != M or gF != F or _out_rows(up, M, F, gate.dtype, "up") != ld:
+        raise ValueError(f"gate and up must be of shape [..., {F}] with {M} rows, of one type and row stride")
+    return ld, _dtype_code(gate)
+
+
+class MatmulWorkspace:
+    """Device workspace of fp8_matmul for M rows, N outputs and K channels,
+    zero-filled once at creation."""
+
+    def __init__(self, M: int, N: int, K: int, device=None, stream=None):
+        n = int(lib().hyena_fp8_matmul_workspace_size(M, N, K))
+        if n == 0:
+            raise ValueError("invalid workspace shape")
+        self.nbytes = n
+        self.buf = _zeroed(n, device, stream)
+
+
+class FfnWorkspace:
+    """Device workspace of gated_ffn and gated_ffn_fp8 for M rows (with
+    ``backward``, of gated_ffn_backward too), zero-filled once at creation."""
+
+    def __init__(self, M: int, D: int, F: int, backward: bool = False, device=None, stream=None):
+        n = int(lib().hyena_gated_ffn_workspace_size(M, D, F, 1 if backward else 0))
+        if n == 0:
+            raise ValueError("invalid workspace shape")
+        self.nbytes = n
+        self.buf = _zeroed(n, device, stream)
+
+
+def fp8_quantize(x, block=1, q=None, scales=None, stream=None):
+    """e4m3 codes of x ([rows, D] or [B, L, D], bf16 or fp32) with one fp32 scale
+    per row and 128 channels (block = 1, scales [rows, ceil(D / 128)]:
+    activations) or per 128 rows x 128 channels (block = 128, scales
+    [ceil(rows / 128), ceil(D / 128)]: weights): returns (q, scales) with
+    x ~ q scale, q float8_e4m3fn of x's shape."""
+    if stream is not None:
+        with _current(stream):
+            return fp8_quantize(x, block, q, scales)
+    torch = _torch()
+    M, D, ld = _rows(x, "x", (torch.bfloat16, torch.float32))
+    if block not in (1, 128):
+        raise ValueError("block must be 1 (rows of activations) or 128 (blocks of a weight)")
+    here = _here(x, q, scales)
+    if q is None:
+        q, ld_q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), D
+    else:
+        qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
+        if qM != M or qD != D:
+            raise ValueError("q shape differs from x")
+    want = (M if block == 1 else -(-M // 128), -(-D // 128))
+    if scales is None:
+        scales = x.new_empty(want, dtype=torch.float32)
+    else:
+        _f32(scales, want, "scales")
+    rc = lib().hyena_fp8_quantize(x.data_ptr(), ld, _dtype_code(x), q.data_ptr(), ld_q, scales.data_ptr(), block, M, D,
+                                  here)
+    check("hyena_fp8_quantize", rc)
+    return q, scales
+
+
+def fp8_matmul(x, x_scales, weight, weight_scales, y=None, dtype=None, workspace: MatmulWorkspace | None = None,
+               stream=None):
+    """x weight^T of e4m3 tensors with scales, summed in fp32: x [M, K] or
+    [B, L, K] with x_scales [M, 1] or [M, ceil(K / 128)] (as rms_norm_fp8 and
+    fp8_quantize leave them), weight [N, K] with weight_scales
+    [ceil(N / 128), ceil(K / 128)] (fp8_quantize with block = 128).  Returns y
+    ([..., N], bf16 or the given dtype bf16 or fp32, allocated if not given).
+    Row strides of x and weight: multiples of 16.
+
+    A device wait that ran out leaves NaN and is reported by workspace_check,
+    after which the workspace has to be made anew."""
+    if stream is not None:
+        with _current(stream):
+            return fp8_matmul(x, x_scales, weight, weight_scales, y, dtype, workspace)
+    torch = _torch()
+    M, K, ld, group = _codes(x, x_scales, "x")
+    if len(weight.shape) != 2 or weight.shape[1] != K:
+        raise ValueError("weight must be [N, K]")
+    N = weight.shape[0]
+    ld_w = _mat(weight, weight.shape, torch.float8_e4m3fn, "weight")
+    _weight_scales(weight_scales, N, K, "weight_scales")
+    here = _here(x, x_scales, weight, weight_scales, y, None if workspace is None else workspace.buf)
+    if y is None:
+        if dtype is None:
+            dtype = torch.bfloat16
+        elif dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise ValueError("dtype must be bf16 or fp32")
+        y, ld_y = x.new_empty((*x.shape[:-1], N), dtype=dtype), N
+    else:
+        if dtype not in (None, y.dtype) or y.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("y must be bf16 or fp32, and of the given dtype")
+        ld_y = _out_rows(y, M, N, y.dtype, "y")
+    if workspace is None:
+        workspace = MatmulWorkspace(M, N, K)
+    rc = lib().hyena_fp8_matmul(x.data_ptr(), ld, x_scales.data_ptr(), group, weight.data_ptr(), ld_w,
+                                weight_scales.data_ptr(), y.data_ptr(), ld_y, _dtype_code(y), M, N, K,
+                                workspace.buf.data_ptr(), workspace.nbytes, here)
+    check("hyena_fp8_matmul", rc)
+    return y
+
+
+def gated_ffn(x, gate_weight, up_weight, activation="silu", y=None, gate_out=None, up_out=None,
+              workspace: FfnWorkspace | None = None, stream=None):
+    """Gated feed-forward block up to its down projection: y = act(x Wg^T) (x Wu^T).
+    x: [M, D] or [B, L, D] bf16; gate_weight, up_weight: [F, D] bf16 with one
+    row stride; activation: silu, gelu, gelu_tanh or identity; gate_out,
+    up_out: [M, F] (or [B, L, F]), both bf16 or both fp32, or None: the two
+    products, kept for the gradient.  Returns y ([..., F] bf16, allocated if
+    not given)."""
+    if stream is not None:
+        with _current(stream):
+            return gated_ffn(x, gate_weight, up_weight, activation, y, gate_out, up_out, workspace)
+    torch = _torch()
+    act = _act(activation)
+    M, D, ld = _rows(x, "x", (torch.bfloat16,))
+    F, Dw, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"))
+    if Dw != D or gate_weight.dtype is not torch.bfloat16:
+        raise ValueError("weights must be bf16 tensors of shape [F, D]")
+    here = _here(x, gate_weight, up_weight, y, gate_out, up_out, None if workspace is None else workspace.buf)
+    if y is None:
+        y, ld_y = x.new_empty((*x.shape[:-1], F)), F
+    else:
+        ld_y = _out_rows(y, M, F, torch.bfloat16, "y")
+    ld_g, kind = (0, 1) if gate_out is None and up_out is None else _kept(gate_out, up_out, M, F)
+    if workspace is None:
+        workspace = FfnWorkspace(M, D, F)
+    rc = lib().hyena_gated_ffn(x.data_ptr(), ld, gate_weight.data_ptr(), up_weight.data_ptr(), ld_w, act, y.data_ptr(),
+                               ld_y, _opt(gate_out), _opt(up_out), ld_g, kind, M, D, F, workspace.buf.data_ptr(),
+                               workspace.nbytes, here)
+    check("hyena_gated_ffn", rc)
+    return y
+
+
+def gated_ffn_fp8(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, activation="silu", fp8_out=False,
+                  y=None, q=None, scales=None, workspace: FfnWorkspace | None = None, stream=None):
+    """``gated_ffn`` of e4m3 operands with scales as in ``fp8_matmul``.  Returns
+    y ([..., F] bf16), or with ``fp8_out`` (q, scales): y's codes with one scale
+    per row and 128 of its values, as the down projection by ``fp8_matmul``
+    takes them (F a multiple of 16)."""
+    if stream is not None:
+        with _current(stream):
+            return gated_ffn_fp8(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, activation, fp8_out, y,
+                                 q, scales, workspace)
+    torch = _torch()
+    e4m3 = torch.float8_e4m3fn
+    act = _act(activation)
+    M, D, ld, group = _codes(x, x_scales, "x")
+    F, Dw, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"))
+    if Dw != D or gate_weight.dtype is not e4m3:
+        raise ValueError("weights must be e4m3 tensors of shape [F, D]")
+    _weight_scales(gate_scales, F, D, "gate_scales")
+    _weight_scales(up_scales, F, D, "up_scales")
+    here = _here(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, y, q, scales,
+                 None if workspace is None else workspace.buf)
+    ld_y = ld_q = 0
+    if fp8_out:
+        if y is not None:
+            raise ValueError("y is the bf16 output: give q and scales with fp8_out")
+        if q is None:
+            q, ld_q = torch.empty((*x.shape[:-1], F), dtype=e4m3, device=x.device), F
+        else:
+            ld_q = _out_rows(q, M, F, e4m3, "q")
+        want = (M, -(-F // 128))
+        if scales is None:
+            scales = x_scales.new_empty(want)
+        else:
+            _f32(scales, want, "scales")
+    else:
+        if q is not None or scales is not None:
+            raise ValueError("q and scales are the output of fp8_out")
+        if y is None:
+            y, ld_y = torch.empty((*x.shape[:-1], F), dtype=torch.bfloat16, device=x.device), F
+        else:
+            ld_y = _out_rows(y, M, F, torch.bfloat16, "y")
+    if workspace is None:
+        workspace = FfnWorkspace(M, D, F)
+    rc = lib().hyena_gated_ffn_fp8(x.data_ptr(), ld, x_scales.data_ptr(), group, gate_weight.data_ptr(),
+                                   gate_scales.data_ptr(), up_weight.data_ptr(), up_scales.data_ptr(), ld_w, act,
+                                   _opt(y), ld_y, _opt(q), ld_q, _opt(scales), M, D, F, workspace.buf.data_ptr(),
+                                   workspace.nbytes, here)
+    check("hyena_gated_ffn_fp8", rc)
+    return (q, scales) if fp8_out else y
+
+
+class FfnGrads(NamedTuple):
+    """Gradients of gated_ffn: of x and of the two weights (bf16)."""
+    dx: object
+    dgate_weight: object
+    dup_weight: object
+
+
+def gated_ffn_backward(dy, x, gate_weight, up_weight, gate, up, activation="silu", dx=None, dgate_weight=None,
+                       dup_weight=None, workspace: FfnWorkspace | None = None, stream=None) -> FfnGrads:
+    """Gradients of ``gated_ffn`` from dy ([..., F] bf16), the forward call's
+    inputs and the gate and up products it kept.  dx and the weights' gradients
+    (bf16, written not added to; one row stride) are allocated if not given;
+    ``workspace``: an FfnWorkspace made with backward = True."""
+    if stream is not None:
+        with _current(stream):
+            return gated_ffn_backward(dy, x, gate_weight, up_weight, gate, up, activation, dx, dgate_weight,
+                                      dup_weight, workspace)
+    torch = _torch()
+    b = torch.bfloat16
+    act = _act(activation)
+    M, D, ld = _rows(x, "x", (b,))
+    F, Dw, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"))
+    if Dw != D or gate_weight.dtype is not b:
+        raise ValueError("weights must be bf16 tensors of shape [F, D]")
+    ld_dy = _out_rows(dy, M, F, b, "dy")
+    ld_g, kind = _kept(gate, up, M, F)
+    here = _here(dy, x, gate_weight, up_weight, gate, up, dx, dgate_weight, dup_weight,
+                 None if workspace is None else workspace.buf)
+    if dx is None:
+        dx, ld_dx = torch.empty_like(x, memory_format=torch.contiguous_format), D
+    else:
+        ld_dx = _out_rows(dx, M, D, b, "dx")
+    if dgate_weight is None and dup_weight is None:
+        dgate_weight, dup_weight, ld_dw = x.new_empty((F, D)), x.new_empty((F, D)), D
+    elif dgate_weight is None or dup_weight is None:
+        raise ValueError("give both of dgate_weight and dup_weight or neither")
+    else:
+        ld_dw = _mat(dgate_weight, (F, D), b, "dgate_weight")
+        if _mat(dup_weight, (F, D), b, "dup_weight") != ld_dw:
+            raise ValueError("dgate_weight and dup_weight must share one row stride")
+    if workspace is None:
+        workspace = FfnWorkspace(M, D, F, backward=True)
+    rc = lib().hyena_gated_ffn_backward(dy.data_ptr(), ld_dy, x.data_ptr(), ld, gate_weight.data_ptr(),
+                                        up_weight.data_ptr(), ld_w, gate.data_ptr(), up.data_ptr(), ld_g, kind, act,
+                                        dx.data_ptr(), ld_dx, dgate_weight.data_ptr(), dup_weight.data_ptr(), ld_dw,
+                                        M, D, F, workspace.buf.data_ptr(), workspace.nbytes, here)
+    check("hyena_gated_ffn_backward", rc)
+    return FfnGrads(dx, dgate_weight, dup_weight)

@@ -74,6 +74,15 @@ SIGNATURES = {
     "hyena_rms_norm_backward_workspace_size": (_SZ, [_I64, _I]),
     "hyena_rms_norm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I,
                                      _P, _SZ, _P]),
+    "hyena_fp8_quantize": (_I, [_P, _I64, _I, _P, _I64, _P, _I, _I64, _I, _P]),
+    "hyena_fp8_matmul_workspace_size": (_SZ, [_I64, _I, _I]),
+    "hyena_fp8_matmul": (_I, [_P, _I64, _P, _I, _P, _I64, _P, _P, _I64, _I, _I64, _I, _I, _P, _SZ, _P]),
+    "hyena_gated_ffn_workspace_size": (_SZ, [_I64, _I, _I, _I]),
+    "hyena_gated_ffn": (_I, [_P, _I64, _P, _P, _I64, _I, _P, _I64, _P, _P, _I64, _I, _I64, _I, _I, _P, _SZ, _P]),
+    "hyena_gated_ffn_fp8": (_I, [_P, _I64, _P, _I, _P, _P, _P, _P, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _I, _I,
+                                 _P, _SZ, _P]),
+    "hyena_gated_ffn_backward": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _P, _I64, _P, _P, _I64,
+                                      _I64, _I, _I, _P, _SZ, _P]),
     "hyena_modal_state_init": (_I, [_P, _I, _I, _I, _P]),
     "hyena_workspace_check": (_I, [_P, _P]),
 }

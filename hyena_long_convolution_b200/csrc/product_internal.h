@@ -1,0 +1,70 @@
+// product_internal.h -- host-side declarations of the 8-bit products and the
+// feed-forward block, shared by their entry points and launchers (not part of
+// the public interface).
+#pragma once
+
+#include "layer_internal.h"
+
+namespace hyena {
+
+constexpr int kScaleGroup = 128;  // channels (and weight rows) per scale
+
+struct QuantArgs {
+    const void *x;
+    long long ld_x;
+    bool x_bf16;
+    uint8_t *q;
+    long long ld_q;
+    float *scales;
+    int block;
+    long long rows;
+    int D;
+};
+
+int launch_fp8_quantize(const QuantArgs &a, cudaStream_t st);
+
+// y = x w1^T, or act(x w1^T) (x w2^T): forward products of either operand type.
+struct ProductArgs {
+    const void *x, *w1, *w2;  // bf16, or e4m3 codes
+    long long ld_x, ld_w;
+    bool fp8;
+    const float *sx, *sw1, *sw2;  // scales of codes
+    int sx_row, sx_step;          // scale of (row m, group j): sx[m sx_row + j sx_step]
+    bool gated;                   // two weights and the activation between them
+    int act;
+    void *y;                      // bf16 or fp32, or
+    bool y_f32;
+    long long ld_y;
+    uint8_t *q;                   // e4m3 codes with scales
+    long long ld_q;
+    float *scales;
+    void *g, *u;                  // kept products or null
+    long long ld_g;
+    bool g_f32;
+    long long M;
+    int N, K;
+    void *workspace;
+};
+
+int launch_product(const ProductArgs &a, cudaStream_t st);
+
+struct FfnBackArgs {
+    const uint16_t *dy, *x, *w1, *w2;
+    long long ld_dy, ld_x, ld_w;
+    const void *g, *u;
+    long long ld_g;
+    bool g_f32;
+    int act;
+    uint16_t *dx, *dw1, *dw2;
+    long long ld_dx, ld_dw;
+    long long M;
+    int D, F;
+    void *workspace;
+};
+
+int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st);
+
+size_t product_workspace(long long M, int N, int K, bool fp8, bool gated);
+size_t ffn_backward_workspace(long long M, int D, int F);
+
+}  // namespace hyena

@@ -42,8 +42,6 @@ __device__ __forceinline__ float sqrt_approx(float x)
     return r;
 }
 
-__device__ __forceinline__ float2 bcast2(float x) { return make_float2(x, x); }
-
 // Products that a sum takes are written as one __ffma2_rn below: left apart,
 // the compiler contracts __fmul2_rn and __fadd2_rn where the product has no
 // other use, so that kernels would differ in the last bit.

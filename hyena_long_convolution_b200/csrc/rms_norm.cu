@@ -14,8 +14,6 @@
 // 8-channel vectors i, i + T, ...  HBM-bound: 32768 rows of 4096 channels with a
 // bf16 residual take 168-173 us, 97-99% of the measured copy bandwidth; 8192 rows
 // with an fp32 residual and an e4m3 output 66-68 us, 85-87%.
-#include <cuda_fp8.h>
-
 #include "layer_device.cuh"
 #include "layer_internal.h"
 
@@ -30,8 +28,6 @@ constexpr int kNarrowWidth = 256;    // widest row that lanes of one warp take
 constexpr int kNarrowThreads = 256;
 constexpr int kNarrowTurns = 3;
 constexpr int kNarrowCtas = 2;  // an SM, by its registers
-constexpr float kE4m3Max = 448.f;
-constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100: a zero row keeps a finite scale
 constexpr unsigned int kFullMask = 0xffffffffu;
 
 __device__ __forceinline__ void load_bf16x8(float (&v)[8], const uint16_t *p)
@@ -74,8 +70,6 @@ __device__ __forceinline__ void store_f32x8(float *p, const float (&v)[8])
     for (int i = 0; i < 8; i += 4)
         *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
-
-__device__ __forceinline__ float2 bcast2(float x) { return make_float2(x, x); }
 
 // A tensor of type kind R (0 absent, 1 bf16, 2 fp32), 8 values at element o.
 template <int R>
@@ -193,53 +187,6 @@ __device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *
     v = part[0];
     for (int w = 1; w < warps; ++w) v = max(v, part[w]);
     return v;
-}
-
-__device__ __forceinline__ float scale_of(unsigned int amax_bits)
-{
-    const float a = __uint_as_float(amax_bits);
-    return a < kAmaxFloor ? kAmaxFloor / kE4m3Max : a / kE4m3Max;  // NaN stays
-}
-
-// The codes of the fp32 quotients v / scale.  The product with the rounded
-// reciprocal is up to two units in the last place off, the other code next to the
-// border of two; one step with its remainder v - z scale (Markstein, 1990), which
-// one FMA forms, puts every z at, above or below a border as the quotient is: all
-// 2^23 significands of a scale, with the 13 values of v around each border, give
-// the same.  It costs 2 to 15% (8192 x 4096 with a bf16 residual 52 -> 55 us, 65536 x
-// 1024 without one 50 -> 57), division 22% (32768 x 4096 without one 139 -> 169).
-// kPairs: in packed arithmetic, which takes 132 us there where one value at a time
-// takes 151, but holds registers that cost a CTA an SM with a bf16 residual (8192 x
-// 4096 with one scale per row: 61) and with four vectors a thread (65536 x 1024: 61).
-template <bool kPairs>
-__device__ __forceinline__ void store_e4m3x8(uint8_t *p, float (&v)[8], float scale)
-{
-    if (scale < 0x1p-60f) {  // the same quotients, with no subnormal remainder
-        scale *= 0x1p+64f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= 0x1p+64f;
-    }
-    const float inv = 1.f / scale;
-    const bool step = scale < INFINITY;  // else the product: 0, NaN of an Inf, NaN
-    unsigned short h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 y = make_float2(v[2 * i], v[2 * i + 1]);
-        float2 z;
-        if constexpr (kPairs) {
-            z = __fmul2_rn(y, bcast2(inv));
-            if (step) z = __ffma2_rn(__ffma2_rn(z, bcast2(-scale), y), bcast2(inv), z);
-        } else {
-            z = make_float2(y.x * inv, y.y * inv);
-            if (step) z.x = __fmaf_rn(__fmaf_rn(z.x, -scale, y.x), inv, z.x);
-            if (step) z.y = __fmaf_rn(__fmaf_rn(z.y, -scale, y.y), inv, z.y);
-        }
-        h[i] = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
-    }
-    uint2 q;
-    q.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
-    q.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-    *reinterpret_cast<uint2 *>(p) = q;
 }
 
 // R: the residual's type kind.  Q: 0 bf16 output, 1 e4m3 with a scale per row,

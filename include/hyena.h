@@ -650,6 +650,128 @@ hyena_status_t hyena_rms_norm_backward(const hyena_bf16_t *dy, int64_t ld_dy,
                                        void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * e4m3 codes with scales of a bf16 or fp32 tensor: the operands of
+ * hyena_fp8_matmul and hyena_gated_ffn_fp8 (evo2_flash README, hook table row
+ * "blocks.N.projections": the input projection is an fp8 product).
+ *
+ *   scale = max(max|x|, 2^-100) / 448 over each group;  q = x / scale rounded
+ *
+ * as in hyena_rms_norm_fp8, NaN and Inf included.
+ *
+ * block     1: a group is 128 channels of one row, scales
+ *           [rows, ceil(D / 128)] (activations); 128: 128 rows x 128 channels,
+ *           scales [ceil(rows / 128), ceil(D / 128)] (weights).
+ * rows, D   0 <= rows < 2^31; D a multiple of 8, at most HYENA_MAX_WIDTH.
+ * x         of type x_type, ld_x (in elements, a multiple of 8, >= D).
+ * q         one byte each, ld_q a multiple of 8 (the products want 16).
+ */
+#define HYENA_MAX_WIDTH (1 << 20)
+
+hyena_status_t hyena_fp8_quantize(const void *x, int64_t ld_x, hyena_dtype_t x_type,
+                                  uint8_t *q, int64_t ld_q, float *scales, int block,
+                                  int64_t rows, int D, void *stream);
+
+/*
+ * Product of e4m3 tensors with scales:
+ *
+ *   y[m, n] = sum_k (x[m, k] x_scales[m, k / 128]) (w[n, k] w_scales[n / 128, k / 128])
+ *
+ * x         codes [M, K], row stride ld_x; x_scales [M, ceil(K / 128)]
+ *           (x_group = 128) or one per row, [M] (x_group = 0), as
+ *           hyena_rms_norm_fp8 and hyena_fp8_quantize leave them.
+ * w         codes [N, K], row stride ld_w; w_scales [ceil(N / 128),
+ *           ceil(K / 128)].
+ * y         [M, N] of type y_type, ld_y; rounded once from fp32.
+ * M, N, K   0 <= M < 2^31; N, K multiples of 8, at most HYENA_MAX_WIDTH; ld_x
+ *           and ld_w multiples of 16, ld_y of 8.
+ * workspace at least hyena_fp8_matmul_workspace_size bytes; zero-filled once
+ *           (hyena_modal_workspace_init) and then reused, by calls in order on
+ *           one stream (or ordered otherwise); hyena_workspace_check reports a
+ *           device wait that ran out, whose call leaves NaN in the results
+ *           that it did not reach, and after which the workspace must be
+ *           zero-filled again.
+ *
+ * Products of codes are exact and summed in fp32 over each 128 channels; the
+ * sums times their scales are summed in fp32 in the order of k.  Work split
+ * over k (few rows) is joined in that order too, whichever part is done last.
+ * x and w are not written; y may overlap none of the inputs.
+ */
+size_t hyena_fp8_matmul_workspace_size(int64_t M, int N, int K);
+
+hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_scales, int x_group,
+                                const uint8_t *w, int64_t ld_w, const float *w_scales,
+                                void *y, int64_t ld_y, hyena_dtype_t y_type,
+                                int64_t M, int N, int K,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated feed-forward block up to its down projection (evo2_flash README, hook
+ * table rows "blocks.N.mlp.l1" and "l2"):
+ *
+ *   g = x Wg^T;  u = x Wu^T;  y = act(g) u
+ *
+ * act       silu g / (1 + e^-g); gelu g Phi(g); gelu_tanh, gelu's form by
+ *           tanh(sqrt(2 / pi) (g + 0.044715 g^3)); identity.
+ * x         [M, D] bf16, ld_x.  gate_w, up_w: [F, D] bf16, ld_w each.
+ * y         [M, F] bf16, ld_y, rounded once from fp32.
+ * gate_out, up_out  [M, F] of type keep_type, ld_g, or both NULL: g and u for
+ *           the gradient (y comes from the unrounded ones).
+ * M, D, F   0 <= M < 2^31; D, F multiples of 8, at most HYENA_MAX_WIDTH; every
+ *           row stride a multiple of 8.
+ * workspace as hyena_fp8_matmul, hyena_gated_ffn_workspace_size(M, D, F, 0)
+ *           bytes (a workspace for the gradient serves the forward too).
+ */
+typedef enum {
+    HYENA_ACT_SILU = 1,
+    HYENA_ACT_GELU = 2,
+    HYENA_ACT_GELU_TANH = 3,
+    HYENA_ACT_IDENTITY = 4
+} hyena_activation_t;
+
+size_t hyena_gated_ffn_workspace_size(int64_t M, int D, int F, int backward);
+
+hyena_status_t hyena_gated_ffn(const hyena_bf16_t *x, int64_t ld_x,
+                               const hyena_bf16_t *gate_w, const hyena_bf16_t *up_w, int64_t ld_w,
+                               hyena_activation_t act, hyena_bf16_t *y, int64_t ld_y,
+                               void *gate_out, void *up_out, int64_t ld_g, hyena_dtype_t keep_type,
+                               int64_t M, int D, int F,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same with e4m3 operands and scales as in hyena_fp8_matmul, and an output
+ * in bf16 (y, ld_y; q and scales NULL) or as e4m3 codes with a scale per row
+ * and 128 of its F values (q, ld_q a multiple of 16, scales [M, ceil(F / 128)];
+ * y NULL), which the down projection by hyena_fp8_matmul reads.  The maximum
+ * is taken of the unrounded y.
+ */
+hyena_status_t hyena_gated_ffn_fp8(const uint8_t *x, int64_t ld_x, const float *x_scales, int x_group,
+                                   const uint8_t *gate_w, const float *gate_scales,
+                                   const uint8_t *up_w, const float *up_scales, int64_t ld_w,
+                                   hyena_activation_t act, hyena_bf16_t *y, int64_t ld_y,
+                                   uint8_t *q, int64_t ld_q, float *scales,
+                                   int64_t M, int D, int F,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of hyena_gated_ffn from dy [M, F] bf16 and the g and u it kept:
+ *
+ *   dg = dy u act'(g);  du = dy act(g)   (rounded to bf16: operands of the products)
+ *   dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x
+ *
+ * dx        [M, D] bf16, ld_dx.  dgate_w, dup_w: [F, D] bf16, ld_dw each,
+ *           written not added to (zero for M = 0).  Each rounded once from fp32.
+ * workspace hyena_gated_ffn_workspace_size(M, D, F, 1) bytes, as above.
+ */
+hyena_status_t hyena_gated_ffn_backward(const hyena_bf16_t *dy, int64_t ld_dy,
+                                        const hyena_bf16_t *x, int64_t ld_x,
+                                        const hyena_bf16_t *gate_w, const hyena_bf16_t *up_w, int64_t ld_w,
+                                        const void *gate, const void *up, int64_t ld_g, hyena_dtype_t keep_type,
+                                        hyena_activation_t act, hyena_bf16_t *dx, int64_t ld_dx,
+                                        hyena_bf16_t *dgate_w, hyena_bf16_t *dup_w, int64_t ld_dw,
+                                        int64_t M, int D, int F,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) a device-side error that
  * calls using this workspace recorded: HYENA_ERR_TIMEOUT if a bounded wait
  * ran out, HYENA_OK otherwise.
