@@ -1,5 +1,6 @@
 // product_device.cuh -- device-side helpers of the products and the
-// feed-forward block.
+// feed-forward block: tcgen05 (tensor cores, tensor memory), clusters of two
+// CTAs, bounded waits, activations.  Hand-written inline PTX; no library code.
 #pragma once
 
 #include "layer_device.cuh"
@@ -7,7 +8,211 @@
 
 namespace hyena {
 
-// act(g) of the gated block (HYENA_ACT_*), and with it act'(g).
+// ---------------------------------------------------------------- waits
+
+// Waits for the phase with the given parity, at most four seconds of the time
+// that the CTA runs (a look that comes late, after the CTA was suspended, counts
+// as 10 ms).  `dead` is the CTA's: once one wait ran out, the others end too.
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile unsigned int *dead)
+{
+    unsigned long long last = global_timer_ns(), spent = 0;
+    while (*dead == 0u) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long now = global_timer_ns();
+        const unsigned long long step = now - last;
+        spent += step < 10000000ull ? step : 10000000ull;
+        last = now;
+        if (spent > 4 * kWaitLimitNs) *dead = 1u;
+    }
+    return false;
+}
+
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile unsigned int *dead)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, dead);
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The address of `p` in CTA `rank` of this cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A 2-D TMA load of one CTA of a pair, counted by a barrier of either.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t cluster_bar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(cluster_bar)
+        : "memory");
+}
+
+// ---------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+constexpr uint32_t kTmemAll = 512;  // columns
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot)
+{
+    if constexpr (kCtas == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                     "r"(kTmemAll)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                     "r"(kTmemAll)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base)
+{
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTmemAll));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTmemAll));
+}
+
+// Shared-memory operand of 128-byte rows as TMA's 128-byte swizzle leaves them,
+// tile at a 1024-byte boundary.  K-major (rows of the operand's M or N, 128 bytes
+// of k each): groups of 8 rows 1024 bytes apart; the next MMA's k is 32 bytes on.
+// MN-major (a row for each k, 64 bf16 of M or N each): groups of 8 k 1024 bytes
+// apart, the next 64 of M or N `lbo` bytes on; the next MMA's k is 2048 bytes on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// fp32 accumulators; bf16 (kind::f16) or e4m3 (kind::f8f6f4) operands.
+__host__ __device__ constexpr uint32_t instruction_desc(bool f8, int m, int n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | ((f8 ? 0u : 1u) << 7) | ((f8 ? 0u : 1u) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D (tensor memory) (+)= A B, one thread.
+template <int kCtas, bool kF8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    const uint32_t en = add ? 1u : 0u;
+#define HYENA_MMA(group, kind)                                                                                       \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::" group ".kind::" kind        \
+                 " [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),                                                            \
+                 "l"(a), "l"(b), "r"(idesc), "r"(en)                                                                 \
+                 : "memory")
+    if constexpr (kCtas == 2) {
+        if constexpr (kF8)
+            HYENA_MMA("2", "f8f6f4");
+        else
+            HYENA_MMA("2", "f16");
+    } else {
+        if constexpr (kF8)
+            HYENA_MMA("1", "f8f6f4");
+        else
+            HYENA_MMA("1", "f16");
+    }
+#undef HYENA_MMA
+}
+
+// `bar` (of both CTAs of a pair) is told when the MMAs issued so far are done.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit_to(uint64_t *bar)
+{
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+}
+
+// Consecutive fp32 columns of the warp's 32 lanes of tensor memory, a lane a
+// thread; complete after tmem_wait, through which the values go so that nothing
+// reads them before.
+#define HYENA_R8(v, o)                                                                                             \
+    "=f"(v[o]), "=f"(v[o + 1]), "=f"(v[o + 2]), "=f"(v[o + 3]), "=f"(v[o + 4]), "=f"(v[o + 5]), "=f"(v[o + 6]),     \
+        "=f"(v[o + 7])
+__device__ __forceinline__ void tmem_ld(float (&v)[8], uint32_t a)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : HYENA_R8(v, 0) : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld(float (&v)[16], uint32_t a)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : HYENA_R8(v, 0), HYENA_R8(v, 8)
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld(float (&v)[32], uint32_t a)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : HYENA_R8(v, 0), HYENA_R8(v, 8), HYENA_R8(v, 16), HYENA_R8(v, 24)
+        : "r"(a));
+}
+#undef HYENA_R8
+#define HYENA_W8(v, o)                                                                                             \
+    "+f"(v[o]), "+f"(v[o + 1]), "+f"(v[o + 2]), "+f"(v[o + 3]), "+f"(v[o + 4]), "+f"(v[o + 5]), "+f"(v[o + 6]),     \
+        "+f"(v[o + 7])
+__device__ __forceinline__ void tmem_wait(float (&v)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : HYENA_W8(v, 0)::"memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : HYENA_W8(v, 0), HYENA_W8(v, 8)::"memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : HYENA_W8(v, 0), HYENA_W8(v, 8), HYENA_W8(v, 16), HYENA_W8(v, 24)::"memory");
+}
+#undef HYENA_W8
+
+// ---------------------------------------------------------------- activations
+
+// act(g) of the gated block (HYENA_ACT_*).
 template <int kAct>
 __device__ __forceinline__ float activation(float g)
 {
@@ -22,6 +227,7 @@ __device__ __forceinline__ float activation(float g)
     }
 }
 
+// (act(g), act'(g)).
 template <int kAct>
 __device__ __forceinline__ float2 activation_slope(float g)
 {
@@ -41,6 +247,5 @@ __device__ __forceinline__ float2 activation_slope(float g)
 }
 
 __device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
-__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 
 }  // namespace hyena

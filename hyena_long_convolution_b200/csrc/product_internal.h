@@ -64,6 +64,21 @@ struct FfnBackArgs {
 
 int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st);
 
+// Up to kNarrowRows rows the weights are the operand with 128 rows and the tokens
+// the other, in the smallest of 16, 32, 64 or 128 that holds them.
+constexpr int kNarrowRows = 128;
+inline int narrow_tokens(long long M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+
+int launch_product_narrow(const ProductArgs &a, cudaStream_t st);
+int launch_product_wide(const ProductArgs &a, cudaStream_t st);
+int launch_ffn_dx(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st);
+int launch_ffn_dw(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st);
+
+// Map of a [rows, cols] matrix of bf16 or codes with boxes of 128 bytes of a row
+// times box_rows rows, laid out with the 128-byte swizzle.
+bool encode_matrix(CUtensorMap *m, const void *p, bool fp8, long long rows, int cols, long long ld, int box_rows);
+int product_sms();
+
 size_t product_workspace(long long M, int N, int K, bool fp8, bool gated);
 size_t ffn_backward_workspace(long long M, int D, int F);
 

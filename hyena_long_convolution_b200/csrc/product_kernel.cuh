@@ -1,0 +1,207 @@
+// product_kernel.cuh -- what the two tensor-core product kernels share: the
+// division of their work, the joining of partial sums, the outputs.
+#pragma once
+
+#include "product_device.cuh"
+
+namespace hyena {
+
+constexpr int kEpiWarps = 8;                      // read tensor memory: warp w lanes 32 (w % 4) .. + 31
+constexpr int kEpiThreads = 32 * kEpiWarps;
+constexpr int kThreadsProduct = kEpiThreads + 128; // + a TMA warp, an MMA warp and two that only end
+// Registers: the reading warps hold 128 sums a thread.  256 x 208 + 128 x 88 = 384 x
+// 168, what the kernels are launched with.
+constexpr int kRegsEpi = 208, kRegsAux = 88;
+constexpr int kRowBytes = 128;                    // of a k-block: 64 bf16 or 128 codes
+constexpr size_t kProductHeader = 4096;           // 256 bytes of header, then a counter for each split tile
+constexpr int kMaxSplitTiles = (kProductHeader - 256) / 4;
+
+// How a product is divided: tiles of the output, k-blocks of a tile, units (CTAs,
+// or pairs of CTAs) that walk through them.  The first `split` tiles' k-blocks are
+// dealt out evenly, a contiguous run a unit, so that few tiles (or the last of
+// many) keep every unit busy; the others go whole, one after another.
+struct Plan {
+    int tiles_m, tiles_n, tiles;
+    int blocks;  // k-blocks of a tile
+    int split, units;
+    __device__ __forceinline__ long long first(int unit) const
+    {
+        return static_cast<long long>(split) * blocks * unit / units;
+    }
+};
+
+struct Walk {
+    const Plan &p;
+    long long pos, end;
+    int whole;
+    int tile, k0, k1;
+    __device__ __forceinline__ Walk(const Plan &plan, int unit)
+        : p(plan), pos(plan.first(unit)), end(plan.first(unit + 1)), whole(plan.split + unit)
+    {
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (pos < end) {
+            tile = static_cast<int>(pos / p.blocks);
+            k0 = static_cast<int>(pos - static_cast<long long>(tile) * p.blocks);
+            k1 = end - pos < p.blocks - k0 ? k0 + static_cast<int>(end - pos) : p.blocks;
+            pos += k1 - k0;
+            return true;
+        }
+        if (whole >= p.tiles) return false;
+        tile = whole;
+        whole += p.units;
+        k0 = 0;
+        k1 = p.blocks;
+        return true;
+    }
+};
+
+// The sums of a part of a tile go to memory, and the CTA whose part is the last to
+// arrive adds them up in the order of k, so that the result does not depend on
+// which that was.  `kCtas` CTAs of a unit each have their own half of the tile.
+// v: this thread's kV sums; thread `t` of the kEpiThreads keeps them at
+// [i][t] of its part's slot.  True in the CTA that holds the tile's sums.
+template <int kCtas, int kV>
+__device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int unit, int rank, int tile, int k0, int t,
+                                           unsigned char *workspace, unsigned int *flag)
+{
+    constexpr size_t kSlot = static_cast<size_t>(kV) * kEpiThreads;
+    float *slots = reinterpret_cast<float *>(workspace + kProductHeader) + t;
+    const long long begin = static_cast<long long>(tile) * p.blocks;
+    // a unit has at most two parts: one that begins inside a tile and one at its start
+    auto slot = [&](int u) {
+        return slots + ((2ll * u + (p.first(u) > begin ? 0 : 1)) * kCtas + rank) * kSlot;
+    };
+    float *own = slot(unit);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) own[i * kEpiThreads] = v[i];
+    // the units whose runs meet this tile; few k-blocks leave some without any
+    auto takes_part = [&](int u) { return p.first(u) < p.first(u + 1) ? 1 : 0; };
+    int first = unit, past = unit + 1, parts = 1;
+    while (first > 0 && p.first(first) > begin) parts += takes_part(--first);
+    while (p.first(past) < begin + p.blocks) parts += takes_part(past++);
+    __threadfence();
+    named_sync(1, kEpiThreads);
+    if (t == 0) {
+        unsigned int *count = reinterpret_cast<unsigned int *>(workspace + 256) + tile * kCtas + rank;
+        const unsigned int before = atomicAdd(count, 1u);
+        const bool last = before + 1 == static_cast<unsigned int>(parts);
+        if (last) *count = 0u;  // for the next call
+        __threadfence();
+        *flag = last ? 1u : 0u;
+    }
+    named_sync(1, kEpiThreads);
+    const bool last = *flag != 0u;
+    if (!last) return false;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = 0.f;
+    for (int u = first; u < past; ++u) {
+        if (!takes_part(u)) continue;
+        const float *q = slot(u);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[i] += __ldcg(q + i * kEpiThreads);
+    }
+    return true;
+}
+
+// g[i] <- act(g[i]) u[i]
+template <int kAct, int kV>
+__device__ __forceinline__ void gate(float (&v)[2 * kV])
+{
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = activation<kAct>(v[i]) * v[kV + i];
+}
+
+template <int kV>
+__device__ __forceinline__ void gate(float (&v)[2 * kV], int act)
+{
+    switch (act) {
+        case HYENA_ACT_SILU: gate<HYENA_ACT_SILU, kV>(v); break;
+        case HYENA_ACT_GELU: gate<HYENA_ACT_GELU, kV>(v); break;
+        case HYENA_ACT_GELU_TANH: gate<HYENA_ACT_GELU_TANH, kV>(v); break;
+        default: gate<HYENA_ACT_IDENTITY, kV>(v); break;
+    }
+}
+
+__device__ __forceinline__ void load8_bf16(float (&v)[8], const uint16_t *p)
+{
+    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = bf16x2_to_float2(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void load8_f32(float (&v)[8], const float *p)
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// kV consecutive values of a row that ends after `left` of them (a multiple of 8,
+// as is every row's start).
+template <int kV>
+__device__ __forceinline__ void store_bf16_row(uint16_t *p, const float *v, int left)
+{
+#pragma unroll
+    for (int i = 0; i < kV; i += 8) {
+        if (i >= left) break;
+        uint4 q;
+        q.x = float2_to_bf16x2(make_float2(v[i], v[i + 1]));
+        q.y = float2_to_bf16x2(make_float2(v[i + 2], v[i + 3]));
+        q.z = float2_to_bf16x2(make_float2(v[i + 4], v[i + 5]));
+        q.w = float2_to_bf16x2(make_float2(v[i + 6], v[i + 7]));
+        *reinterpret_cast<uint4 *>(p + i) = q;
+    }
+}
+
+template <int kV>
+__device__ __forceinline__ void store_f32_row(float *p, const float *v, int left)
+{
+#pragma unroll
+    for (int i = 0; i < kV; i += 4) {
+        if (i >= left) break;
+        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
+template <int kV>
+__device__ __forceinline__ void store_row(void *p, bool f32, long long at, const float *v, int left)
+{
+    if (f32)
+        store_f32_row<kV>(static_cast<float *>(p) + at, v, left);
+    else
+        store_bf16_row<kV>(static_cast<uint16_t *>(p) + at, v, left);
+}
+
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi)); }
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux)); }
+
+// Shared memory of a CTA beside its stages.
+template <int kStages>
+struct ProductShared {
+    uint64_t full[kStages];   // a stage's operands arrived
+    uint64_t empty[kStages];  // the MMAs that read a stage are done
+    uint64_t tfull[2];        // a half of tensor memory holds sums
+    uint64_t tempty[2];       // it has been read
+    uint32_t tmem;
+    unsigned int dead;        // a wait ran out
+    unsigned int flag;
+    unsigned int amax[kEpiThreads];
+};
+
+// What a CTA whose wait ran out does before it ends: its copies and MMAs under
+// way land within microseconds or not at all; 20 ms are given them.
+__device__ __forceinline__ void let_land()
+{
+    const unsigned long long t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 20000000ull) {
+    }
+}
+
+}  // namespace hyena

@@ -1,0 +1,402 @@
+// product_wide.cu -- products with many rows on the tensor cores of sm_100a, a
+// pair of CTAs to a tile of 256 x 256 sums:
+//
+//   forward   y = x w^T, or act(x Wg^T) (x Wu^T): the pair's 256 columns are 128 of
+//             the gate's and the same 128 of the up projection's
+//   dx        dg Wg + du Wu: k runs through F twice
+//   dW        dg^T x, du^T x: k runs through the tokens
+//
+// bf16: sums stay in tensor memory over the whole of k.  e4m3 codes: the sums
+// over each 128 k go times their scales into registers.
+#include "product_kernel.cuh"
+
+namespace hyena {
+
+namespace {
+
+constexpr int kTile = 128;                       // rows of a CTA's operands
+constexpr int kStages = 6;
+constexpr int kOperand = kTile * kRowBytes;      // 16 KB
+constexpr int kStage = 2 * kOperand;
+constexpr int kSmem = kStages * kStage + 1024;
+constexpr int kHalf = 64;                        // columns of each group of 128 a thread has
+constexpr int kBand = 8;                         // tile rows that are walked together, for L2
+
+enum { kForward = 0, kDx = 1, kDw = 2 };
+
+struct WideArgs {
+    Plan plan;
+    long long rows;      // of the output
+    int cols;
+    int blocks1;         // dx: k-blocks of the first pair of operands
+    int tile_cols;       // output columns of a tile
+    ProductArgs a;       // forward
+    uint16_t *c[2];      // dx: c[0]; dW: both
+    long long ld_c;
+    unsigned int *hdr;
+};
+
+template <int kMode, bool kF8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
+    product_wide_kernel(const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap a2,
+                        const __grid_constant__ CUtensorMap b1, const __grid_constant__ CUtensorMap b2,
+                        const __grid_constant__ WideArgs A)
+{
+    constexpr bool kAmn = kMode == kDw, kBmn = kMode != kForward;
+    constexpr int kBlock = kF8 ? 128 : 64;  // k of a block
+    extern __shared__ unsigned char raw[];
+    __shared__ ProductShared<kStages> sh;
+    unsigned char *stages = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(cluster_rank()), unit = blockIdx.x >> 1;
+    const Plan &P = A.plan;
+    volatile unsigned int *dead = &sh.dead;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(sh.full + i, 1);
+            mbar_init(sh.empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sh.tfull + i, 1);
+            mbar_init(sh.tempty + i, 2 * kEpiWarps);
+        }
+        sh.dead = 0u;
+        fence_mbar_init();
+    }
+    if (warp == kEpiWarps + 1) tmem_alloc<2>(&sh.tmem);
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    // tile -> (tile row, tile column): bands of kBand tile rows, columns within
+    auto place = [&](int tile, int &tm, int &tn) {
+        const int per = kBand * P.tiles_n;
+        const int band = tile / per, r = tile - band * per;
+        const int rows = min(kBand, P.tiles_m - band * kBand);
+        tn = r / rows;
+        tm = band * kBand + (r - tn * rows);
+    };
+
+    if (warp >= kEpiWarps) {
+        fewer_registers();
+        if (warp == kEpiWarps && lane == 0) {  // --------------------- TMA
+            int s = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            for (Walk w(P, unit); ok && w.next();) {
+                int tm, tn;
+                place(w.tile, tm, tn);
+                const CUtensorMap *ma = &a1;
+                int m = tm * 256 + rank * kTile;
+                if (kMode == kDw && tm >= P.tiles_m / 2) {
+                    ma = &a2;
+                    m -= P.tiles_m / 2 * 256;
+                }
+                const bool gated = kMode == kForward && A.a.gated;
+                const int n = tn * A.tile_cols + (gated ? 0 : rank * kTile);
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    if (!(ok = wait_phase(sh.empty + s, ph, dead))) break;
+                    if (rank == 0) mbar_arrive_expect_tx(sh.full + s, 2 * kStage);
+                    const uint32_t bar = cluster_addr(sh.full + s, 0);
+                    unsigned char *pa = stages + s * kStage, *pb = pa + kOperand;
+                    const bool second = kMode == kDx && kb >= A.blocks1;
+                    const int k = (second ? kb - A.blocks1 : kb) * kBlock;
+                    if constexpr (kAmn) {
+                        tma_load_pair(pa, ma, bar, m, k);
+                        tma_load_pair(pa + kOperand / 2, ma, bar, m + 64, k);
+                    } else {
+                        tma_load_pair(pa, second ? &a2 : ma, bar, k, m);
+                    }
+                    if constexpr (kBmn) {
+                        const CUtensorMap *mb = second ? &b2 : &b1;
+                        tma_load_pair(pb, mb, bar, n, k);
+                        tma_load_pair(pb + kOperand / 2, mb, bar, n + 64, k);
+                    } else {
+                        tma_load_pair(pb, gated && rank ? &b2 : &b1, bar, k, n);
+                    }
+                    if (++s == kStages) s = 0, ph ^= 1;
+                }
+            }
+            if (!ok) let_land();
+        } else if (warp == kEpiWarps + 1 && lane == 0 && rank == 0) {  // MMA
+            constexpr uint32_t idesc = instruction_desc(kF8, 256, 256, kAmn, kBmn);
+            constexpr uint32_t kStepA = kAmn ? 2048 : 32, kStepB = kBmn ? 2048 : 32;
+            const uint32_t base = smem_u32(stages);
+            int s = 0, buf = 0;
+            uint32_t ph = 0, tph = 1;
+            bool ok = true;
+            for (Walk w(P, unit); ok && w.next();) {
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    const bool fresh = kF8 || kb == w.k0;
+                    if (fresh && !(ok = wait_phase(sh.tempty + buf, tph, dead))) break;
+                    if (!(ok = wait_phase(sh.full + s, ph, dead))) break;
+                    tc_fence_after();
+                    const uint32_t pa = base + s * kStage, pb = pa + kOperand;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma<2, kF8>(tmem + buf * 256, operand_desc(pa + i * kStepA, kOperand / 2),
+                                    operand_desc(pb + i * kStepB, kOperand / 2), idesc, !(fresh && i == 0));
+                    mma_commit_to<2>(sh.empty + s);
+                    if (kF8 || kb + 1 == w.k1) {
+                        mma_commit_to<2>(sh.tfull + buf);
+                        buf ^= 1;
+                        if (buf == 0) tph ^= 1;
+                    }
+                    if (++s == kStages) s = 0, ph ^= 1;
+                }
+            }
+            if (!ok) let_land();
+        }
+        __syncwarp();
+    } else {  // ------------------------------------------------- sums, outputs
+        more_registers();
+        const int hh = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + hh * kHalf;
+        const uint32_t tempty0 = cluster_addr(sh.tempty, 0), tempty1 = cluster_addr(sh.tempty + 1, 0);
+        const int groups = P.blocks;  // of codes: one a k-block
+        int buf = 0;
+        uint32_t tph = 0;
+        bool ok = true;
+        for (Walk w(P, unit); w.next();) {
+            int tm, tn;
+            place(w.tile, tm, tn);
+            const long long m = static_cast<long long>(tm) * 256 + rank * kTile + row;
+            float v[2 * kHalf];
+            auto done_reading = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(buf ? tempty1 : tempty0);
+                buf ^= 1;
+                if (buf == 0) tph ^= 1;
+            };
+            if constexpr (kF8) {
+#pragma unroll
+                for (int i = 0; i < 2 * kHalf; ++i) v[i] = 0.f;
+                // scales of the first k-block; then each one's while the one before is summed
+                const bool live = m < A.rows;
+                const float *sx = A.a.sx + (live ? m * A.a.sx_row : 0);
+                const float *s1 = A.a.gated ? A.a.sw1 + static_cast<long long>(tn) * groups
+                                            : A.a.sw1 + 2ll * tn * groups;
+                const bool two = A.a.gated || tn * A.tile_cols + kTile < A.cols;
+                const float *s2 = A.a.gated ? A.a.sw2 + static_cast<long long>(tn) * groups : s1 + (two ? groups : 0);
+                float x = live ? __ldg(sx + static_cast<long long>(w.k0) * A.a.sx_step) : 0.f;
+                float f1 = __ldg(s1 + w.k0), f2 = __ldg(s2 + w.k0);
+                for (int kb = w.k0; kb < w.k1; ++kb) {
+                    const float2 c1 = bcast2(x * f1), c2 = bcast2(x * f2);
+                    if (kb + 1 < w.k1) {
+                        x = live ? __ldg(sx + static_cast<long long>(kb + 1) * A.a.sx_step) : 0.f;
+                        f1 = __ldg(s1 + kb + 1);
+                        f2 = __ldg(s2 + kb + 1);
+                    }
+                    if (ok) ok = wait_phase(sh.tfull + buf, tph, dead);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = lanes + buf * 256;
+                    float d[2][16];
+                    tmem_ld(d[0], at);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        tmem_wait(d[i & 1]);
+                        if (i < 7) tmem_ld(d[(i + 1) & 1], at + (i + 1) / 4 * kTile + (i + 1) % 4 * 16);
+                        const float2 c = i < 4 ? c1 : c2;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 r = __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]), c,
+                                                        make_float2(v[i * 16 + j], v[i * 16 + j + 1]));
+                            v[i * 16 + j] = r.x;
+                            v[i * 16 + j + 1] = r.y;
+                        }
+                    }
+                    done_reading();
+                }
+            } else {
+                if (ok) ok = wait_phase(sh.tfull + buf, tph, dead);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t at = lanes + buf * 256;
+                    float d[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld(d[i], at + i / 2 * kTile + i % 2 * 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        tmem_wait(d[i]);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[i * 32 + j] = d[i][j];
+                    }
+                    done_reading();
+                }
+            }
+            if (!ok) {
+#pragma unroll
+                for (int i = 0; i < 2 * kHalf; ++i) v[i] = __uint_as_float(0x7fffffffu);
+            }
+            if (w.k1 - w.k0 < P.blocks &&
+                !join_parts<2>(v, P, unit, rank, w.tile, w.k0, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
+                continue;
+            const int n = tn * A.tile_cols + hh * kHalf;
+            const int left = A.cols - n;
+            if constexpr (kMode != kForward) {
+                long long r = m;
+                uint16_t *c = A.c[0];
+                if (kMode == kDw && tm >= P.tiles_m / 2) {
+                    r -= P.tiles_m / 2 * 256ll;
+                    c = A.c[1];
+                }
+                if (r < A.rows) {
+                    store_bf16_row<kHalf>(c + r * A.ld_c + n, v, left);
+                    store_bf16_row<kHalf>(c + r * A.ld_c + n + kTile, v + kHalf, left - kTile);
+                }
+            } else if (!A.a.gated) {
+                if (m < A.rows) {
+                    store_row<kHalf>(A.a.y, A.a.y_f32, m * A.a.ld_y + n, v, left);
+                    store_row<kHalf>(A.a.y, A.a.y_f32, m * A.a.ld_y + n + kTile, v + kHalf, left - kTile);
+                }
+            } else {
+                if (A.a.g && m < A.rows) {
+                    store_row<kHalf>(A.a.g, A.a.g_f32, m * A.a.ld_g + n, v, left);
+                    store_row<kHalf>(A.a.u, A.a.g_f32, m * A.a.ld_g + n, v + kHalf, left);
+                }
+                gate<kHalf>(v, A.a.act);
+                if (kF8 && A.a.q) {
+                    // the largest of the row's 128 values: this half's and the other's
+                    unsigned int mx = 0;
+#pragma unroll
+                    for (int i = 0; i < kHalf; ++i)
+                        if (i < left) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
+                    sh.amax[tid] = mx;
+                    named_sync(1, kEpiThreads);
+                    mx = max(mx, sh.amax[tid ^ kTile]);
+                    named_sync(1, kEpiThreads);
+                    const float scale = scale_of(mx);
+                    if (m < A.rows) {
+                        uint8_t *q = A.a.q + m * A.a.ld_q + n;
+#pragma unroll
+                        for (int i = 0; i < kHalf; i += 8) {
+                            if (i >= left) break;
+                            store_e4m3x8<true>(q + i, reinterpret_cast<float(&)[8]>(v[i]), scale);
+                        }
+                        if (hh == 0) A.a.scales[m * P.tiles_n + tn] = scale;
+                    }
+                } else if (m < A.rows) {
+                    store_bf16_row<kHalf>(static_cast<uint16_t *>(A.a.y) + m * A.a.ld_y + n, v, left);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync();  // the other CTA may still tell this one's barriers
+    if (warp == kEpiWarps + 1) tmem_dealloc<2>(tmem);
+    if (tid == 0 && sh.dead != 0u) atomicOr(A.hdr + 2, kErrLocalTimeout);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- host
+
+namespace {
+
+int pairs()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return -1;
+    return sms / 2;
+}
+
+void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
+{
+    p.tiles_m = tiles_m;
+    p.tiles_n = tiles_n;
+    p.tiles = tiles_m * tiles_n;
+    p.blocks = blocks;
+    const int rest = p.tiles % units;
+    p.split = rest;
+    p.units = units;
+    if (p.tiles < units) {
+        const long long all = static_cast<long long>(p.tiles) * blocks;
+        const long long most = all / 4 > p.tiles ? all / 4 : p.tiles;
+        p.units = most < units ? static_cast<int>(most) : units;
+        if (p.units == p.tiles) p.split = 0;
+    }
+}
+
+template <int kMode, bool kF8>
+int start(const CUtensorMap &a1, const CUtensorMap &a2, const CUtensorMap &b1, const CUtensorMap &b2, const WideArgs &w,
+          cudaStream_t st)
+{
+    HYENA_TRY(cudaFuncSetAttribute(product_wide_kernel<kMode, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+              "product (wide) attribute");
+    product_wide_kernel<kMode, kF8><<<2 * w.plan.units, kThreadsProduct, kSmem, st>>>(a1, a2, b1, b2, w);
+    HYENA_TRY(cudaGetLastError(), "product (wide) launch");
+    return 1;
+}
+
+}  // namespace
+
+int launch_product_wide(const ProductArgs &a, cudaStream_t st)
+{
+    const int u = pairs();
+    if (u < 1) return -1;
+    CUtensorMap x, w1, w2;
+    const int kb = a.fp8 ? 128 : 64;
+    if (!encode_matrix(&x, a.x, a.fp8, a.M, a.K, a.ld_x, kTile) ||
+        !encode_matrix(&w1, a.w1, a.fp8, a.N, a.K, a.ld_w, kTile) ||
+        !encode_matrix(&w2, a.gated ? a.w2 : a.w1, a.fp8, a.N, a.K, a.ld_w, kTile))
+        return -1;
+    WideArgs w{};
+    w.tile_cols = a.gated ? kTile : 2 * kTile;
+    make_plan(w.plan, u, static_cast<int>((a.M + 255) / 256), (a.N + w.tile_cols - 1) / w.tile_cols,
+              (a.K + kb - 1) / kb);
+    w.rows = a.M;
+    w.cols = a.N;
+    w.a = a;
+    w.hdr = static_cast<unsigned int *>(a.workspace);
+    return a.fp8 ? start<kForward, true>(x, x, w1, w2, w, st) : start<kForward, false>(x, x, w1, w2, w, st);
+}
+
+int launch_ffn_dx(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
+{
+    const int u = pairs();
+    if (u < 1) return -1;
+    CUtensorMap g, q, w1, w2;
+    if (!encode_matrix(&g, dg, false, a.M, a.F, a.F, kTile) || !encode_matrix(&q, du, false, a.M, a.F, a.F, kTile) ||
+        !encode_matrix(&w1, a.w1, false, a.F, a.D, a.ld_w, 64) || !encode_matrix(&w2, a.w2, false, a.F, a.D, a.ld_w, 64))
+        return -1;
+    WideArgs w{};
+    w.tile_cols = 2 * kTile;
+    w.blocks1 = (a.F + 63) / 64;
+    make_plan(w.plan, u, static_cast<int>((a.M + 255) / 256), (a.D + 255) / 256, 2 * w.blocks1);
+    w.rows = a.M;
+    w.cols = a.D;
+    w.c[0] = a.dx;
+    w.ld_c = a.ld_dx;
+    w.hdr = static_cast<unsigned int *>(a.workspace);
+    return start<kDx, false>(g, q, w1, w2, w, st);
+}
+
+int launch_ffn_dw(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
+{
+    const int u = pairs();
+    if (u < 1) return -1;
+    CUtensorMap g, q, x;
+    if (!encode_matrix(&g, dg, false, a.M, a.F, a.F, 64) || !encode_matrix(&q, du, false, a.M, a.F, a.F, 64) ||
+        !encode_matrix(&x, a.x, false, a.M, a.D, a.ld_x, 64))
+        return -1;
+    WideArgs w{};
+    w.tile_cols = 2 * kTile;
+    make_plan(w.plan, u, 2 * ((a.F + 255) / 256), (a.D + 255) / 256, static_cast<int>((a.M + 63) / 64));
+    w.rows = a.F;
+    w.cols = a.D;
+    w.c[0] = a.dw1;
+    w.c[1] = a.dw2;
+    w.ld_c = a.ld_dw;
+    w.hdr = static_cast<unsigned int *>(a.workspace);
+    return start<kDw, false>(g, q, x, x, w, st);
+}
+
+}  // namespace hyena
