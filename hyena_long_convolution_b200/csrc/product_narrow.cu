@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 
     if (warp >= kEpiWarps) {
         fewer_registers();
-        if (warp == kEpiWarps && lane == 0) {  // --------------------- TMA
+        if (warp == kEpiWarps) {  // ----------------------------------- TMA
             int s = 0;
             uint32_t ph = 1;
             bool ok = true;
@@ -85,18 +85,21 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 const int tn = w.tile / P.tiles_m, tm = w.tile - tn * P.tiles_m;
                 const int n = tn * A.tile_cols;
                 for (int kb = w.k0; kb < w.k1; ++kb) {
-                    if (!(ok = wait_phase(sh.empty + s, ph, dead))) break;
-                    unsigned char *p = stages + s * kStage;
-                    mbar_arrive_expect_tx(sh.full + s, kStage);
-                    tma_load_2d(p, &m1, sh.full + s, kb * kBlock, n);
-                    tma_load_2d(p + kOperand, A.a.gated ? &m2 : &m1, sh.full + s, kb * kBlock,
-                                A.a.gated ? n : n + kTile);
-                    tma_load_2d(p + 2 * kOperand, &mx, sh.full + s, kb * kBlock, tm * kNT);
+                    if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
+                    if (elect_one()) {
+                        unsigned char *p = stages + s * kStage;
+                        mbar_arrive_expect_tx(sh.full + s, kStage);
+                        tma_load_2d(p, &m1, sh.full + s, kb * kBlock, n);
+                        tma_load_2d(p + kOperand, A.a.gated ? &m2 : &m1, sh.full + s, kb * kBlock,
+                                    A.a.gated ? n : n + kTile);
+                        tma_load_2d(p + 2 * kOperand, &mx, sh.full + s, kb * kBlock, tm * kNT);
+                    }
+                    __syncwarp();
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
             if (!ok) let_land();
-        } else if (warp == kEpiWarps + 1 && lane == 0) {  // MMA
+        } else if (warp == kEpiWarps + 1) {  // ----------------------- MMA
             constexpr uint32_t idesc = instruction_desc(kF8, kTile, kNT, false, false);
             const uint32_t base = smem_u32(stages);
             int s = 0, buf = 0;
@@ -105,19 +108,24 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             for (Walk w(P, unit); ok && w.next();) {
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     const bool fresh = kF8 || kb == w.k0;
-                    if (fresh && !(ok = wait_phase(sh.tempty + buf, tph, dead))) break;
-                    if (!(ok = wait_phase(sh.full + s, ph, dead))) break;
+                    if (fresh && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
+                    if (!(ok = warp_wait(sh.full + s, ph, dead))) break;
                     tc_fence_after();
-                    const uint32_t pw = base + s * kStage, px = pw + 2 * kOperand;
+                    const uint64_t dw = operand_desc(base + s * kStage, 16);
+                    const uint64_t dx = operand_desc(base + s * kStage + 2 * kOperand, 16);
+                    const bool last = kF8 || kb + 1 == w.k1;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g)
+                        for (int g = 0; g < 2; ++g)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma<1, kF8>(tmem + buf * 256 + g * kTile, operand_desc(pw + g * kOperand + i * 32, 16),
-                                        operand_desc(px + i * 32, 16), idesc, !(fresh && i == 0));
-                    mma_commit_to<1>(sh.empty + s);
-                    if (kF8 || kb + 1 == w.k1) {
-                        mma_commit_to<1>(sh.tfull + buf);
+                            for (int i = 0; i < 4; ++i)
+                                mma<1, kF8>(tmem + buf * 256 + g * kTile, dw + (g * kOperand + i * 32) / 16, dx + i * 2,
+                                            idesc, !(fresh && i == 0));
+                        mma_commit_to<1>(sh.empty + s);
+                        if (last) mma_commit_to<1>(sh.tfull + buf);
+                    }
+                    __syncwarp();
+                    if (last) {
                         buf ^= 1;
                         if (buf == 0) tph ^= 1;
                     }

@@ -81,7 +81,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
 
     if (warp >= kEpiWarps) {
         fewer_registers();
-        if (warp == kEpiWarps && lane == 0) {  // --------------------- TMA
+        if (warp == kEpiWarps) {  // ----------------------------------- TMA
+            const uint32_t full0 = cluster_addr(sh.full, 0);
             int s = 0;
             uint32_t ph = 1;
             bool ok = true;
@@ -97,32 +98,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                 const bool gated = kMode == kForward && A.a.gated;
                 const int n = tn * A.tile_cols + (gated ? 0 : rank * kTile);
                 for (int kb = w.k0; kb < w.k1; ++kb) {
-                    if (!(ok = wait_phase(sh.empty + s, ph, dead))) break;
-                    if (rank == 0) mbar_arrive_expect_tx(sh.full + s, 2 * kStage);
-                    const uint32_t bar = cluster_addr(sh.full + s, 0);
-                    unsigned char *pa = stages + s * kStage, *pb = pa + kOperand;
-                    const bool second = kMode == kDx && kb >= A.blocks1;
-                    const int k = (second ? kb - A.blocks1 : kb) * kBlock;
-                    if constexpr (kAmn) {
-                        tma_load_pair(pa, ma, bar, m, k);
-                        tma_load_pair(pa + kOperand / 2, ma, bar, m + 64, k);
-                    } else {
-                        tma_load_pair(pa, second ? &a2 : ma, bar, k, m);
+                    if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(sh.full + s, 2 * kStage);
+                        const uint32_t bar = full0 + 8 * s;
+                        unsigned char *pa = stages + s * kStage, *pb = pa + kOperand;
+                        const bool second = kMode == kDx && kb >= A.blocks1;
+                        const int k = (second ? kb - A.blocks1 : kb) * kBlock;
+                        if constexpr (kAmn) {
+                            tma_load_pair(pa, ma, bar, m, k);
+                            tma_load_pair(pa + kOperand / 2, ma, bar, m + 64, k);
+                        } else {
+                            tma_load_pair(pa, second ? &a2 : ma, bar, k, m);
+                        }
+                        if constexpr (kBmn) {
+                            const CUtensorMap *mb = second ? &b2 : &b1;
+                            tma_load_pair(pb, mb, bar, n, k);
+                            tma_load_pair(pb + kOperand / 2, mb, bar, n + 64, k);
+                        } else {
+                            tma_load_pair(pb, gated && rank ? &b2 : &b1, bar, k, n);
+                        }
                     }
-                    if constexpr (kBmn) {
-                        const CUtensorMap *mb = second ? &b2 : &b1;
-                        tma_load_pair(pb, mb, bar, n, k);
-                        tma_load_pair(pb + kOperand / 2, mb, bar, n + 64, k);
-                    } else {
-                        tma_load_pair(pb, gated && rank ? &b2 : &b1, bar, k, n);
-                    }
+                    __syncwarp();
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
             if (!ok) let_land();
-        } else if (warp == kEpiWarps + 1 && lane == 0 && rank == 0) {  // MMA
+        } else if (warp == kEpiWarps + 1 && rank == 0) {  // ---------- MMA
             constexpr uint32_t idesc = instruction_desc(kF8, 256, 256, kAmn, kBmn);
-            constexpr uint32_t kStepA = kAmn ? 2048 : 32, kStepB = kBmn ? 2048 : 32;
+            constexpr uint64_t kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;
             const uint32_t base = smem_u32(stages);
             int s = 0, buf = 0;
             uint32_t ph = 0, tph = 1;
@@ -130,17 +134,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
             for (Walk w(P, unit); ok && w.next();) {
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     const bool fresh = kF8 || kb == w.k0;
-                    if (fresh && !(ok = wait_phase(sh.tempty + buf, tph, dead))) break;
-                    if (!(ok = wait_phase(sh.full + s, ph, dead))) break;
+                    if (fresh && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
+                    if (!(ok = warp_wait(sh.full + s, ph, dead))) break;
                     tc_fence_after();
-                    const uint32_t pa = base + s * kStage, pb = pa + kOperand;
+                    const uint64_t da = operand_desc(base + s * kStage, kOperand / 2);
+                    const uint64_t db = operand_desc(base + s * kStage + kOperand, kOperand / 2);
+                    const bool last = kF8 || kb + 1 == w.k1;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma<2, kF8>(tmem + buf * 256, operand_desc(pa + i * kStepA, kOperand / 2),
-                                    operand_desc(pb + i * kStepB, kOperand / 2), idesc, !(fresh && i == 0));
-                    mma_commit_to<2>(sh.empty + s);
-                    if (kF8 || kb + 1 == w.k1) {
-                        mma_commit_to<2>(sh.tfull + buf);
+                        for (int i = 0; i < 4; ++i)
+                            mma<2, kF8>(tmem + buf * 256, da + i * kStepA, db + i * kStepB, idesc, !(fresh && i == 0));
+                        mma_commit_to<2>(sh.empty + s);
+                        if (last) mma_commit_to<2>(sh.tfull + buf);
+                    }
+                    __syncwarp();
+                    if (last) {
                         buf ^= 1;
                         if (buf == 0) tph ^= 1;
                     }
