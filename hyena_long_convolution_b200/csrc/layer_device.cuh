@@ -50,7 +50,7 @@ __device__ __forceinline__ float scale_of(unsigned int amax_bits)
 // takes 151, but holds registers that cost a CTA an SM with a bf16 residual (8192 x
 // 4096 with one scale per row: 61) and with four vectors a thread (65536 x 1024: 61).
 template <bool kPairs>
-__device__ __forceinline__ void store_e4m3x8(uint8_t *p, float (&v)[8], float scale)
+__device__ __forceinline__ uint2 e4m3x8(float (&v)[8], float scale)
 {
     if (scale < 0x1p-60f) {  // the same quotients, with no subnormal remainder
         scale *= 0x1p+64f;
@@ -77,7 +77,13 @@ __device__ __forceinline__ void store_e4m3x8(uint8_t *p, float (&v)[8], float sc
     uint2 q;
     q.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
     q.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-    *reinterpret_cast<uint2 *>(p) = q;
+    return q;
+}
+
+template <bool kPairs>
+__device__ __forceinline__ void store_e4m3x8(uint8_t *p, float (&v)[8], float scale)
+{
+    *reinterpret_cast<uint2 *>(p) = e4m3x8<kPairs>(v, scale);
 }
 
 }  // namespace hyena

@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(256) slopes_kernel(const FfnBackArgs A, uint16
             a[j] = d[j] * u[j] * s.y;
             b[j] = d[j] * s.x;
         }
-        store_bf16_row<8>(dg + i * 8, a, 8);
-        store_bf16_row<8>(du + i * 8, b, 8);
+        *reinterpret_cast<uint4 *>(dg + i * 8) = pack_bf16(a);
+        *reinterpret_cast<uint4 *>(du + i * 8) = pack_bf16(b);
     }
 }
 

@@ -143,40 +143,68 @@ __device__ __forceinline__ void load8_f32(float (&v)[8], const float *p)
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-// kV consecutive values of a row that ends after `left` of them (a multiple of 8,
-// as is every row's start).
-template <int kV>
-__device__ __forceinline__ void store_bf16_row(uint16_t *p, const float *v, int left)
+// 8 values to 16 bytes of bf16.
+__device__ __forceinline__ uint4 pack_bf16(const float *v)
 {
+    uint4 q;
+    q.x = float2_to_bf16x2(make_float2(v[0], v[1]));
+    q.y = float2_to_bf16x2(make_float2(v[2], v[3]));
+    q.z = float2_to_bf16x2(make_float2(v[4], v[5]));
+    q.w = float2_to_bf16x2(make_float2(v[6], v[7]));
+    return q;
+}
+
+// A warp's 32 rows of outputs, a row a lane in registers, written a row by several
+// lanes: through 4 KB of shared memory, in rows of 128 bytes whose 16-byte chunks
+// are permuted by the row (chunk c of row r at c ^ (r % 8)), which keeps both ways
+// free of bank conflicts.  Straight from the registers a store touches 32 rows, 16
+// bytes of each: 8000 cycles for a CTA's 128 x 256 sums, this way 4000.
+constexpr int kPatch = 4096;
+
+// One patch of kChunks x 16 bytes a row: `chunk(c)` gives a lane's 16 bytes, row r
+// goes to p + r * pitch (bytes), `left` bytes of it, `rows` rows.
+template <int kChunks, class F>
+__device__ __forceinline__ void store_patch(unsigned char *patch, int lane, unsigned char *p, long long pitch, int left,
+                                            int rows, F chunk)
+{
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kV; i += 8) {
-        if (i >= left) break;
-        uint4 q;
-        q.x = float2_to_bf16x2(make_float2(v[i], v[i + 1]));
-        q.y = float2_to_bf16x2(make_float2(v[i + 2], v[i + 3]));
-        q.z = float2_to_bf16x2(make_float2(v[i + 4], v[i + 5]));
-        q.w = float2_to_bf16x2(make_float2(v[i + 6], v[i + 7]));
-        *reinterpret_cast<uint4 *>(p + i) = q;
+    for (int c = 0; c < kChunks; ++c)
+        *reinterpret_cast<uint4 *>(patch + lane * 128 + ((c ^ (lane & 7)) << 4)) = chunk(c);
+    __syncwarp();
+    constexpr int kRows = 32 / kChunks;  // at a time
+    const int c = lane % kChunks;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int r = i * kRows + lane / kChunks;
+        const uint4 q = *reinterpret_cast<const uint4 *>(patch + r * 128 + ((c ^ (r & 7)) << 4));
+        unsigned char *to = p + r * pitch + c * 16;
+        if (r >= rows || c * 16 >= left) continue;
+        if (c * 16 + 16 <= left)
+            *reinterpret_cast<uint4 *>(to) = q;
+        else  // 8 codes
+            *reinterpret_cast<uint2 *>(to) = make_uint2(q.x, q.y);
     }
 }
 
-template <int kV>
-__device__ __forceinline__ void store_f32_row(float *p, const float *v, int left)
+// 64 values of each of the warp's rows as bf16 or fp32; `left` of them lie inside.
+__device__ __forceinline__ void store_rows(unsigned char *patch, int lane, void *p, bool f32, long long at, long long ld,
+                                           const float *v, int left, int rows)
 {
-#pragma unroll
-    for (int i = 0; i < kV; i += 4) {
-        if (i >= left) break;
-        *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    if (f32) {
+        unsigned char *to = static_cast<unsigned char *>(p) + at * 4;
+        store_patch<8>(patch, lane, to, ld * 4, left * 4, rows, [&](int c) {
+            return make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                              __float_as_uint(v[4 * c + 3]));
+        });
+        store_patch<8>(patch, lane, to + 128, ld * 4, left * 4 - 128, rows, [&](int c) {
+            return make_uint4(__float_as_uint(v[32 + 4 * c]), __float_as_uint(v[33 + 4 * c]),
+                              __float_as_uint(v[34 + 4 * c]), __float_as_uint(v[35 + 4 * c]));
+        });
+    } else {
+        store_patch<8>(patch, lane, static_cast<unsigned char *>(p) + at * 2, ld * 2, left * 2, rows,
+                       [&](int c) { return pack_bf16(v + 8 * c); });
     }
-}
-
-template <int kV>
-__device__ __forceinline__ void store_row(void *p, bool f32, long long at, const float *v, int left)
-{
-    if (f32)
-        store_f32_row<kV>(static_cast<float *>(p) + at, v, left);
-    else
-        store_bf16_row<kV>(static_cast<uint16_t *>(p) + at, v, left);
 }
 
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi)); }

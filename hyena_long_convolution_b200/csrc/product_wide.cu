@@ -18,7 +18,7 @@ constexpr int kTile = 128;                       // rows of a CTA's operands
 constexpr int kStages = 6;
 constexpr int kOperand = kTile * kRowBytes;      // 16 KB
 constexpr int kStage = 2 * kOperand;
-constexpr int kSmem = kStages * kStage + 1024;
+constexpr int kSmem = kStages * kStage + kEpiWarps * kPatch + 1024;
 constexpr int kHalf = 64;                        // columns of each group of 128 a thread has
 constexpr int kBand = 8;                         // tile rows that are walked together, for L2
 
@@ -134,8 +134,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
             for (Walk w(P, unit); ok && w.next();) {
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     const bool fresh = kF8 || kb == w.k0;
-                    if (fresh && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
                     if (!(ok = warp_wait(sh.full + s, ph, dead))) break;
+                    if (fresh && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
                     tc_fence_after();
                     const uint64_t da = operand_desc(base + s * kStage, kOperand / 2);
                     const uint64_t db = operand_desc(base + s * kStage + kOperand, kOperand / 2);
@@ -164,6 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + hh * kHalf;
         const uint32_t tempty0 = cluster_addr(sh.tempty, 0), tempty1 = cluster_addr(sh.tempty + 1, 0);
         const int groups = P.blocks;  // of codes: one a k-block
+        unsigned char *patch = stages + kStages * kStage + warp * kPatch;
         int buf = 0;
         uint32_t tph = 0;
         bool ok = true;
@@ -247,26 +248,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                 continue;
             const int n = tn * A.tile_cols + hh * kHalf;
             const int left = A.cols - n;
+            // the warp's first row and how many there are (maybe none)
+            const long long m0 = m - lane;
+            auto rows_of = [&](long long r) { return static_cast<int>(A.rows - r < 32 ? A.rows - r : 32); };
             if constexpr (kMode != kForward) {
-                long long r = m;
+                long long r = m0;
                 uint16_t *c = A.c[0];
                 if (kMode == kDw && tm >= P.tiles_m / 2) {
                     r -= P.tiles_m / 2 * 256ll;
                     c = A.c[1];
                 }
-                if (r < A.rows) {
-                    store_bf16_row<kHalf>(c + r * A.ld_c + n, v, left);
-                    store_bf16_row<kHalf>(c + r * A.ld_c + n + kTile, v + kHalf, left - kTile);
-                }
+                store_rows(patch, lane, c, false, r * A.ld_c + n, A.ld_c, v, left, rows_of(r));
+                store_rows(patch, lane, c, false, r * A.ld_c + n + kTile, A.ld_c, v + kHalf, left - kTile, rows_of(r));
             } else if (!A.a.gated) {
-                if (m < A.rows) {
-                    store_row<kHalf>(A.a.y, A.a.y_f32, m * A.a.ld_y + n, v, left);
-                    store_row<kHalf>(A.a.y, A.a.y_f32, m * A.a.ld_y + n + kTile, v + kHalf, left - kTile);
-                }
+                store_rows(patch, lane, A.a.y, A.a.y_f32, m0 * A.a.ld_y + n, A.a.ld_y, v, left, rows_of(m0));
+                store_rows(patch, lane, A.a.y, A.a.y_f32, m0 * A.a.ld_y + n + kTile, A.a.ld_y, v + kHalf, left - kTile,
+                           rows_of(m0));
             } else {
-                if (A.a.g && m < A.rows) {
-                    store_row<kHalf>(A.a.g, A.a.g_f32, m * A.a.ld_g + n, v, left);
-                    store_row<kHalf>(A.a.u, A.a.g_f32, m * A.a.ld_g + n, v + kHalf, left);
+                if (A.a.g) {
+                    store_rows(patch, lane, A.a.g, A.a.g_f32, m0 * A.a.ld_g + n, A.a.ld_g, v, left, rows_of(m0));
+                    store_rows(patch, lane, A.a.u, A.a.g_f32, m0 * A.a.ld_g + n, A.a.ld_g, v + kHalf, left, rows_of(m0));
                 }
                 gate<kHalf>(v, A.a.act);
                 if (kF8 && A.a.q) {
@@ -280,17 +281,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                     mx = max(mx, sh.amax[tid ^ kTile]);
                     named_sync(1, kEpiThreads);
                     const float scale = scale_of(mx);
-                    if (m < A.rows) {
-                        uint8_t *q = A.a.q + m * A.a.ld_q + n;
-#pragma unroll
-                        for (int i = 0; i < kHalf; i += 8) {
-                            if (i >= left) break;
-                            store_e4m3x8<true>(q + i, reinterpret_cast<float(&)[8]>(v[i]), scale);
-                        }
-                        if (hh == 0) A.a.scales[m * P.tiles_n + tn] = scale;
-                    }
-                } else if (m < A.rows) {
-                    store_bf16_row<kHalf>(static_cast<uint16_t *>(A.a.y) + m * A.a.ld_y + n, v, left);
+                    store_patch<4>(patch, lane, A.a.q + m0 * A.a.ld_q + n, A.a.ld_q, left, rows_of(m0), [&](int c) {
+                        const uint2 lo = e4m3x8<true>(reinterpret_cast<float(&)[8]>(v[16 * c]), scale);
+                        const uint2 hi = e4m3x8<true>(reinterpret_cast<float(&)[8]>(v[16 * c + 8]), scale);
+                        return make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    });
+                    if (hh == 0 && m < A.rows) A.a.scales[m * P.tiles_n + tn] = scale;
+                } else {
+                    store_rows(patch, lane, A.a.y, false, m0 * A.a.ld_y + n, A.a.ld_y, v, left, rows_of(m0));
                 }
             }
         }
