@@ -168,10 +168,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
         int buf = 0;
         uint32_t tph = 0;
         bool ok = true;
-        for (Walk w(P, unit); w.next();) {
-            int tm, tn;
+        Walk w(P, unit);
+        int tm = 0, tn = 0;
+        const float *sx = nullptr, *s1 = nullptr, *s2 = nullptr;
+        float x = 0.f, f1 = 0.f, f2 = 0.f;
+        bool live = false;
+        // The next tile and, of codes, the scales of its first k-block: asked for before
+        // the outputs of the tile in hand are written.
+        auto advance = [&] {
+            if (!w.next()) return false;
             place(w.tile, tm, tn);
-            const long long m = static_cast<long long>(tm) * 256 + rank * kTile + row;
+            if constexpr (kF8) {
+                const long long m = static_cast<long long>(tm) * 256 + rank * kTile + row;
+                live = m < A.rows;
+                sx = A.a.sx + (live ? m * A.a.sx_row + static_cast<long long>(w.k0) * A.a.sx_step : 0);
+                const int n1 = A.a.gated ? tn : 2 * tn;
+                // the second group of 128 columns may lie outside
+                const int n2 = n1 + (!A.a.gated && tn * A.tile_cols + kTile < A.cols ? 1 : 0);
+                s1 = A.a.sw1 + static_cast<long long>(n1) * groups + w.k0;
+                s2 = (A.a.gated ? A.a.sw2 : A.a.sw1) + static_cast<long long>(n2) * groups + w.k0;
+                x = live ? __ldg(sx) : 0.f;
+                f1 = __ldg(s1);
+                f2 = __ldg(s2);
+            }
+            return true;
+        };
+        for (bool more = advance(); more;) {
+            const int tile = w.tile, k0 = w.k0, k1 = w.k1, row0 = tm, col0 = tn;
             float v[2 * kHalf];
             auto done_reading = [&] {
                 tc_fence_before();
@@ -183,24 +206,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
             if constexpr (kF8) {
 #pragma unroll
                 for (int i = 0; i < 2 * kHalf; ++i) v[i] = 0.f;
-                // scales of the first k-block; then each one's while the one before is summed
-                const bool live = m < A.rows;
-                const float *sx = A.a.sx + (live ? m * A.a.sx_row : 0);
-                const float *s1 = A.a.gated ? A.a.sw1 + static_cast<long long>(tn) * groups
-                                            : A.a.sw1 + 2ll * tn * groups;
-                const bool two = A.a.gated || tn * A.tile_cols + kTile < A.cols;
-                const float *s2 = A.a.gated ? A.a.sw2 + static_cast<long long>(tn) * groups : s1 + (two ? groups : 0);
-                float x = live ? __ldg(sx + static_cast<long long>(w.k0) * A.a.sx_step) : 0.f;
-                float f1 = __ldg(s1 + w.k0), f2 = __ldg(s2 + w.k0);
-                for (int kb = w.k0; kb < w.k1; ++kb) {
+                for (int kb = k0; kb < k1; ++kb) {
                     const float2 c1 = bcast2(x * f1), c2 = bcast2(x * f2);
-                    if (kb + 1 < w.k1) {
-                        x = live ? __ldg(sx + static_cast<long long>(kb + 1) * A.a.sx_step) : 0.f;
-                        f1 = __ldg(s1 + kb + 1);
-                        f2 = __ldg(s2 + kb + 1);
+                    if (kb + 1 < k1) {  // the next k-block's scales while this one's sums come in
+                        sx += A.a.sx_step;
+                        x = live ? __ldg(sx) : 0.f;
+                        f1 = __ldg(++s1);
+                        f2 = __ldg(++s2);
                     }
-                    if (ok) ok = wait_phase(sh.tfull + buf, tph, dead);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = ok && warp_wait(sh.tfull + buf, tph, dead);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t at = lanes + buf * 256;
@@ -209,7 +223,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         tmem_wait(d[i & 1]);
-                        if (i < 7) tmem_ld(d[(i + 1) & 1], at + (i + 1) / 4 * kTile + (i + 1) % 4 * 16);
+                        if (i < 7)
+                            tmem_ld(d[(i + 1) & 1], at + (i + 1) / 4 * kTile + (i + 1) % 4 * 16);
+                        else
+                            done_reading();
                         const float2 c = i < 4 ? c1 : c2;
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
@@ -219,11 +236,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                             v[i * 16 + j + 1] = r.y;
                         }
                     }
-                    done_reading();
                 }
             } else {
-                if (ok) ok = wait_phase(sh.tfull + buf, tph, dead);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = ok && warp_wait(sh.tfull + buf, tph, dead);
                 if (ok) {
                     tc_fence_after();
                     const uint32_t at = lanes + buf * 256;
@@ -243,10 +258,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * kHalf; ++i) v[i] = __uint_as_float(0x7fffffffu);
             }
-            if (w.k1 - w.k0 < P.blocks &&
-                !join_parts<2>(v, P, unit, rank, w.tile, w.k0, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
+            more = advance();
+            if (k1 - k0 < P.blocks &&
+                !join_parts<2>(v, P, unit, rank, tile, k0, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
                 continue;
-            const int n = tn * A.tile_cols + hh * kHalf;
+            const long long m = static_cast<long long>(row0) * 256 + rank * kTile + row;
+            const int n = col0 * A.tile_cols + hh * kHalf;
             const int left = A.cols - n;
             // the warp's first row and how many there are (maybe none)
             const long long m0 = m - lane;
@@ -254,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
             if constexpr (kMode != kForward) {
                 long long r = m0;
                 uint16_t *c = A.c[0];
-                if (kMode == kDw && tm >= P.tiles_m / 2) {
+                if (kMode == kDw && row0 >= P.tiles_m / 2) {
                     r -= P.tiles_m / 2 * 256ll;
                     c = A.c[1];
                 }
@@ -286,7 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                         const uint2 hi = e4m3x8<true>(reinterpret_cast<float(&)[8]>(v[16 * c + 8]), scale);
                         return make_uint4(lo.x, lo.y, hi.x, hi.y);
                     });
-                    if (hh == 0 && m < A.rows) A.a.scales[m * P.tiles_n + tn] = scale;
+                    if (hh == 0 && m < A.rows) A.a.scales[m * P.tiles_n + col0] = scale;
                 } else {
                     store_rows(patch, lane, A.a.y, false, m0 * A.a.ld_y + n, A.a.ld_y, v, left, rows_of(m0));
                 }
