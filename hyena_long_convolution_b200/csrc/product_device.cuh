@@ -85,6 +85,12 @@ __device__ __forceinline__ void named_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Brings a tensor map close, before the first load that needs it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // A 2-D TMA load of one CTA of a pair, counted by a barrier of either.
 __device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t cluster_bar, int c0, int c1)
 {

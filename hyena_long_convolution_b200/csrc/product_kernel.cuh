@@ -105,22 +105,25 @@ __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int un
     return true;
 }
 
-// g[i] <- act(g[i]) u[i]
+// g[i] <- act(g[i]) u[i], the first `count` of kV
 template <int kAct, int kV>
-__device__ __forceinline__ void gate(float (&v)[2 * kV])
+__device__ __forceinline__ void gate(float (&v)[2 * kV], int count)
 {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = activation<kAct>(v[i]) * v[kV + i];
+    for (int i = 0; i < kV; ++i) {
+        if (i >= count) break;
+        v[i] = activation<kAct>(v[i]) * v[kV + i];
+    }
 }
 
 template <int kV>
-__device__ __forceinline__ void gate(float (&v)[2 * kV], int act)
+__device__ __forceinline__ void gate(float (&v)[2 * kV], int act, int count)
 {
     switch (act) {
-        case HYENA_ACT_SILU: gate<HYENA_ACT_SILU, kV>(v); break;
-        case HYENA_ACT_GELU: gate<HYENA_ACT_GELU, kV>(v); break;
-        case HYENA_ACT_GELU_TANH: gate<HYENA_ACT_GELU_TANH, kV>(v); break;
-        default: gate<HYENA_ACT_IDENTITY, kV>(v); break;
+        case HYENA_ACT_SILU: gate<HYENA_ACT_SILU, kV>(v, count); break;
+        case HYENA_ACT_GELU: gate<HYENA_ACT_GELU, kV>(v, count); break;
+        case HYENA_ACT_GELU_TANH: gate<HYENA_ACT_GELU_TANH, kV>(v, count); break;
+        default: gate<HYENA_ACT_IDENTITY, kV>(v, count); break;
     }
 }
 

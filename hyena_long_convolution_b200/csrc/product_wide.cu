@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                     store_rows(patch, lane, A.a.g, A.a.g_f32, m0 * A.a.ld_g + n, A.a.ld_g, v, left, rows_of(m0));
                     store_rows(patch, lane, A.a.u, A.a.g_f32, m0 * A.a.ld_g + n, A.a.ld_g, v + kHalf, left, rows_of(m0));
                 }
-                gate<kHalf>(v, A.a.act);
+                gate<kHalf>(v, A.a.act, kHalf);
                 if (kF8 && A.a.q) {
                     // the largest of the row's 128 values: this half's and the other's
                     unsigned int mx = 0;
