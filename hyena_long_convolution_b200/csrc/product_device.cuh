@@ -59,12 +59,16 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// The address of `p` in CTA `rank` of this cluster.
-__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+// The address of shared memory (of `p`) in CTA `rank` of this cluster.
+__device__ __forceinline__ uint32_t cluster_addr_of(uint32_t addr, uint32_t rank)
 {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     return a;
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    return cluster_addr_of(smem_u32(p), rank);
 }
 
 __device__ __forceinline__ void cluster_sync()

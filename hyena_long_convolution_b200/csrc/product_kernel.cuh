@@ -105,15 +105,45 @@ __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int un
     return true;
 }
 
+// Eight of a thread's values at a time, in a loop that stays one: each turn ends by
+// moving all of them eight places on, and the last leaves them where they were.
+// Code run once per value, 64 times over, waits for its instructions: with 128
+// tokens the gate took 13 us that way and the codes 40.
+template <int kV>
+__device__ __forceinline__ void turn(float *v)
+{
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < kV - 8; ++i) v[i] = v[i + 8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[kV - 8 + i] = t[i];
+}
+
+template <int kV, class F>
+__device__ __forceinline__ void by_eights(F f)
+{
+    if constexpr (kV == 8) {
+        f(0);
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < kV; j += 8) f(j);
+    }
+}
+
 // g[i] <- act(g[i]) u[i], the first `count` of kV
 template <int kAct, int kV>
 __device__ __forceinline__ void gate(float (&v)[2 * kV], int count)
 {
+    by_eights<kV>([&](int j) {
+        if (j < count) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        if (i >= count) break;
-        v[i] = activation<kAct>(v[i]) * v[kV + i];
-    }
+            for (int i = 0; i < 8; ++i) v[i] = activation<kAct>(v[i]) * v[kV + i];
+        }
+        turn<kV>(v);
+        turn<kV>(v + kV);
+    });
 }
 
 template <int kV>
@@ -218,8 +248,8 @@ template <int kStages>
 struct ProductShared {
     uint64_t full[kStages];   // a stage's operands arrived
     uint64_t empty[kStages];  // the MMAs that read a stage are done
-    uint64_t tfull[2];        // a half of tensor memory holds sums
-    uint64_t tempty[2];       // it has been read
+    uint64_t tfull[8];        // a part of tensor memory holds sums
+    uint64_t tempty[8];       // it has been read
     uint32_t tmem;
     unsigned int dead;        // a wait ran out
     unsigned int flag;

@@ -26,6 +26,9 @@ struct Narrow {
     static constexpr int kSmem = kStages * kStage + 1024;
     static constexpr int kH = kNT / 2;            // tokens of a thread
     static constexpr int kC = kH < 16 ? kH : 16;  // of them at a time
+    // Parts of tensor memory that sums alternate between.  Codes' sums go to registers
+    // after each 128 k, and a turn through both takes longer than the MMAs between.
+    static constexpr int kBufs = 512 / (kG * kNT) < 8 ? 512 / (kG * kNT) : 8;
     static_assert(kG * kNT * kTile * 4 <= kStages * kStage, "a tile's sums fit the stages");
 };
 
@@ -57,7 +60,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                           const __grid_constant__ CUtensorMap m2, const __grid_constant__ NarrowArgs A)
 {
     using T = Narrow<kNT, kGated>;
-    constexpr int kStages = T::kStages, kStage = T::kStage, kH = T::kH, kC = T::kC, kG = T::kG;
+    constexpr int kStages = T::kStages, kStage = T::kStage, kH = T::kH, kC = T::kC, kG = T::kG, kBufs = T::kBufs;
     constexpr int kBlock = kF8 ? 128 : 64;  // k of a block
     extern __shared__ unsigned char raw[];
     __shared__ ProductShared<kStages> sh;
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             mbar_init(sh.full + i, 1);
             mbar_init(sh.empty + i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(sh.tfull + i, 1);
             mbar_init(sh.tempty + i, kEpiWarps);
         }
@@ -134,16 +137,13 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                         for (int g = 0; g < kG; ++g)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                mma<1, kF8>(tmem + buf * 256 + g * kTile, dw + (g * kOperand + i * 32) / 16, dx + i * 2,
+                                mma<1, kF8>(tmem + (buf * kG + g) * kNT, dw + (g * kOperand + i * 32) / 16, dx + i * 2,
                                             idesc, !(fresh && i == 0));
                         mma_commit_to<1>(sh.empty + s);
                         if (last) mma_commit_to<1>(sh.tfull + buf);
                     }
                     __syncwarp();
-                    if (last) {
-                        buf ^= 1;
-                        if (buf == 0) tph ^= 1;
-                    }
+                    if (last && ++buf == kBufs) buf = 0, tph ^= 1;
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sh.tempty + buf);
-                buf ^= 1;
-                if (buf == 0) tph ^= 1;
+                if (++buf == kBufs) buf = 0, tph ^= 1;
             };
             if constexpr (kF8) {
 #pragma unroll
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     if (!ok) break;
                     tc_fence_after();
                     __syncwarp();
-                    const uint32_t at = lanes + buf * 256;
+                    const uint32_t at = lanes + buf * (kG * kNT);
                     constexpr int kChunks = kH / kC;
                     float d[2][kC];
                     tmem_ld(d[0], at);
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     for (int i = 0; i < kG * kChunks; ++i) {
                         tmem_wait(d[i & 1]);
                         if (i + 1 < kG * kChunks)
-                            tmem_ld(d[(i + 1) & 1], at + (i + 1) / kChunks * kTile + (i + 1) % kChunks * kC);
+                            tmem_ld(d[(i + 1) & 1], at + (i + 1) / kChunks * kNT + (i + 1) % kChunks * kC);
 #pragma unroll
                         for (int j = 0; j < kC; j += 2) {
                             const float2 x = *reinterpret_cast<const float2 *>(&token_scale[warp][i % kChunks * kC + j]);
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 #pragma unroll
                     for (int i = 0; i < kG * kH / kC; ++i) {
                         float d[kC];
-                        tmem_ld(d, lanes + buf * 256 + i / (kH / kC) * kTile + i % (kH / kC) * kC);
+                        tmem_ld(d, lanes + (buf * kG + i / (kH / kC)) * kNT + i % (kH / kC) * kC);
                         tmem_wait(d);
 #pragma unroll
                         for (int j = 0; j < kC; ++j) v[i * kC + j] = d[j];
@@ -252,66 +251,65 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 count = kH / share;
                 const int t0 = (2 * rank + hh) * count;
                 m = static_cast<long long>(tm) * kNT + t0;
+                const uint32_t at = smem_u32(red + t0 * kTile + row);
 #pragma unroll
-                for (int j = 0; j < kH / 2; ++j) {
-                    if (j >= count) break;
+                for (int i = 0; i < kG * kH; ++i) v[i] = 0.f;
+#pragma unroll 1
+                for (int r = 0; r < share; ++r) {  // in the order of k
+                    const uint32_t from = cluster_addr_of(at, r);
 #pragma unroll
-                    for (int g = 0; g < kG; ++g) {
-                        float sum = 0.f;
-                        for (int r = 0; r < share; ++r)
-                            sum += ld_cluster(cluster_addr(red + (g * kNT + t0 + j) * kTile + row, r));
-                        v[g * kH + j] = sum;
-                    }
+                    for (int g = 0; g < kG; ++g)
+#pragma unroll
+                        for (int j = 0; j < kH / 2; ++j)
+                            if (j < count) v[g * kH + j] += ld_cluster(from + (g * kNT + j) * kTile * 4);
                 }
             }
             const int n = tn * kTile + row;
             const int tokens = static_cast<int>(A.a.M - m < count ? A.a.M - m : count);  // may be negative
             const bool inside = n < A.a.N;
+            // f(j, values of token j) for each token inside
+            auto each = [&](auto f) {
+                by_eights<kH>([&](int j) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (j + i < tokens) f(j + i, v[i], v[kGated ? kH + i : i]);
+                    if (kH > 8) turn<kH>(v);
+                    if (kH > 8 && kGated) turn<kH>(v + kH);
+                });
+            };
             if constexpr (!kGated) {
-#pragma unroll
-                for (int j = 0; j < kH; ++j) {
-                    if (j >= tokens) break;
-                    if (inside) store_one(A.a.y, A.a.y_f32, (m + j) * A.a.ld_y + n, v[j]);
-                }
+                each([&](int j, float y, float) {
+                    if (inside) store_one(A.a.y, A.a.y_f32, (m + j) * A.a.ld_y + n, y);
+                });
             } else {
-                if (A.a.g && inside) {
-#pragma unroll
-                    for (int j = 0; j < kH; ++j) {
-                        if (j >= tokens) break;
-                        store_one(A.a.g, A.a.g_f32, (m + j) * A.a.ld_g + n, v[j]);
-                        store_one(A.a.u, A.a.g_f32, (m + j) * A.a.ld_g + n, v[kH + j]);
-                    }
-                }
+                if (A.a.g && inside)
+                    each([&](int j, float g, float u) {
+                        store_one(A.a.g, A.a.g_f32, (m + j) * A.a.ld_g + n, g);
+                        store_one(A.a.u, A.a.g_f32, (m + j) * A.a.ld_g + n, u);
+                    });
                 gate<kH>(v, A.a.act, tokens);
                 if (kF8 && A.a.q) {
                     // the largest of each token's 128 values: four warps' lanes
-#pragma unroll
-                    for (int j = 0; j < kH; ++j) {
-                        if (j >= tokens) break;
-                        const unsigned int b = inside ? __float_as_uint(v[j]) & 0x7fffffffu : 0u;
+                    each([&](int j, float y, float) {
+                        const unsigned int b = inside ? __float_as_uint(y) & 0x7fffffffu : 0u;
                         const unsigned int mx = __reduce_max_sync(0xffffffffu, b);
                         if (lane == 0) token_max[warp][j] = mx;
-                    }
+                    });
                     named_sync(2 + hh, kEpiThreads / 2);
-#pragma unroll
-                    for (int j = 0; j < kH; ++j) {
-                        if (j >= tokens) break;
+                    each([&](int j, float y, float) {
                         unsigned int mx = token_max[4 * hh][j];
 #pragma unroll
                         for (int i = 1; i < 4; ++i) mx = max(mx, token_max[4 * hh + i][j]);
                         const float scale = scale_of(mx);
                         if (inside)
-                            A.a.q[(m + j) * A.a.ld_q + n] =
-                                __nv_cvt_float_to_fp8(v[j] / scale, __NV_SATFINITE, __NV_E4M3);
+                            A.a.q[(m + j) * A.a.ld_q + n] = __nv_cvt_float_to_fp8(y / scale, __NV_SATFINITE, __NV_E4M3);
                         if (row == 0) A.a.scales[(m + j) * (A.tiles / A.tiles_m) + tn] = scale;
-                    }
+                    });
                     named_sync(2 + hh, kEpiThreads / 2);
-                } else if (inside) {
-#pragma unroll
-                    for (int j = 0; j < kH; ++j) {
-                        if (j >= tokens) break;
-                        static_cast<uint16_t *>(A.a.y)[(m + j) * A.a.ld_y + n] = bf16_bits(v[j]);
-                    }
+                } else {
+                    each([&](int j, float y, float) {
+                        if (inside) static_cast<uint16_t *>(A.a.y)[(m + j) * A.a.ld_y + n] = bf16_bits(y);
+                    });
                 }
             }
         }
