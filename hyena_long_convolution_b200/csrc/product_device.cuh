@@ -34,14 +34,16 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
     return wait_slow(bar, parity, dead);
 }
 
-// One lane of a whole warp, the same at every call; the loops around it are run by
-// all lanes, so that what they hand to TMA and the tensor cores stays in uniform
-// registers.
-__device__ __forceinline__ bool elect_one()
+// 1 in one lane of a whole warp.  The loops that feed TMA and the tensor cores are
+// run by all lanes of a warp, and only the instructions themselves by this one, by
+// predicate: operands stay in uniform registers and the warp never parts.  (A
+// k-block's turn of the MMA warp, by a branch around them: 770 cycles, of which the
+// MMAs take 120.)
+__device__ __forceinline__ uint32_t elected_lane()
 {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
+    return p;
 }
 
 // wait_phase by all lanes of a warp, which agree on the outcome.
@@ -95,14 +97,36 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// A 2-D TMA load of one CTA of a pair, counted by a barrier of either.
-__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, uint32_t cluster_bar, int c0, int c1)
+// The lane with `on` != 0 ...
+// ... arrives at a barrier and adds to the bytes that it waits for;
+__device__ __forceinline__ void expect_tx(uint32_t on, uint64_t *bar, uint32_t bytes)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(cluster_bar)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], "
+        "%2;\n\t}" ::"r"(on),
+        "r"(smem_u32(bar)), "r"(bytes)
         : "memory");
+}
+
+// ... loads a box of a matrix into this CTA's shared memory, counted by its barrier,
+// or, of a pair of CTAs, by a barrier of either.
+template <int kCtas>
+__device__ __forceinline__ void load_box(uint32_t on, void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1)
+{
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%1], [%2, {%3, %4}], [%5];\n\t}" ::"r"(on),
+            "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%1], [%2, {%3, %4}], [%5];\n\t}" ::"r"(on),
+            "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
 }
 
 // ---------------------------------------------------------------- tcgen05
@@ -156,15 +180,14 @@ __host__ __device__ constexpr uint32_t instruction_desc(bool f8, int m, int n, b
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// D (tensor memory) (+)= A B, one thread.
+// The lane with `on` != 0: D (tensor memory) (+)= A B.
 template <int kCtas, bool kF8>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
-    const uint32_t en = add ? 1u : 0u;
 #define HYENA_MMA(group, kind)                                                                                       \
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::" group ".kind::" kind        \
-                 " [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),                                                            \
-                 "l"(a), "l"(b), "r"(idesc), "r"(en)                                                                 \
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"                       \
+                 "@q tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),         \
+                 "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(on)                                                       \
                  : "memory")
     if constexpr (kCtas == 2) {
         if constexpr (kF8)
@@ -180,19 +203,24 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 #undef HYENA_MMA
 }
 
-// `bar` (of both CTAs of a pair) is told when the MMAs issued so far are done.
+// The lane with `on` != 0 has `bar` (of both CTAs of a pair) told when the MMAs that
+// it issued so far are done.
 template <int kCtas>
-__device__ __forceinline__ void mma_commit_to(uint64_t *bar)
+__device__ __forceinline__ void mma_commit_to(uint32_t on, uint64_t *bar)
 {
     if constexpr (kCtas == 2)
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                smem_u32(bar)),
-            "h"(static_cast<uint16_t>(3))
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+            "%1;\n\t}" ::"r"(smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3)), "r"(on)
             : "memory");
     else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                     : "memory");
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+            "r"(on)
+            : "memory");
 }
 
 // Consecutive fp32 columns of the warp's 32 lanes of tensor memory, a lane a

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     const int k0 = A.blocks * rank / share, k1 = A.blocks * (rank + 1) / share;
     volatile unsigned int *dead = &sh.dead;
 
-    if (warp == kEpiWarps && elect_one()) {
+    if (tid == kEpiThreads) {
         prefetch_map(&m1);
         prefetch_map(&mx);
         if (kGated) prefetch_map(&m2);
@@ -98,22 +98,21 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 
     if (warp >= kEpiWarps) {
         fewer_registers();
+        const uint32_t on = elected_lane();
+        int s = 0;
+        bool ok = true;
         if (warp == kEpiWarps) {  // ----------------------------------- TMA
-            int s = 0;
             uint32_t ph = 1;
-            bool ok = true;
             for (int tile = unit; ok && tile < A.tiles; tile += units) {
                 const int tn = tile / A.tiles_m, tm = tile - tn * A.tiles_m;
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
-                    if (elect_one()) {
-                        unsigned char *p = stages + s * kStage;
-                        mbar_arrive_expect_tx(sh.full + s, kStage);
-                        tma_load_2d(p, &m1, sh.full + s, kb * kBlock, tn * kTile);
-                        if (kGated) tma_load_2d(p + kOperand, &m2, sh.full + s, kb * kBlock, tn * kTile);
-                        tma_load_2d(p + kG * kOperand, &mx, sh.full + s, kb * kBlock, tm * kNT);
-                    }
-                    __syncwarp();
+                    unsigned char *p = stages + s * kStage;
+                    const uint32_t bar = smem_u32(sh.full + s);
+                    expect_tx(on, sh.full + s, kStage);
+                    load_box<1>(on, p, &m1, bar, kb * kBlock, tn * kTile);
+                    if (kGated) load_box<1>(on, p + kOperand, &m2, bar, kb * kBlock, tn * kTile);
+                    load_box<1>(on, p + kG * kOperand, &mx, bar, kb * kBlock, tm * kNT);
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
@@ -121,30 +120,32 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         } else if (warp == kEpiWarps + 1) {  // ----------------------- MMA
             constexpr uint32_t idesc = instruction_desc(kF8, kTile, kNT, false, false);
             const uint32_t base = smem_u32(stages);
-            int s = 0, buf = 0;
+            int buf = 0;
             uint32_t ph = 0, tph = 1;
-            bool ok = true;
+            bool stage_full = false, part_free = false;  // seen while the MMAs before were issued
             for (int tile = unit; ok && tile < A.tiles; tile += units) {
                 for (int kb = k0; kb < k1; ++kb) {
                     const bool fresh = kF8 || kb == k0, last = kF8 || kb + 1 == k1;
-                    if (!(ok = warp_wait(sh.full + s, ph, dead))) break;
-                    if (fresh && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
+                    if (!stage_full && !(ok = warp_wait(sh.full + s, ph, dead))) break;
+                    if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
                     tc_fence_after();
                     const uint64_t dw = operand_desc(base + s * kStage, 16);
                     const uint64_t dx = operand_desc(base + s * kStage + kG * kOperand, 16);
-                    if (elect_one()) {
+                    const uint32_t d = tmem + buf * (kG * kNT);
+                    uint64_t *const empty = sh.empty + s, *const tfull = sh.tfull + buf;
+                    if (++s == kStages) s = 0, ph ^= 1;
+                    if (last && ++buf == kBufs) buf = 0, tph ^= 1;
+                    const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int g = 0; g < kG; ++g)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma<1, kF8>(tmem + (buf * kG + g) * kNT, dw + (g * kOperand + i * 32) / 16, dx + i * 2,
-                                            idesc, !(fresh && i == 0));
-                        mma_commit_to<1>(sh.empty + s);
-                        if (last) mma_commit_to<1>(sh.tfull + buf);
-                    }
-                    __syncwarp();
-                    if (last && ++buf == kBufs) buf = 0, tph ^= 1;
-                    if (++s == kStages) s = 0, ph ^= 1;
+                            mma<1, kF8>(on, d + g * kNT, dw + (g * kOperand + i * 32) / 16, dx + i * 2, idesc,
+                                        fresh && i == 0 ? 0u : 1u);
+                    mma_commit_to<1>(on, empty);
+                    if (last) mma_commit_to<1>(on, tfull);
+                    stage_full = __all_sync(0xffffffffu, f);
+                    part_free = __all_sync(0xffffffffu, e);
                 }
             }
             if (!ok) let_land();

@@ -81,11 +81,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
 
     if (warp >= kEpiWarps) {
         fewer_registers();
+        const uint32_t on = elected_lane();
+        int s = 0;
+        bool ok = true;
         if (warp == kEpiWarps) {  // ----------------------------------- TMA
-            const uint32_t full0 = cluster_addr(sh.full, 0);
-            int s = 0;
+            const uint32_t full0 = cluster_addr(sh.full, 0), first = rank == 0 ? on : 0u;
             uint32_t ph = 1;
-            bool ok = true;
             for (Walk w(P, unit); ok && w.next();) {
                 int tm, tn;
                 place(w.tile, tm, tn);
@@ -97,29 +98,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
                 }
                 const bool gated = kMode == kForward && A.a.gated;
                 const int n = tn * A.tile_cols + (gated ? 0 : rank * kTile);
+                const CUtensorMap *mb = gated && rank ? &b2 : &b1;
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
-                    if (elect_one()) {
-                        if (rank == 0) mbar_arrive_expect_tx(sh.full + s, 2 * kStage);
-                        const uint32_t bar = full0 + 8 * s;
-                        unsigned char *pa = stages + s * kStage, *pb = pa + kOperand;
-                        const bool second = kMode == kDx && kb >= A.blocks1;
-                        const int k = (second ? kb - A.blocks1 : kb) * kBlock;
-                        if constexpr (kAmn) {
-                            tma_load_pair(pa, ma, bar, m, k);
-                            tma_load_pair(pa + kOperand / 2, ma, bar, m + 64, k);
-                        } else {
-                            tma_load_pair(pa, second ? &a2 : ma, bar, k, m);
-                        }
-                        if constexpr (kBmn) {
-                            const CUtensorMap *mb = second ? &b2 : &b1;
-                            tma_load_pair(pb, mb, bar, n, k);
-                            tma_load_pair(pb + kOperand / 2, mb, bar, n + 64, k);
-                        } else {
-                            tma_load_pair(pb, gated && rank ? &b2 : &b1, bar, k, n);
-                        }
+                    expect_tx(first, sh.full + s, 2 * kStage);
+                    const uint32_t bar = full0 + 8 * s;
+                    unsigned char *pa = stages + s * kStage, *pb = pa + kOperand;
+                    int k = kb * kBlock;
+                    if (kMode == kDx && kb >= A.blocks1) {
+                        k -= A.blocks1 * kBlock;
+                        ma = &a2;
+                        mb = &b2;
                     }
-                    __syncwarp();
+                    if constexpr (kAmn) {
+                        load_box<2>(on, pa, ma, bar, m, k);
+                        load_box<2>(on, pa + kOperand / 2, ma, bar, m + 64, k);
+                    } else {
+                        load_box<2>(on, pa, ma, bar, k, m);
+                    }
+                    if constexpr (kBmn) {
+                        load_box<2>(on, pb, mb, bar, n, k);
+                        load_box<2>(on, pb + kOperand / 2, mb, bar, n + 64, k);
+                    } else {
+                        load_box<2>(on, pb, mb, bar, k, n);
+                    }
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
@@ -128,31 +130,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
             constexpr uint32_t idesc = instruction_desc(kF8, 256, 256, kAmn, kBmn);
             constexpr uint64_t kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;
             const uint32_t base = smem_u32(stages);
-            int s = 0, buf = 0;
+            int buf = 0;
             uint32_t ph = 0, tph = 1;
-            bool ok = true;
+            bool stage_full = false, part_free = false;  // seen while the MMAs before were issued
             for (Walk w(P, unit); ok && w.next();) {
                 for (int kb = w.k0; kb < w.k1; ++kb) {
-                    const bool fresh = kF8 || kb == w.k0;
-                    if (!(ok = warp_wait(sh.full + s, ph, dead))) break;
-                    if (fresh && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
+                    const bool fresh = kF8 || kb == w.k0, last = kF8 || kb + 1 == w.k1;
+                    if (!stage_full && !(ok = warp_wait(sh.full + s, ph, dead))) break;
+                    if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
                     tc_fence_after();
                     const uint64_t da = operand_desc(base + s * kStage, kOperand / 2);
                     const uint64_t db = operand_desc(base + s * kStage + kOperand, kOperand / 2);
-                    const bool last = kF8 || kb + 1 == w.k1;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma<2, kF8>(tmem + buf * 256, da + i * kStepA, db + i * kStepB, idesc, !(fresh && i == 0));
-                        mma_commit_to<2>(sh.empty + s);
-                        if (last) mma_commit_to<2>(sh.tfull + buf);
-                    }
-                    __syncwarp();
+                    const uint32_t d = tmem + buf * 256;
+                    uint64_t *const empty = sh.empty + s, *const tfull = sh.tfull + buf;
+                    if (++s == kStages) s = 0, ph ^= 1;
                     if (last) {
                         buf ^= 1;
                         if (buf == 0) tph ^= 1;
                     }
-                    if (++s == kStages) s = 0, ph ^= 1;
+                    const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma<2, kF8>(on, d, da + i * kStepA, db + i * kStepB, idesc, fresh && i == 0 ? 0u : 1u);
+                    mma_commit_to<2>(on, empty);
+                    if (last) mma_commit_to<2>(on, tfull);
+                    stage_full = __all_sync(0xffffffffu, f);
+                    part_free = __all_sync(0xffffffffu, e);
                 }
             }
             if (!ok) let_land();
