@@ -14,67 +14,77 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLanes = kScaleGroup / 8;  // lanes of a group's row, 8 channels each
-constexpr int kTurns = 4;                // groups a half-warp takes, all loads first
+constexpr int kHalfWarps = kThreads / kLanes;
 
+// 8 values as they are in memory, zeros where there are none.
 template <bool kBf16>
-__device__ __forceinline__ void load8(float (&v)[8], const void *p, long long o)
-{
-    if constexpr (kBf16) {
-        const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + o);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+struct Eight {
+    uint4 q[kBf16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *p, long long o, bool inside)
+    {
+        const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p) + o * (kBf16 ? 2 : 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = bf16x2_to_float2(w[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+        for (int i = 0; i < (kBf16 ? 1 : 2); ++i) q[i] = inside ? __ldcs(from + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        if constexpr (kBf16) {
+            const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = bf16x2_to_float2(w[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        } else {
+            const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
         }
-    } else {
-        const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + o);
-        const float4 a = f[0], b = f[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
-}
-
-// Bits of the largest magnitude (as integers, so that NaN is the largest).
-__device__ __forceinline__ unsigned int amax8(const float (&v)[8])
-{
-    unsigned int m = 0;
+    // Bits of the largest magnitude (as integers, so that NaN is the largest).
+    __device__ __forceinline__ unsigned int largest() const
+    {
+        float v[8];
+        values(v);
+        unsigned int m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
-}
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        return m;
+    }
+};
 
-// Groups of 128 channels of one row: a half-warp each.
+// Groups of 128 channels of one row: a half-warp each, kTurns rows one after
+// another with all their loads first.  Of a CTA's 16 half-warps 1 << wide lie side by
+// side in a row and the others below them, so that narrow rows fill it too.
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs A, int groups)
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs A, int groups, int wide)
 {
-    const long long items = A.rows * groups;
-    const int lane = threadIdx.x % kLanes;
-    const long long first = static_cast<long long>(blockIdx.x) * (kThreads / kLanes) * kTurns + threadIdx.x / kLanes;
-    float v[kTurns][8];
-    long long row[kTurns];
-    int c[kTurns], grp[kTurns];
+    constexpr int kTurns = kBf16 ? 8 : 4;
+    const int lane = threadIdx.x % kLanes, hw = threadIdx.x / kLanes;
+    const int grp = (blockIdx.y << wide) + (hw & ((1 << wide) - 1));
+    const int below = kHalfWarps >> wide;
+    const long long r0 = static_cast<long long>(blockIdx.x) * (below * kTurns) + (hw >> wide);
+    const int c = grp * kScaleGroup + lane * 8;
+    const bool inside = c < A.D;
+    Eight<kBf16> x[kTurns];
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-        const long long i = first + t * (kThreads / kLanes);
-        row[t] = i / groups;
-        grp[t] = static_cast<int>(i - row[t] * groups);
-        c[t] = grp[t] * kScaleGroup + lane * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[t][j] = 0.f;
-        if (i >= items) c[t] = A.D;  // nothing to read or write
-        if (c[t] < A.D) load8<kBf16>(v[t], A.x, row[t] * A.ld_x + c[t]);
+        const long long r = r0 + t * below;
+        x[t].load(A.x, r * A.ld_x + c, inside && r < A.rows);
     }
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-        unsigned int m = amax8(v[t]);
+        const long long r = r0 + t * below;
+        unsigned int m = x[t].largest();
 #pragma unroll
         for (int d = kLanes / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
         const float scale = scale_of(m);
-        if (c[t] < A.D) {
-            store_e4m3x8<true>(A.q + row[t] * A.ld_q + c[t], v[t], scale);
-            if (lane == 0) A.scales[row[t] * groups + grp[t]] = scale;
+        if (inside && r < A.rows) {
+            float v[8];
+            x[t].values(v);
+            store_e4m3x8<true>(A.q + r * A.ld_q + c, v, scale);
+            if (lane == 0) A.scales[r * groups + grp] = scale;
         }
     }
 }
@@ -84,36 +94,37 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const QuantArgs A, int groups)
 {
-    constexpr int kRows = kScaleGroup * kLanes / kThreads;
+    constexpr int kRows = kScaleGroup / kHalfWarps;
     __shared__ unsigned int part[kThreads / 32];
     const int lane = threadIdx.x % kLanes;
-    const long long blk = blockIdx.x;
-    const long long band = blk / groups;
-    const int grp = static_cast<int>(blk - band * groups);
+    const long long band = blockIdx.x;
+    const int grp = blockIdx.y;
     const int c = grp * kScaleGroup + lane * 8;
     const long long r0 = band * kScaleGroup + threadIdx.x / kLanes;
-    float v[kRows][8];
+    Eight<kBf16> x[kRows];
     unsigned int m = 0;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-        const long long r = r0 + j * (kThreads / kLanes);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-        if (c < A.D && r < A.rows) load8<kBf16>(v[j], A.x, r * A.ld_x + c);
+        const long long r = r0 + j * kHalfWarps;
+        x[j].load(A.x, r * A.ld_x + c, c < A.D && r < A.rows);
     }
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) m = max(m, amax8(v[j]));
+    for (int j = 0; j < kRows; ++j) m = max(m, x[j].largest());
     m = __reduce_max_sync(0xffffffffu, m);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
     const float scale = scale_of(m);
-    if (threadIdx.x == 0) A.scales[blk] = scale;
+    if (threadIdx.x == 0) A.scales[band * groups + grp] = scale;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-        const long long r = r0 + j * (kThreads / kLanes);
-        if (c < A.D && r < A.rows) store_e4m3x8<true>(A.q + r * A.ld_q + c, v[j], scale);
+        const long long r = r0 + j * kHalfWarps;
+        if (c < A.D && r < A.rows) {
+            float v[8];
+            x[j].values(v);
+            store_e4m3x8<true>(A.q + r * A.ld_q + c, v, scale);
+        }
     }
 }
 
@@ -123,14 +134,16 @@ int launch_fp8_quantize(const QuantArgs &a, cudaStream_t st)
 {
     const int groups = (a.D + kScaleGroup - 1) / kScaleGroup;
     if (a.block == 1) {
-        const long long per = (kThreads / kLanes) * kTurns;
-        const unsigned int grid = static_cast<unsigned int>((a.rows * groups + per - 1) / per);
+        int wide = 0;
+        while ((1 << wide) < kHalfWarps && (1 << wide) < groups) ++wide;
+        const int rows = (kHalfWarps >> wide) * (a.x_bf16 ? 8 : 4);  // of a CTA
+        const dim3 grid(static_cast<unsigned int>((a.rows + rows - 1) / rows), (groups + (1 << wide) - 1) >> wide);
         if (a.x_bf16)
-            quantize_rows_kernel<true><<<grid, kThreads, 0, st>>>(a, groups);
+            quantize_rows_kernel<true><<<grid, kThreads, 0, st>>>(a, groups, wide);
         else
-            quantize_rows_kernel<false><<<grid, kThreads, 0, st>>>(a, groups);
+            quantize_rows_kernel<false><<<grid, kThreads, 0, st>>>(a, groups, wide);
     } else {
-        const unsigned int grid = static_cast<unsigned int>((a.rows + kScaleGroup - 1) / kScaleGroup * groups);
+        const dim3 grid(static_cast<unsigned int>((a.rows + kScaleGroup - 1) / kScaleGroup), groups);
         if (a.x_bf16)
             quantize_blocks_kernel<true><<<grid, kThreads, 0, st>>>(a, groups);
         else
