@@ -50,14 +50,8 @@ __device__ __forceinline__ float scale_of(unsigned int amax_bits)
 // takes 151, but holds registers that cost a CTA an SM with a bf16 residual (8192 x
 // 4096 with one scale per row: 61) and with four vectors a thread (65536 x 1024: 61).
 template <bool kPairs>
-__device__ __forceinline__ uint2 e4m3x8(float (&v)[8], float scale)
+__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float scale, float inv)
 {
-    if (scale < 0x1p-60f) {  // the same quotients, with no subnormal remainder
-        scale *= 0x1p+64f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= 0x1p+64f;
-    }
-    const float inv = 1.f / scale;
     const bool step = scale < INFINITY;  // else the product: 0, NaN of an Inf, NaN
     unsigned short h[4];
 #pragma unroll
@@ -78,6 +72,20 @@ __device__ __forceinline__ uint2 e4m3x8(float (&v)[8], float scale)
     q.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
     q.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
     return q;
+}
+
+
+constexpr float kSmallScale = 0x1p-60f;  // below it a remainder may be subnormal
+
+template <bool kPairs>
+__device__ __forceinline__ uint2 e4m3x8(float (&v)[8], float scale)
+{
+    if (scale < kSmallScale) {  // the same quotients
+        scale *= 0x1p+64f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= 0x1p+64f;
+    }
+    return e4m3x8<kPairs>(v, scale, 1.f / scale);
 }
 
 template <bool kPairs>
