@@ -269,16 +269,22 @@ __device__ __forceinline__ void tmem_wait(float (&v)[32])
 
 // ---------------------------------------------------------------- activations
 
+// 1 / (1 + e^-x), to 4 units in the last place: the quotient by the approximate
+// reciprocal, which is zero where e^-x passes 2^126.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+
+constexpr float kGeluTanh = 1.59576912160573072f;  // 2 sqrt(2 / pi): (1 + tanh z) / 2 = sigmoid(2 z)
+
 // act(g) of the gated block (HYENA_ACT_*).
 template <int kAct>
 __device__ __forceinline__ float activation(float g)
 {
     if constexpr (kAct == HYENA_ACT_SILU) {
-        return g / (1.f + expf(-g));
+        return g * sigmoid(g);
     } else if constexpr (kAct == HYENA_ACT_GELU) {
         return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
-        return 0.5f * g * (1.f + tanhf(0.79788456080286536f * fmaf(0.044715f * g * g, g, g)));
+        return g * sigmoid(kGeluTanh * fmaf(0.044715f * g * g, g, g));
     } else {
         return g;
     }
@@ -289,15 +295,15 @@ template <int kAct>
 __device__ __forceinline__ float2 activation_slope(float g)
 {
     if constexpr (kAct == HYENA_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-g));
+        const float s = sigmoid(g);
         return make_float2(g * s, s * fmaf(g, 1.f - s, 1.f));
     } else if constexpr (kAct == HYENA_ACT_GELU) {
         const float c = 0.5f * (1.f + erff(g * 0.70710678118654752f));
         return make_float2(g * c, fmaf(g, 0.39894228040143268f * expf(-0.5f * g * g), c));
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
-        const float t = tanhf(0.79788456080286536f * fmaf(0.044715f * g * g, g, g));
-        const float in = 0.79788456080286536f * fmaf(3.f * 0.044715f * g, g, 1.f);
-        return make_float2(0.5f * g * (1.f + t), 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * in);
+        const float s = sigmoid(kGeluTanh * fmaf(0.044715f * g * g, g, g));
+        const float in = kGeluTanh * fmaf(3.f * 0.044715f * g, g, 1.f);
+        return make_float2(g * s, fmaf(g * s * (1.f - s), in, s));
     } else {
         return make_float2(g, 1.f);
     }

@@ -16,18 +16,17 @@ constexpr int kRowBytes = 128;                    // of a k-block: 64 bf16 or 12
 constexpr size_t kProductHeader = 4096;           // 256 bytes of header, then a counter for each split tile
 constexpr int kMaxSplitTiles = (kProductHeader - 256) / 4;
 
-// How a product is divided: tiles of the output, k-blocks of a tile, units (CTAs,
-// or pairs of CTAs) that walk through them.  The first `split` tiles' k-blocks are
-// dealt out evenly, a contiguous run a unit, so that few tiles (or the last of
-// many) keep every unit busy; the others go whole, one after another.
+// How a product is divided: tiles of the output, k-blocks of a tile, units (pairs of
+// CTAs) that walk through them.  The first `split` tiles' k-blocks are dealt out
+// evenly, a contiguous run a unit (unit u begins at u each + min(u, more)), so that
+// every unit is busy to the end; the others go whole, one after another.
 struct Plan {
     int tiles_m, tiles_n, tiles;
     int blocks;  // k-blocks of a tile
     int split, units;
-    __device__ __forceinline__ long long first(int unit) const
-    {
-        return static_cast<long long>(split) * blocks * unit / units;
-    }
+    long long each;
+    int more;
+    __device__ __forceinline__ long long first(int unit) const { return unit * each + min(unit, more); }
 };
 
 struct Walk {
@@ -38,12 +37,14 @@ struct Walk {
     __device__ __forceinline__ Walk(const Plan &plan, int unit)
         : p(plan), pos(plan.first(unit)), end(plan.first(unit + 1)), whole(plan.split + unit)
     {
+        tile = pos < end ? static_cast<int>(pos / p.blocks) : 0;
+        k1 = static_cast<int>(pos - static_cast<long long>(tile) * p.blocks);
     }
     __device__ __forceinline__ bool next()
     {
         if (pos < end) {
-            tile = static_cast<int>(pos / p.blocks);
-            k0 = static_cast<int>(pos - static_cast<long long>(tile) * p.blocks);
+            if (k1 == p.blocks) k1 = 0, ++tile;
+            k0 = k1;
             k1 = end - pos < p.blocks - k0 ? k0 + static_cast<int>(end - pos) : p.blocks;
             pos += k1 - k0;
             return true;
@@ -59,90 +60,98 @@ struct Walk {
 
 // The sums of a part of a tile go to memory, and the CTA whose part is the last to
 // arrive adds them up in the order of k, so that the result does not depend on
-// which that was.  `kCtas` CTAs of a unit each have their own half of the tile.
-// v: this thread's kV sums; thread `t` of the kEpiThreads keeps them at
-// [i][t] of its part's slot.  True in the CTA that holds the tile's sums.
-template <int kCtas, int kV>
-__device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int unit, int rank, int tile, int k0, int t,
+// which that was.  The two CTAs of a pair each have their own half of the tile.
+// v: this thread's sums, kept as float4 [i][thread] of its part's slot.  True in the
+// CTA that holds the tile's sums.
+template <int kV>
+__device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int unit, int rank, int tile, int t,
                                            unsigned char *workspace, unsigned int *flag)
 {
-    constexpr size_t kSlot = static_cast<size_t>(kV) * kEpiThreads;
-    float *slots = reinterpret_cast<float *>(workspace + kProductHeader) + t;
+    constexpr size_t kSlot = static_cast<size_t>(kV / 4) * kEpiThreads;
+    float4 *slots = reinterpret_cast<float4 *>(workspace + kProductHeader) + t;
     const long long begin = static_cast<long long>(tile) * p.blocks;
     // a unit has at most two parts: one that begins inside a tile and one at its start
-    auto slot = [&](int u) {
-        return slots + ((2ll * u + (p.first(u) > begin ? 0 : 1)) * kCtas + rank) * kSlot;
-    };
-    float *own = slot(unit);
+    auto slot = [&](int u) { return slots + (2ll * (2ll * u + (p.first(u) > begin ? 0 : 1)) + rank) * kSlot; };
+    float4 *own = slot(unit);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) own[i * kEpiThreads] = v[i];
-    // the units whose runs meet this tile; few k-blocks leave some without any
-    auto takes_part = [&](int u) { return p.first(u) < p.first(u + 1) ? 1 : 0; };
-    int first = unit, past = unit + 1, parts = 1;
-    while (first > 0 && p.first(first) > begin) parts += takes_part(--first);
-    while (p.first(past) < begin + p.blocks) parts += takes_part(past++);
-    __threadfence();
+    for (int i = 0; i < kV / 4; ++i)
+        own[i * kEpiThreads] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    // the units whose runs meet this tile (every run has a k-block)
+    int first = unit, past = unit + 1;
+    while (p.first(first) > begin) --first;
+    while (p.first(past) < begin + p.blocks) ++past;
     named_sync(1, kEpiThreads);
     if (t == 0) {
-        unsigned int *count = reinterpret_cast<unsigned int *>(workspace + 256) + tile * kCtas + rank;
-        const unsigned int before = atomicAdd(count, 1u);
-        const bool last = before + 1 == static_cast<unsigned int>(parts);
+        __threadfence();  // the stores of all, which the barrier has ordered before it
+        unsigned int *count = reinterpret_cast<unsigned int *>(workspace + 256) + 2 * tile + rank;
+        const bool last = atomicAdd(count, 1u) + 1 == static_cast<unsigned int>(past - first);
         if (last) *count = 0u;  // for the next call
         __threadfence();
         *flag = last ? 1u : 0u;
     }
     named_sync(1, kEpiThreads);
-    const bool last = *flag != 0u;
-    if (!last) return false;
+    if (*flag == 0u) return false;
 #pragma unroll
     for (int i = 0; i < kV; ++i) v[i] = 0.f;
+#pragma unroll 1
     for (int u = first; u < past; ++u) {
-        if (!takes_part(u)) continue;
-        const float *q = slot(u);
+        const float4 *q = slot(u);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) v[i] += __ldcg(q + i * kEpiThreads);
+        for (int i = 0; i < kV / 4; ++i) {
+            const float4 f = __ldcg(q + i * kEpiThreads);
+            v[4 * i] += f.x;
+            v[4 * i + 1] += f.y;
+            v[4 * i + 2] += f.z;
+            v[4 * i + 3] += f.w;
+        }
     }
     return true;
 }
 
-// Eight of a thread's values at a time, in a loop that stays one: each turn ends by
-// moving all of them eight places on, and the last leaves them where they were.
-// Code run once per value, 64 times over, waits for its instructions: with 128
-// tokens the gate took 13 us that way and the codes 40.
-template <int kV>
+// A thread's values kN at a time, in a loop that stays one: each turn ends by moving
+// all of them kN places on, and the last leaves them where they were.  Code run once
+// per value, 64 times over, waits for its instructions: with 128 tokens the codes of
+// the outputs took 40 us that way.
+template <int kV, int kN>
 __device__ __forceinline__ void turn(float *v)
 {
-    float t[8];
+    float t[kN];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = v[i];
+    for (int i = 0; i < kN; ++i) t[i] = v[i];
 #pragma unroll
-    for (int i = 0; i < kV - 8; ++i) v[i] = v[i + 8];
+    for (int i = 0; i < kV - kN; ++i) v[i] = v[i + kN];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[kV - 8 + i] = t[i];
+    for (int i = 0; i < kN; ++i) v[kV - kN + i] = t[i];
 }
 
-template <int kV, class F>
-__device__ __forceinline__ void by_eights(F f)
+template <int kV, int kN, class F>
+__device__ __forceinline__ void in_turns(F f)
 {
-    if constexpr (kV == 8) {
+    if constexpr (kV == kN) {
         f(0);
     } else {
 #pragma unroll 1
-        for (int j = 0; j < kV; j += 8) f(j);
+        for (int j = 0; j < kV; j += kN) f(j);
     }
 }
 
-// g[i] <- act(g[i]) u[i], the first `count` of kV
+// g[i] <- act(g[i]) u[i], the first `count` of kV.  The error function's 25
+// instructions in turns of 16, the others' straight.
 template <int kAct, int kV>
 __device__ __forceinline__ void gate(float (&v)[2 * kV], int count)
 {
-    by_eights<kV>([&](int j) {
-        if (j < count) {
+    constexpr int kN = kAct == HYENA_ACT_GELU && kV > 16 ? 16 : kV;
+    in_turns<kV, kN>([&](int j) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = activation<kAct>(v[i]) * v[kV + i];
+        for (int i = 0; i < kN; i += 8) {
+            if (j + i >= count) continue;
+#pragma unroll
+            for (int l = i; l < i + 8; ++l) v[l] = activation<kAct>(v[l]) * v[kV + l];
         }
-        turn<kV>(v);
-        turn<kV>(v + kV);
+        if constexpr (kN < kV) {
+            turn<kV, kN>(v);
+            turn<kV, kN>(v + kV);
+        }
     });
 }
 

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     constexpr int kBlock = kF8 ? 128 : 64;  // k of a block
     extern __shared__ unsigned char raw[];
     __shared__ ProductShared<kStages> sh;
-    __shared__ float token_scale[kEpiWarps][kH];
+    __shared__ __align__(16) float token_scale[kEpiWarps][kH];
     __shared__ unsigned int token_max[kEpiWarps][kH];
     unsigned char *stages = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -204,21 +204,28 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     const uint32_t at = lanes + buf * (kG * kNT);
                     constexpr int kChunks = kH / kC;
                     float d[2][kC];
+                    float4 xs[kC / 4];
                     tmem_ld(d[0], at);
 #pragma unroll
-                    for (int i = 0; i < kG * kChunks; ++i) {
+                    for (int i = 0; i < kG * kChunks; ++i) {  // a chunk of tokens, of each weight in turn
+                        const int chunk = i / kG, g = i % kG;
                         tmem_wait(d[i & 1]);
                         if (i + 1 < kG * kChunks)
-                            tmem_ld(d[(i + 1) & 1], at + (i + 1) / kChunks * kNT + (i + 1) % kChunks * kC);
+                            tmem_ld(d[(i + 1) & 1], at + (i + 1) % kG * kNT + (i + 1) / kG * kC);
+                        if (g == 0) {
+#pragma unroll
+                            for (int j = 0; j < kC; j += 4)
+                                xs[j / 4] = *reinterpret_cast<const float4 *>(&token_scale[warp][chunk * kC + j]);
+                        }
 #pragma unroll
                         for (int j = 0; j < kC; j += 2) {
-                            const float2 x = *reinterpret_cast<const float2 *>(&token_scale[warp][i % kChunks * kC + j]);
-                            const float2 r =
-                                __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]),
-                                           __fmul2_rn(x, i < kChunks ? c1 : c2),
-                                           make_float2(v[i * kC + j], v[i * kC + j + 1]));
-                            v[i * kC + j] = r.x;
-                            v[i * kC + j + 1] = r.y;
+                            const float4 x4 = xs[j / 4];
+                            const float2 x = j % 4 ? make_float2(x4.z, x4.w) : make_float2(x4.x, x4.y);
+                            float *t = v + g * kH + chunk * kC + j;
+                            const float2 r = __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]),
+                                                        __fmul2_rn(x, g ? c2 : c1), make_float2(t[0], t[1]));
+                            t[0] = r.x;
+                            t[1] = r.y;
                         }
                     }
                     done_reading();
@@ -270,12 +277,12 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             const bool inside = n < A.a.N;
             // f(j, values of token j) for each token inside
             auto each = [&](auto f) {
-                by_eights<kH>([&](int j) {
+                in_turns<kH, 8>([&](int j) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (j + i < tokens) f(j + i, v[i], v[kGated ? kH + i : i]);
-                    if (kH > 8) turn<kH>(v);
-                    if (kH > 8 && kGated) turn<kH>(v + kH);
+                    if (kH > 8) turn<kH, 8>(v);
+                    if (kH > 8 && kGated) turn<kH, 8>(v + kH);
                 });
             };
             if constexpr (!kGated) {
@@ -297,14 +304,18 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                         if (lane == 0) token_max[warp][j] = mx;
                     });
                     named_sync(2 + hh, kEpiThreads / 2);
-                    each([&](int j, float y, float) {
-                        unsigned int mx = token_max[4 * hh][j];
+                    if (row < tokens) {  // a thread a token
+                        unsigned int mx = token_max[4 * hh][row];
 #pragma unroll
-                        for (int i = 1; i < 4; ++i) mx = max(mx, token_max[4 * hh + i][j]);
+                        for (int i = 1; i < 4; ++i) mx = max(mx, token_max[4 * hh + i][row]);
                         const float scale = scale_of(mx);
-                        if (inside)
-                            A.a.q[(m + j) * A.a.ld_q + n] = __nv_cvt_float_to_fp8(y / scale, __NV_SATFINITE, __NV_E4M3);
-                        if (row == 0) A.a.scales[(m + j) * (A.tiles / A.tiles_m) + tn] = scale;
+                        A.a.scales[(m + row) * (A.tiles / A.tiles_m) + tn] = scale;
+                        token_scale[4 * hh][row] = scale;
+                    }
+                    named_sync(2 + hh, kEpiThreads / 2);
+                    each([&](int j, float y, float) {
+                        const float z = y / token_scale[4 * hh][j];
+                        if (inside) A.a.q[(m + j) * A.a.ld_q + n] = __nv_cvt_float_to_fp8(z, __NV_SATFINITE, __NV_E4M3);
                     });
                     named_sync(2 + hh, kEpiThreads / 2);
                 } else {

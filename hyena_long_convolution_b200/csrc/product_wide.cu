@@ -263,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
             }
             more = advance();
             if (k1 - k0 < P.blocks &&
-                !join_parts<2>(v, P, unit, rank, tile, k0, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
+                !join_parts(v, P, unit, rank, tile, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
                 continue;
             const long long m = static_cast<long long>(row0) * 256 + rank * kTile + row;
             const int n = col0 * A.tile_cols + hh * kHalf;
@@ -334,21 +334,29 @@ int pairs()
     return sms / 2;
 }
 
+// Whole tiles, wave after wave, unless sharing out the last one or two waves' k-blocks
+// saves more than the joining costs, which is about that of kJoin k-blocks.
+constexpr int kJoin = 28;
+
 void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
 {
     p.tiles_m = tiles_m;
     p.tiles_n = tiles_n;
     p.tiles = tiles_m * tiles_n;
     p.blocks = blocks;
+    p.units = p.tiles < units ? p.tiles : units;
+    p.split = 0;
     const int rest = p.tiles % units;
-    p.split = rest;
-    p.units = units;
-    if (p.tiles < units) {
-        const long long all = static_cast<long long>(p.tiles) * blocks;
-        const long long most = all / 4 > p.tiles ? all / 4 : p.tiles;
-        p.units = most < units ? static_cast<int>(most) : units;
-        if (p.units == p.tiles) p.split = 0;
+    if (rest != 0) {
+        const long long all = static_cast<long long>(rest) * blocks;
+        if (blocks - (all + units - 1) / units > kJoin) {
+            p.units = units;
+            p.split = p.tiles < units ? rest : rest + units;  // 0.5 to 2 tiles a unit, few parts a tile
+        }
     }
+    const long long run = static_cast<long long>(p.split) * blocks;
+    p.each = run / p.units;
+    p.more = static_cast<int>(run % p.units);
 }
 
 template <int kMode, bool kF8>
