@@ -5,8 +5,7 @@
 //
 // One pass: a group sits in registers between its maximum and its codes, so x is
 // read once.  HBM-bound: 3 bytes a bf16 value.
-#include "layer_device.cuh"
-#include "product_internal.h"
+#include "product_device.cuh"
 
 namespace hyena {
 
@@ -88,6 +87,7 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantArgs A, int groups, int wide)
 {
     constexpr int kTurns = kBf16 ? 8 : 4;
+    wait_for_stream();
     const int lane = threadIdx.x % kLanes, hw = threadIdx.x / kLanes;
     const int grp = (blockIdx.y << wide) + (hw & ((1 << wide) - 1));
     const int below = kHalfWarps >> wide;
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const QuantAr
 {
     constexpr int kRows = kScaleGroup / kHalfWarps;
     __shared__ unsigned int part[kThreads / 32];
+    wait_for_stream();
     const int lane = threadIdx.x % kLanes;
     const long long band = blockIdx.x;
     const int grp = blockIdx.y;
@@ -173,19 +174,12 @@ int launch_fp8_quantize(const QuantArgs &a, cudaStream_t st)
         while (wide > 0 && (((groups - 1) >> wide) + 1) << (wide + 3) > 9 * groups) --wide;
         const int rows = (kHalfWarps >> wide) * (a.x_bf16 ? 8 : 4);  // of a CTA
         const dim3 grid(static_cast<unsigned int>((a.rows + rows - 1) / rows), (groups + (1 << wide) - 1) >> wide);
-        if (a.x_bf16)
-            quantize_rows_kernel<true><<<grid, kThreads, 0, st>>>(a, groups, wide);
-        else
-            quantize_rows_kernel<false><<<grid, kThreads, 0, st>>>(a, groups, wide);
-    } else {
-        const dim3 grid(static_cast<unsigned int>((a.rows + kScaleGroup - 1) / kScaleGroup), groups);
-        if (a.x_bf16)
-            quantize_blocks_kernel<true><<<grid, kThreads, 0, st>>>(a, groups);
-        else
-            quantize_blocks_kernel<false><<<grid, kThreads, 0, st>>>(a, groups);
+        return launch_early(a.x_bf16 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>, grid, kThreads, 0, 1, st,
+                            "fp8_quantize launch", a, groups, wide);
     }
-    HYENA_TRY(cudaGetLastError(), "fp8_quantize launch");
-    return 1;
+    const dim3 grid(static_cast<unsigned int>((a.rows + kScaleGroup - 1) / kScaleGroup), groups);
+    return launch_early(a.x_bf16 ? quantize_blocks_kernel<true> : quantize_blocks_kernel<false>, grid, kThreads, 0, 1, st,
+                        "fp8_quantize launch", a, groups);
 }
 
 }  // namespace hyena

@@ -27,6 +27,7 @@ void resolve_encode()
 template <int kAct, bool kF32>
 __global__ void __launch_bounds__(256) slopes_kernel(const FfnBackArgs A, uint16_t *dg, uint16_t *du)
 {
+    wait_for_stream();
     const long long per = A.F / 8, n = A.M * per;
     for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n; i += gridDim.x * 256ll) {
         const long long m = i / per, f = (i - m * per) * 8;
@@ -51,12 +52,10 @@ __global__ void __launch_bounds__(256) slopes_kernel(const FfnBackArgs A, uint16
 }
 
 template <int kAct>
-void start_slopes(const FfnBackArgs &a, uint16_t *dg, uint16_t *du, int grid, cudaStream_t st)
+int start_slopes(const FfnBackArgs &a, uint16_t *dg, uint16_t *du, int grid, cudaStream_t st)
 {
-    if (a.g_f32)
-        slopes_kernel<kAct, true><<<grid, 256, 0, st>>>(a, dg, du);
-    else
-        slopes_kernel<kAct, false><<<grid, 256, 0, st>>>(a, dg, du);
+    return launch_early(a.g_f32 ? slopes_kernel<kAct, true> : slopes_kernel<kAct, false>, dim3(grid), 256, 0, 1, st,
+                        "ffn slopes launch", a, dg, du);
 }
 
 size_t part_bytes(long long M)
@@ -116,17 +115,18 @@ int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st)
     uint16_t *du = dg + a.M * a.F;
     const long long ctas = (a.M * (a.F / 8) + 255) / 256;
     const int grid = ctas < sms * 8ll ? static_cast<int>(ctas) : sms * 8;
+    int n = 0;
     switch (a.act) {
-        case HYENA_ACT_SILU: start_slopes<HYENA_ACT_SILU>(a, dg, du, grid, st); break;
-        case HYENA_ACT_GELU: start_slopes<HYENA_ACT_GELU>(a, dg, du, grid, st); break;
-        case HYENA_ACT_GELU_TANH: start_slopes<HYENA_ACT_GELU_TANH>(a, dg, du, grid, st); break;
-        default: start_slopes<HYENA_ACT_IDENTITY>(a, dg, du, grid, st); break;
+        case HYENA_ACT_SILU: n = start_slopes<HYENA_ACT_SILU>(a, dg, du, grid, st); break;
+        case HYENA_ACT_GELU: n = start_slopes<HYENA_ACT_GELU>(a, dg, du, grid, st); break;
+        case HYENA_ACT_GELU_TANH: n = start_slopes<HYENA_ACT_GELU_TANH>(a, dg, du, grid, st); break;
+        default: n = start_slopes<HYENA_ACT_IDENTITY>(a, dg, du, grid, st); break;
     }
-    HYENA_TRY(cudaGetLastError(), "ffn slopes launch");
+    if (n < 0) return -1;
     const int x = launch_ffn_dx(a, dg, du, st);
     if (x < 0) return -1;
     const int w = launch_ffn_dw(a, dg, du, st);
-    return w < 0 ? -1 : 1 + x + w;
+    return w < 0 ? -1 : n + x + w;
 }
 
 }  // namespace hyena

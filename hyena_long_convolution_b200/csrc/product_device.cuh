@@ -52,6 +52,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, wait_phase(bar, parity, dead)) != 0;
 }
 
+// ---------------------------------------------------------------- launches
+
+// The kernels here are launched before the one ahead of them in the stream has ended
+// (launch_early): what comes before this reads and writes no global memory.
+__device__ __forceinline__ void wait_for_stream()
+{
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank()

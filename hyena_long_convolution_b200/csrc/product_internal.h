@@ -82,4 +82,27 @@ int product_sms();
 size_t product_workspace(long long M, int N, int K, bool fp8, bool gated);
 size_t ffn_backward_workspace(long long M, int D, int F);
 
+// Launches a kernel that waits for the stream itself (wait_for_stream), so that its
+// launch and its setup overlap the end of the kernel before it: 1.5 to 3 us a call.
+template <class... P, class... Q>
+int launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                 const char *what, const Q &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    HYENA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...), what);
+    return 1;
+}
+
 }  // namespace hyena

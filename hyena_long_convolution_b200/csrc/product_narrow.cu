@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_stream();
     const uint32_t tmem = sh.tmem;
 
     if (warp >= kEpiWarps) {
@@ -341,19 +342,8 @@ int start(const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, co
     constexpr int kSmem = Narrow<kNT, kGated>::kSmem;
     HYENA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
               "product (narrow) attribute");
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(units * w.share);
-    cfg.blockDim = dim3(kThreadsProduct);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute cluster{};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = w.share;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    cfg.attrs = &cluster;
-    cfg.numAttrs = 1;
-    HYENA_TRY(cudaLaunchKernelEx(&cfg, kernel, x, w1, w2, w), "product (narrow) launch");
-    return 1;
+    return launch_early(kernel, dim3(units * w.share), kThreadsProduct, kSmem, w.share, st, "product (narrow) launch", x,
+                        w1, w2, w);
 }
 
 template <bool kF8, bool kGated>

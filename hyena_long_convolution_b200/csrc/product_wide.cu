@@ -37,7 +37,7 @@ struct WideArgs {
 };
 
 template <int kMode, bool kF8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
+__global__ void __launch_bounds__(kThreadsProduct, 1)
     product_wide_kernel(const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap a2,
                         const __grid_constant__ CUtensorMap b1, const __grid_constant__ CUtensorMap b2,
                         const __grid_constant__ WideArgs A)
@@ -52,6 +52,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
     const Plan &P = A.plan;
     volatile unsigned int *dead = &sh.dead;
 
+    if (tid == kEpiThreads) {
+        prefetch_map(&a1);
+        prefetch_map(&b1);
+    }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(sh.full + i, 1);
@@ -68,6 +72,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsProduct, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
+    wait_for_stream();
     const uint32_t tmem = sh.tmem;
 
     // tile -> (tile row, tile column): bands of kBand tile rows, columns within
@@ -365,9 +370,8 @@ int start(const CUtensorMap &a1, const CUtensorMap &a2, const CUtensorMap &b1, c
 {
     HYENA_TRY(cudaFuncSetAttribute(product_wide_kernel<kMode, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
               "product (wide) attribute");
-    product_wide_kernel<kMode, kF8><<<2 * w.plan.units, kThreadsProduct, kSmem, st>>>(a1, a2, b1, b2, w);
-    HYENA_TRY(cudaGetLastError(), "product (wide) launch");
-    return 1;
+    return launch_early(product_wide_kernel<kMode, kF8>, dim3(2 * w.plan.units), kThreadsProduct, kSmem, 2, st,
+                        "product (wide) launch", a1, a2, b1, b2, w);
 }
 
 }  // namespace
