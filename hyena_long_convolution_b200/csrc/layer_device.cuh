@@ -88,6 +88,17 @@ __device__ __forceinline__ uint2 e4m3x8(float (&v)[8], float scale)
     return e4m3x8<kPairs>(v, scale, 1.f / scale);
 }
 
+// The same of one value.
+__device__ __forceinline__ uint8_t e4m3_code(float v, float scale, float inv)
+{
+    float z = v * inv;
+    if (scale < kSmallScale)
+        z = v / scale;
+    else if (scale < INFINITY)
+        z = __fmaf_rn(__fmaf_rn(z, -scale, v), inv, z);
+    return __nv_cvt_float_to_fp8(z, __NV_SATFINITE, __NV_E4M3);
+}
+
 template <bool kPairs>
 __device__ __forceinline__ void store_e4m3x8(uint8_t *p, float (&v)[8], float scale)
 {

@@ -284,6 +284,26 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f +
 
 constexpr float kGeluTanh = 1.59576912160573072f;  // 2 sqrt(2 / pi): (1 + tanh z) / 2 = sigmoid(2 z)
 
+// The normal distribution's Phi(g), and e^{-g^2 / 2} in e.  Phi(-|g|) = t p(t)
+// e^{-g^2 / 2} with t = 1 / (1 + 0.3 |g|) and p of degree 7 fitted to the function in
+// the relative maximum norm for |g| <= 14.5 (1.6e-7; with the arithmetic, 13 half steps
+// of fp32 for |g| < 5), which keeps the digits that 1 + erf loses where g is negative.
+__device__ __forceinline__ float normal_cdf(float g, float &e)
+{
+    const float t = __fdividef(1.f, fmaf(0.3f, fabsf(g), 1.f));
+    float p = 0.03542377054691315f;
+    p = fmaf(p, t, -0.15615858137607574f);
+    p = fmaf(p, t, 0.20455701649188995f);
+    p = fmaf(p, t, -0.05203420668840408f);
+    p = fmaf(p, t, 0.1276918649673462f);
+    p = fmaf(p, t, 0.10017592459917068f);
+    p = fmaf(p, t, 0.12071213871240616f);
+    p = fmaf(p, t, 0.11963200569152832f);
+    e = expf(-0.5f * g * g);
+    const float tail = p * t * e;
+    return g < 0.f ? tail : 1.f - tail;
+}
+
 // act(g) of the gated block (HYENA_ACT_*).
 template <int kAct>
 __device__ __forceinline__ float activation(float g)
@@ -291,7 +311,8 @@ __device__ __forceinline__ float activation(float g)
     if constexpr (kAct == HYENA_ACT_SILU) {
         return g * sigmoid(g);
     } else if constexpr (kAct == HYENA_ACT_GELU) {
-        return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+        float e;
+        return g * normal_cdf(g, e);
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
         return g * sigmoid(kGeluTanh * fmaf(0.044715f * g * g, g, g));
     } else {
@@ -307,8 +328,9 @@ __device__ __forceinline__ float2 activation_slope(float g)
         const float s = sigmoid(g);
         return make_float2(g * s, s * fmaf(g, 1.f - s, 1.f));
     } else if constexpr (kAct == HYENA_ACT_GELU) {
-        const float c = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-        return make_float2(g * c, fmaf(g, 0.39894228040143268f * expf(-0.5f * g * g), c));
+        float e;
+        const float c = normal_cdf(g, e);
+        return make_float2(g * c, fmaf(g, 0.39894228040143268f * e, c));
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
         const float s = sigmoid(kGeluTanh * fmaf(0.044715f * g * g, g, g));
         const float in = kGeluTanh * fmaf(3.f * 0.044715f * g, g, 1.f);

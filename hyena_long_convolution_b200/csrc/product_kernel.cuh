@@ -135,7 +135,7 @@ __device__ __forceinline__ void in_turns(F f)
     }
 }
 
-// g[i] <- act(g[i]) u[i], the first `count` of kV.  The error function's 25
+// g[i] <- act(g[i]) u[i], the first `count` of kV.  The normal distribution's 20
 // instructions in turns of 16, the others' straight.
 template <int kAct, int kV>
 __device__ __forceinline__ void gate(float (&v)[2 * kV], int count)

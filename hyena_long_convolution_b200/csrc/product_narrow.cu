@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     constexpr int kBlock = kF8 ? 128 : 64;  // k of a block
     extern __shared__ unsigned char raw[];
     __shared__ ProductShared<kStages> sh;
-    __shared__ __align__(16) float token_scale[kEpiWarps][kH];
+    __shared__ __align__(16) float token_scale[kEpiWarps][2][kH];
     __shared__ unsigned int token_max[kEpiWarps][kH];
     unsigned char *stages = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -189,9 +189,12 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 float f1 = __ldg(s1 + k0), f2 = __ldg(s2 + k0);
                 for (int kb = k0; kb < k1; ++kb) {
                     __syncwarp();
-                    if (lane < kH) token_scale[warp][lane] = x0;
-                    if constexpr (kH > 32) token_scale[warp][lane + 32] = x1;
-                    const float2 c1 = bcast2(f1), c2 = bcast2(f2);
+                    // a token's scale times each weight's
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        if (lane < kH) token_scale[warp][g][lane] = x0 * (g ? f2 : f1);
+                        if constexpr (kH > 32) token_scale[warp][g][lane + 32] = x1 * (g ? f2 : f1);
+                    }
                     if (kb + 1 < k1) {
                         x0 = scale_at(sx0, kb + 1);
                         x1 = scale_at(sx1, kb + 1);
@@ -205,28 +208,22 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     const uint32_t at = lanes + buf * (kG * kNT);
                     constexpr int kChunks = kH / kC;
                     float d[2][kC];
-                    float4 xs[kC / 4];
                     tmem_ld(d[0], at);
 #pragma unroll
-                    for (int i = 0; i < kG * kChunks; ++i) {  // a chunk of tokens, of each weight in turn
-                        const int chunk = i / kG, g = i % kG;
+                    for (int i = 0; i < kG * kChunks; ++i) {
+                        const int g = i / kChunks, first = i % kChunks * kC;
                         tmem_wait(d[i & 1]);
                         if (i + 1 < kG * kChunks)
-                            tmem_ld(d[(i + 1) & 1], at + (i + 1) % kG * kNT + (i + 1) / kG * kC);
-                        if (g == 0) {
+                            tmem_ld(d[(i + 1) & 1], at + (i + 1) / kChunks * kNT + (i + 1) % kChunks * kC);
 #pragma unroll
-                            for (int j = 0; j < kC; j += 4)
-                                xs[j / 4] = *reinterpret_cast<const float4 *>(&token_scale[warp][chunk * kC + j]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < kC; j += 2) {
-                            const float4 x4 = xs[j / 4];
-                            const float2 x = j % 4 ? make_float2(x4.z, x4.w) : make_float2(x4.x, x4.y);
-                            float *t = v + g * kH + chunk * kC + j;
-                            const float2 r = __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]),
-                                                        __fmul2_rn(x, g ? c2 : c1), make_float2(t[0], t[1]));
-                            t[0] = r.x;
-                            t[1] = r.y;
+                        for (int j = 0; j < kC; j += 4) {
+                            const float4 c = *reinterpret_cast<const float4 *>(&token_scale[warp][g][first + j]);
+                            float *t = v + g * kH + first + j;
+                            const float2 lo = __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]), make_float2(c.x, c.y),
+                                                         make_float2(t[0], t[1]));
+                            const float2 hi = __ffma2_rn(make_float2(d[i & 1][j + 2], d[i & 1][j + 3]),
+                                                         make_float2(c.z, c.w), make_float2(t[2], t[3]));
+                            t[0] = lo.x, t[1] = lo.y, t[2] = hi.x, t[3] = hi.y;
                         }
                     }
                     done_reading();
@@ -311,12 +308,13 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                         for (int i = 1; i < 4; ++i) mx = max(mx, token_max[4 * hh + i][row]);
                         const float scale = scale_of(mx);
                         A.a.scales[(m + row) * (A.tiles / A.tiles_m) + tn] = scale;
-                        token_scale[4 * hh][row] = scale;
+                        token_scale[4 * hh][0][row] = scale;
+                        token_scale[4 * hh][1][row] = 1.f / scale;
                     }
                     named_sync(2 + hh, kEpiThreads / 2);
                     each([&](int j, float y, float) {
-                        const float z = y / token_scale[4 * hh][j];
-                        if (inside) A.a.q[(m + j) * A.a.ld_q + n] = __nv_cvt_float_to_fp8(z, __NV_SATFINITE, __NV_E4M3);
+                        const uint8_t code = e4m3_code(y, token_scale[4 * hh][0][j], token_scale[4 * hh][1][j]);
+                        if (inside) A.a.q[(m + j) * A.a.ld_q + n] = code;
                     });
                     named_sync(2 + hh, kEpiThreads / 2);
                 } else {
