@@ -41,10 +41,13 @@ __global__ void __launch_bounds__(256) slopes_kernel(const FfnBackArgs A, uint16
         }
         load8_bf16(d, A.dy + m * A.ld_dy + f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 s = activation_slope<kAct>(g[j]);
-            a[j] = d[j] * u[j] * s.y;
-            b[j] = d[j] * s.x;
+        for (int j = 0; j < 8; j += 2) {
+            float2 slope;
+            const float2 y = activation_slope2<kAct>(make_float2(g[j], g[j + 1]), slope);
+            const float2 dy = make_float2(d[j], d[j + 1]);
+            const float2 dgate = __fmul2_rn(__fmul2_rn(dy, make_float2(u[j], u[j + 1])), slope), dup = __fmul2_rn(dy, y);
+            a[j] = dgate.x, a[j + 1] = dgate.y;
+            b[j] = dup.x, b[j + 1] = dup.y;
         }
         *reinterpret_cast<uint4 *>(dg + i * 8) = pack_bf16(a);
         *reinterpret_cast<uint4 *>(du + i * 8) = pack_bf16(b);

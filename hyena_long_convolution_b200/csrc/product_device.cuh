@@ -278,65 +278,98 @@ __device__ __forceinline__ void tmem_wait(float (&v)[32])
 
 // ---------------------------------------------------------------- activations
 
-// 1 / (1 + e^-x), to 4 units in the last place: the quotient by the approximate
-// reciprocal, which is zero where e^-x passes 2^126.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// Two values at a time, in packed arithmetic.  2^x and 1 / x are the hardware's
+// approximations, 2^-22 off, and an exponential's argument is rounded once, so that
+// e^x is up to (|x| + 4) 2^-24 off.
+__device__ __forceinline__ float2 exp2_2(float2 x)
+{
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+}
+__device__ __forceinline__ float2 reciprocal2(float2 x)
+{
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+}
 
-constexpr float kGeluTanh = 1.59576912160573072f;  // 2 sqrt(2 / pi): (1 + tanh z) / 2 = sigmoid(2 z)
+constexpr float kLog2E = 1.44269504088896341f;
+
+// 1 / (1 + e^(-c x)), zero where the exponential passes 2^126.
+__device__ __forceinline__ float2 sigmoid2(float2 x, float c)
+{
+    const float2 e = exp2_2(__fmul2_rn(x, bcast2(-c * kLog2E)));
+    return reciprocal2(__fadd2_rn(e, bcast2(1.f)));
+}
 
 // The normal distribution's Phi(g), and e^{-g^2 / 2} in e.  Phi(-|g|) = t p(t)
 // e^{-g^2 / 2} with t = 1 / (1 + 0.3 |g|) and p of degree 7 fitted to the function in
-// the relative maximum norm for |g| <= 14.5 (1.6e-7; with the arithmetic, 13 half steps
-// of fp32 for |g| < 5), which keeps the digits that 1 + erf loses where g is negative.
-__device__ __forceinline__ float normal_cdf(float g, float &e)
+// the relative maximum norm for |g| <= 14.5 (1.6e-7; with the arithmetic some 20 half
+// steps of fp32 for |g| < 5), which keeps the digits that 1 + erf loses where g is
+// negative.
+__device__ __forceinline__ float2 normal_cdf2(float2 g, float2 &e)
 {
-    const float t = __fdividef(1.f, fmaf(0.3f, fabsf(g), 1.f));
-    float p = 0.03542377054691315f;
-    p = fmaf(p, t, -0.15615858137607574f);
-    p = fmaf(p, t, 0.20455701649188995f);
-    p = fmaf(p, t, -0.05203420668840408f);
-    p = fmaf(p, t, 0.1276918649673462f);
-    p = fmaf(p, t, 0.10017592459917068f);
-    p = fmaf(p, t, 0.12071213871240616f);
-    p = fmaf(p, t, 0.11963200569152832f);
-    e = expf(-0.5f * g * g);
-    const float tail = p * t * e;
-    return g < 0.f ? tail : 1.f - tail;
+    const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
+    const float2 t = reciprocal2(__ffma2_rn(a, bcast2(0.3f), bcast2(1.f)));
+    float2 p = bcast2(0.03542377054691315f);
+    p = __ffma2_rn(p, t, bcast2(-0.15615858137607574f));
+    p = __ffma2_rn(p, t, bcast2(0.20455701649188995f));
+    p = __ffma2_rn(p, t, bcast2(-0.05203420668840408f));
+    p = __ffma2_rn(p, t, bcast2(0.1276918649673462f));
+    p = __ffma2_rn(p, t, bcast2(0.10017592459917068f));
+    p = __ffma2_rn(p, t, bcast2(0.12071213871240616f));
+    p = __ffma2_rn(p, t, bcast2(0.11963200569152832f));
+    e = exp2_2(__fmul2_rn(__fmul2_rn(g, g), bcast2(-0.5f * kLog2E)));
+    const float2 tail = __fmul2_rn(__fmul2_rn(p, t), e);
+    const float2 rest = __ffma2_rn(tail, bcast2(-1.f), bcast2(1.f));
+    return make_float2(g.x < 0.f ? tail.x : rest.x, g.y < 0.f ? tail.y : rest.y);
 }
+
+constexpr float kGeluTanh = 1.59576912160573072f;  // 2 sqrt(2 / pi): (1 + tanh z) / 2 = sigmoid(2 z)
 
 // act(g) of the gated block (HYENA_ACT_*).
 template <int kAct>
-__device__ __forceinline__ float activation(float g)
+__device__ __forceinline__ float2 activation2(float2 g)
 {
     if constexpr (kAct == HYENA_ACT_SILU) {
-        return g * sigmoid(g);
+        return __fmul2_rn(g, sigmoid2(g, 1.f));
     } else if constexpr (kAct == HYENA_ACT_GELU) {
-        float e;
-        return g * normal_cdf(g, e);
+        float2 e;
+        return __fmul2_rn(g, normal_cdf2(g, e));
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
-        return g * sigmoid(kGeluTanh * fmaf(0.044715f * g * g, g, g));
+        const float2 z = __ffma2_rn(__fmul2_rn(__fmul2_rn(g, g), bcast2(0.044715f)), g, g);
+        return __fmul2_rn(g, sigmoid2(z, kGeluTanh));
     } else {
         return g;
     }
 }
 
-// (act(g), act'(g)).
+// act(g), and act'(g) in d.
 template <int kAct>
-__device__ __forceinline__ float2 activation_slope(float g)
+__device__ __forceinline__ float2 activation_slope2(float2 g, float2 &d)
 {
     if constexpr (kAct == HYENA_ACT_SILU) {
-        const float s = sigmoid(g);
-        return make_float2(g * s, s * fmaf(g, 1.f - s, 1.f));
+        const float2 s = sigmoid2(g, 1.f), rest = __ffma2_rn(s, bcast2(-1.f), bcast2(1.f));
+        d = __fmul2_rn(s, __ffma2_rn(g, rest, bcast2(1.f)));
+        return __fmul2_rn(g, s);
     } else if constexpr (kAct == HYENA_ACT_GELU) {
-        float e;
-        const float c = normal_cdf(g, e);
-        return make_float2(g * c, fmaf(g, 0.39894228040143268f * e, c));
+        float2 e;
+        const float2 c = normal_cdf2(g, e);
+        d = __ffma2_rn(g, __fmul2_rn(e, bcast2(0.39894228040143268f)), c);
+        return __fmul2_rn(g, c);
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
-        const float s = sigmoid(kGeluTanh * fmaf(0.044715f * g * g, g, g));
-        const float in = kGeluTanh * fmaf(3.f * 0.044715f * g, g, 1.f);
-        return make_float2(g * s, fmaf(g * s * (1.f - s), in, s));
+        const float2 g2 = __fmul2_rn(g, g);
+        const float2 s = sigmoid2(__ffma2_rn(__fmul2_rn(g2, bcast2(0.044715f)), g, g), kGeluTanh);
+        const float2 in = __ffma2_rn(g2, bcast2(3.f * 0.044715f * kGeluTanh), bcast2(kGeluTanh));
+        const float2 y = __fmul2_rn(g, s);
+        d = __ffma2_rn(__fmul2_rn(y, __ffma2_rn(s, bcast2(-1.f), bcast2(1.f))), in, s);
+        return y;
     } else {
-        return make_float2(g, 1.f);
+        d = bcast2(1.f);
+        return g;
     }
 }
 

@@ -135,24 +135,21 @@ __device__ __forceinline__ void in_turns(F f)
     }
 }
 
-// g[i] <- act(g[i]) u[i], the first `count` of kV.  The normal distribution's 20
-// instructions in turns of 16, the others' straight.
+// g[i] <- act(g[i]) u[i], the first `count` of kV.
 template <int kAct, int kV>
 __device__ __forceinline__ void gate(float (&v)[2 * kV], int count)
 {
-    constexpr int kN = kAct == HYENA_ACT_GELU && kV > 16 ? 16 : kV;
-    in_turns<kV, kN>([&](int j) {
 #pragma unroll
-        for (int i = 0; i < kN; i += 8) {
-            if (j + i >= count) continue;
+    for (int j = 0; j < kV; j += 8) {
+        if (j >= count) break;
 #pragma unroll
-            for (int l = i; l < i + 8; ++l) v[l] = activation<kAct>(v[l]) * v[kV + l];
+        for (int i = j; i < j + 8; i += 2) {
+            const float2 y = __fmul2_rn(activation2<kAct>(make_float2(v[i], v[i + 1])),
+                                        make_float2(v[kV + i], v[kV + i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
         }
-        if constexpr (kN < kV) {
-            turn<kV, kN>(v);
-            turn<kV, kN>(v + kV);
-        }
-    });
+    }
 }
 
 template <int kV>

@@ -298,17 +298,28 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 if (kF8 && A.a.q) {
                     // the largest of the row's 128 values: this half's and the other's
                     unsigned int mx = 0;
+                    if (left >= kHalf) {
 #pragma unroll
-                    for (int i = 0; i < kHalf; ++i)
-                        if (i < left) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
+                        for (int i = 0; i < kHalf; ++i) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kHalf; ++i)
+                            if (i < left) mx = max(mx, __float_as_uint(v[i]) & 0x7fffffffu);
+                    }
                     sh.amax[tid] = mx;
                     named_sync(1, kEpiThreads);
                     mx = max(mx, sh.amax[tid ^ kTile]);
                     named_sync(1, kEpiThreads);
                     const float scale = scale_of(mx);
+                    const bool small = scale < kSmallScale;
+                    const float by = small ? scale * 0x1p+64f : scale, inv = 1.f / by;
+                    if (small) {  // the same quotients
+#pragma unroll
+                        for (int i = 0; i < kHalf; ++i) v[i] *= 0x1p+64f;
+                    }
                     store_patch<4>(patch, lane, A.a.q + m0 * A.a.ld_q + n, A.a.ld_q, left, rows_of(m0), [&](int c) {
-                        const uint2 lo = e4m3x8<true>(reinterpret_cast<float(&)[8]>(v[16 * c]), scale);
-                        const uint2 hi = e4m3x8<true>(reinterpret_cast<float(&)[8]>(v[16 * c + 8]), scale);
+                        const uint2 lo = e4m3x8<true>(reinterpret_cast<const float(&)[8]>(v[16 * c]), by, inv);
+                        const uint2 hi = e4m3x8<true>(reinterpret_cast<const float(&)[8]>(v[16 * c + 8]), by, inv);
                         return make_uint4(lo.x, lo.y, hi.x, hi.y);
                     });
                     if (hh == 0 && m < A.rows) A.a.scales[m * P.tiles_n + col0] = scale;
