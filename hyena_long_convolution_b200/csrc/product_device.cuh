@@ -52,6 +52,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, wait_phase(bar, parity, dead)) != 0;
 }
 
+// A read-only load that is issued where it stands: left to the compiler, a value that is
+// asked for early may be loaded where it is used.
+__device__ __forceinline__ float load_here(const float *p)
+{
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // ---------------------------------------------------------------- launches
 
 // The kernels here are launched before the one ahead of them in the stream has ended

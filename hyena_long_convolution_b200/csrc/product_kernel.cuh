@@ -16,12 +16,33 @@ constexpr int kRowBytes = 128;                    // of a k-block: 64 bf16 or 12
 constexpr size_t kProductHeader = 4096;           // 256 bytes of header, then a counter for each split tile
 constexpr int kMaxSplitTiles = (kProductHeader - 256) / 4;
 
+// Quotients by a number that the host knows, of 0 <= n < 2^31: the high part of a
+// product (m = ceil(2^(31 + s) / d), 2^s >= d).  An integer division takes 150 cycles,
+// of which a tile's place needs two.
+struct Divide {
+    unsigned int m;
+    int s;
+    void set(int d)
+    {
+        s = 0;
+        while ((1ll << s) < d) ++s;
+        m = static_cast<unsigned int>(((1ull << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned int>(n)) * m) >> (31 + s));
+    }
+};
+
+constexpr int kBand = 8;  // tile rows that are walked together, so that L2 holds what they share
+
 // How a product is divided: tiles of the output, k-blocks of a tile, units (pairs of
 // CTAs) that walk through them.  The first `split` tiles' k-blocks are dealt out
 // evenly, a contiguous run a unit (unit u begins at u each + min(u, more)), so that
 // every unit is busy to the end; the others go whole, one after another.
 struct Plan {
     int tiles_m, tiles_n, tiles;
+    Divide by_band, by_last;  // by the tiles of a band of kBand tile rows, and by the rows of the last, smaller one
     int blocks;  // k-blocks of a tile
     int split, units;
     long long each;

@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 const float *sx0 = m + lane < A.a.M && lane < kH ? A.a.sx + (m + lane) * A.a.sx_row : nullptr;
                 const float *sx1 = kH > 32 && m + 32 + lane < A.a.M ? A.a.sx + (m + 32 + lane) * A.a.sx_row : nullptr;
                 const auto scale_at = [&](const float *p, int kb) {
-                    return p ? __ldg(p + static_cast<long long>(kb) * A.a.sx_step) : 0.f;
+                    return p ? load_here(p + static_cast<long long>(kb) * A.a.sx_step) : 0.f;
                 };
                 float x0 = scale_at(sx0, k0), x1 = scale_at(sx1, k0);
-                float f1 = __ldg(s1 + k0), f2 = __ldg(s2 + k0);
+                float f1 = load_here(s1 + k0), f2 = load_here(s2 + k0);
                 for (int kb = k0; kb < k1; ++kb) {
                     __syncwarp();
                     // a token's scale times each weight's
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     if (kb + 1 < k1) {
                         x0 = scale_at(sx0, kb + 1);
                         x1 = scale_at(sx1, kb + 1);
-                        f1 = __ldg(s1 + kb + 1);
-                        f2 = __ldg(s2 + kb + 1);
+                        f1 = load_here(s1 + kb + 1);
+                        f2 = load_here(s2 + kb + 1);
                     }
                     ok = ok && warp_wait(sh.tfull + buf, tph, dead);
                     if (!ok) break;

@@ -20,7 +20,6 @@ constexpr int kOperand = kTile * kRowBytes;      // 16 KB
 constexpr int kStage = 2 * kOperand;
 constexpr int kSmem = kStages * kStage + kEpiWarps * kPatch + 1024;
 constexpr int kHalf = 64;                        // columns of each group of 128 a thread has
-constexpr int kBand = 8;                         // tile rows that are walked together, for L2
 
 enum { kForward = 0, kDx = 1, kDw = 2 };
 
@@ -77,11 +76,15 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 
     // tile -> (tile row, tile column): bands of kBand tile rows, columns within
     auto place = [&](int tile, int &tm, int &tn) {
-        const int per = kBand * P.tiles_n;
-        const int band = tile / per, r = tile - band * per;
-        const int rows = min(kBand, P.tiles_m - band * kBand);
-        tn = r / rows;
-        tm = band * kBand + (r - tn * rows);
+        const int band = P.by_band(tile), r = tile - band * (kBand * P.tiles_n);
+        const int rows = P.tiles_m - band * kBand;
+        if (rows >= kBand) {
+            tn = r / kBand;
+            tm = band * kBand + r % kBand;
+        } else {
+            tn = P.by_last(r);
+            tm = band * kBand + (r - tn * rows);
+        }
     };
 
     if (warp >= kEpiWarps) {
@@ -195,9 +198,9 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 const int n2 = n1 + (!A.a.gated && tn * A.tile_cols + kTile < A.cols ? 1 : 0);
                 s1 = A.a.sw1 + static_cast<long long>(n1) * groups + w.k0;
                 s2 = (A.a.gated ? A.a.sw2 : A.a.sw1) + static_cast<long long>(n2) * groups + w.k0;
-                x = live ? __ldg(sx) : 0.f;
-                f1 = __ldg(s1);
-                f2 = __ldg(s2);
+                x = live ? load_here(sx) : 0.f;
+                f1 = load_here(s1);
+                f2 = load_here(s2);
             }
             return true;
         };
@@ -218,9 +221,9 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     const float2 c1 = bcast2(x * f1), c2 = bcast2(x * f2);
                     if (kb + 1 < k1) {  // the next k-block's scales while this one's sums come in
                         sx += A.a.sx_step;
-                        x = live ? __ldg(sx) : 0.f;
-                        f1 = __ldg(++s1);
-                        f2 = __ldg(++s2);
+                        x = live ? load_here(sx) : 0.f;
+                        f1 = load_here(++s1);
+                        f2 = load_here(++s2);
                     }
                     ok = ok && warp_wait(sh.tfull + buf, tph, dead);
                     if (!ok) break;
@@ -359,6 +362,8 @@ void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
     p.tiles_m = tiles_m;
     p.tiles_n = tiles_n;
     p.tiles = tiles_m * tiles_n;
+    p.by_band.set(kBand * tiles_n);
+    p.by_last.set(tiles_m % kBand ? tiles_m % kBand : 1);
     p.blocks = blocks;
     p.units = p.tiles < units ? p.tiles : units;
     p.split = 0;
