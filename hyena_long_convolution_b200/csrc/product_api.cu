@@ -28,6 +28,8 @@ hyena_status_t check_sizes(int64_t rows, int a, int b)
     if (rows < 0 || a < 1 || b < 1) return HYENA_ERR_INVALID_ARG;
     if (a % 8 || b % 8) return HYENA_ERR_ALIGNMENT;
     if (rows >= (1ll << 31) || a > HYENA_MAX_WIDTH || b > HYENA_MAX_WIDTH) return HYENA_ERR_UNSUPPORTED;
+    // tiles of 256 rows x 128 columns are counted in 31 bits
+    if (((rows + 255) / 256) * ((a > b ? a : b) / 128 + 1) >= (1ll << 31)) return HYENA_ERR_UNSUPPORTED;
     return HYENA_OK;
 }
 
