@@ -70,17 +70,18 @@ size_t part_bytes(long long M)
 
 }  // namespace
 
-bool encode_matrix(CUtensorMap *m, const void *p, bool fp8, long long rows, int cols, long long ld, int box_rows)
+bool encode_matrix(CUtensorMap *m, const void *p, int size, long long rows, int cols, long long ld, int box_rows)
 {
     std::call_once(g_encode_once, resolve_encode);
     if (g_encode == nullptr) return false;
-    const int size = fp8 ? 1 : 2;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * size};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(kRowBytes / size), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1u, 1u};
-    return g_encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                    const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUtensorMapDataType type = size == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return g_encode(m, type, 2, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

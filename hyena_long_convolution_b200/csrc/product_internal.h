@@ -74,9 +74,9 @@ int launch_product_wide(const ProductArgs &a, cudaStream_t st);
 int launch_ffn_dx(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st);
 int launch_ffn_dw(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st);
 
-// Map of a [rows, cols] matrix of bf16 or codes with boxes of 128 bytes of a row
+// Map of a [rows, cols] matrix of codes, bf16 or fp32 (size 1, 2, 4) with boxes of 128 bytes of a row
 // times box_rows rows, laid out with the 128-byte swizzle.
-bool encode_matrix(CUtensorMap *m, const void *p, bool fp8, long long rows, int cols, long long ld, int box_rows);
+bool encode_matrix(CUtensorMap *m, const void *p, int size, long long rows, int cols, long long ld, int box_rows);
 int product_sms();
 
 size_t product_workspace(long long M, int N, int K, bool fp8, bool gated);

@@ -214,25 +214,26 @@ __device__ __forceinline__ uint4 pack_bf16(const float *v)
     return q;
 }
 
-// A warp's 32 rows of outputs, a row a lane in registers, written a row by several
-// lanes: through 4 KB of shared memory, in rows of 128 bytes whose 16-byte chunks
-// are permuted by the row (chunk c of row r at c ^ (r % 8)), which keeps both ways
-// free of bank conflicts.  Straight from the registers a store touches 32 rows, 16
-// bytes of each: 8000 cycles for a CTA's 128 x 256 sums, this way 4000.
+// A warp's 32 rows of outputs, a row a lane in registers, go through 4 KB of shared
+// memory, in rows of 128 bytes whose 16-byte chunks are permuted by the row (chunk c
+// of row r at c ^ (r % 8)): free of bank conflicts, and TMA's 128-byte swizzle.
+// Straight from the registers a store touches 32 rows, 16 bytes of each: 8000 cycles
+// for a CTA's 128 x 256 sums; from the patch by the lanes 2800.
 constexpr int kPatch = 4096;
+constexpr int kPatches = 2;  // of a warp: one is filled while TMA reads the other
 
-// One patch of kChunks x 16 bytes a row: `chunk(c)` gives a lane's 16 bytes, row r
-// goes to p + r * pitch (bytes), `left` bytes of it, `rows` rows.
-template <int kChunks, class F>
-__device__ __forceinline__ void store_patch(unsigned char *patch, int lane, unsigned char *p, long long pitch, int left,
+// Codes, 64 bytes a row, are written by the lanes: `chunk(c)` gives a lane's 16 bytes,
+// row r goes to p + r * pitch, `left` bytes (a multiple of 8) of it, `rows` rows.
+template <class F>
+__device__ __forceinline__ void store_codes(unsigned char *patch, int lane, unsigned char *p, long long pitch, int left,
                                             int rows, F chunk)
 {
+    constexpr int kChunks = 4, kRows = 32 / kChunks;
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
         *reinterpret_cast<uint4 *>(patch + lane * 128 + ((c ^ (lane & 7)) << 4)) = chunk(c);
     __syncwarp();
-    constexpr int kRows = 32 / kChunks;  // at a time
     const int c = lane % kChunks;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -242,30 +243,64 @@ __device__ __forceinline__ void store_patch(unsigned char *patch, int lane, unsi
         if (r >= rows || c * 16 >= left) continue;
         if (c * 16 + 16 <= left)
             *reinterpret_cast<uint4 *>(to) = q;
-        else  // 8 codes
+        else
             *reinterpret_cast<uint2 *>(to) = make_uint2(q.x, q.y);
     }
 }
 
-// 64 values of each of the warp's rows as bf16 or fp32; `left` of them lie inside.
-__device__ __forceinline__ void store_rows(unsigned char *patch, int lane, void *p, bool f32, long long at, long long ld,
-                                           const float *v, int left, int rows)
-{
-    if (f32) {
-        unsigned char *to = static_cast<unsigned char *>(p) + at * 4;
-        store_patch<8>(patch, lane, to, ld * 4, left * 4, rows, [&](int c) {
-            return make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-                              __float_as_uint(v[4 * c + 3]));
-        });
-        store_patch<8>(patch, lane, to + 128, ld * 4, left * 4 - 128, rows, [&](int c) {
-            return make_uint4(__float_as_uint(v[32 + 4 * c]), __float_as_uint(v[33 + 4 * c]),
-                              __float_as_uint(v[34 + 4 * c]), __float_as_uint(v[35 + 4 * c]));
-        });
-    } else {
-        store_patch<8>(patch, lane, static_cast<unsigned char *>(p) + at * 2, ld * 2, left * 2, rows,
-                       [&](int c) { return pack_bf16(v + 8 * c); });
+// Values go by TMA, which leaves out what lies outside the matrix.
+struct RowStore {
+    unsigned char *patches;
+    int lane, next;
+    __device__ __forceinline__ RowStore(unsigned char *p, int l) : patches(p), lane(l), next(0) {}
+
+    // 128 bytes of each row at (column, row) of the matrix
+    template <class F>
+    __device__ __forceinline__ void put(const CUtensorMap *map, int column, int row, F chunk)
+    {
+        unsigned char *patch = patches + next * kPatch;
+        next ^= 1;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPatches - 1) : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4 *>(patch + lane * 128 + ((c ^ (lane & 7)) << 4)) = chunk(c);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                "r"(column), "r"(row), "r"(smem_u32(patch))
+                : "memory");
     }
-}
+
+    // 64 values as bf16 or fp32; `left` columns of the matrix from there on (maybe none)
+    __device__ __forceinline__ void values(const CUtensorMap *map, bool f32, int column, int row, const float *v, int left)
+    {
+        if (left <= 0) return;
+        if (!f32) {
+            put(map, column, row, [&](int c) { return pack_bf16(v + 8 * c); });
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (left <= 32 * h) return;
+            put(map, column + 32 * h, row, [&](int c) {
+                const float *f = v + 32 * h + 4 * c;
+                return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                  __float_as_uint(f[3]));
+            });
+        }
+    }
+
+    // before the CTA ends: everything written
+    __device__ __forceinline__ void finish()
+    {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+};
 
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi)); }
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsAux)); }

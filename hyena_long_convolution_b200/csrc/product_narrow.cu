@@ -365,12 +365,12 @@ int launch_product_narrow(const ProductArgs &a, cudaStream_t st)
     const int nt = narrow_tokens(a.M);
     const int kb = a.fp8 ? 128 : 64;
     CUtensorMap x, w1, w2;
-    if (!encode_matrix(&x, a.x, a.fp8, a.M, a.K, a.ld_x, nt) ||
-        !encode_matrix(&w1, a.w1, a.fp8, a.N, a.K, a.ld_w, kTile))
+    if (!encode_matrix(&x, a.x, a.fp8 ? 1 : 2, a.M, a.K, a.ld_x, nt) ||
+        !encode_matrix(&w1, a.w1, a.fp8 ? 1 : 2, a.N, a.K, a.ld_w, kTile))
         return -1;
     if (!a.gated)
         w2 = w1;
-    else if (!encode_matrix(&w2, a.w2, a.fp8, a.N, a.K, a.ld_w, kTile))
+    else if (!encode_matrix(&w2, a.w2, a.fp8 ? 1 : 2, a.N, a.K, a.ld_w, kTile))
         return -1;
     NarrowArgs w{};
     w.tiles_m = static_cast<int>((a.M + nt - 1) / nt);

@@ -15,10 +15,10 @@ namespace hyena {
 namespace {
 
 constexpr int kTile = 128;                       // rows of a CTA's operands
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperand = kTile * kRowBytes;      // 16 KB
 constexpr int kStage = 2 * kOperand;
-constexpr int kSmem = kStages * kStage + kEpiWarps * kPatch + 1024;
+constexpr int kSmem = kStages * kStage + kEpiWarps * kPatches * kPatch + 1024;
 constexpr int kHalf = 64;                        // columns of each group of 128 a thread has
 
 enum { kForward = 0, kDx = 1, kDw = 2 };
@@ -30,8 +30,6 @@ struct WideArgs {
     int blocks1;         // dx: k-blocks of the first pair of operands
     int tile_cols;       // output columns of a tile
     ProductArgs a;       // forward
-    uint16_t *c[2];      // dx: c[0]; dW: both
-    long long ld_c;
     unsigned int *hdr;
 };
 
@@ -39,7 +37,8 @@ template <int kMode, bool kF8>
 __global__ void __launch_bounds__(kThreadsProduct, 1)
     product_wide_kernel(const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap a2,
                         const __grid_constant__ CUtensorMap b1, const __grid_constant__ CUtensorMap b2,
-                        const __grid_constant__ WideArgs A)
+                        const __grid_constant__ CUtensorMap c1, const __grid_constant__ CUtensorMap c2,
+                        const __grid_constant__ CUtensorMap c3, const __grid_constant__ WideArgs A)
 {
     constexpr bool kAmn = kMode == kDw, kBmn = kMode != kForward;
     constexpr int kBlock = kF8 ? 128 : 64;  // k of a block
@@ -175,7 +174,8 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + hh * kHalf;
         const uint32_t tempty0 = cluster_addr(sh.tempty, 0), tempty1 = cluster_addr(sh.tempty + 1, 0);
         const int groups = P.blocks;  // of codes: one a k-block
-        unsigned char *patch = stages + kStages * kStage + warp * kPatch;
+        unsigned char *patch = stages + kStages * kStage + warp * (kPatches * kPatch);
+        RowStore out(patch, lane);
         int buf = 0;
         uint32_t tph = 0;
         bool ok = true;
@@ -276,26 +276,25 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             const long long m = static_cast<long long>(row0) * 256 + rank * kTile + row;
             const int n = col0 * A.tile_cols + hh * kHalf;
             const int left = A.cols - n;
-            // the warp's first row and how many there are (maybe none)
-            const long long m0 = m - lane;
-            auto rows_of = [&](long long r) { return static_cast<int>(A.rows - r < 32 ? A.rows - r : 32); };
+            // the warp's first row; none of its rows may lie inside
+            const int m0 = static_cast<int>(m) - lane;
             if constexpr (kMode != kForward) {
-                long long r = m0;
-                uint16_t *c = A.c[0];
-                if (kMode == kDw && row0 >= P.tiles_m / 2) {
-                    r -= P.tiles_m / 2 * 256ll;
-                    c = A.c[1];
+                // dW: the tile rows of the gate's, then those of the up projection's
+                const bool second = kMode == kDw && row0 >= P.tiles_m / 2;
+                const int r = second ? m0 - P.tiles_m / 2 * 256 : m0;
+                if (r < A.rows) {
+                    out.values(second ? &c2 : &c1, false, n, r, v, left);
+                    out.values(second ? &c2 : &c1, false, n + kTile, r, v + kHalf, left - kTile);
                 }
-                store_rows(patch, lane, c, false, r * A.ld_c + n, A.ld_c, v, left, rows_of(r));
-                store_rows(patch, lane, c, false, r * A.ld_c + n + kTile, A.ld_c, v + kHalf, left - kTile, rows_of(r));
             } else if (!A.a.gated) {
-                store_rows(patch, lane, A.a.y, A.a.y_f32, m0 * A.a.ld_y + n, A.a.ld_y, v, left, rows_of(m0));
-                store_rows(patch, lane, A.a.y, A.a.y_f32, m0 * A.a.ld_y + n + kTile, A.a.ld_y, v + kHalf, left - kTile,
-                           rows_of(m0));
+                if (m0 < A.rows) {
+                    out.values(&c1, A.a.y_f32, n, m0, v, left);
+                    out.values(&c1, A.a.y_f32, n + kTile, m0, v + kHalf, left - kTile);
+                }
             } else {
-                if (A.a.g) {
-                    store_rows(patch, lane, A.a.g, A.a.g_f32, m0 * A.a.ld_g + n, A.a.ld_g, v, left, rows_of(m0));
-                    store_rows(patch, lane, A.a.u, A.a.g_f32, m0 * A.a.ld_g + n, A.a.ld_g, v + kHalf, left, rows_of(m0));
+                if (A.a.g && m0 < A.rows) {
+                    out.values(&c2, A.a.g_f32, n, m0, v, left);
+                    out.values(&c3, A.a.g_f32, n, m0, v + kHalf, left);
                 }
                 gate<kHalf>(v, A.a.act, kHalf);
                 if (kF8 && A.a.q) {
@@ -320,17 +319,19 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 #pragma unroll
                         for (int i = 0; i < kHalf; ++i) v[i] *= 0x1p+64f;
                     }
-                    store_patch<4>(patch, lane, A.a.q + m0 * A.a.ld_q + n, A.a.ld_q, left, rows_of(m0), [&](int c) {
+                    const int rows = static_cast<int>(A.rows - m0 < 32 ? A.rows - m0 : 32);
+                    store_codes(patch, lane, A.a.q + static_cast<long long>(m0) * A.a.ld_q + n, A.a.ld_q, left, rows, [&](int c) {
                         const uint2 lo = e4m3x8<true>(reinterpret_cast<const float(&)[8]>(v[16 * c]), by, inv);
                         const uint2 hi = e4m3x8<true>(reinterpret_cast<const float(&)[8]>(v[16 * c + 8]), by, inv);
                         return make_uint4(lo.x, lo.y, hi.x, hi.y);
                     });
                     if (hh == 0 && m < A.rows) A.a.scales[m * P.tiles_n + col0] = scale;
-                } else {
-                    store_rows(patch, lane, A.a.y, false, m0 * A.a.ld_y + n, A.a.ld_y, v, left, rows_of(m0));
+                } else if (m0 < A.rows) {
+                    out.values(&c1, false, n, m0, v, left);
                 }
             }
         }
+        out.finish();
     }
     tc_fence_before();
     cluster_sync();  // the other CTA may still tell this one's barriers
@@ -356,6 +357,7 @@ int pairs()
 // Whole tiles, wave after wave, unless sharing out the last one or two waves' k-blocks
 // saves more than the joining costs, which is about that of kJoin k-blocks.
 constexpr int kJoin = 28;
+constexpr int kParts = 6;
 
 void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
 {
@@ -369,10 +371,12 @@ void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
     p.split = 0;
     const int rest = p.tiles % units;
     if (rest != 0) {
+        // a tile's parts are added up by one CTA, so that more than kParts cost what they save
+        const int most = p.tiles < units && p.tiles * kParts < units ? p.tiles * kParts : units;
         const long long all = static_cast<long long>(rest) * blocks;
-        if (blocks - (all + units - 1) / units > kJoin) {
-            p.units = units;
-            p.split = p.tiles < units ? rest : rest + units;  // 0.5 to 2 tiles a unit, few parts a tile
+        if (blocks - (all + most - 1) / most > kJoin) {
+            p.units = most;
+            p.split = p.tiles < units ? rest : rest + units;  // 0.2 to 2 tiles a unit
         }
     }
     const long long run = static_cast<long long>(p.split) * blocks;
@@ -380,14 +384,23 @@ void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
     p.more = static_cast<int>(run % p.units);
 }
 
+struct Maps {
+    CUtensorMap a1, a2, b1, b2, c1, c2, c3;
+};
+
+// Outputs leave in boxes of 128 bytes of each of 32 rows.
+bool encode_output(CUtensorMap *m, const void *p, bool f32, long long rows, int cols, long long ld)
+{
+    return encode_matrix(m, p, f32 ? 4 : 2, rows, cols, ld, 32);
+}
+
 template <int kMode, bool kF8>
-int start(const CUtensorMap &a1, const CUtensorMap &a2, const CUtensorMap &b1, const CUtensorMap &b2, const WideArgs &w,
-          cudaStream_t st)
+int start(const Maps &m, const WideArgs &w, cudaStream_t st)
 {
     HYENA_TRY(cudaFuncSetAttribute(product_wide_kernel<kMode, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
               "product (wide) attribute");
     return launch_early(product_wide_kernel<kMode, kF8>, dim3(2 * w.plan.units), kThreadsProduct, kSmem, 2, st,
-                        "product (wide) launch", a1, a2, b1, b2, w);
+                        "product (wide) launch", m.a1, m.a2, m.b1, m.b2, m.c1, m.c2, m.c3, w);
 }
 
 }  // namespace
@@ -396,12 +409,19 @@ int launch_product_wide(const ProductArgs &a, cudaStream_t st)
 {
     const int u = pairs();
     if (u < 1) return -1;
-    CUtensorMap x, w1, w2;
-    const int kb = a.fp8 ? 128 : 64;
-    if (!encode_matrix(&x, a.x, a.fp8, a.M, a.K, a.ld_x, kTile) ||
-        !encode_matrix(&w1, a.w1, a.fp8, a.N, a.K, a.ld_w, kTile) ||
-        !encode_matrix(&w2, a.gated ? a.w2 : a.w1, a.fp8, a.N, a.K, a.ld_w, kTile))
-        return -1;
+    const int kb = a.fp8 ? 128 : 64, size = a.fp8 ? 1 : 2;
+    Maps m;
+    bool ok = encode_matrix(&m.a1, a.x, size, a.M, a.K, a.ld_x, kTile) &&
+              encode_matrix(&m.b1, a.w1, size, a.N, a.K, a.ld_w, kTile) &&
+              (!a.gated || encode_matrix(&m.b2, a.w2, size, a.N, a.K, a.ld_w, kTile)) &&
+              (!a.y || encode_output(&m.c1, a.y, a.y_f32, a.M, a.N, a.ld_y)) &&
+              (!a.g || (encode_output(&m.c2, a.g, a.g_f32, a.M, a.N, a.ld_g) &&
+                        encode_output(&m.c3, a.u, a.g_f32, a.M, a.N, a.ld_g)));
+    if (!ok) return -1;
+    m.a2 = m.a1;
+    if (!a.gated) m.b2 = m.b1;
+    if (!a.y) m.c1 = m.a1;  // not read
+    if (!a.g) m.c2 = m.c3 = m.c1;
     WideArgs w{};
     w.tile_cols = a.gated ? kTile : 2 * kTile;
     make_plan(w.plan, u, static_cast<int>((a.M + 255) / 256), (a.N + w.tile_cols - 1) / w.tile_cols,
@@ -410,47 +430,47 @@ int launch_product_wide(const ProductArgs &a, cudaStream_t st)
     w.cols = a.N;
     w.a = a;
     w.hdr = static_cast<unsigned int *>(a.workspace);
-    return a.fp8 ? start<kForward, true>(x, x, w1, w2, w, st) : start<kForward, false>(x, x, w1, w2, w, st);
+    return a.fp8 ? start<kForward, true>(m, w, st) : start<kForward, false>(m, w, st);
 }
 
 int launch_ffn_dx(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
 {
     const int u = pairs();
     if (u < 1) return -1;
-    CUtensorMap g, q, w1, w2;
-    if (!encode_matrix(&g, dg, false, a.M, a.F, a.F, kTile) || !encode_matrix(&q, du, false, a.M, a.F, a.F, kTile) ||
-        !encode_matrix(&w1, a.w1, false, a.F, a.D, a.ld_w, 64) || !encode_matrix(&w2, a.w2, false, a.F, a.D, a.ld_w, 64))
+    Maps m;
+    if (!encode_matrix(&m.a1, dg, 2, a.M, a.F, a.F, kTile) || !encode_matrix(&m.a2, du, 2, a.M, a.F, a.F, kTile) ||
+        !encode_matrix(&m.b1, a.w1, 2, a.F, a.D, a.ld_w, 64) || !encode_matrix(&m.b2, a.w2, 2, a.F, a.D, a.ld_w, 64) ||
+        !encode_output(&m.c1, a.dx, false, a.M, a.D, a.ld_dx))
         return -1;
+    m.c2 = m.c3 = m.c1;
     WideArgs w{};
     w.tile_cols = 2 * kTile;
     w.blocks1 = (a.F + 63) / 64;
     make_plan(w.plan, u, static_cast<int>((a.M + 255) / 256), (a.D + 255) / 256, 2 * w.blocks1);
     w.rows = a.M;
     w.cols = a.D;
-    w.c[0] = a.dx;
-    w.ld_c = a.ld_dx;
     w.hdr = static_cast<unsigned int *>(a.workspace);
-    return start<kDx, false>(g, q, w1, w2, w, st);
+    return start<kDx, false>(m, w, st);
 }
 
 int launch_ffn_dw(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
 {
     const int u = pairs();
     if (u < 1) return -1;
-    CUtensorMap g, q, x;
-    if (!encode_matrix(&g, dg, false, a.M, a.F, a.F, 64) || !encode_matrix(&q, du, false, a.M, a.F, a.F, 64) ||
-        !encode_matrix(&x, a.x, false, a.M, a.D, a.ld_x, 64))
+    Maps m;
+    if (!encode_matrix(&m.a1, dg, 2, a.M, a.F, a.F, 64) || !encode_matrix(&m.a2, du, 2, a.M, a.F, a.F, 64) ||
+        !encode_matrix(&m.b1, a.x, 2, a.M, a.D, a.ld_x, 64) ||
+        !encode_output(&m.c1, a.dw1, false, a.F, a.D, a.ld_dw) || !encode_output(&m.c2, a.dw2, false, a.F, a.D, a.ld_dw))
         return -1;
+    m.b2 = m.b1;
+    m.c3 = m.c1;
     WideArgs w{};
     w.tile_cols = 2 * kTile;
     make_plan(w.plan, u, 2 * ((a.F + 255) / 256), (a.D + 255) / 256, static_cast<int>((a.M + 63) / 64));
     w.rows = a.F;
     w.cols = a.D;
-    w.c[0] = a.dw1;
-    w.c[1] = a.dw2;
-    w.ld_c = a.ld_dw;
     w.hdr = static_cast<unsigned int *>(a.workspace);
-    return start<kDw, false>(g, q, x, x, w, st);
+    return start<kDw, false>(m, w, st);
 }
 
 }  // namespace hyena
