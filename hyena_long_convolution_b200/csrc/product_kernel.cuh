@@ -14,7 +14,6 @@ constexpr int kThreadsProduct = kEpiThreads + 128; // + a TMA warp, an MMA warp 
 constexpr int kRegsEpi = 208, kRegsAux = 88;
 constexpr int kRowBytes = 128;                    // of a k-block: 64 bf16 or 128 codes
 constexpr size_t kProductHeader = 4096;           // 256 bytes of header, then a counter for each split tile
-constexpr int kMaxSplitTiles = (kProductHeader - 256) / 4;
 
 // Quotients by a number that the host knows, of 0 <= n < 2^31: the high part of a
 // product (m = ceil(2^(31 + s) / d), 2^s >= d).  An integer division takes 150 cycles,
@@ -37,42 +36,47 @@ struct Divide {
 constexpr int kBand = 8;  // tile rows that are walked together, so that L2 holds what they share
 
 // How a product is divided: tiles of the output, k-blocks of a tile, units (pairs of
-// CTAs) that walk through them.  The first `split` tiles' k-blocks are dealt out
-// evenly, a contiguous run a unit (unit u begins at u each + min(u, more)), so that
-// every unit is busy to the end; the others go whole, one after another.
+// CTAs) that walk through them, whole tiles one after another.  With fewer tiles than
+// units they may be `shared`: all tiles' k-blocks dealt out evenly, a contiguous run a
+// unit (unit u begins at u each + min(u, more)), and a tile's parts joined.  (Sharing
+// out what is left of many tiles after whole waves costs more than it saves, at every
+// number of tiles from 76 to 1376.)
 struct Plan {
     int tiles_m, tiles_n, tiles;
     Divide by_band, by_last;  // by the tiles of a band of kBand tile rows, and by the rows of the last, smaller one
-    int blocks;  // k-blocks of a tile
-    int split, units;
-    long long each;
-    int more;
-    __device__ __forceinline__ long long first(int unit) const { return unit * each + min(unit, more); }
+    int blocks;               // k-blocks of a tile
+    int units;
+    bool shared;
+    int each, more;
+    __device__ __forceinline__ int first(int unit) const { return unit * each + min(unit, more); }
 };
 
 struct Walk {
     const Plan &p;
-    long long pos, end;
-    int whole;
+    int step, end;  // the next whole tile; of a run, the k-blocks left
     int tile, k0, k1;
-    __device__ __forceinline__ Walk(const Plan &plan, int unit)
-        : p(plan), pos(plan.first(unit)), end(plan.first(unit + 1)), whole(plan.split + unit)
+    __device__ __forceinline__ Walk(const Plan &plan, int unit) : p(plan), step(unit), end(0), tile(0), k1(0)
     {
-        tile = pos < end ? static_cast<int>(pos / p.blocks) : 0;
-        k1 = static_cast<int>(pos - static_cast<long long>(tile) * p.blocks);
+        if (p.shared) {
+            const int pos = p.first(unit);
+            end = p.first(unit + 1) - pos;
+            tile = pos / p.blocks;
+            k1 = pos - tile * p.blocks;
+        }
     }
     __device__ __forceinline__ bool next()
     {
-        if (pos < end) {
+        if (p.shared) {
+            if (end == 0) return false;
             if (k1 == p.blocks) k1 = 0, ++tile;
             k0 = k1;
-            k1 = end - pos < p.blocks - k0 ? k0 + static_cast<int>(end - pos) : p.blocks;
-            pos += k1 - k0;
+            k1 = min(p.blocks, k0 + end);
+            end -= k1 - k0;
             return true;
         }
-        if (whole >= p.tiles) return false;
-        tile = whole;
-        whole += p.units;
+        if (step >= p.tiles) return false;
+        tile = step;
+        step += p.units;
         k0 = 0;
         k1 = p.blocks;
         return true;
@@ -90,7 +94,7 @@ __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int un
 {
     constexpr size_t kSlot = static_cast<size_t>(kV / 4) * kEpiThreads;
     float4 *slots = reinterpret_cast<float4 *>(workspace + kProductHeader) + t;
-    const long long begin = static_cast<long long>(tile) * p.blocks;
+    const int begin = tile * p.blocks;
     // a unit has at most two parts: one that begins inside a tile and one at its start
     auto slot = [&](int u) { return slots + (2ll * (2ll * u + (p.first(u) > begin ? 0 : 1)) + rank) * kSlot; };
     float4 *own = slot(unit);
