@@ -61,11 +61,11 @@ int start_slopes(const FfnBackArgs &a, uint16_t *dg, uint16_t *du, int grid, cud
                         "ffn slopes launch", a, dg, du);
 }
 
-size_t part_bytes(long long M)
+// Parts of shared tiles: fp32 sums of 128 x 256 for each CTA.
+size_t part_bytes()
 {
-    // two parts a CTA of 148 (or of as many as there are), fp32 sums of 2 x 128 x tokens or, of a pair, 128 x 256
     const int sms = product_sms();
-    return static_cast<size_t>(2) * (sms > 0 ? sms : 148) * 2 * 128 * 4 * (M <= kNarrowRows ? narrow_tokens(M) : 128);
+    return static_cast<size_t>(sms > 0 ? sms : 148) * 128 * 256 * 4;
 }
 
 }  // namespace
@@ -98,11 +98,11 @@ int product_sms()
     return sms;
 }
 
-size_t product_workspace(long long M, int, int, bool, bool) { return kProductHeader + part_bytes(M); }
+size_t product_workspace(long long M, int, int, bool, bool) { return kProductHeader + (M > kNarrowRows ? part_bytes() : 0); }
 
 size_t ffn_backward_workspace(long long M, int, int F)
 {
-    return kProductHeader + part_bytes(1 << 30) + static_cast<size_t>(M) * F * 4;
+    return kProductHeader + part_bytes() + static_cast<size_t>(M) * F * 4;
 }
 
 int launch_product(const ProductArgs &a, cudaStream_t st)
@@ -115,7 +115,7 @@ int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st)
     const int sms = product_sms();
     if (sms < 1) return -1;
     uint16_t *dg = reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(a.workspace) + kProductHeader +
-                                                part_bytes(1 << 30));
+                                                part_bytes());
     uint16_t *du = dg + a.M * a.F;
     const long long ctas = (a.M * (a.F / 8) + 255) / 256;
     const int grid = ctas < sms * 8ll ? static_cast<int>(ctas) : sms * 8;

@@ -36,52 +36,51 @@ struct Divide {
 constexpr int kBand = 8;  // tile rows that are walked together, so that L2 holds what they share
 
 // How a product is divided: tiles of the output, k-blocks of a tile, units (pairs of
-// CTAs) that walk through them, whole tiles one after another.  With fewer tiles than
-// units they may be `shared`: all tiles' k-blocks dealt out evenly, a contiguous run a
-// unit (unit u begins at u each + min(u, more)), and a tile's parts joined.  (Sharing
-// out what is left of many tiles after whole waves costs more than it saves, at every
-// number of tiles from 76 to 1376.)
+// CTAs).  A unit takes whole tiles one after another; or, with few tiles, `share`
+// units take an even part of a tile's k-blocks each and the parts are joined.
+// (Sharing out what is left of many tiles after whole waves costs more than it saves,
+// at every number of tiles from 76 to 1376; runs that cross from one tile into the
+// next have two joins to wait for.)
 struct Plan {
     int tiles_m, tiles_n, tiles;
     Divide by_band, by_last;  // by the tiles of a band of kBand tile rows, and by the rows of the last, smaller one
     int blocks;               // k-blocks of a tile
-    int units;
-    bool shared;
-    int each, more;
-    __device__ __forceinline__ int first(int unit) const { return unit * each + min(unit, more); }
+    int units, share;
 };
 
 struct Walk {
-    const Plan &p;
-    int step, end;  // the next whole tile; of a run, the k-blocks left
-    int tile, k0, k1;
-    __device__ __forceinline__ Walk(const Plan &plan, int unit) : p(plan), step(unit), end(0), tile(0), k1(0)
+    int tile, k0, k1, step, end;
+    __device__ __forceinline__ Walk(const Plan &p, int unit)
     {
-        if (p.shared) {
-            const int pos = p.first(unit);
-            end = p.first(unit + 1) - pos;
-            tile = pos / p.blocks;
-            k1 = pos - tile * p.blocks;
-        }
+        const int part = unit % p.share;
+        step = p.share > 1 ? p.tiles : p.units;  // a part: one tile
+        tile = unit / p.share - step;
+        end = p.tiles;
+        k0 = static_cast<int>(static_cast<long long>(p.blocks) * part / p.share);
+        k1 = static_cast<int>(static_cast<long long>(p.blocks) * (part + 1) / p.share);
     }
-    __device__ __forceinline__ bool next()
-    {
-        if (p.shared) {
-            if (end == 0) return false;
-            if (k1 == p.blocks) k1 = 0, ++tile;
-            k0 = k1;
-            k1 = min(p.blocks, k0 + end);
-            end -= k1 - k0;
-            return true;
-        }
-        if (step >= p.tiles) return false;
-        tile = step;
-        step += p.units;
-        k0 = 0;
-        k1 = p.blocks;
-        return true;
-    }
+    __device__ __forceinline__ bool next() { return (tile += step) < end; }
 };
+
+constexpr int kMostParts = 4;
+
+// v = the parts' sums, in order.  Written out for each number of parts, so that many
+// loads are under way: part by part, 2.8 us each.
+template <int kParts, int kV>
+__device__ __forceinline__ void add_parts(float (&v)[kV], const float4 *parts)
+{
+    constexpr size_t kNext = 2ull * (kV / 4) * kEpiThreads;  // the next unit's slot of the same half
+#pragma unroll
+    for (int i = 0; i < kV / 4; ++i) {
+        float4 f = __ldcg(parts + i * kEpiThreads);
+#pragma unroll
+        for (int u = 1; u < kParts; ++u) {
+            const float4 g = __ldcg(parts + u * kNext + i * kEpiThreads);
+            f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+        }
+        v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+}
 
 // The sums of a part of a tile go to memory, and the CTA whose part is the last to
 // arrive adds them up in the order of k, so that the result does not depend on
@@ -94,42 +93,28 @@ __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int un
 {
     constexpr size_t kSlot = static_cast<size_t>(kV / 4) * kEpiThreads;
     float4 *slots = reinterpret_cast<float4 *>(workspace + kProductHeader) + t;
-    const int begin = tile * p.blocks;
-    // a unit has at most two parts: one that begins inside a tile and one at its start
-    auto slot = [&](int u) { return slots + (2ll * (2ll * u + (p.first(u) > begin ? 0 : 1)) + rank) * kSlot; };
-    float4 *own = slot(unit);
+    float4 *own = slots + (2ll * unit + rank) * kSlot;
 #pragma unroll
     for (int i = 0; i < kV / 4; ++i)
         own[i * kEpiThreads] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    // the units whose runs meet this tile (every run has a k-block)
-    int first = unit, past = unit + 1;
-    while (p.first(first) > begin) --first;
-    while (p.first(past) < begin + p.blocks) ++past;
     named_sync(1, kEpiThreads);
     if (t == 0) {
         __threadfence();  // the stores of all, which the barrier has ordered before it
         unsigned int *count = reinterpret_cast<unsigned int *>(workspace + 256) + 2 * tile + rank;
-        const bool last = atomicAdd(count, 1u) + 1 == static_cast<unsigned int>(past - first);
+        const bool last = atomicAdd(count, 1u) + 1 == static_cast<unsigned int>(p.share);
         if (last) *count = 0u;  // for the next call
         __threadfence();
         *flag = last ? 1u : 0u;
     }
     named_sync(1, kEpiThreads);
     if (*flag == 0u) return false;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = 0.f;
-#pragma unroll 1
-    for (int u = first; u < past; ++u) {
-        const float4 *q = slot(u);
-#pragma unroll
-        for (int i = 0; i < kV / 4; ++i) {
-            const float4 f = __ldcg(q + i * kEpiThreads);
-            v[4 * i] += f.x;
-            v[4 * i + 1] += f.y;
-            v[4 * i + 2] += f.z;
-            v[4 * i + 3] += f.w;
-        }
-    }
+    const float4 *parts = slots + (2ll * tile * p.share + rank) * kSlot;
+    if (p.share == 2)
+        add_parts<2, kV>(v, parts);
+    else if (p.share == 3)
+        add_parts<3, kV>(v, parts);
+    else
+        add_parts<4, kV>(v, parts);
     return true;
 }
 

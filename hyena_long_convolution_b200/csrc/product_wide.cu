@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 for (int i = 0; i < 2 * kHalf; ++i) v[i] = __uint_as_float(0x7fffffffu);
             }
             more = advance();
-            if (k1 - k0 < P.blocks &&
+            if (P.share > 1 &&
                 !join_parts(v, P, unit, rank, tile, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
                 continue;
             const long long m = static_cast<long long>(row0) * 256 + rank * kTile + row;
@@ -354,12 +354,9 @@ int pairs()
     return sms / 2;
 }
 
-// Fewer tiles than units are shared out if that takes kJoin k-blocks off a unit's run,
-// which is about what the joining costs; at most kParts units to a tile, since its
-// parts are added up by one pair (1.3 us each).  4096 -> 4096 x 11008 in e4m3: 512 rows
-// 51 us whole, 38 shared; 1032 -> 1032 x 5520: 1 row 50 us by 15 parts, 24 by 6.
-constexpr int kJoin = 28;
-constexpr int kParts = 6;
+// Units to a tile, where that takes kJoin k-blocks off a unit's run, which is about
+// what the joining costs.
+constexpr int kJoin = 16;
 
 void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
 {
@@ -369,19 +366,9 @@ void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
     p.by_band.set(kBand * tiles_n);
     p.by_last.set(tiles_m % kBand ? tiles_m % kBand : 1);
     p.blocks = blocks;
-    p.units = p.tiles < units ? p.tiles : units;
-    p.shared = false;
-    p.each = p.more = 0;
-    if (p.tiles < units) {
-        const int most = p.tiles * kParts < units ? p.tiles * kParts : units;
-        const long long all = static_cast<long long>(p.tiles) * blocks;
-        if (blocks - all / most > kJoin && all < (1ll << 30)) {
-            p.units = most;
-            p.shared = true;
-            p.each = static_cast<int>(all / most);
-            p.more = static_cast<int>(all % most);
-        }
-    }
+    p.share = units / p.tiles < kMostParts ? units / p.tiles : kMostParts;
+    if (p.share < 2 || blocks - blocks / p.share <= kJoin) p.share = 1;
+    p.units = p.share > 1 ? p.tiles * p.share : (p.tiles < units ? p.tiles : units);
 }
 
 struct Maps {
