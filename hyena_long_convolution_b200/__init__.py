@@ -79,12 +79,14 @@ ACTIVATIONS = {"silu": 1, "gelu": 2, "gelu_tanh": 3, "identity": 4}
 
 
 _torch_module = None  # imported by the first call; a statement in each costs it 0.1 us every time
+_BF16 = _F32 = _E4M3 = None  # its types, likewise
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _BF16, _F32, _E4M3
     if _torch_module is None:
         import torch
+        _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
         _torch_module = torch
     return _torch_module
 
@@ -1110,45 +1112,43 @@ def _act(name):
     return code
 
 
-def _mat(t, shape, dtype, name):
-    """Row stride of a [rows, width] tensor with unit stride within a row."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
-    st = t.stride()
-    if st[1] != 1:
-        raise ValueError(f"{name} must be contiguous within its rows")
-    return st[0] if shape[0] > 1 else max(st[0], shape[1])
+def _matrix(t, name, dtype):
+    """(rows, width, row stride) of a weight with unit stride within a row."""
+    sh, st = t.shape, t.stride()
+    if t.dtype is not dtype or len(sh) != 2 or st[1] != 1:
+        kind = "e4m3" if dtype is _E4M3 else "bf16"
+        raise ValueError(f"{name} must be a {kind} CUDA tensor [rows, width], contiguous within its rows")
+    rows, width = sh
+    return rows, width, st[0] if rows > 1 else max(st[0], width)
 
 
-def _pair(a, b, names):
-    """Two weights of one shape and row stride -> (rows, width, ld)."""
-    if len(a.shape) != 2:
-        raise ValueError(f"{names[0]} must be [F, D]")
-    ld = _mat(a, a.shape, a.dtype, names[0])
-    if _mat(b, a.shape, a.dtype, names[1]) != ld:
-        raise ValueError(f"{names[0]} and {names[1]} must share one row stride")
-    return a.shape[0], a.shape[1], ld
+def _pair(a, b, names, dtype, D):
+    """Two weights [F, D] of one shape and row stride -> (F, row stride)."""
+    F, width, ld = _matrix(a, names[0], dtype)
+    if width != D:
+        raise ValueError(f"weights must be of shape [F, {D}]")
+    if b.dtype is not dtype or b.shape != a.shape or b.stride() != a.stride() and _matrix(b, names[1], dtype)[2] != ld:
+        raise ValueError(f"{names[1]} must have the type, shape and row stride of {names[0]}")
+    return F, ld
 
 
 def _codes(x, x_scales, name):
     """Codes [M, K] or [B, L, K] with scales [M, 1] or [M, ceil(K / 128)] ->
     (M, K, ld, group)."""
-    M, K, ld = _rows(x, name, (_torch().float8_e4m3fn,))
+    M, K, ld = _rows(x, name, (_E4M3,))
     if M == 1:  # no second row: any stride will do
         ld = -(-K // 16) * 16
     groups = -(-K // 128)
-    if x_scales.shape == (M, groups) and groups > 1:
-        group = 128
-    else:  # one scale a row; the same thing where a row is one group
-        group = 0
-        if x_scales.shape != (M, 1):
-            raise ValueError(f"{name}'s scales must be of shape {(M, 1)} or {(M, groups)}")
-    _f32(x_scales, x_scales.shape, f"{name}'s scales", False)
-    return M, K, ld, group
+    sh = x_scales.shape
+    if len(sh) != 2 or sh[0] != M or (sh[1] != 1 and sh[1] != groups) or x_scales.dtype is not _F32 \
+            or not x_scales.is_contiguous():
+        raise ValueError(f"{name}'s scales must be a contiguous fp32 tensor of shape {(M, 1)} or {(M, groups)}")
+    return M, K, ld, 0 if sh[1] == 1 else 128  # one scale a row; the same thing where a row is one group
 
 
 def _weight_scales(t, N, K, name):
-    _f32(t, (-(-N // 128), -(-K // 128)), name, False)
+    if t.dtype is not _F32 or t.shape != (-(-N // 128), -(-K // 128)) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(-(-N // 128), -(-K // 128))}")
 
 
 def _out_rows(t, M, width, dtype, name):
@@ -1241,10 +1241,9 @@ def fp8_matmul(x, x_scales, weight, weight_scales, y=None, dtype=None, workspace
             return fp8_matmul(x, x_scales, weight, weight_scales, y, dtype, workspace)
     torch = _torch()
     M, K, ld, group = _codes(x, x_scales, "x")
-    if len(weight.shape) != 2 or weight.shape[1] != K:
-        raise ValueError("weight must be [N, K]")
-    N = weight.shape[0]
-    ld_w = _mat(weight, weight.shape, torch.float8_e4m3fn, "weight")
+    N, Kw, ld_w = _matrix(weight, "weight", _E4M3)
+    if Kw != K:
+        raise ValueError(f"weight must be [N, {K}]")
     _weight_scales(weight_scales, N, K, "weight_scales")
     here = _here(x, x_scales, weight, weight_scales, y, None if workspace is None else workspace.buf)
     if y is None:
@@ -1280,9 +1279,7 @@ def gated_ffn(x, gate_weight, up_weight, activation="silu", y=None, gate_out=Non
     torch = _torch()
     act = _act(activation)
     M, D, ld = _rows(x, "x", (torch.bfloat16,))
-    F, Dw, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"))
-    if Dw != D or gate_weight.dtype is not torch.bfloat16:
-        raise ValueError("weights must be bf16 tensors of shape [F, D]")
+    F, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"), _BF16, D)
     here = _here(x, gate_weight, up_weight, y, gate_out, up_out, None if workspace is None else workspace.buf)
     if y is None:
         y, ld_y = x.new_empty((*x.shape[:-1], F)), F
@@ -1312,9 +1309,7 @@ def gated_ffn_fp8(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, a
     e4m3 = torch.float8_e4m3fn
     act = _act(activation)
     M, D, ld, group = _codes(x, x_scales, "x")
-    F, Dw, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"))
-    if Dw != D or gate_weight.dtype is not e4m3:
-        raise ValueError("weights must be e4m3 tensors of shape [F, D]")
+    F, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"), e4m3, D)
     _weight_scales(gate_scales, F, D, "gate_scales")
     _weight_scales(up_scales, F, D, "up_scales")
     here = _here(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, y, q, scales,
@@ -1370,9 +1365,7 @@ def gated_ffn_backward(dy, x, gate_weight, up_weight, gate, up, activation="silu
     b = torch.bfloat16
     act = _act(activation)
     M, D, ld = _rows(x, "x", (b,))
-    F, Dw, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"))
-    if Dw != D or gate_weight.dtype is not b:
-        raise ValueError("weights must be bf16 tensors of shape [F, D]")
+    F, ld_w = _pair(gate_weight, up_weight, ("gate_weight", "up_weight"), b, D)
     ld_dy = _out_rows(dy, M, F, b, "dy")
     ld_g, kind = _kept(gate, up, M, F)
     here = _here(dy, x, gate_weight, up_weight, gate, up, dx, dgate_weight, dup_weight,
@@ -1386,9 +1379,9 @@ def gated_ffn_backward(dy, x, gate_weight, up_weight, gate, up, activation="silu
     elif dgate_weight is None or dup_weight is None:
         raise ValueError("give both of dgate_weight and dup_weight or neither")
     else:
-        ld_dw = _mat(dgate_weight, (F, D), b, "dgate_weight")
-        if _mat(dup_weight, (F, D), b, "dup_weight") != ld_dw:
-            raise ValueError("dgate_weight and dup_weight must share one row stride")
+        if dgate_weight.shape != (F, D):
+            raise ValueError(f"dgate_weight must be of shape {(F, D)}")
+        ld_dw = _pair(dgate_weight, dup_weight, ("dgate_weight", "dup_weight"), b, D)[1]
     if workspace is None:
         workspace = FfnWorkspace(M, D, F, backward=True)
     rc = lib().hyena_gated_ffn_backward(dy.data_ptr(), ld_dy, x.data_ptr(), ld, gate_weight.data_ptr(),

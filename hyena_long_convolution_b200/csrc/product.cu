@@ -98,6 +98,17 @@ int product_sms()
     return sms;
 }
 
+int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    HYENA_TRY(cudaGetDevice(&dev), "current device");
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return 0;
+    HYENA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), "product attribute");
+    if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return 0;
+}
+
 size_t product_workspace(long long M, int, int, bool, bool) { return kProductHeader + (M > kNarrowRows ? part_bytes() : 0); }
 
 size_t ffn_backward_workspace(long long M, int, int F)

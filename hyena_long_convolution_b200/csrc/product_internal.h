@@ -3,6 +3,8 @@
 // the public interface).
 #pragma once
 
+#include <atomic>
+
 #include "layer_internal.h"
 
 namespace hyena {
@@ -81,6 +83,9 @@ int product_sms();
 
 size_t product_workspace(long long M, int N, int K, bool fp8, bool gated);
 size_t ffn_backward_workspace(long long M, int D, int F);
+
+// Lets a kernel have `bytes` of shared memory, once a device (`done`: a bit each).
+int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> &done);
 
 // Launches a kernel that waits for the stream itself (wait_for_stream), so that its
 // launch and its setup overlap the end of the kernel before it: 1.5 to 3 us a call.

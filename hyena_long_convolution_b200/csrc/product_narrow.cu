@@ -54,6 +54,24 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
     return v;
 }
 
+// The sums of a thread's share of the tokens, of all CTAs of the cluster in the order
+// of k, from [weight][token][row] in each one's shared memory.
+template <int kShare, int kG, int kH>
+__device__ __forceinline__ void join_shares(float (&v)[kG * kH], uint32_t at)
+{
+    constexpr int kCount = kH / kShare;
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) {
+            float sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < kShare; ++r)
+                sum += ld_cluster(cluster_addr_of(at, r) + (g * 2 * kH + j) * kTile * 4);
+            v[g * kH + j] = sum;
+        }
+}
+
 template <int kNT, bool kF8, bool kGated>
 __global__ void __launch_bounds__(kThreadsProduct, 1)
     product_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m1,
@@ -258,17 +276,12 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 const int t0 = (2 * rank + hh) * count;
                 m = static_cast<long long>(tm) * kNT + t0;
                 const uint32_t at = smem_u32(red + t0 * kTile + row);
-#pragma unroll
-                for (int i = 0; i < kG * kH; ++i) v[i] = 0.f;
-#pragma unroll 1
-                for (int r = 0; r < share; ++r) {  // in the order of k
-                    const uint32_t from = cluster_addr_of(at, r);
-#pragma unroll
-                    for (int g = 0; g < kG; ++g)
-#pragma unroll
-                        for (int j = 0; j < kH / 2; ++j)
-                            if (j < count) v[g * kH + j] += ld_cluster(from + (g * kNT + j) * kTile * 4);
-                }
+                if (share == 2)
+                    join_shares<2, kG, kH>(v, at);
+                else if (share == 4)
+                    join_shares<4, kG, kH>(v, at);
+                else
+                    join_shares<8, kG, kH>(v, at);
             }
             const int n = tn * kTile + row;
             const int tokens = static_cast<int>(A.a.M - m < count ? A.a.M - m : count);  // may be negative
@@ -338,8 +351,8 @@ int start(const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, co
 {
     const auto kernel = product_narrow_kernel<kNT, kF8, kGated>;
     constexpr int kSmem = Narrow<kNT, kGated>::kSmem;
-    HYENA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-              "product (narrow) attribute");
+    static std::atomic<unsigned long long> done{0};
+    if (allow_shared(reinterpret_cast<const void *>(kernel), kSmem, done) < 0) return -1;
     return launch_early(kernel, dim3(units * w.share), kThreadsProduct, kSmem, w.share, st, "product (narrow) launch", x,
                         w1, w2, w);
 }

@@ -345,14 +345,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 
 namespace {
 
-int pairs()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return -1;
-    return sms / 2;
-}
+int pairs() { return product_sms() / 2; }
 
 // Units to a tile, where that takes kJoin k-blocks off a unit's run, which is about
 // what the joining costs.
@@ -384,9 +377,10 @@ bool encode_output(CUtensorMap *m, const void *p, bool f32, long long rows, int 
 template <int kMode, bool kF8>
 int start(const Maps &m, const WideArgs &w, cudaStream_t st)
 {
-    HYENA_TRY(cudaFuncSetAttribute(product_wide_kernel<kMode, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
-              "product (wide) attribute");
-    return launch_early(product_wide_kernel<kMode, kF8>, dim3(2 * w.plan.units), kThreadsProduct, kSmem, 2, st,
+    static std::atomic<unsigned long long> done{0};
+    const auto kernel = product_wide_kernel<kMode, kF8>;
+    if (allow_shared(reinterpret_cast<const void *>(kernel), kSmem, done) < 0) return -1;
+    return launch_early(kernel, dim3(2 * w.plan.units), kThreadsProduct, kSmem, 2, st,
                         "product (wide) launch", m.a1, m.a2, m.b1, m.b2, m.c1, m.c2, m.c3, w);
 }
 
