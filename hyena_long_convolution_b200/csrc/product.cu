@@ -109,7 +109,23 @@ int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> 
     return 0;
 }
 
-size_t product_workspace(long long M, int, int, bool, bool) { return kProductHeader + (M > kNarrowRows ? part_bytes() : 0); }
+// Up to 64 rows the narrow kernel reads the weights at the rate of HBM, where the wide
+// one has most of its 256 rows empty (4096 -> 4096 x 11008 in e4m3, 16 rows: 13 and 26
+// us).  Beyond, its smaller tiles pay while they leave SMs to share a tile's k (1024 x
+// 4096, 256 rows in e4m3: 12 and 18 us; 4096 x 4096: 17 and 20; 74 tiles and more: 21
+// and 20); of two weights in bf16 half as many (4096 x 2048, 256 rows: 64 tiles 18 and
+// 16 us), but where the wide kernel's tiles of 256 rows would begin a second wave for
+// 128 rows (11008 x 4096: 43 and 51 us).
+bool product_is_narrow(long long M, int N, bool fp8, bool gated)
+{
+    if (M <= 64) return true;
+    const int nt = narrow_tokens(M, fp8 && gated), sms = product_sms();
+    const long long tiles = (M + nt - 1) / nt * ((N + 127) / 128);
+    if (!gated || fp8) return tiles <= sms / 2;
+    return tiles <= sms / 4 || (M <= 128 && tiles > sms / 2 && tiles <= sms);
+}
+
+size_t product_workspace(long long M, int, int, bool, bool) { return kProductHeader + (M > 64 ? part_bytes() : 0); }
 
 size_t ffn_backward_workspace(long long M, int, int F)
 {
@@ -118,7 +134,7 @@ size_t ffn_backward_workspace(long long M, int, int F)
 
 int launch_product(const ProductArgs &a, cudaStream_t st)
 {
-    return a.M <= kNarrowRows ? launch_product_narrow(a, st) : launch_product_wide(a, st);
+    return product_is_narrow(a.M, a.N, a.fp8, a.gated) ? launch_product_narrow(a, st) : launch_product_wide(a, st);
 }
 
 int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st)

@@ -66,10 +66,14 @@ struct FfnBackArgs {
 
 int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st);
 
-// Up to kNarrowRows rows the weights are the operand with 128 rows and the tokens
-// the other, in the smallest of 16, 32, 64 or 128 that holds them.
-constexpr int kNarrowRows = 128;
-inline int narrow_tokens(long long M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+// The narrow kernel's tokens: the smallest of 16, 32, 64 or (not with two weights in
+// codes, whose sums would fill the registers) 128 that holds the rows, or several of
+// the largest.
+inline int narrow_tokens(long long M, bool fp8_gated)
+{
+    return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 || fp8_gated ? 64 : 128));
+}
+bool product_is_narrow(long long M, int N, bool fp8, bool gated);
 
 int launch_product_narrow(const ProductArgs &a, cudaStream_t st);
 int launch_product_wide(const ProductArgs &a, cudaStream_t st);

@@ -3,11 +3,13 @@
 //
 // The weights are the operand with 128 rows and the tokens the one with kNT <= 128:
 // a CTA's tile is 128 weight rows (128 of the gate's and the same of the up
-// projection's) times kNT tokens, read through a ring of TMA stages as deep as
-// shared memory allows.  With few tokens reading the weights is all the time there
-// is to spend, and some 80 CTAs with 200 KB under way each are enough to do it at
-// the rate of HBM.  With fewer tiles than that a cluster of CTAs shares a tile's k
-// and joins its sums through their shared memory, in the order of k.
+// projection's) times all tokens, read through a ring of TMA stages as deep as shared
+// memory allows.  With few tokens reading the weights is all the time there is to
+// spend, and some 80 CTAs with 200 KB under way each are enough to do it at the rate
+// of HBM.  With fewer tiles than that a cluster of CTAs shares a tile's k and joins its
+// sums through their shared memory, in the order of k.  The sums leave through shared
+// memory in any case: a warp then has a token's 128 values, four a lane, for wide
+// stores and the maximum that codes need.
 #include "product_kernel.cuh"
 
 namespace hyena {
@@ -33,43 +35,39 @@ struct Narrow {
 };
 
 struct NarrowArgs {
-    int tiles_m, tiles, blocks;  // tiles of tokens, of the output; k-blocks
-    int share;                   // CTAs of a cluster, which share a tile's k (then a cluster has one tile)
+    int tiles_m; // tiles of tokens
+    int blocks;  // k-blocks
+    int share;   // CTAs of a cluster, which share a tile's k
     ProductArgs a;
     unsigned int *hdr;
 };
 
-__device__ __forceinline__ void store_one(void *p, bool f32, long long at, float v)
+__device__ __forceinline__ void store_four(void *p, bool f32, long long at, float2 lo, float2 hi)
 {
     if (f32)
-        static_cast<float *>(p)[at] = v;
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(lo.x, lo.y, hi.x, hi.y);
     else
-        static_cast<uint16_t *>(p)[at] = bf16_bits(v);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) =
+            make_uint2(float2_to_bf16x2(lo), float2_to_bf16x2(hi));
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr)
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
     return v;
 }
 
-// The sums of a thread's share of the tokens, of all CTAs of the cluster in the order
-// of k, from [weight][token][row] in each one's shared memory.
-template <int kShare, int kG, int kH>
-__device__ __forceinline__ void join_shares(float (&v)[kG * kH], uint32_t at)
+__device__ __forceinline__ float2 activate(float2 g, int act)
 {
-    constexpr int kCount = kH / kShare;
-#pragma unroll
-    for (int g = 0; g < kG; ++g)
-#pragma unroll
-        for (int j = 0; j < kCount; ++j) {
-            float sum = 0.f;
-#pragma unroll
-            for (int r = 0; r < kShare; ++r)
-                sum += ld_cluster(cluster_addr_of(at, r) + (g * 2 * kH + j) * kTile * 4);
-            v[g * kH + j] = sum;
-        }
+    switch (act) {
+        case HYENA_ACT_SILU: return activation2<HYENA_ACT_SILU>(g);
+        case HYENA_ACT_GELU: return activation2<HYENA_ACT_GELU>(g);
+        case HYENA_ACT_GELU_TANH: return activation2<HYENA_ACT_GELU_TANH>(g);
+        default: return g;
+    }
 }
 
 template <int kNT, bool kF8, bool kGated>
@@ -83,11 +81,10 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     extern __shared__ unsigned char raw[];
     __shared__ ProductShared<kStages> sh;
     __shared__ __align__(16) float token_scale[kEpiWarps][2][kH];
-    __shared__ unsigned int token_max[kEpiWarps][kH];
     unsigned char *stages = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int share = A.share, rank = share > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int unit = blockIdx.x / share, units = gridDim.x / share;
+    const int tn = blockIdx.x / share / A.tiles_m, m0 = (blockIdx.x / share - tn * A.tiles_m) * kNT;
     const int k0 = A.blocks * rank / share, k1 = A.blocks * (rank + 1) / share;
     volatile unsigned int *dead = &sh.dead;
 
@@ -122,18 +119,15 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         bool ok = true;
         if (warp == kEpiWarps) {  // ----------------------------------- TMA
             uint32_t ph = 1;
-            for (int tile = unit; ok && tile < A.tiles; tile += units) {
-                const int tn = tile / A.tiles_m, tm = tile - tn * A.tiles_m;
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
-                    unsigned char *p = stages + s * kStage;
-                    const uint32_t bar = smem_u32(sh.full + s);
-                    expect_tx(on, sh.full + s, kStage);
-                    load_box<1>(on, p, &m1, bar, kb * kBlock, tn * kTile);
-                    if (kGated) load_box<1>(on, p + kOperand, &m2, bar, kb * kBlock, tn * kTile);
-                    load_box<1>(on, p + kG * kOperand, &mx, bar, kb * kBlock, tm * kNT);
-                    if (++s == kStages) s = 0, ph ^= 1;
-                }
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
+                unsigned char *p = stages + s * kStage;
+                const uint32_t bar = smem_u32(sh.full + s);
+                expect_tx(on, sh.full + s, kStage);
+                load_box<1>(on, p, &m1, bar, kb * kBlock, tn * kTile);
+                if (kGated) load_box<1>(on, p + kOperand, &m2, bar, kb * kBlock, tn * kTile);
+                load_box<1>(on, p + kG * kOperand, &mx, bar, kb * kBlock, m0);
+                if (++s == kStages) s = 0, ph ^= 1;
             }
             if (!ok) let_land();
         } else if (warp == kEpiWarps + 1) {  // ----------------------- MMA
@@ -142,30 +136,28 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             int buf = 0;
             uint32_t ph = 0, tph = 1;
             bool stage_full = false, part_free = false;  // seen while the MMAs before were issued
-            for (int tile = unit; ok && tile < A.tiles; tile += units) {
-                for (int kb = k0; kb < k1; ++kb) {
-                    const bool fresh = kF8 || kb == k0, last = kF8 || kb + 1 == k1;
-                    if (!stage_full && !(ok = warp_wait(sh.full + s, ph, dead))) break;
-                    if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
-                    tc_fence_after();
-                    const uint64_t dw = operand_desc(base + s * kStage, 16);
-                    const uint64_t dx = operand_desc(base + s * kStage + kG * kOperand, 16);
-                    const uint32_t d = tmem + buf * (kG * kNT);
-                    uint64_t *const empty = sh.empty + s, *const tfull = sh.tfull + buf;
-                    if (++s == kStages) s = 0, ph ^= 1;
-                    if (last && ++buf == kBufs) buf = 0, tph ^= 1;
-                    const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
+            for (int kb = k0; kb < k1; ++kb) {
+                const bool fresh = kF8 || kb == k0, last = kF8 || kb + 1 == k1;
+                if (!stage_full && !(ok = warp_wait(sh.full + s, ph, dead))) break;
+                if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
+                tc_fence_after();
+                const uint64_t dw = operand_desc(base + s * kStage, 16);
+                const uint64_t dx = operand_desc(base + s * kStage + kG * kOperand, 16);
+                const uint32_t d = tmem + buf * (kG * kNT);
+                uint64_t *const empty = sh.empty + s, *const tfull = sh.tfull + buf;
+                if (++s == kStages) s = 0, ph ^= 1;
+                if (last && ++buf == kBufs) buf = 0, tph ^= 1;
+                const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int g = 0; g < kG; ++g)
-                            mma<1, kF8>(on, d + g * kNT, dw + (g * kOperand + i * 32) / 16, dx + i * 2, idesc,
-                                        fresh && i == 0 ? 0u : 1u);
-                    mma_commit_to<1>(on, empty);
-                    if (last) mma_commit_to<1>(on, tfull);
-                    stage_full = __all_sync(0xffffffffu, f);
-                    part_free = __all_sync(0xffffffffu, e);
-                }
+                    for (int g = 0; g < kG; ++g)
+                        mma<1, kF8>(on, d + g * kNT, dw + (g * kOperand + i * 32) / 16, dx + i * 2, idesc,
+                                    fresh && i == 0 ? 0u : 1u);
+                mma_commit_to<1>(on, empty);
+                if (last) mma_commit_to<1>(on, tfull);
+                stage_full = __all_sync(0xffffffffu, f);
+                part_free = __all_sync(0xffffffffu, e);
             }
             if (!ok) let_land();
         }
@@ -182,160 +174,142 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         int buf = 0;
         uint32_t tph = 0;
         bool ok = true;
-        for (int tile = unit; tile < A.tiles; tile += units) {
-            const int tn = tile / A.tiles_m, tm = tile - tn * A.tiles_m;
-            long long m = static_cast<long long>(tm) * kNT + hh * kH;  // this thread's first token
-            float v[kG * kH];
-            auto done_reading = [&] {
-                tc_fence_before();
+        const int m = m0 + hh * kH;  // this thread's first token
+        float v[kG * kH];
+        auto done_reading = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.tempty + buf);
+            if (++buf == kBufs) buf = 0, tph ^= 1;
+        };
+        if constexpr (kF8) {
+#pragma unroll
+            for (int i = 0; i < kG * kH; ++i) v[i] = 0.f;
+            const float *s1 = A.a.sw1 + static_cast<long long>(tn) * groups;
+            const float *s2 = kGated ? A.a.sw2 + static_cast<long long>(tn) * groups : s1;
+            // the scales of the warp's tokens, a token a lane, one k-block ahead
+            const float *sx0 = m + lane < A.a.M && lane < kH ? A.a.sx + (m + lane) * static_cast<long long>(A.a.sx_row) : nullptr;
+            const float *sx1 = kH > 32 && m + 32 + lane < A.a.M
+                                   ? A.a.sx + (m + 32 + lane) * static_cast<long long>(A.a.sx_row)
+                                   : nullptr;
+            const auto scale_at = [&](const float *p, int kb) {
+                return p ? load_here(p + static_cast<long long>(kb) * A.a.sx_step) : 0.f;
+            };
+            float x0 = scale_at(sx0, k0), x1 = scale_at(sx1, k0);
+            float f1 = load_here(s1 + k0), f2 = load_here(s2 + k0);
+            for (int kb = k0; kb < k1; ++kb) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sh.tempty + buf);
-                if (++buf == kBufs) buf = 0, tph ^= 1;
-            };
-            if constexpr (kF8) {
+                // a token's scale times each weight's
 #pragma unroll
-                for (int i = 0; i < kG * kH; ++i) v[i] = 0.f;
-                const float *s1 = A.a.sw1 + static_cast<long long>(tn) * groups;
-                const float *s2 = kGated ? A.a.sw2 + static_cast<long long>(tn) * groups : s1;
-                // the scales of the warp's tokens, a token a lane, one k-block ahead
-                const float *sx0 = m + lane < A.a.M && lane < kH ? A.a.sx + (m + lane) * A.a.sx_row : nullptr;
-                const float *sx1 = kH > 32 && m + 32 + lane < A.a.M ? A.a.sx + (m + 32 + lane) * A.a.sx_row : nullptr;
-                const auto scale_at = [&](const float *p, int kb) {
-                    return p ? load_here(p + static_cast<long long>(kb) * A.a.sx_step) : 0.f;
-                };
-                float x0 = scale_at(sx0, k0), x1 = scale_at(sx1, k0);
-                float f1 = load_here(s1 + k0), f2 = load_here(s2 + k0);
-                for (int kb = k0; kb < k1; ++kb) {
-                    __syncwarp();
-                    // a token's scale times each weight's
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) {
-                        if (lane < kH) token_scale[warp][g][lane] = x0 * (g ? f2 : f1);
-                        if constexpr (kH > 32) token_scale[warp][g][lane + 32] = x1 * (g ? f2 : f1);
-                    }
-                    if (kb + 1 < k1) {
-                        x0 = scale_at(sx0, kb + 1);
-                        x1 = scale_at(sx1, kb + 1);
-                        f1 = load_here(s1 + kb + 1);
-                        f2 = load_here(s2 + kb + 1);
-                    }
-                    ok = ok && warp_wait(sh.tfull + buf, tph, dead);
-                    if (!ok) break;
-                    tc_fence_after();
-                    __syncwarp();
-                    const uint32_t at = lanes + buf * (kG * kNT);
-                    constexpr int kChunks = kH / kC;
-                    float d[2][kC];
-                    tmem_ld(d[0], at);
-#pragma unroll
-                    for (int i = 0; i < kG * kChunks; ++i) {
-                        const int g = i / kChunks, first = i % kChunks * kC;
-                        tmem_wait(d[i & 1]);
-                        if (i + 1 < kG * kChunks)
-                            tmem_ld(d[(i + 1) & 1], at + (i + 1) / kChunks * kNT + (i + 1) % kChunks * kC);
-#pragma unroll
-                        for (int j = 0; j < kC; j += 4) {
-                            const float4 c = *reinterpret_cast<const float4 *>(&token_scale[warp][g][first + j]);
-                            float *t = v + g * kH + first + j;
-                            const float2 lo = __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]), make_float2(c.x, c.y),
-                                                         make_float2(t[0], t[1]));
-                            const float2 hi = __ffma2_rn(make_float2(d[i & 1][j + 2], d[i & 1][j + 3]),
-                                                         make_float2(c.z, c.w), make_float2(t[2], t[3]));
-                            t[0] = lo.x, t[1] = lo.y, t[2] = hi.x, t[3] = hi.y;
-                        }
-                    }
-                    done_reading();
+                for (int g = 0; g < kG; ++g) {
+                    if (lane < kH) token_scale[warp][g][lane] = x0 * (g ? f2 : f1);
+                    if constexpr (kH > 32) token_scale[warp][g][lane + 32] = x1 * (g ? f2 : f1);
                 }
-            } else {
+                if (kb + 1 < k1) {
+                    x0 = scale_at(sx0, kb + 1);
+                    x1 = scale_at(sx1, kb + 1);
+                    f1 = load_here(s1 + kb + 1);
+                    f2 = load_here(s2 + kb + 1);
+                }
                 ok = ok && warp_wait(sh.tfull + buf, tph, dead);
-                if (ok) {
-                    tc_fence_after();
+                if (!ok) break;
+                tc_fence_after();
+                __syncwarp();
+                const uint32_t at = lanes + buf * (kG * kNT);
+                constexpr int kChunks = kH / kC;
+                float d[2][kC];
+                tmem_ld(d[0], at);
 #pragma unroll
-                    for (int i = 0; i < kG * kH / kC; ++i) {
-                        float d[kC];
-                        tmem_ld(d, lanes + (buf * kG + i / (kH / kC)) * kNT + i % (kH / kC) * kC);
-                        tmem_wait(d);
+                for (int i = 0; i < kG * kChunks; ++i) {
+                    const int g = i / kChunks, first = i % kChunks * kC;
+                    tmem_wait(d[i & 1]);
+                    if (i + 1 < kG * kChunks)
+                        tmem_ld(d[(i + 1) & 1], at + (i + 1) / kChunks * kNT + (i + 1) % kChunks * kC);
 #pragma unroll
-                        for (int j = 0; j < kC; ++j) v[i * kC + j] = d[j];
+                    for (int j = 0; j < kC; j += 4) {
+                        const float4 c = *reinterpret_cast<const float4 *>(&token_scale[warp][g][first + j]);
+                        float *t = v + g * kH + first + j;
+                        const float2 lo = __ffma2_rn(make_float2(d[i & 1][j], d[i & 1][j + 1]), make_float2(c.x, c.y),
+                                                     make_float2(t[0], t[1]));
+                        const float2 hi = __ffma2_rn(make_float2(d[i & 1][j + 2], d[i & 1][j + 3]),
+                                                     make_float2(c.z, c.w), make_float2(t[2], t[3]));
+                        t[0] = lo.x, t[1] = lo.y, t[2] = hi.x, t[3] = hi.y;
                     }
-                    done_reading();
                 }
+                done_reading();
             }
-            if (!ok) {
+        } else {
+            ok = ok && warp_wait(sh.tfull + buf, tph, dead);
+            if (ok) {
+                tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < kG * kH; ++i) v[i] = __uint_as_float(0x7fffffffu);
+                for (int i = 0; i < kG * kH / kC; ++i) {
+                    float d[kC];
+                    tmem_ld(d, lanes + (buf * kG + i / (kH / kC)) * kNT + i % (kH / kC) * kC);
+                    tmem_wait(d);
+#pragma unroll
+                    for (int j = 0; j < kC; ++j) v[i * kC + j] = d[j];
+                }
+                done_reading();
             }
-            int count = kH;  // tokens of this thread
-            if (share > 1) {
-                // sums as [weight][token][row]; CTA r then has the r-th share of the tokens
-                float *red = reinterpret_cast<float *>(stages);
+        }
+        if (!ok) {
 #pragma unroll
-                for (int i = 0; i < kG * kH; ++i) red[(i / kH * kNT + hh * kH + i % kH) * kTile + row] = v[i];
-                cluster_sync();
-                count = kH / share;
-                const int t0 = (2 * rank + hh) * count;
-                m = static_cast<long long>(tm) * kNT + t0;
-                const uint32_t at = smem_u32(red + t0 * kTile + row);
-                if (share == 2)
-                    join_shares<2, kG, kH>(v, at);
-                else if (share == 4)
-                    join_shares<4, kG, kH>(v, at);
-                else
-                    join_shares<8, kG, kH>(v, at);
+            for (int i = 0; i < kG * kH; ++i) v[i] = __uint_as_float(0x7fffffffu);
+        }
+        // the sums as [weight][token][row], in place of the stages
+        float *red = reinterpret_cast<float *>(stages);
+#pragma unroll
+        for (int i = 0; i < kG * kH; ++i) red[(i / kH * kNT + hh * kH + i % kH) * kTile + row] = v[i];
+        if (share > 1)
+            cluster_sync();
+        else
+            named_sync(1, kEpiThreads);
+        // this CTA's share of the tokens, a warp each in turn, four rows of the weights a lane
+        const int n = tn * kTile + 4 * lane;
+        const bool inside = n < A.a.N;
+        const int first = rank * (kNT / share);
+        const int tokens = static_cast<int>(A.a.M - m0 < kNT ? A.a.M - m0 : kNT);
+        const int end = min(tokens, first + kNT / share);
+#pragma unroll 1
+        for (int t = first + warp; t < end; t += kEpiWarps) {
+            float2 lo[kG], hi[kG];
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                const uint32_t at = smem_u32(red + (g * kNT + t) * kTile + 4 * lane);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {  // in the order of k
+                    if (r >= share) break;
+                    const float4 f = share > 1 ? ld_cluster(cluster_addr_of(at, r)) : ld_cluster(at);
+                    sum = make_float4(sum.x + f.x, sum.y + f.y, sum.z + f.z, sum.w + f.w);
+                }
+                lo[g] = make_float2(sum.x, sum.y);
+                hi[g] = make_float2(sum.z, sum.w);
             }
-            const int n = tn * kTile + row;
-            const int tokens = static_cast<int>(A.a.M - m < count ? A.a.M - m : count);  // may be negative
-            const bool inside = n < A.a.N;
-            // f(j, values of token j) for each token inside
-            auto each = [&](auto f) {
-                in_turns<kH, 8>([&](int j) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (j + i < tokens) f(j + i, v[i], v[kGated ? kH + i : i]);
-                    if (kH > 8) turn<kH, 8>(v);
-                    if (kH > 8 && kGated) turn<kH, 8>(v + kH);
-                });
-            };
-            if constexpr (!kGated) {
-                each([&](int j, float y, float) {
-                    if (inside) store_one(A.a.y, A.a.y_f32, (m + j) * A.a.ld_y + n, y);
-                });
-            } else {
-                if (A.a.g && inside)
-                    each([&](int j, float g, float u) {
-                        store_one(A.a.g, A.a.g_f32, (m + j) * A.a.ld_g + n, g);
-                        store_one(A.a.u, A.a.g_f32, (m + j) * A.a.ld_g + n, u);
-                    });
-                gate<kH>(v, A.a.act, tokens);
+            const long long row_y = (m0 + static_cast<long long>(t)) * A.a.ld_y + n;
+            if constexpr (kGated) {
+                if (A.a.g && inside) {
+                    const long long row_g = (m0 + static_cast<long long>(t)) * A.a.ld_g + n;
+                    store_four(A.a.g, A.a.g_f32, row_g, lo[0], hi[0]);
+                    store_four(A.a.u, A.a.g_f32, row_g, lo[1], hi[1]);
+                }
+                lo[0] = __fmul2_rn(activate(lo[0], A.a.act), lo[1]);
+                hi[0] = __fmul2_rn(activate(hi[0], A.a.act), hi[1]);
                 if (kF8 && A.a.q) {
-                    // the largest of each token's 128 values: four warps' lanes
-                    each([&](int j, float y, float) {
-                        const unsigned int b = inside ? __float_as_uint(y) & 0x7fffffffu : 0u;
-                        const unsigned int mx = __reduce_max_sync(0xffffffffu, b);
-                        if (lane == 0) token_max[warp][j] = mx;
-                    });
-                    named_sync(2 + hh, kEpiThreads / 2);
-                    if (row < tokens) {  // a thread a token
-                        unsigned int mx = token_max[4 * hh][row];
-#pragma unroll
-                        for (int i = 1; i < 4; ++i) mx = max(mx, token_max[4 * hh + i][row]);
-                        const float scale = scale_of(mx);
-                        A.a.scales[(m + row) * (A.tiles / A.tiles_m) + tn] = scale;
-                        token_scale[4 * hh][0][row] = scale;
-                        token_scale[4 * hh][1][row] = 1.f / scale;
-                    }
-                    named_sync(2 + hh, kEpiThreads / 2);
-                    each([&](int j, float y, float) {
-                        const uint8_t code = e4m3_code(y, token_scale[4 * hh][0][j], token_scale[4 * hh][1][j]);
-                        if (inside) A.a.q[(m + j) * A.a.ld_q + n] = code;
-                    });
-                    named_sync(2 + hh, kEpiThreads / 2);
-                } else {
-                    each([&](int j, float y, float) {
-                        if (inside) static_cast<uint16_t *>(A.a.y)[(m + j) * A.a.ld_y + n] = bf16_bits(y);
-                    });
+                    constexpr unsigned int kMag = 0x7fffffffu;
+                    unsigned int mx = max(max(__float_as_uint(lo[0].x) & kMag, __float_as_uint(lo[0].y) & kMag),
+                                          max(__float_as_uint(hi[0].x) & kMag, __float_as_uint(hi[0].y) & kMag));
+                    const float scale = scale_of(__reduce_max_sync(0xffffffffu, inside ? mx : 0u)), inv = 1.f / scale;
+                    const uint32_t code = e4m3_code(lo[0].x, scale, inv) | e4m3_code(lo[0].y, scale, inv) << 8 |
+                                          e4m3_code(hi[0].x, scale, inv) << 16 |
+                                          static_cast<uint32_t>(e4m3_code(hi[0].y, scale, inv)) << 24;
+                    if (inside) *reinterpret_cast<uint32_t *>(A.a.q + (m0 + static_cast<long long>(t)) * A.a.ld_q + n) = code;
+                    if (lane == 0) A.a.scales[(m0 + static_cast<long long>(t)) * ((A.a.N + kTile - 1) / kTile) + tn] = scale;
+                    continue;
                 }
             }
+            if (inside) store_four(A.a.y, A.a.y_f32, row_y, lo[0], hi[0]);
         }
         if (share > 1) cluster_sync();  // the others have read this CTA's sums
     }
@@ -346,26 +320,30 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 }
 
 template <int kNT, bool kF8, bool kGated>
-int start(const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, const NarrowArgs &w, int units,
+int start(const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, const NarrowArgs &w, int tiles,
           cudaStream_t st)
 {
     const auto kernel = product_narrow_kernel<kNT, kF8, kGated>;
     constexpr int kSmem = Narrow<kNT, kGated>::kSmem;
     static std::atomic<unsigned long long> done{0};
     if (allow_shared(reinterpret_cast<const void *>(kernel), kSmem, done) < 0) return -1;
-    return launch_early(kernel, dim3(units * w.share), kThreadsProduct, kSmem, w.share, st, "product (narrow) launch", x,
+    return launch_early(kernel, dim3(tiles * w.share), kThreadsProduct, kSmem, w.share, st, "product (narrow) launch", x,
                         w1, w2, w);
 }
 
 template <bool kF8, bool kGated>
 int start_by_tokens(int nt, const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, const NarrowArgs &w,
-                    int units, cudaStream_t st)
+                    int tiles, cudaStream_t st)
 {
     switch (nt) {
-        case 16: return start<16, kF8, kGated>(x, w1, w2, w, units, st);
-        case 32: return start<32, kF8, kGated>(x, w1, w2, w, units, st);
-        case 64: return start<64, kF8, kGated>(x, w1, w2, w, units, st);
-        default: return start<128, kF8, kGated>(x, w1, w2, w, units, st);
+        case 16: return start<16, kF8, kGated>(x, w1, w2, w, tiles, st);
+        case 32: return start<32, kF8, kGated>(x, w1, w2, w, tiles, st);
+        case 64: return start<64, kF8, kGated>(x, w1, w2, w, tiles, st);
+        default:
+            if constexpr (kF8 && kGated)
+                return -1;  // not asked for
+            else
+                return start<128, kF8, kGated>(x, w1, w2, w, tiles, st);
     }
 }
 
@@ -375,29 +353,30 @@ int launch_product_narrow(const ProductArgs &a, cudaStream_t st)
 {
     const int sms = product_sms();
     if (sms < 1) return -1;
-    const int nt = narrow_tokens(a.M);
-    const int kb = a.fp8 ? 128 : 64;
+    const int nt = narrow_tokens(a.M, a.fp8 && a.gated);
+    const int kb = a.fp8 ? 128 : 64, size = a.fp8 ? 1 : 2;
     CUtensorMap x, w1, w2;
-    if (!encode_matrix(&x, a.x, a.fp8 ? 1 : 2, a.M, a.K, a.ld_x, nt) ||
-        !encode_matrix(&w1, a.w1, a.fp8 ? 1 : 2, a.N, a.K, a.ld_w, kTile))
+    if (!encode_matrix(&x, a.x, size, a.M, a.K, a.ld_x, nt) || !encode_matrix(&w1, a.w1, size, a.N, a.K, a.ld_w, kTile))
         return -1;
     if (!a.gated)
         w2 = w1;
-    else if (!encode_matrix(&w2, a.w2, a.fp8 ? 1 : 2, a.N, a.K, a.ld_w, kTile))
+    else if (!encode_matrix(&w2, a.w2, size, a.N, a.K, a.ld_w, kTile))
         return -1;
     NarrowArgs w{};
     w.tiles_m = static_cast<int>((a.M + nt - 1) / nt);
-    w.tiles = w.tiles_m * ((a.N + kTile - 1) / kTile);
+    const int tiles = w.tiles_m * ((a.N + kTile - 1) / kTile);
     w.blocks = (a.K + kb - 1) / kb;
-    // clusters of up to 8 while they all fit and each CTA keeps 4 k-blocks
+    // clusters of up to 8 while all fit at once (a GPU of 148 SMs holds 74 of two CTAs of
+    // this size, 33 of four, 15 of eight) and each CTA keeps 4 k-blocks
     w.share = 1;
-    while (w.share < 8 && 2 * w.share * w.tiles <= sms - 2 * w.share && w.blocks >= 8 * w.share) w.share *= 2;
+    if (tiles <= sms / 2 && w.blocks >= 8) w.share = 2;
+    if (tiles <= (sms - 16) / 4 && w.blocks >= 16) w.share = 4;
+    if (tiles <= (sms - 28) / 8 && w.blocks >= 32) w.share = 8;
     w.a = a;
     w.hdr = static_cast<unsigned int *>(a.workspace);
-    const int units = w.tiles < sms ? w.tiles : sms;  // share > 1: a tile each
-    if (!a.gated) return start_by_tokens<true, false>(nt, x, w1, w2, w, units, st);
-    return a.fp8 ? start_by_tokens<true, true>(nt, x, w1, w2, w, units, st)
-                 : start_by_tokens<false, true>(nt, x, w1, w2, w, units, st);
+    if (!a.gated) return start_by_tokens<true, false>(nt, x, w1, w2, w, tiles, st);
+    return a.fp8 ? start_by_tokens<true, true>(nt, x, w1, w2, w, tiles, st)
+                 : start_by_tokens<false, true>(nt, x, w1, w2, w, tiles, st);
 }
 
 }  // namespace hyena
