@@ -63,12 +63,12 @@ __device__ __forceinline__ float load_here(const float *p)
 
 // ---------------------------------------------------------------- launches
 
-// The kernels here are launched before the one ahead of them in the stream has ended
-// (launch_early): what comes before this reads and writes no global memory.
-__device__ __forceinline__ void wait_for_stream()
-{
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-}
+// The kernels here are launched while the one ahead of them in the stream ends
+// (launch_early): what comes before this reads and writes no global memory.  They do
+// not let the next one start early (griddepcontrol.launch_dependents), since one that
+// reads its inputs before it waits, as the modal scan's short passes do, would read
+// outputs that are not written yet.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- clusters
 

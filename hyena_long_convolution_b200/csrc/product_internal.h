@@ -92,7 +92,7 @@ size_t ffn_backward_workspace(long long M, int D, int F);
 int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> &done);
 
 // Launches a kernel that waits for the stream itself (wait_for_stream), so that its
-// launch and its setup overlap the end of the kernel before it: 1.5 to 3 us a call.
+// launch and its setup overlap the end of the kernel before it.
 template <class... P, class... Q>
 int launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
                  const char *what, const Q &...args)

@@ -176,6 +176,31 @@ def test_calls_in_a_row_see_each_other():
         assert not hy.fp8_matmul(q, s, wq, sw).any()
 
 
+@pytest.mark.parametrize("M", [128, 1024])
+def test_before_a_kernel_that_reads_early(M):
+    """The prepared modal convolution asks for its input rows before it waits for the kernel ahead of it."""
+    import torch
+    import hyena_long_convolution_b200 as hy
+    D, N = 512, 8
+    g = torch.Generator().manual_seed(0)
+    poles = (-torch.exp(torch.rand(D, N, generator=g) * 6.9 - 6.9)).cuda()
+    res = (torch.randn(D, N, generator=g) / N).cuda()
+    ws = hy.ModalWorkspace(1, D, N)
+    hy.modal_prepare(poles, res, None, ws)
+    w, sw = hy.fp8_quantize(normal(3 * D, 4096, seed=1, scale=1 / 64), block=128)
+    wide = hy.MatmulWorkspace(M, 3 * D, 4096)
+    z = torch.empty(1, M, 3 * D, dtype=torch.bfloat16, device="cuda")
+    xs = [z[..., i * D:(i + 1) * D] for i in range(3)]
+    for seed in range(10):
+        q, s = hy.fp8_quantize(normal(1, M, 4096, seed=seed))
+        z.fill_(float("nan"))
+        torch.cuda.synchronize()
+        hy.fp8_matmul(q, s, w, sw, y=z, workspace=wide)
+        y = hy.modal_long_conv_prepared(*xs, N, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, hy.modal_long_conv_prepared(*xs, N, ws)), seed
+
+
 def test_other_streams():
     import torch
     main = [call(None) for call in cases()]
