@@ -17,6 +17,11 @@ channels as [x1 | x2 | x3] (group = 1: per-channel triples x1_c x2_c x3_c).
 The ``*_complex`` variants take complex modes (poles and residues as [D, N, 2]
 fp32 pairs; h_c[t] = Re sum_n R p^t), and the ``*_decode`` functions advance
 the modal state or the FIR window by one generated token.
+
+Around the mixers: ``gated_recurrence`` (a modal filter of one mode whose pole
+depends on the token), ``rms_norm`` and ``rms_norm_fp8``, the 8-bit projections
+``fp8_quantize`` and ``fp8_matmul``, and the gated feed-forward block
+``gated_ffn`` (with ``gated_ffn_backward``) and ``gated_ffn_fp8``.
 """
 from __future__ import annotations
 
@@ -1171,8 +1176,8 @@ def _kept(gate, up, M, F):
 
 
 class MatmulWorkspace:
-    """Device workspace of fp8_matmul for M rows, N outputs and K channels,
-    zero-filled once at creation."""
+    """Device workspace of fp8_matmul for up to M rows, N outputs and K channels,
+    zero-filled once at creation; for calls in order on one stream."""
 
     def __init__(self, M: int, N: int, K: int, device=None, stream=None):
         n = int(lib().hyena_fp8_matmul_workspace_size(M, N, K))
@@ -1183,8 +1188,9 @@ class MatmulWorkspace:
 
 
 class FfnWorkspace:
-    """Device workspace of gated_ffn and gated_ffn_fp8 for M rows (with
-    ``backward``, of gated_ffn_backward too), zero-filled once at creation."""
+    """Device workspace of gated_ffn and gated_ffn_fp8 for up to M rows (with
+    ``backward``, of gated_ffn_backward too), zero-filled once at creation; for
+    calls in order on one stream."""
 
     def __init__(self, M: int, D: int, F: int, backward: bool = False, device=None, stream=None):
         n = int(lib().hyena_gated_ffn_workspace_size(M, D, F, 1 if backward else 0))
@@ -1234,8 +1240,8 @@ def fp8_matmul(x, x_scales, weight, weight_scales, y=None, dtype=None, workspace
     ([..., N], bf16 or the given dtype bf16 or fp32, allocated if not given).
     Row strides of x and weight: multiples of 16.
 
-    A device wait that ran out leaves NaN and is reported by workspace_check,
-    after which the workspace has to be made anew."""
+    A device wait that ran out leaves NaN and is reported by workspace_check; a
+    call without a ``workspace`` uses one of its own."""
     if stream is not None:
         with _current(stream):
             return fp8_matmul(x, x_scales, weight, weight_scales, y, dtype, workspace)
@@ -1271,7 +1277,8 @@ def gated_ffn(x, gate_weight, up_weight, activation="silu", y=None, gate_out=Non
     x: [M, D] or [B, L, D] bf16; gate_weight, up_weight: [F, D] bf16 with one
     row stride; activation: silu, gelu, gelu_tanh or identity; gate_out,
     up_out: [M, F] (or [B, L, F]), both bf16 or both fp32, or None: the two
-    products, kept for the gradient.  Returns y ([..., F] bf16, allocated if
+    products, kept for the gradient (in bf16 its error is 3.0e-3 of its norm, in
+    fp32 2.3e-3, of which 1.7e-3 is its own rounding).  Returns y ([..., F] bf16, allocated if
     not given)."""
     if stream is not None:
         with _current(stream):

@@ -4,7 +4,8 @@
 //   (activations) or of 128 rows x 128 channels (weights);  q = x / scale rounded
 //
 // One pass: a group sits in registers between its maximum and its codes, so x is
-// read once.  HBM-bound: 3 bytes a bf16 value.
+// read once.  HBM-bound, 3 bytes a bf16 value: 32768 x 4096 68 us, 6.0 TB/s (92% of the
+// measured copy), 11008 x 4096 by blocks 23.3 us (89%), 32768 x 4096 of fp32 104 us (99%).
 #include "product_device.cuh"
 
 namespace hyena {

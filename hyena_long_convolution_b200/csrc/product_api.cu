@@ -101,7 +101,7 @@ hyena_status_t hyena_fp8_quantize(const void *x, int64_t ld_x, hyena_dtype_t x_t
 
 size_t hyena_fp8_matmul_workspace_size(int64_t M, int N, int K)
 {
-    return check_sizes(M, N, K) == HYENA_OK ? product_workspace(M, N, K, true, false) : 0;
+    return check_sizes(M, N, K) == HYENA_OK ? product_workspace(M) : 0;
 }
 
 hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_scales, int x_group, const uint8_t *w,
@@ -120,7 +120,7 @@ hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_s
     if (st != HYENA_OK) return st;
     set_last_launches(0);
     if (M == 0) return HYENA_OK;
-    st = check_workspace(workspace, workspace_bytes, product_workspace(M, N, K, true, false));
+    st = check_workspace(workspace, workspace_bytes, product_workspace(M));
     if (st != HYENA_OK) return st;
     ProductArgs a{};
     a.x = x;
@@ -145,9 +145,7 @@ hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_s
 size_t hyena_gated_ffn_workspace_size(int64_t M, int D, int F, int backward)
 {
     if (check_sizes(M, D, F) != HYENA_OK) return 0;
-    const size_t f = product_workspace(M, F, D, false, true), q = product_workspace(M, F, D, true, true);
-    const size_t n = f > q ? f : q, b = backward ? ffn_backward_workspace(M, D, F) : 0;
-    return n > b ? n : b;
+    return backward ? ffn_backward_workspace(M, F) : product_workspace(M);
 }
 
 hyena_status_t hyena_gated_ffn(const hyena_bf16_t *x, int64_t ld_x, const hyena_bf16_t *gate_w,
@@ -171,7 +169,7 @@ hyena_status_t hyena_gated_ffn(const hyena_bf16_t *x, int64_t ld_x, const hyena_
     if (st != HYENA_OK) return st;
     set_last_launches(0);
     if (M == 0) return HYENA_OK;
-    st = check_workspace(workspace, workspace_bytes, product_workspace(M, F, D, false, true));
+    st = check_workspace(workspace, workspace_bytes, product_workspace(M));
     if (st != HYENA_OK) return st;
     ProductArgs a{};
     a.x = x;
@@ -216,7 +214,7 @@ hyena_status_t hyena_gated_ffn_fp8(const uint8_t *x, int64_t ld_x, const float *
     if (st != HYENA_OK) return st;
     set_last_launches(0);
     if (M == 0) return HYENA_OK;
-    st = check_workspace(workspace, workspace_bytes, product_workspace(M, F, D, true, true));
+    st = check_workspace(workspace, workspace_bytes, product_workspace(M));
     if (st != HYENA_OK) return st;
     ProductArgs a{};
     a.x = x;
@@ -275,7 +273,7 @@ hyena_status_t hyena_gated_ffn_backward(const hyena_bf16_t *dy, int64_t ld_dy, c
         set_last_launches(2);
         return HYENA_OK;
     }
-    st = check_workspace(workspace, workspace_bytes, ffn_backward_workspace(M, D, F));
+    st = check_workspace(workspace, workspace_bytes, ffn_backward_workspace(M, F));
     if (st != HYENA_OK) return st;
     FfnBackArgs a{};
     a.dy = dy;

@@ -85,8 +85,10 @@ int launch_ffn_dw(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, 
 bool encode_matrix(CUtensorMap *m, const void *p, int size, long long rows, int cols, long long ld, int box_rows);
 int product_sms();
 
-size_t product_workspace(long long M, int N, int K, bool fp8, bool gated);
-size_t ffn_backward_workspace(long long M, int D, int F);
+// Header and, where the wide kernel may share a tile's k, the parts; of the gradient dg
+// and du too.
+size_t product_workspace(long long M);
+size_t ffn_backward_workspace(long long M, int F);
 
 // Lets a kernel have `bytes` of shared memory, once a device (`done`: a bit each).
 int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> &done);

@@ -10,6 +10,15 @@
 // sums through their shared memory, in the order of k.  The sums leave through shared
 // memory in any case: a warp then has a token's 128 values, four a lane, for wide
 // stores and the maximum that codes need.
+//
+// Bound by HBM and by what comes before and after the stream: launch, first data 2.5 us
+// after, sums and outputs 1 to 3.  On the device, weights from HBM: one token through
+// 4096 -> 2 x 11008 in bf16 31-32 us (5.7 TB/s, 87% of the measured copy), through 4096
+// -> 12288 in e4m3 12 us (4.2 TB/s); 16 through 4096 -> 2 x 11008 in e4m3, codes out,
+// 18.7 (4.8 TB/s); 64 through 11008 -> 4096 in e4m3 15.8, by clusters of four.  Parts in
+// global memory, added up by the last CTA to arrive, took 22 and 40 us where clusters
+// take 15 and 17; the outputs straight from the registers, 64 times the same code, 40 us
+// for 128 tokens' codes.
 #include "product_kernel.cuh"
 
 namespace hyena {

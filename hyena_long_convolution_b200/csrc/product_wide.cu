@@ -6,8 +6,27 @@
 //   dx        dg Wg + du Wu: k runs through F twice
 //   dW        dg^T x, du^T x: k runs through the tokens
 //
-// bf16: sums stay in tensor memory over the whole of k.  e4m3 codes: the sums
-// over each 128 k go times their scales into registers.
+// A TMA warp fills a ring of stages (128 rows x 128 bytes of each operand a CTA; where
+// k is not the contiguous axis, boxes of 64 columns x 64 k, which the MMA takes as they
+// are), one warp of the pair issues the MMAs, eight warps a CTA read tensor memory.
+// The pair halves what each SM fetches of the second operand: a k-block is 32 KB for
+// 512 cycles of MMAs.
+//
+// bf16: sums stay in tensor memory over the whole of k, in one of two halves, so that a
+// tile's outputs are worked out while the next one's MMAs run.  Bound by the tensor
+// cores (86% of cycles active in 2048 x 4096 -> 11008) and, in long runs, by power: 8192
+// x 4096 -> 11008 with silu 928-963 us, 1.53-1.59 PFLOP/s, where the measured library
+// product does 1.62.
+//
+// e4m3 codes: the sums over each 128 k go times their scales into registers (128 a
+// thread), since the scales are any fp32 numbers; the two halves of tensor memory then
+// change places every k-block.  8192 x 4096 -> 12288: 389-393 us, 2.1 PFLOP/s, 51% of
+// cycles active.  Of a tile's 31000 cycles 26000 go to 32 k-blocks of 815, which is the
+// way round: 512 of MMAs, then commit, 300 for the eight warps to read the half, their
+// arrival at the other CTA's MMA warp, over two halves; the rest to the outputs, which
+// the MMAs run ahead of by two k-blocks only.  (Each group of 128 columns by MMAs and
+// barriers of its own, four parts of tensor memory: 460 us, since N = 128 takes as long
+// as N = 256.  32 columns a load instead of 16: as fast.  Polling: 686.)
 #include "product_kernel.cuh"
 
 namespace hyena {

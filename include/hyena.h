@@ -688,8 +688,7 @@ hyena_status_t hyena_fp8_quantize(const void *x, int64_t ld_x, hyena_dtype_t x_t
  *           (hyena_modal_workspace_init) and then reused, by calls in order on
  *           one stream (or ordered otherwise); hyena_workspace_check reports a
  *           device wait that ran out, whose call leaves NaN in the results
- *           that it did not reach, and after which the workspace must be
- *           zero-filled again.
+ *           that it did not reach.  One for M rows serves fewer, and any N, K.
  *
  * Products of codes are exact and summed in fp32 over each 128 channels; the
  * sums times their scales are summed in fp32 in the order of k.  Work split
