@@ -44,7 +44,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and not ptxas_verbose and up_to_date():
         return SO
     tmp = SO + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "--threads", "0", "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-cudart", "static", "-I", os.path.join(ROOT, "include"), *sources(), "-o", tmp]
     if ptxas_verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -138,12 +138,34 @@ def test_matmul_sizes(M, Nn, K, per_row):
     check_matmul(M, Nn, K, per_row, torch.bfloat16)
 
 
+# many rows by tiles of 256 x 256, whole or (few tiles, much k) in 2, 3 and 4 parts
+@pytest.mark.parametrize("M,Nn,K", [(640, 2056, 264), (1300, 1160, 136), (257, 9608, 520), (2049, 1032, 1040),
+                                    (300, 3328, 4400), (520, 1928, 4112), (300, 3336, 5200), (130, 4872, 8208)])
+def test_matmul_many_rows(M, Nn, K):
+    import torch
+    check_matmul(M, Nn, K, False, torch.float32, seed=M)
+    check_matmul(M, Nn, K, True, torch.bfloat16, seed=M)
+
+
+@pytest.mark.parametrize("M,D,F,keep", [(300, 2056, 1664, "fp32"), (520, 136, 2696, "bf16"), (260, 4104, 1288, "bf16"),
+                                        (700, 2184, 776, None)])
+def test_ffn_many_rows(M, D, F, keep):
+    import torch
+    check_ffn(M, D, F, "gelu", {"fp32": torch.float32, "bf16": torch.bfloat16, None: None}[keep])
+
+
+@pytest.mark.parametrize("M,D,F", [(300, 4400, 1936), (700, 272, 2064), (520, 5136, 1296), (1030, 528, 1040)])
+def test_ffn_fp8_many_rows(M, D, F):
+    check_ffn_fp8(M, D, F, "gelu_tanh", M % 3 == 1)
+
+
 def test_matmul_is_exact_on_whole_numbers():
     """Products and sums that fp32 holds exactly: every order gives the same."""
     import torch
     import hyena_long_convolution_b200 as hy
     g = torch.Generator().manual_seed(0)
-    for M, Nn, K in ((1, 264, 4096), (20, 1000, 4096), (150, 264, 2064), (300, 520, 1040)):
+    for M, Nn, K in ((1, 264, 4096), (20, 1000, 4096), (150, 264, 2064), (300, 520, 1040), (300, 3328, 4400),
+                     (640, 2568, 272)):
         x = torch.randint(-8, 9, (M, K), generator=g).float()
         w = torch.randint(-8, 9, (Nn, K), generator=g).float()
         s = 2.0 ** torch.randint(-3, 4, (M, -(-K // 128)), generator=g).float()
