@@ -160,10 +160,8 @@ int launch_ffn_backward(const FfnBackArgs &a, cudaStream_t st)
         default: n = start_slopes<HYENA_ACT_IDENTITY>(a, dg, du, grid, st); break;
     }
     if (n < 0) return -1;
-    const int x = launch_ffn_dx(a, dg, du, st);
-    if (x < 0) return -1;
-    const int w = launch_ffn_dw(a, dg, du, st);
-    return w < 0 ? -1 : n + x + w;
+    const int k = launch_ffn_gradients(a, dg, du, st);
+    return k < 0 ? -1 : n + k;
 }
 
 }  // namespace hyena

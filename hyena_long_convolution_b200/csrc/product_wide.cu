@@ -50,6 +50,7 @@ struct WideArgs {
     int tile_cols;       // output columns of a tile
     ProductArgs a;       // forward
     unsigned int *hdr;
+    bool beside;         // dx lets dW start beside it, and dW does not wait for it before its end
 };
 
 template <int kMode, bool kF8>
@@ -89,7 +90,9 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    wait_for_stream();
+    // dW reads dg, du and x, which were complete when dx passed its own wait
+    if (kMode != kDw || !A.beside) wait_for_stream();
+    if (kMode == kDx && A.beside) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = sh.tmem;
 
     // tile -> (tile row, tile column): bands of kBand tile rows, columns within
@@ -356,6 +359,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     cluster_sync();  // the other CTA may still tell this one's barriers
     if (warp == kEpiWarps + 1) tmem_dealloc<2>(tmem);
     if (tid == 0 && sh.dead != 0u) atomicOr(A.hdr + 2, kErrLocalTimeout);
+    if (kMode == kDw && A.beside) wait_for_stream();  // dx, for whoever comes next
 }
 
 }  // namespace
@@ -433,44 +437,37 @@ int launch_product_wide(const ProductArgs &a, cudaStream_t st)
     return a.fp8 ? start<kForward, true>(m, w, st) : start<kForward, false>(m, w, st);
 }
 
-int launch_ffn_dx(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
+int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
 {
     const int u = pairs();
     if (u < 1) return -1;
-    Maps m;
-    if (!encode_matrix(&m.a1, dg, 2, a.M, a.F, a.F, kTile) || !encode_matrix(&m.a2, du, 2, a.M, a.F, a.F, kTile) ||
-        !encode_matrix(&m.b1, a.w1, 2, a.F, a.D, a.ld_w, 64) || !encode_matrix(&m.b2, a.w2, 2, a.F, a.D, a.ld_w, 64) ||
-        !encode_output(&m.c1, a.dx, false, a.M, a.D, a.ld_dx))
+    Maps x, w;  // of dx and of dW
+    if (!encode_matrix(&x.a1, dg, 2, a.M, a.F, a.F, kTile) || !encode_matrix(&x.a2, du, 2, a.M, a.F, a.F, kTile) ||
+        !encode_matrix(&x.b1, a.w1, 2, a.F, a.D, a.ld_w, 64) || !encode_matrix(&x.b2, a.w2, 2, a.F, a.D, a.ld_w, 64) ||
+        !encode_output(&x.c1, a.dx, false, a.M, a.D, a.ld_dx) ||
+        !encode_matrix(&w.a1, dg, 2, a.M, a.F, a.F, 64) || !encode_matrix(&w.a2, du, 2, a.M, a.F, a.F, 64) ||
+        !encode_matrix(&w.b1, a.x, 2, a.M, a.D, a.ld_x, 64) ||
+        !encode_output(&w.c1, a.dw1, false, a.F, a.D, a.ld_dw) || !encode_output(&w.c2, a.dw2, false, a.F, a.D, a.ld_dw))
         return -1;
-    m.c2 = m.c3 = m.c1;
-    WideArgs w{};
-    w.tile_cols = 2 * kTile;
-    w.blocks1 = (a.F + 63) / 64;
-    make_plan(w.plan, u, static_cast<int>((a.M + 255) / 256), (a.D + 255) / 256, 2 * w.blocks1);
-    w.rows = a.M;
-    w.cols = a.D;
-    w.hdr = static_cast<unsigned int *>(a.workspace);
-    return start<kDx, false>(m, w, st);
-}
-
-int launch_ffn_dw(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
-{
-    const int u = pairs();
-    if (u < 1) return -1;
-    Maps m;
-    if (!encode_matrix(&m.a1, dg, 2, a.M, a.F, a.F, 64) || !encode_matrix(&m.a2, du, 2, a.M, a.F, a.F, 64) ||
-        !encode_matrix(&m.b1, a.x, 2, a.M, a.D, a.ld_x, 64) ||
-        !encode_output(&m.c1, a.dw1, false, a.F, a.D, a.ld_dw) || !encode_output(&m.c2, a.dw2, false, a.F, a.D, a.ld_dw))
-        return -1;
-    m.b2 = m.b1;
-    m.c3 = m.c1;
-    WideArgs w{};
-    w.tile_cols = 2 * kTile;
-    make_plan(w.plan, u, 2 * ((a.F + 255) / 256), (a.D + 255) / 256, static_cast<int>((a.M + 63) / 64));
-    w.rows = a.F;
-    w.cols = a.D;
-    w.hdr = static_cast<unsigned int *>(a.workspace);
-    return start<kDw, false>(m, w, st);
+    x.c2 = x.c3 = x.c1;
+    w.b2 = w.b1;
+    w.c3 = w.c1;
+    WideArgs p{}, q{};
+    p.tile_cols = q.tile_cols = 2 * kTile;
+    p.blocks1 = (a.F + 63) / 64;
+    make_plan(p.plan, u, static_cast<int>((a.M + 255) / 256), (a.D + 255) / 256, 2 * p.blocks1);
+    make_plan(q.plan, u, 2 * ((a.F + 255) / 256), (a.D + 255) / 256, static_cast<int>((a.M + 63) / 64));
+    p.rows = a.M;
+    q.rows = a.F;
+    p.cols = q.cols = a.D;
+    p.hdr = q.hdr = static_cast<unsigned int *>(a.workspace);
+    // Side by side, so that dW's units begin where dx leaves room (step of 1000 x 1032 ->
+    // 2760: 80 us one after the other, 72), unless both put parts in the workspace.
+    p.beside = q.beside = q.plan.share == 1;
+    const int n = start<kDx, false>(x, p, st);
+    if (n < 0) return -1;
+    const int k = start<kDw, false>(w, q, st);
+    return k < 0 ? -1 : n + k;
 }
 
 }  // namespace hyena

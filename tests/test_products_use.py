@@ -201,6 +201,29 @@ def test_before_a_kernel_that_reads_early(M):
         assert torch.equal(y, hy.modal_long_conv_prepared(*xs, N, ws)), seed
 
 
+@pytest.mark.parametrize("M,D,F", [(300, 1032, 1000), (1000, 264, 4104), (40, 2056, 520), (4000, 136, 264)])
+def test_what_follows_a_gradient_sees_all_of_it(M, D, F):
+    """dW is worked out beside dx: the next kernel, of either kind, comes after both."""
+    import torch
+    import hyena_long_convolution_b200 as hy
+    x, wg, wu = normal(M, D, seed=1), normal(F, D, seed=2, scale=D ** -0.5), normal(F, D, seed=3, scale=D ** -0.5)
+    dy, g, u = normal(M, F, seed=4), normal(M, F, seed=5), normal(M, F, seed=6)
+    ws = hy.FfnWorkspace(M, D, F, backward=True)
+    want = hy.gated_ffn_backward(dy, x, wg, wu, g, u, workspace=ws)
+    wq = [hy.fp8_quantize(t)[0].float() for t in want]
+    out = [torch.empty_like(t) for t in want]
+    for _ in range(10):
+        for t in out:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        hy.gated_ffn_backward(dy, x, wg, wu, g, u, dx=out[0], dgate_weight=out[1], dup_weight=out[2], workspace=ws)
+        copies = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(copies, want))
+        hy.gated_ffn_backward(dy, x, wg, wu, g, u, dx=out[0], dgate_weight=out[1], dup_weight=out[2], workspace=ws)
+        codes = [hy.fp8_quantize(t)[0] for t in out]
+        assert all(torch.equal(a.float(), b) for a, b in zip(codes, wq))
+
+
 def test_other_streams():
     import torch
     main = [call(None) for call in cases()]
