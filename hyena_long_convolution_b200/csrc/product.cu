@@ -115,23 +115,27 @@ int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> 
     return 0;
 }
 
-// Up to 64 rows the narrow kernel reads the weights at the rate of HBM, where the wide
-// one has most of its 256 rows empty (4096 -> 4096 x 11008 in e4m3, 16 rows: 13 and 26
-// us).  Beyond, its smaller tiles pay while they leave SMs to share a tile's k (1024 x
-// 4096, 256 rows in e4m3: 12 and 18 us; 4096 x 4096: 17 and 20; 74 tiles and more: 21
-// and 20); of two weights in bf16 half as many (4096 x 2048, 256 rows: 64 tiles 18 and
-// 16 us), but where the wide kernel's tiles of 256 rows would begin a second wave for
-// 128 rows (11008 x 4096: 43 and 51 us).
+// The narrow kernel reads the weights at the rate of HBM, where the wide one has most of
+// its rows empty (32 rows, 4096 -> 4096 x 11008: in e4m3 13 and 23 us, in bf16 34 and
+// 38).  Its smaller tiles pay
+//
+//   up to 64 rows, for one weight in codes up to a tile an SM (4096 -> 18944: 19.4 and
+//   21.4 us; 22016: 33 and 22), for two in bf16 always (19200: 75 and 78);
+//   beyond, and for two weights in codes, while they leave SMs to share a tile's k
+//   (4096 -> 8192, 64 rows, two weights in codes 21.0 and 22.4, 9728: 29 and 23; 128
+//   rows in bf16 32.5 and 35, 41 and 37; 256 rows of 1024 x 4096 in e4m3 12 and 18, 74
+//   tiles and more 21 and 20); of two in bf16 with more than 128 rows half as many
+//   (4096 x 2048, 256 rows: 64 tiles 18 and 16 us).
 bool product_is_narrow(long long M, int N, bool fp8, bool gated)
 {
-    if (M <= 64) return true;
+    if (!product_has_parts(M)) return true;
     const int nt = narrow_tokens(M, fp8 && gated), sms = product_sms();
     const long long tiles = (M + nt - 1) / nt * ((N + 127) / 128);
-    if (!gated || fp8) return tiles <= sms / 2;
-    return tiles <= sms / 4 || (M <= 128 && tiles > sms / 2 && tiles <= sms);
+    if (M <= 64 && !(fp8 && gated)) return !fp8 || tiles <= sms;
+    return tiles <= (fp8 || M <= 128 ? sms / 2 : sms / 4);
 }
 
-size_t product_workspace(long long M) { return kProductHeader + (M > 64 ? part_bytes() : 0); }
+size_t product_workspace(long long M) { return kProductHeader + (product_has_parts(M) ? part_bytes() : 0); }
 
 size_t ffn_backward_workspace(long long M, int F)
 {

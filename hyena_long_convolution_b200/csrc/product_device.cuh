@@ -96,6 +96,16 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// All threads of the CTA, or of the cluster.
+template <int kCtas>
+__device__ __forceinline__ void all_sync()
+{
+    if constexpr (kCtas > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+}
+
 // Tells a barrier of a CTA of this cluster that tensor memory has been read: the
 // reads are complete (tmem_wait), so that nothing has to be released at cluster
 // scope, whose fence took 4.6 of the 17 cycles that an instruction waited.

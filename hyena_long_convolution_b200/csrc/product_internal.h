@@ -73,6 +73,9 @@ inline int narrow_tokens(long long M, bool fp8_gated)
 {
     return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 || fp8_gated ? 64 : 128));
 }
+// Whether the workspace of a call has room for the wide kernel's parts: without it the call is
+// narrow.  One condition for both, so that no part is written where there is no room.
+inline bool product_has_parts(long long M) { return M > 32; }
 bool product_is_narrow(long long M, int N, bool fp8, bool gated);
 
 int launch_product_narrow(const ProductArgs &a, cudaStream_t st);

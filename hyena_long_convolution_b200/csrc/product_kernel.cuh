@@ -62,14 +62,14 @@ struct Walk {
     __device__ __forceinline__ bool next() { return (tile += step) < end; }
 };
 
-constexpr int kMostParts = 4;
+constexpr int kMostParts = 4;  // of a pair's tile; of a single CTA's, never so few, 3
 
 // v = the parts' sums, in order.  Written out for each number of parts, so that many
 // loads are under way: part by part, 2.8 us each.
-template <int kParts, int kV>
+template <int kParts, int kCtas, int kV>
 __device__ __forceinline__ void add_parts(float (&v)[kV], const float4 *parts)
 {
-    constexpr size_t kNext = 2ull * (kV / 4) * kEpiThreads;  // the next unit's slot of the same half
+    constexpr size_t kNext = static_cast<size_t>(kCtas) * (kV / 4) * kEpiThreads;  // the next unit's slot of the same rows
 #pragma unroll
     for (int i = 0; i < kV / 4; ++i) {
         float4 f = __ldcg(parts + i * kEpiThreads);
@@ -87,20 +87,20 @@ __device__ __forceinline__ void add_parts(float (&v)[kV], const float4 *parts)
 // which that was.  The two CTAs of a pair each have their own half of the tile.
 // v: this thread's sums, kept as float4 [i][thread] of its part's slot.  True in the
 // CTA that holds the tile's sums.
-template <int kV>
+template <int kCtas, int kV>
 __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int unit, int rank, int tile, int t,
                                            unsigned char *workspace, unsigned int *flag)
 {
     constexpr size_t kSlot = static_cast<size_t>(kV / 4) * kEpiThreads;
     float4 *slots = reinterpret_cast<float4 *>(workspace + kProductHeader) + t;
-    float4 *own = slots + (2ll * unit + rank) * kSlot;
+    float4 *own = slots + (static_cast<long long>(kCtas) * unit + rank) * kSlot;
 #pragma unroll
     for (int i = 0; i < kV / 4; ++i)
         own[i * kEpiThreads] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     named_sync(1, kEpiThreads);
     if (t == 0) {
         __threadfence();  // the stores of all, which the barrier has ordered before it
-        unsigned int *count = reinterpret_cast<unsigned int *>(workspace + 256) + 2 * tile + rank;
+        unsigned int *count = reinterpret_cast<unsigned int *>(workspace + 256) + kCtas * tile + rank;
         const bool last = atomicAdd(count, 1u) + 1 == static_cast<unsigned int>(p.share);
         if (last) *count = 0u;  // for the next call
         __threadfence();
@@ -108,13 +108,13 @@ __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int un
     }
     named_sync(1, kEpiThreads);
     if (*flag == 0u) return false;
-    const float4 *parts = slots + (2ll * tile * p.share + rank) * kSlot;
+    const float4 *parts = slots + (static_cast<long long>(kCtas) * tile * p.share + rank) * kSlot;
     if (p.share == 2)
-        add_parts<2, kV>(v, parts);
-    else if (p.share == 3)
-        add_parts<3, kV>(v, parts);
+        add_parts<2, kCtas, kV>(v, parts);
+    else if (kCtas == 1 || p.share == 3)
+        add_parts<3, kCtas, kV>(v, parts);
     else
-        add_parts<4, kV>(v, parts);
+        add_parts<kCtas == 1 ? 3 : kMostParts, kCtas, kV>(v, parts);
     return true;
 }
 
@@ -209,7 +209,6 @@ __device__ __forceinline__ uint4 pack_bf16(const float *v)
 // Straight from the registers a store touches 32 rows, 16 bytes of each: 8000 cycles
 // for a CTA's 128 x 256 sums; from the patch by the lanes 2800.
 constexpr int kPatch = 4096;
-constexpr int kPatches = 2;  // of a warp: one is filled while TMA reads the other
 
 // Codes, 64 bytes a row, are written by the lanes: `chunk(c)` gives a lane's 16 bytes,
 // row r goes to p + r * pitch, `left` bytes (a multiple of 8) of it, `rows` rows.
@@ -238,6 +237,8 @@ __device__ __forceinline__ void store_codes(unsigned char *patch, int lane, unsi
 }
 
 // Values go by TMA, which leaves out what lies outside the matrix.
+// kPatches of a warp: with two, one is filled while TMA reads the other.
+template <int kPatches>
 struct RowStore {
     unsigned char *patches;
     int lane, next;
@@ -248,7 +249,7 @@ struct RowStore {
     __device__ __forceinline__ void put(const CUtensorMap *map, int column, int row, F chunk)
     {
         unsigned char *patch = patches + next * kPatch;
-        next ^= 1;
+        next ^= kPatches - 1;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPatches - 1) : "memory");
         __syncwarp();
 #pragma unroll

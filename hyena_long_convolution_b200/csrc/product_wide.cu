@@ -10,7 +10,9 @@
 // k is not the contiguous axis, boxes of 64 columns x 64 k, which the MMA takes as they
 // are), one warp of the pair issues the MMAs, eight warps a CTA read tensor memory.
 // The pair halves what each SM fetches of the second operand: a k-block is 32 KB for
-// 512 cycles of MMAs.
+// 512 cycles of MMAs.  Of the forward products there is also a form with one CTA to a
+// tile of 128 x 256, four stages of 48 KB, for few rows and for tiles that come out in
+// fewer waves that way (see ctas_of).
 //
 // bf16: sums stay in tensor memory over the whole of k, in one of two halves, so that a
 // tile's outputs are worked out while the next one's MMAs run.  Bound by the tensor
@@ -34,11 +36,18 @@ namespace hyena {
 namespace {
 
 constexpr int kTile = 128;                       // rows of a CTA's operands
-constexpr int kStages = 5;
 constexpr int kOperand = kTile * kRowBytes;      // 16 KB
-constexpr int kStage = 2 * kOperand;
-constexpr int kSmem = kStages * kStage + kEpiWarps * kPatches * kPatch + 1024;
 constexpr int kHalf = 64;                        // columns of each group of 128 a thread has
+
+// kCtas: 2, a pair with half of the second operand each, or 1, which has all of it.
+template <int kCtas>
+struct Wide {
+    static constexpr int kStage = (kCtas == 2 ? 2 : 3) * kOperand;
+    static constexpr int kStages = kCtas == 2 ? 5 : 4;
+    static constexpr int kPatches = kCtas == 2 ? 2 : 1;  // of a warp
+    static constexpr int kSmem = kStages * kStage + kEpiWarps * kPatches * kPatch + 1024;
+    static constexpr int kRows = kCtas * kTile;  // of a tile
+};
 
 enum { kForward = 0, kDx = 1, kDw = 2 };
 
@@ -53,7 +62,7 @@ struct WideArgs {
     bool beside;         // dx lets dW start beside it, and dW does not wait for it before its end
 };
 
-template <int kMode, bool kF8>
+template <int kMode, bool kF8, int kCtas>
 __global__ void __launch_bounds__(kThreadsProduct, 1)
     product_wide_kernel(const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap a2,
                         const __grid_constant__ CUtensorMap b1, const __grid_constant__ CUtensorMap b2,
@@ -62,11 +71,13 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 {
     constexpr bool kAmn = kMode == kDw, kBmn = kMode != kForward;
     constexpr int kBlock = kF8 ? 128 : 64;  // k of a block
+    constexpr int kStage = Wide<kCtas>::kStage, kStages = Wide<kCtas>::kStages, kPatches = Wide<kCtas>::kPatches;
+    constexpr int kRows = Wide<kCtas>::kRows;
     extern __shared__ unsigned char raw[];
     __shared__ ProductShared<kStages> sh;
     unsigned char *stages = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = static_cast<int>(cluster_rank()), unit = blockIdx.x >> 1;
+    const int rank = kCtas == 2 ? static_cast<int>(cluster_rank()) : 0, unit = blockIdx.x / kCtas;
     const Plan &P = A.plan;
     volatile unsigned int *dead = &sh.dead;
 
@@ -81,14 +92,14 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.tfull + i, 1);
-            mbar_init(sh.tempty + i, 2 * kEpiWarps);
+            mbar_init(sh.tempty + i, kCtas * kEpiWarps);
         }
         sh.dead = 0u;
         fence_mbar_init();
     }
-    if (warp == kEpiWarps + 1) tmem_alloc<2>(&sh.tmem);
+    if (warp == kEpiWarps + 1) tmem_alloc<kCtas>(&sh.tmem);
     tc_fence_before();
-    cluster_sync();
+    all_sync<kCtas>();
     tc_fence_after();
     // dW reads dg, du and x, which were complete when dx passed its own wait
     if (kMode != kDw || !A.beside) wait_for_stream();
@@ -114,13 +125,14 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         int s = 0;
         bool ok = true;
         if (warp == kEpiWarps) {  // ----------------------------------- TMA
-            const uint32_t full0 = cluster_addr(sh.full, 0), first = rank == 0 ? on : 0u;
+            const uint32_t full0 = kCtas == 2 ? cluster_addr(sh.full, 0) : smem_u32(sh.full);
+            const uint32_t first = rank == 0 ? on : 0u;
             uint32_t ph = 1;
             for (Walk w(P, unit); ok && w.next();) {
                 int tm, tn;
                 place(w.tile, tm, tn);
                 const CUtensorMap *ma = &a1;
-                int m = tm * 256 + rank * kTile;
+                int m = tm * kRows + rank * kTile;
                 if (kMode == kDw && tm >= P.tiles_m / 2) {
                     ma = &a2;
                     m -= P.tiles_m / 2 * 256;
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 const CUtensorMap *mb = gated && rank ? &b2 : &b1;
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     if (!(ok = warp_wait(sh.empty + s, ph, dead))) break;
-                    expect_tx(first, sh.full + s, 2 * kStage);
+                    expect_tx(first, sh.full + s, kCtas * kStage);
                     const uint32_t bar = full0 + 8 * s;
                     unsigned char *pa = stages + s * kStage, *pb = pa + kOperand;
                     int k = kb * kBlock;
@@ -140,23 +152,25 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                         mb = &b2;
                     }
                     if constexpr (kAmn) {
-                        load_box<2>(on, pa, ma, bar, m, k);
-                        load_box<2>(on, pa + kOperand / 2, ma, bar, m + 64, k);
+                        load_box<kCtas>(on, pa, ma, bar, m, k);
+                        load_box<kCtas>(on, pa + kOperand / 2, ma, bar, m + 64, k);
                     } else {
-                        load_box<2>(on, pa, ma, bar, k, m);
+                        load_box<kCtas>(on, pa, ma, bar, k, m);
                     }
                     if constexpr (kBmn) {
-                        load_box<2>(on, pb, mb, bar, n, k);
-                        load_box<2>(on, pb + kOperand / 2, mb, bar, n + 64, k);
+                        load_box<kCtas>(on, pb, mb, bar, n, k);
+                        load_box<kCtas>(on, pb + kOperand / 2, mb, bar, n + 64, k);
                     } else {
-                        load_box<2>(on, pb, mb, bar, k, n);
+                        load_box<kCtas>(on, pb, mb, bar, k, n);
+                        if (kCtas == 1)
+                            load_box<kCtas>(on, pb + kOperand, gated ? &b2 : &b1, bar, k, gated ? n : n + kTile);
                     }
                     if (++s == kStages) s = 0, ph ^= 1;
                 }
             }
             if (!ok) let_land();
         } else if (warp == kEpiWarps + 1 && rank == 0) {  // ---------- MMA
-            constexpr uint32_t idesc = instruction_desc(kF8, 256, 256, kAmn, kBmn);
+            constexpr uint32_t idesc = instruction_desc(kF8, kRows, 256, kAmn, kBmn);
             constexpr uint64_t kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;
             const uint32_t base = smem_u32(stages);
             int buf = 0;
@@ -180,9 +194,9 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        mma<2, kF8>(on, d, da + i * kStepA, db + i * kStepB, idesc, fresh && i == 0 ? 0u : 1u);
-                    mma_commit_to<2>(on, empty);
-                    if (last) mma_commit_to<2>(on, tfull);
+                        mma<kCtas, kF8>(on, d, da + i * kStepA, db + i * kStepB, idesc, fresh && i == 0 ? 0u : 1u);
+                    mma_commit_to<kCtas>(on, empty);
+                    if (last) mma_commit_to<kCtas>(on, tfull);
                     stage_full = __all_sync(0xffffffffu, f);
                     part_free = __all_sync(0xffffffffu, e);
                 }
@@ -194,10 +208,10 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         more_registers();
         const int hh = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + hh * kHalf;
-        const uint32_t tempty0 = cluster_addr(sh.tempty, 0), tempty1 = cluster_addr(sh.tempty + 1, 0);
+        const uint32_t tempty = kCtas == 2 ? cluster_addr(sh.tempty, 0) : smem_u32(sh.tempty);
         const int groups = P.blocks;  // of codes: one a k-block
         unsigned char *patch = stages + kStages * kStage + warp * (kPatches * kPatch);
-        RowStore out(patch, lane);
+        RowStore<kPatches> out(patch, lane);
         int buf = 0;
         uint32_t tph = 0;
         bool ok = true;
@@ -212,7 +226,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             if (!w.next()) return false;
             place(w.tile, tm, tn);
             if constexpr (kF8) {
-                const long long m = static_cast<long long>(tm) * 256 + rank * kTile + row;
+                const long long m = static_cast<long long>(tm) * kRows + rank * kTile + row;
                 live = m < A.rows;
                 sx = A.a.sx + (live ? m * A.a.sx_row + static_cast<long long>(w.k0) * A.a.sx_step : 0);
                 const int n1 = A.a.gated ? tn : 2 * tn;
@@ -232,7 +246,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             auto done_reading = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(buf ? tempty1 : tempty0);
+                if (lane == 0) arrive_at(tempty + 8 * buf);
                 buf ^= 1;
                 if (buf == 0) tph ^= 1;
             };
@@ -293,9 +307,9 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
             }
             more = advance();
             if (P.share > 1 &&
-                !join_parts(v, P, unit, rank, tile, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
+                !join_parts<kCtas>(v, P, unit, rank, tile, tid, reinterpret_cast<unsigned char *>(A.hdr), &sh.flag))
                 continue;
-            const long long m = static_cast<long long>(row0) * 256 + rank * kTile + row;
+            const long long m = static_cast<long long>(row0) * kRows + rank * kTile + row;
             const int n = col0 * A.tile_cols + hh * kHalf;
             const int left = A.cols - n;
             // the warp's first row; none of its rows may lie inside
@@ -356,8 +370,8 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
         out.finish();
     }
     tc_fence_before();
-    cluster_sync();  // the other CTA may still tell this one's barriers
-    if (warp == kEpiWarps + 1) tmem_dealloc<2>(tmem);
+    all_sync<kCtas>();  // the other CTA may still tell this one's barriers
+    if (warp == kEpiWarps + 1) tmem_dealloc<kCtas>(tmem);
     if (tid == 0 && sh.dead != 0u) atomicOr(A.hdr + 2, kErrLocalTimeout);
     if (kMode == kDw && A.beside) wait_for_stream();  // dx, for whoever comes next
 }
@@ -368,21 +382,20 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
 
 namespace {
 
-int pairs() { return product_sms() / 2; }
-
 // Units to a tile, where that takes kJoin k-blocks off a unit's run, which is about
 // what the joining costs.
 constexpr int kJoin = 16;
 
-void make_plan(Plan &p, int units, int tiles_m, int tiles_n, int blocks)
+void make_plan(Plan &p, int ctas, int units, int tiles_m, int tiles_n, int blocks)
 {
+    const int most = ctas == 2 ? kMostParts : kMostParts - 1;
     p.tiles_m = tiles_m;
     p.tiles_n = tiles_n;
     p.tiles = tiles_m * tiles_n;
     p.by_band.set(kBand * tiles_n);
     p.by_last.set(tiles_m % kBand ? tiles_m % kBand : 1);
     p.blocks = blocks;
-    p.share = units / p.tiles < kMostParts ? units / p.tiles : kMostParts;
+    p.share = units / p.tiles < most ? units / p.tiles : most;
     if (p.share < 2 || blocks - blocks / p.share <= kJoin) p.share = 1;
     p.units = p.share > 1 ? p.tiles * p.share : (p.tiles < units ? p.tiles : units);
 }
@@ -397,22 +410,43 @@ bool encode_output(CUtensorMap *m, const void *p, bool f32, long long rows, int 
     return encode_matrix(m, p, f32 ? 4 : 2, rows, cols, ld, 32);
 }
 
-template <int kMode, bool kF8>
+template <int kMode, bool kF8, int kCtas>
 int start(const Maps &m, const WideArgs &w, cudaStream_t st)
 {
     static std::atomic<unsigned long long> done{0};
-    const auto kernel = product_wide_kernel<kMode, kF8>;
-    if (allow_shared(reinterpret_cast<const void *>(kernel), kSmem, done) < 0) return -1;
-    return launch_early(kernel, dim3(2 * w.plan.units), kThreadsProduct, kSmem, 2, st,
+    const auto kernel = product_wide_kernel<kMode, kF8, kCtas>;
+    if (allow_shared(reinterpret_cast<const void *>(kernel), Wide<kCtas>::kSmem, done) < 0) return -1;
+    return launch_early(kernel, dim3(kCtas * w.plan.units), kThreadsProduct, Wide<kCtas>::kSmem, kCtas, st,
                         "product (wide) launch", m.a1, m.a2, m.b1, m.b2, m.c1, m.c2, m.c3, w);
+}
+
+// CTAs to a tile.  Tiles of one, half as many rows, are taken where they make fewer
+// waves, since a wave of them takes 1.0 (codes) to 1.3 (bf16, which they feed 48 KB a
+// k-block instead of 32) of a pair's time: codes from 11 : 10 on, which is up to ten
+// waves, bf16 from 4 : 3.  4096 -> 11008 with silu, pairs and single ones: 300 rows (3
+// waves and 2) in codes 59 and 42 us, in bf16 71 and 61; 1664 rows (9 and 8) 168 and
+// 160, 211 and 225.  -> 14336, 640 rows (5 and 4) 98 and 82, 125 and 118, but -> 8192,
+// 1152 rows (5 and 4) in bf16 117 and 120.  Up to 128 rows a pair has one half empty:
+// with as many waves 23.5 and 22 us (4096 -> 18944 in codes), 22.8 and 24.1 (4096 ->
+// 6144 x 2), with fewer 41 and 25 (11008 x 2).
+int ctas_of(const ProductArgs &a, int sms, int tile_cols)
+{
+    if (a.M <= kTile) return 1;
+    const long long across = (a.N + tile_cols - 1) / tile_cols;
+    const long long one = ((a.M + kTile - 1) / kTile * across + sms - 1) / sms;
+    const long long two = ((a.M + 2 * kTile - 1) / (2 * kTile) * across + sms / 2 - 1) / (sms / 2);
+    return (a.fp8 ? 10 * two >= 11 * one : 3 * two >= 4 * one) ? 1 : 2;
 }
 
 }  // namespace
 
 int launch_product_wide(const ProductArgs &a, cudaStream_t st)
 {
-    const int u = pairs();
-    if (u < 1) return -1;
+    const int sms = product_sms();
+    if (sms < 2) return -1;
+    WideArgs w{};
+    w.tile_cols = a.gated ? kTile : 2 * kTile;
+    const int ctas = ctas_of(a, sms, w.tile_cols), rows = ctas * kTile;
     const int kb = a.fp8 ? 128 : 64, size = a.fp8 ? 1 : 2;
     Maps m;
     bool ok = encode_matrix(&m.a1, a.x, size, a.M, a.K, a.ld_x, kTile) &&
@@ -426,20 +460,19 @@ int launch_product_wide(const ProductArgs &a, cudaStream_t st)
     if (!a.gated) m.b2 = m.b1;
     if (!a.y) m.c1 = m.a1;  // not read
     if (!a.g) m.c2 = m.c3 = m.c1;
-    WideArgs w{};
-    w.tile_cols = a.gated ? kTile : 2 * kTile;
-    make_plan(w.plan, u, static_cast<int>((a.M + 255) / 256), (a.N + w.tile_cols - 1) / w.tile_cols,
-              (a.K + kb - 1) / kb);
+    make_plan(w.plan, ctas, sms / ctas, static_cast<int>((a.M + rows - 1) / rows),
+              (a.N + w.tile_cols - 1) / w.tile_cols, (a.K + kb - 1) / kb);
     w.rows = a.M;
     w.cols = a.N;
     w.a = a;
     w.hdr = static_cast<unsigned int *>(a.workspace);
-    return a.fp8 ? start<kForward, true>(m, w, st) : start<kForward, false>(m, w, st);
+    if (ctas == 1) return a.fp8 ? start<kForward, true, 1>(m, w, st) : start<kForward, false, 1>(m, w, st);
+    return a.fp8 ? start<kForward, true, 2>(m, w, st) : start<kForward, false, 2>(m, w, st);
 }
 
 int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st)
 {
-    const int u = pairs();
+    const int u = product_sms() / 2;
     if (u < 1) return -1;
     Maps x, w;  // of dx and of dW
     if (!encode_matrix(&x.a1, dg, 2, a.M, a.F, a.F, kTile) || !encode_matrix(&x.a2, du, 2, a.M, a.F, a.F, kTile) ||
@@ -455,8 +488,8 @@ int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_
     WideArgs p{}, q{};
     p.tile_cols = q.tile_cols = 2 * kTile;
     p.blocks1 = (a.F + 63) / 64;
-    make_plan(p.plan, u, static_cast<int>((a.M + 255) / 256), (a.D + 255) / 256, 2 * p.blocks1);
-    make_plan(q.plan, u, 2 * ((a.F + 255) / 256), (a.D + 255) / 256, static_cast<int>((a.M + 63) / 64));
+    make_plan(p.plan, 2, u, static_cast<int>((a.M + 255) / 256), (a.D + 255) / 256, 2 * p.blocks1);
+    make_plan(q.plan, 2, u, 2 * ((a.F + 255) / 256), (a.D + 255) / 256, static_cast<int>((a.M + 63) / 64));
     p.rows = a.M;
     q.rows = a.F;
     p.cols = q.cols = a.D;
@@ -464,9 +497,9 @@ int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_
     // Side by side, so that dW's units begin where dx leaves room (step of 1000 x 1032 ->
     // 2760: 80 us one after the other, 72), unless both put parts in the workspace.
     p.beside = q.beside = q.plan.share == 1;
-    const int n = start<kDx, false>(x, p, st);
+    const int n = start<kDx, false, 2>(x, p, st);
     if (n < 0) return -1;
-    const int k = start<kDw, false>(w, q, st);
+    const int k = start<kDw, false, 2>(w, q, st);
     return k < 0 ? -1 : n + k;
 }
 

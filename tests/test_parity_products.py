@@ -159,6 +159,30 @@ def test_ffn_fp8_many_rows(M, D, F):
     check_ffn_fp8(M, D, F, "gelu_tanh", M % 3 == 1)
 
 
+# tiles of 128 x 256, whole ones in one wave and in more, and in 2 and 3 parts; either side of the
+# rows and columns where the kernels change
+@pytest.mark.parametrize("M,Nn,K", [(33, 19080, 136), (64, 18944, 264), (64, 38152, 136), (100, 9608, 4400),
+                                    (65, 14344, 4400), (128, 9480, 520), (300, 11008, 264), (390, 9608, 264),
+                                    (1290, 8200, 136)])
+def test_matmul_tiles_of_one_cta(M, Nn, K):
+    import torch
+    check_matmul(M, Nn, K, False, torch.float32, seed=M)
+    check_matmul(M, Nn, K, True, torch.bfloat16, seed=M)
+
+
+@pytest.mark.parametrize("M,D,F,keep", [(100, 264, 9608, "bf16"), (128, 136, 19080, None), (66, 72, 9480, "fp32"),
+                                        (300, 136, 4872, "fp32"), (290, 264, 10248, "bf16"), (1200, 72, 4104, None)])
+def test_ffn_tiles_of_one_cta(M, D, F, keep):
+    import torch
+    check_ffn(M, D, F, "silu", {"fp32": torch.float32, "bf16": torch.bfloat16, None: None}[keep])
+
+
+@pytest.mark.parametrize("M,D,F", [(33, 272, 9616), (64, 144, 9488), (40, 272, 19088), (100, 4400, 4880),
+                                   (128, 4400, 9344), (300, 144, 4880), (1200, 144, 4112), (390, 272, 9616)])
+def test_ffn_fp8_tiles_of_one_cta(M, D, F):
+    check_ffn_fp8(M, D, F, "gelu", M % 3 == 1)
+
+
 def test_matmul_is_exact_on_whole_numbers():
     """Products and sums that fp32 holds exactly: every order gives the same."""
     import torch
