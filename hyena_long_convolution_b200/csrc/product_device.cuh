@@ -67,7 +67,9 @@ __device__ __forceinline__ float load_here(const float *p)
 // (launch_early): what comes before this reads and writes no global memory.  They do
 // not let the next one start early (griddepcontrol.launch_dependents), since one that
 // reads its inputs before it waits, as the modal scan's short passes do, would read
-// outputs that are not written yet.
+// outputs that are not written yet.  The one exception is dx, which lets dW start beside
+// it: dW reads nothing of dx's and waits for it before it ends, so that what follows dW
+// finds both written.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- clusters
