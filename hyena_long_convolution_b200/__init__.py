@@ -1362,8 +1362,8 @@ def gated_ffn_backward(dy, x, gate_weight, up_weight, gate, up, activation="silu
                        dup_weight=None, workspace: FfnWorkspace | None = None, stream=None) -> FfnGrads:
     """Gradients of ``gated_ffn`` from dy ([..., F] bf16), the forward call's
     inputs and the gate and up products it kept.  dx and the weights' gradients
-    (bf16, written not added to; one row stride) are allocated if not given;
-    ``workspace``: an FfnWorkspace made with backward = True."""
+    (bf16, written not added to; one row stride; in no input's place) are
+    allocated if not given; ``workspace``: an FfnWorkspace made with backward = True."""
     if stream is not None:
         with _current(stream):
             return gated_ffn_backward(dy, x, gate_weight, up_weight, gate, up, activation, dx, dgate_weight,

@@ -52,6 +52,14 @@ hyena_status_t check_group(int group)
     return group < 0 ? HYENA_ERR_INVALID_ARG : HYENA_ERR_UNSUPPORTED;
 }
 
+// An output at the address of one of the others would be written while that is read.
+// (Extents are not compared: columns of one matrix may lie between each other.)
+template <typename... T>
+bool clash(const void *out, const T *...others)
+{
+    return out != nullptr && ((out == static_cast<const void *>(others)) || ...);
+}
+
 int scale_groups(int n) { return (n + kScaleGroup - 1) / kScaleGroup; }
 
 hyena_status_t product(const ProductArgs &a, void *stream)
@@ -83,6 +91,7 @@ hyena_status_t hyena_fp8_quantize(const void *x, int64_t ld_x, hyena_dtype_t x_t
     if (st != HYENA_OK) return st;
     set_last_launches(0);
     if (rows == 0) return HYENA_OK;
+    if (clash(q, x, scales) || clash(scales, x)) return HYENA_ERR_INVALID_ARG;
     QuantArgs a{};
     a.x = x;
     a.ld_x = ld_x;
@@ -122,6 +131,7 @@ hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_s
     if (M == 0) return HYENA_OK;
     st = check_workspace(workspace, workspace_bytes, product_workspace(M));
     if (st != HYENA_OK) return st;
+    if (clash(y, x, w, x_scales, w_scales, workspace)) return HYENA_ERR_INVALID_ARG;
     ProductArgs a{};
     a.x = x;
     a.w1 = w;
@@ -171,6 +181,9 @@ hyena_status_t hyena_gated_ffn(const hyena_bf16_t *x, int64_t ld_x, const hyena_
     if (M == 0) return HYENA_OK;
     st = check_workspace(workspace, workspace_bytes, product_workspace(M));
     if (st != HYENA_OK) return st;
+    if (clash(y, x, gate_w, up_w, gate_out, up_out, workspace) || clash(gate_out, x, gate_w, up_w, up_out, workspace) ||
+        clash(up_out, x, gate_w, up_w, workspace))
+        return HYENA_ERR_INVALID_ARG;
     ProductArgs a{};
     a.x = x;
     a.w1 = gate_w;
@@ -216,6 +229,9 @@ hyena_status_t hyena_gated_ffn_fp8(const uint8_t *x, int64_t ld_x, const float *
     if (M == 0) return HYENA_OK;
     st = check_workspace(workspace, workspace_bytes, product_workspace(M));
     if (st != HYENA_OK) return st;
+    for (const void *out : {static_cast<const void *>(y), static_cast<const void *>(q), static_cast<const void *>(scales)})
+        if (clash(out, x, x_scales, gate_w, gate_scales, up_w, up_scales, workspace)) return HYENA_ERR_INVALID_ARG;
+    if (clash(q, scales)) return HYENA_ERR_INVALID_ARG;
     ProductArgs a{};
     a.x = x;
     a.w1 = gate_w;
@@ -275,6 +291,9 @@ hyena_status_t hyena_gated_ffn_backward(const hyena_bf16_t *dy, int64_t ld_dy, c
     }
     st = check_workspace(workspace, workspace_bytes, ffn_backward_workspace(M, F));
     if (st != HYENA_OK) return st;
+    for (const void *out : {dx, dgate_w, dup_w})
+        if (clash(out, dy, x, gate_w, up_w, gate, up, workspace)) return HYENA_ERR_INVALID_ARG;
+    if (clash(dx, dgate_w, dup_w) || clash(dgate_w, dup_w)) return HYENA_ERR_INVALID_ARG;
     FfnBackArgs a{};
     a.dy = dy;
     a.x = x;

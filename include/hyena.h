@@ -664,6 +664,8 @@ hyena_status_t hyena_rms_norm_backward(const hyena_bf16_t *dy, int64_t ld_dy,
  * rows, D   0 <= rows < 2^31; D a multiple of 8, at most HYENA_MAX_WIDTH.
  * x         of type x_type, ld_x (in elements, a multiple of 8, >= D).
  * q         one byte each, ld_q a multiple of 8 (the products want 16).
+ * q and scales overlap neither x nor one another (here and in the next calls:
+ * an output at the very address of another argument is INVALID_ARG).
  */
 #define HYENA_MAX_WIDTH (1 << 20)
 
@@ -714,7 +716,9 @@ hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_s
  * x         [M, D] bf16, ld_x.  gate_w, up_w: [F, D] bf16, ld_w each.
  * y         [M, F] bf16, ld_y, rounded once from fp32.
  * gate_out, up_out  [M, F] of type keep_type, ld_g, or both NULL: g and u for
- *           the gradient (y comes from the unrounded ones).
+ *           the gradient (y comes from the unrounded ones).  y and these overlap
+ *           neither the inputs nor one another; their columns may lie side by
+ *           side in one matrix.
  * M, D, F   0 <= M < 2^31; D, F multiples of 8, at most HYENA_MAX_WIDTH; every
  *           row stride a multiple of 8.
  * workspace as hyena_fp8_matmul, hyena_gated_ffn_workspace_size(M, D, F, 0)
@@ -759,6 +763,8 @@ hyena_status_t hyena_gated_ffn_fp8(const uint8_t *x, int64_t ld_x, const float *
  *
  * dx        [M, D] bf16, ld_dx.  dgate_w, dup_w: [F, D] bf16, ld_dw each,
  *           written not added to (zero for M = 0).  Each rounded once from fp32.
+ *           They overlap neither the inputs nor one another (dW's x is read while
+ *           dx is written).
  * workspace hyena_gated_ffn_workspace_size(M, D, F, 1) bytes, as above.
  */
 hyena_status_t hyena_gated_ffn_backward(const hyena_bf16_t *dy, int64_t ld_dy,

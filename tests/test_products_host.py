@@ -101,6 +101,19 @@ def test_backward_refuses(kw, code):
     assert backward(**kw) == code
 
 
+@pytest.mark.parametrize("call,outs,ins", [
+    (quantize, ("q", "s"), ("x",)), (matmul, ("y",), ("x", "w", "sx", "sw", "ws")),
+    (ffn, ("y", "g", "u"), ("x", "wg", "wu", "ws")), (ffn_fp8, ("q", "s"), ("x", "sx", "wg", "sg", "wu", "su", "ws")),
+    (backward, ("dx", "dwg", "dwu"), ("dy", "x", "wg", "wu", "g", "u", "ws"))])
+def test_an_output_in_place_of_another_argument_is_refused(call, outs, ins):
+    import itertools
+    names = outs + ins
+    apart = {n: A + i * (1 << 20) for i, n in enumerate(names)}
+    for out, other in itertools.product(outs, names):
+        if out != other:
+            assert call(**{**apart, out: apart[other]}) == INVALID, (out, other)
+
+
 def test_no_rows_launch_nothing():
     assert quantize(M=0, x=None, q=None, s=None) == 0
     assert matmul(M=0, x=None, sx=None, y=None, ws=None) == 0

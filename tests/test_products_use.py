@@ -109,6 +109,9 @@ def cases():
         yield lambda ws, x=x: hy.gated_ffn(x, wg, wu, "gelu", workspace=ws)
         yield lambda ws, q=q, s=s: hy.gated_ffn_fp8(q, s, qg[0][:992], qg[1], qu[0][:992], qu[1], fp8_out=True, workspace=ws)
         yield lambda ws, dy=dy, x=x, g=g, u=u: hy.gated_ffn_backward(dy, x, wg, wu, g, u, workspace=ws)
+    q, s = hy.fp8_quantize(normal(100, 4400, seed=5))
+    w = hy.fp8_quantize(normal(9608, 4400, seed=6), block=128)  # 38 tiles of one CTA, three to each
+    yield lambda ws: hy.fp8_matmul(q, s, *w, workspace=ws)
 
 
 def same(a, b):
