@@ -23,12 +23,17 @@
 // e4m3 codes: the sums over each 128 k go times their scales into registers (128 a
 // thread), since the scales are any fp32 numbers; the two halves of tensor memory then
 // change places every k-block.  8192 x 4096 -> 12288: 389-393 us, 2.1 PFLOP/s, 51% of
-// cycles active.  Of a tile's 31000 cycles 26000 go to 32 k-blocks of 815, which is the
-// way round: 512 of MMAs, then commit, 300 for the eight warps to read the half, their
-// arrival at the other CTA's MMA warp, over two halves; the rest to the outputs, which
-// the MMAs run ahead of by two k-blocks only.  (Each group of 128 columns by MMAs and
-// barriers of its own, four parts of tensor memory: 460 us, since N = 128 takes as long
-// as N = 256.  32 columns a load instead of 16: as fast.  Polling: 686.)
+// cycles active.  Of a tile's 31000 cycles 27000 go to 32 k-blocks of 840, which is the
+// way round of a half, 1700, over two halves: 165 to issue its MMAs, 330 more until
+// warps that wait see them done (660 in the two warps that share a scheduler with the
+// MMA warp, whatever that scheduler is, since MMAs that wait for the tensor core hold
+// up what else is issued there), 400 to read, 60 to say so, 160 until the MMA warp
+// knows, 512 the MMAs themselves; the rest to the outputs, which the MMAs run ahead of
+// by two k-blocks only.  With sums read once a tile only, which is what the MMAs alone
+// could do, 268 us, by power at 1.39 GHz instead of 1.59.  As fast: the MMAs of a
+// k-block 60 to 160 cycles apart, or by a warp for each half; 32 columns a load instead
+// of 16.  Slower: each group of 128 columns by MMAs and barriers of its own, four parts
+// of tensor memory (460 us); polling (686); tiles of one CTA (410).
 #include "product_kernel.cuh"
 
 namespace hyena {
@@ -180,23 +185,23 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 for (int kb = w.k0; kb < w.k1; ++kb) {
                     const bool fresh = kF8 || kb == w.k0, last = kF8 || kb + 1 == w.k1;
                     if (!stage_full && !(ok = warp_wait(sh.full + s, ph, dead))) break;
-                    if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
-                    tc_fence_after();
                     const uint64_t da = operand_desc(base + s * kStage, kOperand / 2);
                     const uint64_t db = operand_desc(base + s * kStage + kOperand, kOperand / 2);
                     const uint32_t d = tmem + buf * 256;
+                    if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
+                    tc_fence_after();
                     uint64_t *const empty = sh.empty + s, *const tfull = sh.tfull + buf;
                     if (++s == kStages) s = 0, ph ^= 1;
                     if (last) {
                         buf ^= 1;
                         if (buf == 0) tph ^= 1;
                     }
-                    const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mma<kCtas, kF8>(on, d, da + i * kStepA, db + i * kStepB, idesc, fresh && i == 0 ? 0u : 1u);
-                    mma_commit_to<kCtas>(on, empty);
                     if (last) mma_commit_to<kCtas>(on, tfull);
+                    mma_commit_to<kCtas>(on, empty);
+                    const bool f = mbar_test_wait(sh.full + s, ph), e = mbar_test_wait(sh.tempty + buf, tph);
                     stage_full = __all_sync(0xffffffffu, f);
                     part_free = __all_sync(0xffffffffu, e);
                 }
