@@ -135,6 +135,16 @@ bool product_is_narrow(long long M, int N, bool fp8, bool gated)
     return tiles <= (fp8 || M <= 128 ? sms / 2 : sms / 4);
 }
 
+// dx of few rows likewise, by the weights' columns (steps, 1 row: 1032 -> 2760 38 and 24 us,
+// 4096 -> 11008 126 and 107; 128 rows 50 and 38, 139 and 126), and of more rows while two
+// CTAs to a tile leave some SMs to dW beside it: 256 rows of 512 -> 1408 (8 tiles) 35 and
+// 25, of 2048 -> 4096 (32) 66 and 56, 700 of 1032 -> 2760 (54) 62 and 60, 200 of 4096 ->
+// 11008 (64) 163 and 165; but 1000 of 1032 -> 2760 (72) 71.5 and 74.6.
+bool ffn_dx_is_narrow(long long M, int D)
+{
+    return M <= 128 || 2 * ((M + 127) / 128) * ((D + 127) / 128) <= product_sms() - 16;
+}
+
 size_t product_workspace(long long M) { return kProductHeader + (product_has_parts(M) ? part_bytes() : 0); }
 
 size_t ffn_backward_workspace(long long M, int F)

@@ -71,6 +71,7 @@ __device__ __forceinline__ float load_here(const float *p)
 // it: dW reads nothing of dx's and waits for it before it ends, so that what follows dW
 // finds both written.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- clusters
 

@@ -80,6 +80,8 @@ bool product_is_narrow(long long M, int N, bool fp8, bool gated);
 
 int launch_product_narrow(const ProductArgs &a, cudaStream_t st);
 int launch_product_wide(const ProductArgs &a, cudaStream_t st);
+int launch_ffn_dx_narrow(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, bool beside, cudaStream_t st);
+bool ffn_dx_is_narrow(long long M, int D);
 int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, cudaStream_t st);
 
 // Map of a [rows, cols] matrix of codes, bf16 or fp32 (size 1, 2, 4) with boxes of 128 bytes of a row

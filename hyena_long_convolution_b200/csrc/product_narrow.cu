@@ -1,5 +1,5 @@
-// product_narrow.cu -- forward products with few rows (generated tokens) on the
-// tensor cores of sm_100a.
+// product_narrow.cu -- products with few rows (generated tokens; dx of the feed-forward
+// block's gradient) on the tensor cores of sm_100a.
 //
 // The weights are the operand with 128 rows and the tokens the one with kNT <= 128:
 // a CTA's tile is 128 weight rows (128 of the gate's and the same of the up
@@ -47,6 +47,8 @@ struct NarrowArgs {
     int tiles_m; // tiles of tokens
     int blocks;  // k-blocks
     int share;   // CTAs of a cluster, which share a tile's k
+    int blocks1; // dx: k-blocks of the first pair of operands
+    bool beside; // dx: dW may start beside it
     ProductArgs a;
     unsigned int *hdr;
 };
@@ -79,10 +81,11 @@ __device__ __forceinline__ float2 activate(float2 g, int act)
     }
 }
 
-template <int kNT, bool kF8, bool kGated>
+template <int kNT, bool kF8, bool kGated, bool kDx>
 __global__ void __launch_bounds__(kThreadsProduct, 1)
-    product_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap m1,
-                          const __grid_constant__ CUtensorMap m2, const __grid_constant__ NarrowArgs A)
+    product_narrow_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mx2,
+                          const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
+                          const __grid_constant__ NarrowArgs A)
 {
     using T = Narrow<kNT, kGated>;
     constexpr int kStages = T::kStages, kStage = T::kStage, kH = T::kH, kC = T::kC, kG = T::kG, kBufs = T::kBufs;
@@ -100,7 +103,8 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     if (tid == kEpiThreads) {
         prefetch_map(&m1);
         prefetch_map(&mx);
-        if (kGated) prefetch_map(&m2);
+        if (kGated || kDx) prefetch_map(&m2);
+        if (kDx) prefetch_map(&mx2);
     }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -119,6 +123,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     __syncthreads();
     tc_fence_after();
     wait_for_stream();
+    if (kDx && A.beside) let_next_start();
     const uint32_t tmem = sh.tmem;
 
     if (warp >= kEpiWarps) {
@@ -133,14 +138,23 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 unsigned char *p = stages + s * kStage;
                 const uint32_t bar = smem_u32(sh.full + s);
                 expect_tx(on, sh.full + s, kStage);
-                load_box<1>(on, p, &m1, bar, kb * kBlock, tn * kTile);
-                if (kGated) load_box<1>(on, p + kOperand, &m2, bar, kb * kBlock, tn * kTile);
-                load_box<1>(on, p + kG * kOperand, &mx, bar, kb * kBlock, m0);
+                if constexpr (kDx) {  // k is not the weights' contiguous axis: boxes of 64 columns x 64 k
+                    const bool up = kb >= A.blocks1;
+                    const int k = (up ? kb - A.blocks1 : kb) * kBlock;
+                    load_box<1>(on, p, up ? &m2 : &m1, bar, tn * kTile, k);
+                    load_box<1>(on, p + kOperand / 2, up ? &m2 : &m1, bar, tn * kTile + 64, k);
+                    load_box<1>(on, p + kOperand, up ? &mx2 : &mx, bar, k, m0);
+                } else {
+                    load_box<1>(on, p, &m1, bar, kb * kBlock, tn * kTile);
+                    if (kGated) load_box<1>(on, p + kOperand, &m2, bar, kb * kBlock, tn * kTile);
+                    load_box<1>(on, p + kG * kOperand, &mx, bar, kb * kBlock, m0);
+                }
                 if (++s == kStages) s = 0, ph ^= 1;
             }
             if (!ok) let_land();
         } else if (warp == kEpiWarps + 1) {  // ----------------------- MMA
-            constexpr uint32_t idesc = instruction_desc(kF8, kTile, kNT, false, false);
+            constexpr uint32_t idesc = instruction_desc(kF8, kTile, kNT, kDx, false);
+            constexpr int kStepW = kDx ? 2048 : 32;  // bytes from one instruction's weights to the next one's
             const uint32_t base = smem_u32(stages);
             int buf = 0;
             uint32_t ph = 0, tph = 1;
@@ -150,7 +164,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 if (!stage_full && !(ok = warp_wait(sh.full + s, ph, dead))) break;
                 if (fresh && !part_free && !(ok = warp_wait(sh.tempty + buf, tph, dead))) break;
                 tc_fence_after();
-                const uint64_t dw = operand_desc(base + s * kStage, 16);
+                const uint64_t dw = operand_desc(base + s * kStage, kDx ? kOperand / 2 : 16);
                 const uint64_t dx = operand_desc(base + s * kStage + kG * kOperand, 16);
                 const uint32_t d = tmem + buf * (kG * kNT);
                 uint64_t *const empty = sh.empty + s, *const tfull = sh.tfull + buf;
@@ -161,7 +175,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int g = 0; g < kG; ++g)
-                        mma<1, kF8>(on, d + g * kNT, dw + (g * kOperand + i * 32) / 16, dx + i * 2, idesc,
+                        mma<1, kF8>(on, d + g * kNT, dw + (g * kOperand + i * kStepW) / 16, dx + i * 2, idesc,
                                     fresh && i == 0 ? 0u : 1u);
                 mma_commit_to<1>(on, empty);
                 if (last) mma_commit_to<1>(on, tfull);
@@ -328,32 +342,43 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     if (tid == 0 && sh.dead != 0u) atomicOr(A.hdr + 2, kErrLocalTimeout);
 }
 
-template <int kNT, bool kF8, bool kGated>
-int start(const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, const NarrowArgs &w, int tiles,
-          cudaStream_t st)
+struct Maps {
+    CUtensorMap x, x2, w1, w2;
+};
+
+template <int kNT, bool kF8, bool kGated, bool kDx>
+int start(const Maps &m, const NarrowArgs &w, int tiles, cudaStream_t st)
 {
-    const auto kernel = product_narrow_kernel<kNT, kF8, kGated>;
+    const auto kernel = product_narrow_kernel<kNT, kF8, kGated, kDx>;
     constexpr int kSmem = Narrow<kNT, kGated>::kSmem;
     static std::atomic<unsigned long long> done{0};
     if (allow_shared(reinterpret_cast<const void *>(kernel), kSmem, done) < 0) return -1;
-    return launch_early(kernel, dim3(tiles * w.share), kThreadsProduct, kSmem, w.share, st, "product (narrow) launch", x,
-                        w1, w2, w);
+    return launch_early(kernel, dim3(tiles * w.share), kThreadsProduct, kSmem, w.share, st, "product (narrow) launch",
+                        m.x, m.x2, m.w1, m.w2, w);
 }
 
-template <bool kF8, bool kGated>
-int start_by_tokens(int nt, const CUtensorMap &x, const CUtensorMap &w1, const CUtensorMap &w2, const NarrowArgs &w,
-                    int tiles, cudaStream_t st)
+template <bool kF8, bool kGated, bool kDx>
+int start_by_tokens(int nt, const Maps &m, const NarrowArgs &w, int tiles, cudaStream_t st)
 {
     switch (nt) {
-        case 16: return start<16, kF8, kGated>(x, w1, w2, w, tiles, st);
-        case 32: return start<32, kF8, kGated>(x, w1, w2, w, tiles, st);
-        case 64: return start<64, kF8, kGated>(x, w1, w2, w, tiles, st);
+        case 16: return start<16, kF8, kGated, kDx>(m, w, tiles, st);
+        case 32: return start<32, kF8, kGated, kDx>(m, w, tiles, st);
+        case 64: return start<64, kF8, kGated, kDx>(m, w, tiles, st);
         default:
             if constexpr (kF8 && kGated)
                 return -1;  // not asked for
             else
-                return start<128, kF8, kGated>(x, w1, w2, w, tiles, st);
+                return start<128, kF8, kGated, kDx>(m, w, tiles, st);
     }
+}
+
+// CTAs to a tile: clusters of up to 8 while all fit at once (a GPU of 148 SMs holds 74
+// of two CTAs of this size, 33 of four, 15 of eight) and each CTA keeps 4 k-blocks.
+int share_of(int tiles, int blocks, int sms)
+{
+    if (tiles <= (sms - 28) / 8 && blocks >= 32) return 8;
+    if (tiles <= (sms - 16) / 4 && blocks >= 16) return 4;
+    return tiles <= sms / 2 && blocks >= 8 ? 2 : 1;
 }
 
 }  // namespace
@@ -364,28 +389,51 @@ int launch_product_narrow(const ProductArgs &a, cudaStream_t st)
     if (sms < 1) return -1;
     const int nt = narrow_tokens(a.M, a.fp8 && a.gated);
     const int kb = a.fp8 ? 128 : 64, size = a.fp8 ? 1 : 2;
-    CUtensorMap x, w1, w2;
-    if (!encode_matrix(&x, a.x, size, a.M, a.K, a.ld_x, nt) || !encode_matrix(&w1, a.w1, size, a.N, a.K, a.ld_w, kTile))
+    Maps m;
+    if (!encode_matrix(&m.x, a.x, size, a.M, a.K, a.ld_x, nt) ||
+        !encode_matrix(&m.w1, a.w1, size, a.N, a.K, a.ld_w, kTile))
         return -1;
+    m.x2 = m.x;
     if (!a.gated)
-        w2 = w1;
-    else if (!encode_matrix(&w2, a.w2, size, a.N, a.K, a.ld_w, kTile))
+        m.w2 = m.w1;
+    else if (!encode_matrix(&m.w2, a.w2, size, a.N, a.K, a.ld_w, kTile))
         return -1;
     NarrowArgs w{};
     w.tiles_m = static_cast<int>((a.M + nt - 1) / nt);
     const int tiles = w.tiles_m * ((a.N + kTile - 1) / kTile);
     w.blocks = (a.K + kb - 1) / kb;
-    // clusters of up to 8 while all fit at once (a GPU of 148 SMs holds 74 of two CTAs of
-    // this size, 33 of four, 15 of eight) and each CTA keeps 4 k-blocks
-    w.share = 1;
-    if (tiles <= sms / 2 && w.blocks >= 8) w.share = 2;
-    if (tiles <= (sms - 16) / 4 && w.blocks >= 16) w.share = 4;
-    if (tiles <= (sms - 28) / 8 && w.blocks >= 32) w.share = 8;
+    w.share = share_of(tiles, w.blocks, sms);
     w.a = a;
     w.hdr = static_cast<unsigned int *>(a.workspace);
-    if (!a.gated) return start_by_tokens<true, false>(nt, x, w1, w2, w, tiles, st);
-    return a.fp8 ? start_by_tokens<true, true>(nt, x, w1, w2, w, tiles, st)
-                 : start_by_tokens<false, true>(nt, x, w1, w2, w, tiles, st);
+    if (!a.gated) return start_by_tokens<true, false, false>(nt, m, w, tiles, st);
+    return a.fp8 ? start_by_tokens<true, true, false>(nt, m, w, tiles, st)
+                 : start_by_tokens<false, true, false>(nt, m, w, tiles, st);
+}
+
+// dx = dg Wg + du Wu as a product with few rows: the weights' columns are the tile's 128
+// rows, and k runs through F twice.
+int launch_ffn_dx_narrow(const FfnBackArgs &a, const uint16_t *dg, const uint16_t *du, bool beside, cudaStream_t st)
+{
+    const int sms = product_sms();
+    if (sms < 1) return -1;
+    const int nt = narrow_tokens(a.M, false);
+    Maps m;
+    if (!encode_matrix(&m.x, dg, 2, a.M, a.F, a.F, nt) || !encode_matrix(&m.x2, du, 2, a.M, a.F, a.F, nt) ||
+        !encode_matrix(&m.w1, a.w1, 2, a.F, a.D, a.ld_w, 64) || !encode_matrix(&m.w2, a.w2, 2, a.F, a.D, a.ld_w, 64))
+        return -1;
+    NarrowArgs w{};
+    w.tiles_m = static_cast<int>((a.M + nt - 1) / nt);
+    const int tiles = w.tiles_m * ((a.D + kTile - 1) / kTile);
+    w.blocks1 = (a.F + 63) / 64;
+    w.blocks = 2 * w.blocks1;
+    w.share = share_of(tiles, w.blocks, sms);
+    w.beside = beside;
+    w.a.y = a.dx;
+    w.a.ld_y = a.ld_dx;
+    w.a.M = a.M;
+    w.a.N = a.D;
+    w.hdr = static_cast<unsigned int *>(a.workspace);
+    return start_by_tokens<false, false, true>(nt, m, w, tiles, st);
 }
 
 }  // namespace hyena

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
     tc_fence_after();
     // dW reads dg, du and x, which were complete when dx passed its own wait
     if (kMode != kDw || !A.beside) wait_for_stream();
-    if (kMode == kDx && A.beside) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (kMode == kDx && A.beside) let_next_start();
     const uint32_t tmem = sh.tmem;
 
     // tile -> (tile row, tile column): bands of kBand tile rows, columns within
@@ -501,8 +501,9 @@ int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_
     p.hdr = q.hdr = static_cast<unsigned int *>(a.workspace);
     // Side by side, so that dW's units begin where dx leaves room (step of 1000 x 1032 ->
     // 2760: 80 us one after the other, 72), unless both put parts in the workspace.
-    p.beside = q.beside = q.plan.share == 1;
-    const int n = start<kDx, false, 2>(x, p, st);
+    const bool narrow = ffn_dx_is_narrow(a.M, a.D);
+    p.beside = q.beside = narrow || p.plan.share == 1 || q.plan.share == 1;
+    const int n = narrow ? launch_ffn_dx_narrow(a, dg, du, p.beside, st) : start<kDx, false, 2>(x, p, st);
     if (n < 0) return -1;
     const int k = start<kDw, false, 2>(w, q, st);
     return k < 0 ? -1 : n + k;

@@ -356,6 +356,16 @@ def test_backward_sizes(M, D, F):
     check_backward(M, D, F, "gelu", torch.float32)
 
 
+# dx by the weights' columns: clusters of 8, 4, 2 and none, one and several tiles of rows; and
+# either side of where it is not
+@pytest.mark.parametrize("M,D,F", [(17, 264, 1096), (520, 264, 1032), (100, 2056, 1096), (128, 4104, 520),
+                                   (300, 1000, 1096), (64, 5000, 264), (40, 9608, 72), (900, 1032, 264),
+                                   (1000, 1032, 264), (129, 4232, 72), (129, 4104, 136)])
+def test_backward_few_rows(M, D, F):
+    import torch
+    check_backward(M, D, F, "silu", torch.float32 if M % 2 else torch.bfloat16, seed=M)
+
+
 def test_no_rows():
     import torch
     import hyena_long_convolution_b200 as hy

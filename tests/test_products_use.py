@@ -204,7 +204,8 @@ def test_before_a_kernel_that_reads_early(M):
         assert torch.equal(y, hy.modal_long_conv_prepared(*xs, N, ws)), seed
 
 
-@pytest.mark.parametrize("M,D,F", [(300, 1032, 1000), (1000, 264, 4104), (40, 2056, 520), (4000, 136, 264)])
+@pytest.mark.parametrize("M,D,F", [(300, 1032, 1000), (1000, 264, 4104), (40, 2056, 520), (4000, 136, 264),
+                                   (2000, 1032, 520), (4000, 2056, 264), (1, 4096, 4096)])
 def test_what_follows_a_gradient_sees_all_of_it(M, D, F):
     """dW is worked out beside dx: the next kernel, of either kind, comes after both."""
     import torch
