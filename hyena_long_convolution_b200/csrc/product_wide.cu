@@ -479,11 +479,14 @@ int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_
 {
     const int u = product_sms() / 2;
     if (u < 1) return -1;
-    Maps x, w;  // of dx and of dW
-    if (!encode_matrix(&x.a1, dg, 2, a.M, a.F, a.F, kTile) || !encode_matrix(&x.a2, du, 2, a.M, a.F, a.F, kTile) ||
-        !encode_matrix(&x.b1, a.w1, 2, a.F, a.D, a.ld_w, 64) || !encode_matrix(&x.b2, a.w2, 2, a.F, a.D, a.ld_w, 64) ||
-        !encode_output(&x.c1, a.dx, false, a.M, a.D, a.ld_dx) ||
-        !encode_matrix(&w.a1, dg, 2, a.M, a.F, a.F, 64) || !encode_matrix(&w.a2, du, 2, a.M, a.F, a.F, 64) ||
+    const bool narrow = ffn_dx_is_narrow(a.M, a.D);
+    Maps x{}, w;  // of dx and of dW
+    if (!narrow &&
+        (!encode_matrix(&x.a1, dg, 2, a.M, a.F, a.F, kTile) || !encode_matrix(&x.a2, du, 2, a.M, a.F, a.F, kTile) ||
+         !encode_matrix(&x.b1, a.w1, 2, a.F, a.D, a.ld_w, 64) || !encode_matrix(&x.b2, a.w2, 2, a.F, a.D, a.ld_w, 64) ||
+         !encode_output(&x.c1, a.dx, false, a.M, a.D, a.ld_dx)))
+        return -1;
+    if (!encode_matrix(&w.a1, dg, 2, a.M, a.F, a.F, 64) || !encode_matrix(&w.a2, du, 2, a.M, a.F, a.F, 64) ||
         !encode_matrix(&w.b1, a.x, 2, a.M, a.D, a.ld_x, 64) ||
         !encode_output(&w.c1, a.dw1, false, a.F, a.D, a.ld_dw) || !encode_output(&w.c2, a.dw2, false, a.F, a.D, a.ld_dw))
         return -1;
@@ -501,7 +504,6 @@ int launch_ffn_gradients(const FfnBackArgs &a, const uint16_t *dg, const uint16_
     p.hdr = q.hdr = static_cast<unsigned int *>(a.workspace);
     // Side by side, so that dW's units begin where dx leaves room (step of 1000 x 1032 ->
     // 2760: 80 us one after the other, 72), unless both put parts in the workspace.
-    const bool narrow = ffn_dx_is_narrow(a.M, a.D);
     p.beside = q.beside = narrow || p.plan.share == 1 || q.plan.share == 1;
     const int n = narrow ? launch_ffn_dx_narrow(a, dg, du, p.beside, st) : start<kDx, false, 2>(x, p, st);
     if (n < 0) return -1;
