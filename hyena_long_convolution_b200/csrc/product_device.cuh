@@ -383,7 +383,8 @@ __device__ __forceinline__ float2 activation_slope2(float2 g, float2 &d)
         d = __ffma2_rn(g, __fmul2_rn(e, bcast2(0.39894228040143268f)), c);
         return __fmul2_rn(g, c);
     } else if constexpr (kAct == HYENA_ACT_GELU_TANH) {
-        const float2 g2 = __fmul2_rn(g, g);
+        // g^2 at most 2^64, beyond which (1 - s) is 0 or y is: times an infinite `in` that is NaN
+        const float2 sq = __fmul2_rn(g, g), g2 = make_float2(fminf(sq.x, 0x1p+64f), fminf(sq.y, 0x1p+64f));
         const float2 s = sigmoid2(__ffma2_rn(__fmul2_rn(g2, bcast2(0.044715f)), g, g), kGeluTanh);
         const float2 in = __ffma2_rn(g2, bcast2(3.f * 0.044715f * kGeluTanh), bcast2(kGeluTanh));
         const float2 y = __fmul2_rn(g, s);
