@@ -956,6 +956,18 @@ def _rows(x, name, dtypes):
     return B * L, D, ld
 
 
+def _new_codes(x, width):
+    """(codes, row stride) for x's rows, `width` a row: a stride of whole 16 bytes,
+    as the products ask of their operands."""
+    sh = x.shape
+    if width % 16 == 0 and width == sh[-1]:  # half the time of the other way
+        torch = _torch()
+        return torch.empty_like(x, dtype=_E4M3, memory_format=torch.contiguous_format), width
+    ld = (width + 15) & ~15
+    q = x.new_empty((*sh[:-1], ld), dtype=_E4M3)
+    return (q if ld == width else q[..., :width]), ld
+
+
 def _weight(t, D):
     """hyena_dtype_t of a norm weight."""
     torch = _torch()
@@ -1020,7 +1032,9 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
                  stream=None):
     """``rms_norm`` with an 8-bit output: returns (q, scales) with y ~ q scale,
     q float8_e4m3fn of x's shape and one fp32 scale per row (group = 0, shape
-    [rows, 1]) or per 128 channels (group = 128, [rows, ceil(D / 128)])."""
+    [rows, 1]) or per 128 channels (group = 128, [rows, ceil(D / 128)]).  An
+    allocated q has its rows at multiples of 16 bytes, as ``fp8_matmul`` takes
+    them: it is contiguous where D is a multiple of 16."""
     if stream is not None:
         with _current(stream):
             return rms_norm_fp8(x, weight, eps, residual, residual_out, group, q, scales, rstd)
@@ -1030,7 +1044,7 @@ def rms_norm_fp8(x, weight, eps=1e-6, residual=None, residual_out=None, group=0,
         raise ValueError("group must be 0 (one scale per row) or 128")
     here = _here(x, weight, residual, residual_out, q, scales, rstd)
     if q is None:
-        q, ld_q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), D
+        q, ld_q = _new_codes(x, D)
     else:
         qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
         if qM != M or qD != D:
@@ -1205,7 +1219,9 @@ def fp8_quantize(x, block=1, q=None, scales=None, stream=None):
     per row and 128 channels (block = 1, scales [rows, ceil(D / 128)]:
     activations) or per 128 rows x 128 channels (block = 128, scales
     [ceil(rows / 128), ceil(D / 128)]: weights): returns (q, scales) with
-    x ~ q scale, q float8_e4m3fn of x's shape."""
+    x ~ q scale, q float8_e4m3fn of x's shape.  An allocated q has its rows at
+    multiples of 16 bytes, as the products take them: it is contiguous where D
+    is a multiple of 16."""
     if stream is not None:
         with _current(stream):
             return fp8_quantize(x, block, q, scales)
@@ -1215,7 +1231,7 @@ def fp8_quantize(x, block=1, q=None, scales=None, stream=None):
         raise ValueError("block must be 1 (rows of activations) or 128 (blocks of a weight)")
     here = _here(x, q, scales)
     if q is None:
-        q, ld_q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), D
+        q, ld_q = _new_codes(x, D)
     else:
         qM, qD, ld_q = _rows(q, "q", (torch.float8_e4m3fn,))
         if qM != M or qD != D:
@@ -1238,7 +1254,8 @@ def fp8_matmul(x, x_scales, weight, weight_scales, y=None, dtype=None, workspace
     fp8_quantize leave them), weight [N, K] with weight_scales
     [ceil(N / 128), ceil(K / 128)] (fp8_quantize with block = 128).  Returns y
     ([..., N], bf16 or the given dtype bf16 or fp32, allocated if not given).
-    Row strides of x and weight: multiples of 16.
+    Row strides of x and weight: multiples of 16, whatever K (the calls that make
+    codes allocate them so).
 
     A device wait that ran out leaves NaN and is reported by workspace_check; a
     call without a ``workspace`` uses one of its own."""
@@ -1307,7 +1324,7 @@ def gated_ffn_fp8(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, a
     """``gated_ffn`` of e4m3 operands with scales as in ``fp8_matmul``.  Returns
     y ([..., F] bf16), or with ``fp8_out`` (q, scales): y's codes with one scale
     per row and 128 of its values, as the down projection by ``fp8_matmul``
-    takes them (F a multiple of 16)."""
+    takes them (an allocated q with its rows at multiples of 16 bytes)."""
     if stream is not None:
         with _current(stream):
             return gated_ffn_fp8(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, activation, fp8_out, y,
@@ -1326,9 +1343,11 @@ def gated_ffn_fp8(x, x_scales, gate_weight, gate_scales, up_weight, up_scales, a
         if y is not None:
             raise ValueError("y is the bf16 output: give q and scales with fp8_out")
         if q is None:
-            q, ld_q = torch.empty((*x.shape[:-1], F), dtype=e4m3, device=x.device), F
+            q, ld_q = _new_codes(x, F)
         else:
             ld_q = _out_rows(q, M, F, e4m3, "q")
+            if M == 1:  # no second row: any stride will do
+                ld_q = (F + 15) & ~15
         want = (M, -(-F // 128))
         if scales is None:
             scales = x_scales.new_empty(want)
