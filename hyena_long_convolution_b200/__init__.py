@@ -80,6 +80,7 @@ MAX_COMPLEX_MODES = 32
 MAX_TAPS = 128
 RECURRENCE_UNIT = 64
 MAX_NORM_WIDTH = 16384
+PRODUCT_HEADER = 4096  # bytes of a product's workspace that have to be zero at first
 ACTIVATIONS = {"silu": 1, "gelu": 2, "gelu_tanh": 3, "identity": 4}
 
 
@@ -156,10 +157,11 @@ def _current(stream):
     return torch.cuda.stream(stream)
 
 
-def _zeroed(n, device, stream):
-    """n zero bytes of device memory, taken and cleared on one stream (the given
-    one, else the device's current one): taken on another, they may be a block
-    that work still pending there writes to after the clearing."""
+def _zeroed(n, device, stream, clear=None):
+    """n bytes of device memory, the first `clear` (None: all) zero, taken and
+    cleared on one stream (the given one, else the device's current one): taken on
+    another, they may be a block that work still pending there writes to after the
+    clearing."""
     torch = _torch()
     if getattr(device, "type", None) == "cuda" and device.index == torch.cuda.current_device():
         device = None  # the usual case, of a tensor's device
@@ -171,9 +173,10 @@ def _zeroed(n, device, stream):
             with torch.cuda.stream(None) if stream is None else _current(stream):
                 if torch.cuda.current_device() != here:
                     raise ValueError("the stream belongs to another device")
-                return _zeroed(n, None, None)
+                return _zeroed(n, None, None, clear)
     buf = torch.empty(n, dtype=torch.uint8, device="cuda")
-    check("hyena_modal_workspace_init", lib().hyena_modal_workspace_init(_ptr(buf), n, _stream(None)))
+    check("hyena_modal_workspace_init",
+          lib().hyena_modal_workspace_init(_ptr(buf), n if clear is None else clear, _stream(None)))
     return buf
 
 
@@ -1191,27 +1194,27 @@ def _kept(gate, up, M, F):
 
 class MatmulWorkspace:
     """Device workspace of fp8_matmul for up to M rows, N outputs and K channels,
-    zero-filled once at creation; for calls in order on one stream."""
+    its header zero-filled once at creation; for calls in order on one stream."""
 
     def __init__(self, M: int, N: int, K: int, device=None, stream=None):
         n = int(lib().hyena_fp8_matmul_workspace_size(M, N, K))
         if n == 0:
             raise ValueError("invalid workspace shape")
         self.nbytes = n
-        self.buf = _zeroed(n, device, stream)
+        self.buf = _zeroed(n, device, stream, PRODUCT_HEADER)
 
 
 class FfnWorkspace:
     """Device workspace of gated_ffn and gated_ffn_fp8 for up to M rows (with
-    ``backward``, of gated_ffn_backward too), zero-filled once at creation; for
-    calls in order on one stream."""
+    ``backward``, of gated_ffn_backward too), its header zero-filled once at
+    creation; for calls in order on one stream."""
 
     def __init__(self, M: int, D: int, F: int, backward: bool = False, device=None, stream=None):
         n = int(lib().hyena_gated_ffn_workspace_size(M, D, F, 1 if backward else 0))
         if n == 0:
             raise ValueError("invalid workspace shape")
         self.nbytes = n
-        self.buf = _zeroed(n, device, stream)
+        self.buf = _zeroed(n, device, stream, PRODUCT_HEADER)
 
 
 def fp8_quantize(x, block=1, q=None, scales=None, stream=None):

@@ -13,7 +13,7 @@ constexpr int kThreadsProduct = kEpiThreads + 128; // + a TMA warp, an MMA warp 
 // 168, what the kernels are launched with.
 constexpr int kRegsEpi = 208, kRegsAux = 88;
 constexpr int kRowBytes = 128;                    // of a k-block: 64 bf16 or 128 codes
-constexpr size_t kProductHeader = 4096;           // 256 bytes of header, then a counter for each split tile
+constexpr size_t kProductHeader = HYENA_PRODUCT_HEADER; // 256 bytes of header, then a counter for each split tile
 
 // Quotients by a number that the host knows, of 0 <= n < 2^31: the high part of a
 // product (m = ceil(2^(31 + s) / d), 2^s >= d).  An integer division takes 150 cycles,

@@ -686,17 +686,20 @@ hyena_status_t hyena_fp8_quantize(const void *x, int64_t ld_x, hyena_dtype_t x_t
  * y         [M, N] of type y_type, ld_y; rounded once from fp32.
  * M, N, K   0 <= M < 2^31; N, K multiples of 8, at most HYENA_MAX_WIDTH; ld_x
  *           and ld_w multiples of 16, ld_y of 8.
- * workspace at least hyena_fp8_matmul_workspace_size bytes; zero-filled once
- *           (hyena_modal_workspace_init) and then reused, by calls in order on
- *           one stream (or ordered otherwise); hyena_workspace_check reports a
- *           device wait that ran out, whose call leaves NaN in the results
- *           that it did not reach.  One for M rows serves fewer, and any N, K.
+ * workspace at least hyena_fp8_matmul_workspace_size bytes, of which the first
+ *           HYENA_PRODUCT_HEADER are zero-filled once (hyena_modal_workspace_init
+ *           of so many), and then reused, by calls in order on one stream (or
+ *           ordered otherwise); hyena_workspace_check reports a device wait that
+ *           ran out, whose call leaves NaN in the results that it did not reach.
+ *           One for M rows serves fewer, and any N, K.
  *
  * Products of codes are exact and summed in fp32 over each 128 channels; the
  * sums times their scales are summed in fp32 in the order of k.  Work split
  * over k (few rows) is joined in that order too, whichever part is done last.
  * x and w are not written; y may overlap none of the inputs.
  */
+#define HYENA_PRODUCT_HEADER 4096
+
 size_t hyena_fp8_matmul_workspace_size(int64_t M, int N, int K);
 
 hyena_status_t hyena_fp8_matmul(const uint8_t *x, int64_t ld_x, const float *x_scales, int x_group,
