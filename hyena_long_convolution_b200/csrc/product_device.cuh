@@ -300,9 +300,12 @@ __device__ __forceinline__ void tmem_wait(float (&v)[32])
 
 // ---------------------------------------------------------------- activations
 
-// Two values at a time, in packed arithmetic.  2^x and 1 / x are the hardware's
-// approximations, 2^-22 off, and an exponential's argument is rounded once, so that
-// e^x is up to (|x| + 4) 2^-24 off.
+// Two values at a time, in packed arithmetic.  With n = 2^-24: 2^x is the hardware's
+// approximation, 4 n off, and 1 / x likewise, 2 n; each rounding on the way to an
+// exponential's argument z moves e^z by n |z|.  There are two for silu (its constant,
+// the product), three for gelu (the square too) and eight for gelu_tanh (four in the
+// cubic, three in its constant), so that e^z is (2, 3, 8 |z| + 4) n off, and the
+// sigmoid, 1 - s of that and 3 n.  Below 2^-126 either is zero.
 __device__ __forceinline__ float2 exp2_2(float2 x)
 {
     float2 r;
@@ -329,9 +332,10 @@ __device__ __forceinline__ float2 sigmoid2(float2 x, float c)
 
 // The normal distribution's Phi(g), and e^{-g^2 / 2} in e.  Phi(-|g|) = t p(t)
 // e^{-g^2 / 2} with t = 1 / (1 + 0.3 |g|) and p of degree 7 fitted to the function in
-// the relative maximum norm for |g| <= 14.5 (1.6e-7; with the arithmetic some 20 half
-// steps of fp32 for |g| < 5), which keeps the digits that 1 + erf loses where g is
-// negative.
+// the relative maximum norm for |g| <= 14.5 (1.9e-7 with the coefficients in fp32;
+// with the arithmetic 30 half steps of fp32 and those of the exponential), which keeps
+// the digits that 1 + erf loses where g is negative.  Beyond 13.2 the exponential, and
+// Phi(-|g|), is zero.
 __device__ __forceinline__ float2 normal_cdf2(float2 g, float2 &e)
 {
     const float2 a = make_float2(fabsf(g.x), fabsf(g.y));

@@ -9,7 +9,7 @@ import numpy as np
 E4M3_MAX = 448.0
 AMAX_FLOOR = 2.0 ** -100
 GROUP = 128
-_erf = np.vectorize(math.erf, otypes=[float])
+_erfc = np.vectorize(math.erfc, otypes=[float])
 
 
 def scales(x, block):
@@ -31,19 +31,27 @@ def values(q, s, block):
     return q * spread(s, block, q.shape)
 
 
+def _sigmoid(z):
+    """(1 / (1 + e^-z), 1 / (1 + e^z)), each to the last digits."""
+    e = np.exp(-np.abs(z))
+    small, large = e / (1 + e), 1 / (1 + e)
+    return np.where(z < 0, small, large), np.where(z < 0, large, small)
+
+
 def act(name, g):
-    """(act(g), act'(g))."""
+    """(act(g), act'(g)), to the last digits where they are small too."""
     if name == "identity":
         return g, np.ones_like(g)
     if name == "silu":
-        s = 1 / (1 + np.exp(-g))
-        return g * s, s * (1 + g * (1 - s))
+        s, rest = _sigmoid(g)
+        return g * s, s * (1 + g * rest)
     if name == "gelu":
-        c = 0.5 * (1 + _erf(g / math.sqrt(2)))
+        c = 0.5 * _erfc(-g / math.sqrt(2))
         return g * c, c + g * np.exp(-g * g / 2) / math.sqrt(2 * math.pi)
-    k = math.sqrt(2 / math.pi)
-    t = np.tanh(k * (g + 0.044715 * g ** 3))
-    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g)
+    # (1 + tanh z) / 2 = 1 / (1 + e^-2z)
+    k = 2 * math.sqrt(2 / math.pi)
+    s, rest = _sigmoid(k * (g + 0.044715 * g ** 3))
+    return g * s, s + g * s * rest * k * (1 + 3 * 0.044715 * g * g)
 
 
 def gated(x, wg, wu, name):
