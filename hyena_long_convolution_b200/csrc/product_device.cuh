@@ -400,6 +400,4 @@ __device__ __forceinline__ float2 activation_slope2(float2 g, float2 &d)
     }
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
-
 }  // namespace hyena

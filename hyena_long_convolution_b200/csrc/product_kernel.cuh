@@ -118,58 +118,27 @@ __device__ __forceinline__ bool join_parts(float (&v)[kV], const Plan &p, int un
     return true;
 }
 
-// A thread's values kN at a time, in a loop that stays one: each turn ends by moving
-// all of them kN places on, and the last leaves them where they were.  Code run once
-// per value, 64 times over, waits for its instructions: with 128 tokens the codes of
-// the outputs took 40 us that way.
-template <int kV, int kN>
-__device__ __forceinline__ void turn(float *v)
-{
-    float t[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) t[i] = v[i];
-#pragma unroll
-    for (int i = 0; i < kV - kN; ++i) v[i] = v[i + kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[kV - kN + i] = t[i];
-}
-
-template <int kV, int kN, class F>
-__device__ __forceinline__ void in_turns(F f)
-{
-    if constexpr (kV == kN) {
-        f(0);
-    } else {
-#pragma unroll 1
-        for (int j = 0; j < kV; j += kN) f(j);
-    }
-}
-
-// g[i] <- act(g[i]) u[i], the first `count` of kV.
+// g[i] <- act(g[i]) u[i] of kV each.
 template <int kAct, int kV>
-__device__ __forceinline__ void gate(float (&v)[2 * kV], int count)
+__device__ __forceinline__ void gate(float (&v)[2 * kV])
 {
 #pragma unroll
-    for (int j = 0; j < kV; j += 8) {
-        if (j >= count) break;
-#pragma unroll
-        for (int i = j; i < j + 8; i += 2) {
-            const float2 y = __fmul2_rn(activation2<kAct>(make_float2(v[i], v[i + 1])),
-                                        make_float2(v[kV + i], v[kV + i + 1]));
-            v[i] = y.x;
-            v[i + 1] = y.y;
-        }
+    for (int i = 0; i < kV; i += 2) {
+        const float2 y = __fmul2_rn(activation2<kAct>(make_float2(v[i], v[i + 1])),
+                                    make_float2(v[kV + i], v[kV + i + 1]));
+        v[i] = y.x;
+        v[i + 1] = y.y;
     }
 }
 
 template <int kV>
-__device__ __forceinline__ void gate(float (&v)[2 * kV], int act, int count)
+__device__ __forceinline__ void gate(float (&v)[2 * kV], int act)
 {
     switch (act) {
-        case HYENA_ACT_SILU: gate<HYENA_ACT_SILU, kV>(v, count); break;
-        case HYENA_ACT_GELU: gate<HYENA_ACT_GELU, kV>(v, count); break;
-        case HYENA_ACT_GELU_TANH: gate<HYENA_ACT_GELU_TANH, kV>(v, count); break;
-        default: gate<HYENA_ACT_IDENTITY, kV>(v, count); break;
+        case HYENA_ACT_SILU: gate<HYENA_ACT_SILU, kV>(v); break;
+        case HYENA_ACT_GELU: gate<HYENA_ACT_GELU, kV>(v); break;
+        case HYENA_ACT_GELU_TANH: gate<HYENA_ACT_GELU_TANH, kV>(v); break;
+        default: gate<HYENA_ACT_IDENTITY, kV>(v); break;
     }
 }
 

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreadsProduct, 1)
                     out.values(&c2, A.a.g_f32, n, m0, v, left);
                     out.values(&c3, A.a.g_f32, n, m0, v + kHalf, left);
                 }
-                gate<kHalf>(v, A.a.act, kHalf);
+                gate<kHalf>(v, A.a.act);
                 if (kF8 && A.a.q) {
                     // the largest of the row's 128 values: this half's and the other's
                     unsigned int mx = 0;
