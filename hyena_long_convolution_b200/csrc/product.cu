@@ -119,6 +119,11 @@ int allow_shared(const void *kernel, int bytes, std::atomic<unsigned long long> 
 // its rows empty (32 rows, 4096 -> 4096 x 11008: in e4m3 13 and 23 us, in bf16 34 and
 // 38).  Its smaller tiles pay
 //
+//   up to 32 rows always, so that a workspace of so few needs no parts.  With one weight
+//   in codes and a little more than a tile an SM that costs 17 to 32 rows something
+//   (4096 -> 19200: 24.9-25.5 and 20.8-22.6 us; 22016: 25.5-26.0 and 21.7-25.0), with
+//   more it saves (38016: 38-39 and 42-43);
+//
 //   up to 64 rows, for one weight in codes up to a tile an SM (4096 -> 18944: 19.4 and
 //   21.4 us; 22016: 33 and 22), for two in bf16 always (19200: 75 and 78);
 //   beyond, and for two weights in codes, while they leave SMs to share a tile's k
@@ -139,7 +144,9 @@ bool product_is_narrow(long long M, int N, bool fp8, bool gated)
 // 4096 -> 11008 126 and 107; 128 rows 50 and 38, 139 and 126), and of more rows while two
 // CTAs to a tile leave some SMs to dW beside it: 256 rows of 512 -> 1408 (8 tiles) 35 and
 // 25, of 2048 -> 4096 (32) 66 and 56, 700 of 1032 -> 2760 (54) 62 and 60, 200 of 4096 ->
-// 11008 (64) 163 and 165; but 1000 of 1032 -> 2760 (72) 71.5 and 74.6.
+// 11008 (64) 163 and 165; but 1000 of 1032 -> 2760 (72) 71.5 and 74.6.  The gradient
+// alone, pairs and columns: 256 rows of 2048 -> 4096 47 and 37, 4096 -> 4096 (64) 57 and
+// 52, 4096 -> 11008 (64) 118 and 119, 700 of 1032 -> 2760 41.5 and 43.
 bool ffn_dx_is_narrow(long long M, int D)
 {
     return M <= 128 || 2 * ((M + 127) / 128) * ((D + 127) / 128) <= product_sms() - 16;

@@ -22,8 +22,8 @@
 //
 // e4m3 codes: the sums over each 128 k go times their scales into registers (128 a
 // thread), since the scales are any fp32 numbers; the two halves of tensor memory then
-// change places every k-block.  8192 x 4096 -> 12288: 389-393 us, 2.1 PFLOP/s, 51% of
-// cycles active.  Of a tile's 31000 cycles 27000 go to 32 k-blocks of 840, which is the
+// change places every k-block.  8192 x 4096 -> 12288: 389-393 us in calls with pauses between
+// them, 2.1 PFLOP/s, 51% of cycles active; 440-460 back to back, by power.  Of a tile's 31000 cycles 27000 go to 32 k-blocks of 840, which is the
 // way round of a half, 1700, over two halves: 165 to issue its MMAs, 330 more until
 // warps that wait see them done (660 in the two warps that share a scheduler with the
 // MMA warp, whatever that scheduler is, since MMAs that wait for the tensor core hold

@@ -694,8 +694,9 @@ hyena_status_t hyena_fp8_quantize(const void *x, int64_t ld_x, hyena_dtype_t x_t
  *           One for M rows serves fewer, and any N, K.
  *
  * Products of codes are exact and summed in fp32 over each 128 channels; the
- * sums times their scales are summed in fp32 in the order of k.  Work split
- * over k (few rows) is joined in that order too, whichever part is done last.
+ * sums times the product of their two scales are summed in fp32 in the order of
+ * k.  (That product is formed first: beyond 3.4e38 it leaves Inf or NaN.)  Work
+ * split over k (few rows) is joined in that order too, whichever part is done last.
  * x and w are not written; y may overlap none of the inputs.
  */
 #define HYENA_PRODUCT_HEADER 4096
